@@ -1,0 +1,175 @@
+// chunk.cu -- several new tokens of each sequence at once: the rows that stay in the residual,
+// the rotation of the queries, and reading a chunk's tokens back.  (The blocks a chunk fills are
+// quantized by quantize.cu, its attention is in attend.cu.)
+#include <cstdint>
+
+#include "chunk_rows.cuh"
+#include "kvq_internal.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// One CTA per new token: its residual rows (keys rotated) when it lies behind its slot's last
+// whole block, and its rotated queries.  The rows of a block's first tokens (positions below
+// R floor(end / R)) were quantized by the launch before.  The CTA of a slot's first new token
+// sets the slot's length, which no CTA reads.
+// Bound by memory: each row is read and written once, 16 bytes a thread.
+template <bool BF16>
+__global__ void __launch_bounds__(kRowThreads) chunk_rows_kernel(const PagedView c, const ChunkTable t, const Rows k,
+                                                                 const Rows v, const RopeArgs rope, const Rows q,
+                                                                 const Rows q_out) {
+    const int64_t row = blockIdx.x;
+    const int b = slot_of(t.offsets, t.B, row);
+    const int64_t first = t.offsets[b], start = t.starts[b], end = start + t.offsets[b + 1] - first;
+    const int64_t tok = start + row - first;
+    if (first > row || end <= tok || start < 0) {           // not this library's table
+        if (threadIdx.x == 0) atomicOr(c.status, 8u);
+        return;
+    }
+    if (row == first && threadIdx.x == 0) c.seq_len[b] = static_cast<int32_t>(end);
+    const RowUnits ru = row_units(c.d, rope), plain = {0, c.d / 8};
+    const int n_k = tok >= end / c.R * c.R ? c.Hkv * ru.n : 0, n_v = n_k ? c.Hkv * plain.n : 0;
+    const int n_q = q.p ? c.Hq * ru.n : 0;
+    for (int i = threadIdx.x; i < n_k + n_v + n_q; i += kRowThreads) {
+        const bool is_k = i < n_k, is_q = i >= n_k + n_v;
+        const int j = is_k ? i : is_q ? i - n_k - n_v : i - n_k;
+        const int per = is_k || is_q ? ru.n : plain.n;
+        const int h = j / per, u = j - h * per;
+        const Rows &in = is_k ? k : is_q ? q : v;
+        uint16_t *dst = is_q ? q_out.p + row * q_out.ts + h * q_out.hs
+                             : (is_k ? c.kr : c.vr) + ((static_cast<int64_t>(b) * c.Hkv + h) * c.R + tok % c.R) * c.d;
+        int va, vb;
+        uint4 x, y;
+        rotated_unit<BF16>(in.p + row * in.ts + h * in.hs, u, is_k || is_q ? ru : plain, tok,
+                           is_k || is_q ? rope : RopeArgs{}, va, vb, x, y);
+        reinterpret_cast<uint4 *>(dst)[va] = x;
+        if (vb >= 0) reinterpret_cast<uint4 *>(dst)[vb] = y;
+    }
+}
+
+// One warp per (16-token tile of a slot that meets its chunk, kv head): the tile's tokens as e.
+// A quantized tile's words are unpacked from the fragment layout (include/kvq.h): each lane holds
+// two tokens x four channels per chunk of keys, two channels x four tokens of values; the
+// elements go through shared memory so that rows leave in 16-byte vectors.
+constexpr int kReadWarps = 4;
+
+template <int D, int N, bool BF16>
+__global__ void __launch_bounds__(32 * kReadWarps) chunk_read_kernel(const PagedView c, const ChunkTable t,
+                                                                     const Rows k_out, const Rows v_out) {
+    __shared__ __align__(16) uint16_t tile_s[kReadWarps][2][16][D + 8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kReadWarps + warp;
+    if (unit >= static_cast<int64_t>(t.n_tiles) * c.Hkv) return;
+    const int64_t ti = unit / c.Hkv;
+    const int h = static_cast<int>(unit % c.Hkv);
+    const int b = slot_of(t.tiles, t.B, ti);
+    const int64_t first = t.offsets[b], start = t.starts[b], end = start + t.offsets[b + 1] - first;
+    const int64_t tok0 = (start / 16 + ti - t.tiles[b]) * 16;
+    const int len = c.seq_len[b];
+    const int64_t tq = len > 0 ? len / c.R * c.R : 0;
+    if (start < 0 || end > len) {                  // the slot holds less than the host knew
+        if (lane == 0) atomicOr(c.status, 8u);
+        return;
+    }
+    uint16_t(*ks)[D + 8] = tile_s[warp][0];
+    uint16_t(*vs)[D + 8] = tile_s[warp][1];
+    if (tok0 >= tq) {
+        for (int i = lane; i < 16 * (D / 8); i += 32) {
+            const int r = i / (D / 8), v = i % (D / 8);
+            const int64_t tok = tok0 + r;
+            if (tok >= start && tok < end) {
+                const int64_t at = ((static_cast<int64_t>(b) * c.Hkv + h) * c.R + tok % c.R) * D;
+                reinterpret_cast<uint4 *>(ks[r])[v] = reinterpret_cast<const uint4 *>(c.kr + at)[v];
+                reinterpret_cast<uint4 *>(vs[r])[v] = reinterpret_cast<const uint4 *>(c.vr + at)[v];
+            }
+        }
+    } else {
+        const int64_t pi = tok0 / c.P;
+        const int page = pi < c.max_pages ? c.page_table[static_cast<int64_t>(b) * c.max_pages + pi] : -1;
+        if (page < 0 || page >= c.num_pages) {
+            if (lane == 0) atomicOr(c.status, 2u);
+            return;
+        }
+        constexpr int W = D * N / 64, TW = D * N / 2, B = 4 / N;
+        const int64_t slice = static_cast<int64_t>(page) * c.Hkv + h, pt = tok0 - pi * c.P;
+        const uint32_t *kw = c.kc + (slice * (c.P / 16) + pt / 16) * TW + lane * W;
+        const uint32_t *vw = c.vc + (slice * (c.P / 16) + pt / 16) * TW + lane * W;
+        const float *s_k = c.ks + (slice * (c.P / c.G) + pt / c.G) * D;
+        const int16_t *z_k = c.kz + (slice * (c.P / c.G) + pt / c.G) * D;
+        const int ngv = D / c.Gv, half_levels = 1 << (N - 1);
+        const float *s_v = c.vs + (slice * c.P + pt) * ngv;
+        const int16_t *z_v = c.vz + (slice * c.P + pt) * ngv;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const uint32_t kword = kw[j / B], vword = vw[j / B];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int sh = N * (2 * (j % B) + half);
+                const int row = (lane >> 2) + 8 * half;       // token of a key, channel of a value
+                uint32_t out[2];
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int ch = 16 * j + 4 * (lane & 3) + e;
+                    const int code = (kword >> (8 * e + sh)) & ((1 << N) - 1);
+                    const int z = c.sym ? half_levels : z_k[ch];
+                    f[e] = __fmul_rn(static_cast<float>(code - z), s_k[ch]);
+                }
+                out[0] = narrow2<BF16>(f[0], f[1]);
+                out[1] = narrow2<BF16>(f[2], f[3]);
+                *reinterpret_cast<uint2 *>(&ks[row][16 * j + 4 * (lane & 3)]) = make_uint2(out[0], out[1]);
+                const int vch = 16 * j + row, g = vch / c.Gv;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tk = 4 * (lane & 3) + e;
+                    const int code = (vword >> (8 * e + sh)) & ((1 << N) - 1);
+                    const int z = c.sym ? half_levels : z_v[tk * ngv + g];
+                    vs[tk][vch] = static_cast<uint16_t>(
+                        narrow2<BF16>(__fmul_rn(static_cast<float>(code - z), s_v[tk * ngv + g]), 0.0f));
+                }
+            }
+        }
+    }
+    __syncwarp();
+    for (int i = lane; i < 16 * (D / 8); i += 32) {
+        const int r = i / (D / 8), v = i % (D / 8);
+        const int64_t tok = tok0 + r, row = first + tok - start;
+        if (tok < start || tok >= end || row < 0 || row >= t.tokens) continue;
+        reinterpret_cast<uint4 *>(k_out.p + row * k_out.ts + h * k_out.hs)[v] = reinterpret_cast<uint4 *>(ks[r])[v];
+        reinterpret_cast<uint4 *>(v_out.p + row * v_out.ts + h * v_out.hs)[v] = reinterpret_cast<uint4 *>(vs[r])[v];
+    }
+}
+
+template <int D, int N>
+void read_launch(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v, unsigned grid, cudaStream_t s) {
+    if (c.bf16) chunk_read_kernel<D, N, true><<<grid, 32 * kReadWarps, 0, s>>>(c, t, k, v);
+    else chunk_read_kernel<D, N, false><<<grid, 32 * kReadWarps, 0, s>>>(c, t, k, v);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_rows(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v,
+                              const RopeArgs &rope, const Rows &q, const Rows &q_out, cudaStream_t s) {
+    if (t.tokens == 0) return cudaSuccess;
+    const unsigned grid = static_cast<unsigned>(t.tokens);
+    if (c.bf16) chunk_rows_kernel<true><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
+    else chunk_rows_kernel<false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_read(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v, cudaStream_t s) {
+    if (t.n_tiles == 0) return cudaSuccess;
+    const int64_t units = static_cast<int64_t>(t.n_tiles) * c.Hkv;
+    const unsigned grid = static_cast<unsigned>((units + kReadWarps - 1) / kReadWarps);
+    if (c.d == 64 && c.bits == 2) read_launch<64, 2>(c, t, k, v, grid, s);
+    else if (c.d == 64) read_launch<64, 4>(c, t, k, v, grid, s);
+    else if (c.bits == 2) read_launch<128, 2>(c, t, k, v, grid, s);
+    else read_launch<128, 4>(c, t, k, v, grid, s);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace kvq

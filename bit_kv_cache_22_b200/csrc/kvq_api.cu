@@ -1093,6 +1093,323 @@ kvq_status kvq_paged_check_device(kvq_paged *h) {
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Chunks: several new tokens of each slot in one call (kvq_chunk).
+//
+// The host lays every decision out in the plan's table: packed offsets, starts, the 16-token
+// tiles a read visits and the blocks an append quantizes.  The kernels take positions from the
+// table, never from the lengths the host keeps, so a captured call replays as it was captured.
+// ---------------------------------------------------------------------------
+namespace {
+
+// The table, as int32: offsets [B + 1], starts [B], read tiles before each slot [B + 1], blocks
+// [n_blocks][2] = (slot, block).
+struct ChunkLayout {
+    int64_t starts, tiles, blocks, end;
+};
+ChunkLayout chunk_layout(int64_t B, int64_t n_blocks) {
+    ChunkLayout l;
+    l.starts = B + 1;
+    l.tiles = l.starts + B;
+    l.blocks = l.tiles + B + 1;
+    l.end = l.blocks + 2 * n_blocks;
+    return l;
+}
+
+constexpr int64_t kMaxInt = 0x7fffffff;
+
+kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t R, const int32_t *counts,
+                      const int32_t *starts, kvq_chunk *out, void *table, size_t table_bytes) {
+    if (!counts || !out) return fail(KVQ_ERR_INVALID_ARG, "counts and out must be non-NULL");
+    if (q_heads / kv_heads > 128)
+        return fail(KVQ_ERR_UNSUPPORTED, "at most 128 query heads per kv head (got %d)", q_heads / kv_heads);
+    int64_t tokens = 0, blocks = 0, tiles = 0;
+    for (int b = 0; b < batch; ++b) {
+        const int64_t n = counts[b], s = starts ? starts[b] : 0;
+        if (n < 0 || s < 0 || s + n > kMaxInt)
+            return fail(KVQ_ERR_INVALID_ARG, "slot %d: %lld tokens from %lld", b, static_cast<long long>(n),
+                        static_cast<long long>(s));
+        if (n == 0) continue;
+        tokens += n;
+        if (R > 0) {
+            blocks += (s + n) / R - s / R;
+            tiles += (s + n + 15) / 16 - s / 16;
+        }
+    }
+    const ChunkLayout l = chunk_layout(batch, blocks);
+    if (tokens * q_heads > kMaxInt || tiles * kv_heads > kMaxInt || l.end > kMaxInt)
+        return fail(KVQ_ERR_INVALID_ARG, "too many tokens for one chunk (%lld)", static_cast<long long>(tokens));
+    std::memset(out, 0, sizeof *out);
+    out->batch = batch;
+    out->q_heads = q_heads;
+    out->kv_heads = kv_heads;
+    out->head_dim = d;
+    out->residual = R;
+    out->blocks = static_cast<int32_t>(blocks);
+    out->read_tiles = static_cast<int32_t>(tiles);
+    out->tokens = tokens;
+    out->table_bytes = static_cast<size_t>(l.end) * sizeof(int32_t);
+    out->counts = counts;
+    out->starts = starts;
+    if (!table) return ok();
+    if (table_bytes < out->table_bytes)
+        return fail(KVQ_ERR_INVALID_ARG, "the table needs %zu bytes, got %zu", out->table_bytes, table_bytes);
+    int32_t *t = static_cast<int32_t *>(table), *blk = t + l.blocks;
+    int32_t row = 0, tile = 0;
+    for (int b = 0; b < batch; ++b) {
+        const int64_t n = counts[b], s = starts ? starts[b] : 0;
+        t[b] = row;
+        t[l.starts + b] = static_cast<int32_t>(s);
+        t[l.tiles + b] = tile;
+        row += static_cast<int32_t>(n);
+        if (R == 0 || n == 0) continue;
+        tile += static_cast<int32_t>((s + n + 15) / 16 - s / 16);
+        for (int64_t i = s / R; i < (s + n) / R; ++i) {
+            *blk++ = b;
+            *blk++ = static_cast<int32_t>(i);
+        }
+    }
+    t[batch] = row;
+    t[l.tiles + batch] = tile;
+    return ok();
+}
+
+kvq::ChunkTable chunk_table(const kvq_chunk *p) {
+    const ChunkLayout l = chunk_layout(p->batch, p->blocks);
+    kvq::ChunkTable t{};
+    t.offsets = p->table;
+    t.starts = p->table + l.starts;
+    t.tiles = p->table + l.tiles;
+    t.blocks = p->table + l.blocks;
+    t.n_blocks = p->blocks;
+    t.n_tiles = p->read_tiles;
+    t.tokens = p->tokens;
+    t.B = p->batch;
+    return t;
+}
+
+kvq_status check_rows(const kvq_rows *r, const char *name) {
+    if (!r || !r->data || !aligned16(r->data))
+        return fail(KVQ_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", name);
+    if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride % 8 != 0 || r->head_stride % 8 != 0)
+        return fail(KVQ_ERR_INVALID_ARG, "the strides of %s must be non-negative multiples of 8 elements", name);
+    return KVQ_OK;
+}
+
+kvq::Rows rows_of(const kvq_rows *r) {
+    return {static_cast<uint16_t *>(r->data), r->token_stride, r->head_stride};
+}
+
+kvq_status check_chunk(const kvq_chunk *p) {
+    if (!p || !p->counts) return fail(KVQ_ERR_INVALID_ARG, "plan is NULL or has no counts");
+    if (!p->table || !aligned16(p->table))
+        return fail(KVQ_ERR_INVALID_ARG, "the plan's table must be on the device, 16-byte aligned");
+    return KVQ_OK;
+}
+
+kvq_status check_chunk_for(const kvq_paged *h, const kvq_chunk *p) {
+    if (!h) return fail(KVQ_ERR_INVALID_ARG, "cache is NULL");
+    const kvq_status st = check_chunk(p);
+    if (st != KVQ_OK) return st;
+    const kvq_config &c = h->base.cfg;
+    if (!p->starts || p->batch != c.batch || p->q_heads != c.q_heads || p->kv_heads != c.kv_heads ||
+        p->head_dim != c.head_dim || p->residual != c.residual)
+        return fail(KVQ_ERR_INVALID_ARG, "the plan is for another geometry");
+    return KVQ_OK;
+}
+
+// Every slot with new tokens holds them (a chunk that is read or attended).
+kvq_status check_held(const kvq_paged *h, const kvq_chunk *p) {
+    for (int b = 0; b < p->batch; ++b)
+        if (p->counts[b] > 0 && static_cast<int64_t>(p->starts[b]) + p->counts[b] > h->len[b])
+            return fail(KVQ_ERR_STATE, "slot %d holds %lld tokens, the chunk ends at %lld", b,
+                        static_cast<long long>(h->len[b]),
+                        static_cast<long long>(p->starts[b]) + p->counts[b]);
+    return KVQ_OK;
+}
+
+kvq::PagedView paged_view(const kvq_paged *h) {
+    const kvq_config &c = h->base.cfg;
+    kvq::PagedView v{};
+    v.kc = static_cast<const uint32_t *>(h->base.buf.k_codes);
+    v.vc = static_cast<const uint32_t *>(h->base.buf.v_codes);
+    v.ks = h->base.buf.k_scales;
+    v.vs = h->base.buf.v_scales;
+    v.kz = h->base.buf.k_zeros;
+    v.vz = h->base.buf.v_zeros;
+    v.kr = static_cast<uint16_t *>(h->base.buf.k_residual);
+    v.vr = static_cast<uint16_t *>(h->base.buf.v_residual);
+    v.page_table = h->page_table;
+    v.seq_len = h->seq_len;
+    v.status = h->base.arrivals + static_cast<int64_t>(c.batch) * c.q_heads;
+    v.max_pages = h->max_pages;
+    v.num_pages = h->num_pages;
+    v.P = h->page_tokens;
+    v.B = c.batch;
+    v.Hq = c.q_heads;
+    v.Hkv = c.kv_heads;
+    v.d = c.head_dim;
+    v.G = c.group_k;
+    v.Gv = c.group_v;
+    v.R = c.residual;
+    v.bits = c.bits;
+    v.sym = c.symmetric != 0;
+    v.bf16 = c.dtype == KVQ_BF16;
+    return v;
+}
+
+kvq::AttendArgs attend_args(const kvq_chunk *p, const kvq_rows *q, const kvq_rows *o, bool bf16) {
+    kvq::AttendArgs a{};
+    a.t = chunk_table(p);
+    a.q = rows_of(q);
+    a.o = rows_of(o);
+    a.B = p->batch;
+    a.Hq = p->q_heads;
+    a.Hkv = p->kv_heads;
+    a.d = p->head_dim;
+    a.bf16 = bf16;
+    a.scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(p->head_dim)));
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_plan_chunk(const kvq_paged_config *cfg, const int32_t *counts, const int32_t *starts, kvq_chunk *out,
+                          void *table, size_t table_bytes) {
+    const kvq_status st = validate_paged(cfg);
+    if (st != KVQ_OK) return st;
+    if (!starts) return fail(KVQ_ERR_INVALID_ARG, "starts is NULL");
+    const kvq_config &g = cfg->geom;
+    return plan_chunk(g.batch, g.q_heads, g.kv_heads, g.head_dim, g.residual, counts, starts, out, table, table_bytes);
+}
+
+kvq_status kvq_plan_prompt(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, const int32_t *counts,
+                           kvq_chunk *out, void *table, size_t table_bytes) {
+    if (batch < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0)
+        return fail(KVQ_ERR_INVALID_ARG, "batch and heads must be >= 1 and q_heads a multiple of kv_heads");
+    if (batch > 65535 || q_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "batch and q_heads must be <= 65535");
+    if (head_dim != 64 && head_dim != 128)
+        return fail(KVQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
+    return plan_chunk(batch, q_heads, kv_heads, head_dim, 0, counts, nullptr, out, table, table_bytes);
+}
+
+kvq_status kvq_prompt_attention(const kvq_chunk *plan, int32_t dtype, const kvq_rows *q, const kvq_rows *k,
+                                const kvq_rows *v, const kvq_rows *o, uint32_t *status, void *stream) {
+    kvq_status st = check_chunk(plan);
+    if (st == KVQ_OK && plan->residual != 0) st = fail(KVQ_ERR_INVALID_ARG, "not a prompt plan");
+    if (st == KVQ_OK && dtype != KVQ_FP16 && dtype != KVQ_BF16)
+        st = fail(KVQ_ERR_INVALID_ARG, "dtype must be KVQ_FP16 or KVQ_BF16");
+    if (st != KVQ_OK) return st;
+    if (plan->tokens == 0) return ok();
+    const kvq_rows *rows[] = {q, k, v, o};
+    const char *names[] = {"q", "k", "v", "o"};
+    for (int i = 0; i < 4 && st == KVQ_OK; ++i) st = check_rows(rows[i], names[i]);
+    if (st != KVQ_OK) return st;
+    kvq::AttendArgs a = attend_args(plan, q, o, dtype == KVQ_BF16);
+    a.k = rows_of(k);
+    a.v = rows_of(v);
+    a.status = status;
+    const cudaError_t e = kvq::launch_attend(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+    return ok();
+}
+
+kvq_status kvq_paged_append_chunk(kvq_paged *h, const kvq_chunk *plan, const kvq_rows *k, const kvq_rows *v,
+                                  const kvq_rope *rope, const kvq_rows *q, const kvq_rows *q_out, void *stream) {
+    kvq_status st = check_chunk_for(h, plan);
+    if (st != KVQ_OK) return st;
+    if (plan->tokens == 0) return ok();
+    st = check_rows(k, "k");
+    if (st == KVQ_OK) st = check_rows(v, "v");
+    if (st == KVQ_OK && q) st = check_rows(q, "q");
+    if (st == KVQ_OK && q) st = check_rows(q_out, "q_out");
+    if (st != KVQ_OK) return st;
+    const kvq_config &c = h->base.cfg;
+    kvq::RopeArgs r{};
+    if (rope) {
+        if (!rope->cos || !rope->sin || !aligned16(rope->cos) || !aligned16(rope->sin))
+            return fail(KVQ_ERR_INVALID_ARG, "cos and sin must be non-NULL and 16-byte aligned");
+        if (rope->rot_dim < 16 || rope->rot_dim > c.head_dim || rope->rot_dim % 16 != 0)
+            return fail(KVQ_ERR_INVALID_ARG, "rot_dim (%d) must be a multiple of 16, at most head_dim", rope->rot_dim);
+        r = {rope->cos, rope->sin, rope->positions, rope->rot_dim, rope->interleaved != 0};
+    } else if (q) {
+        return fail(KVQ_ERR_INVALID_ARG, "queries are given but no rope to rotate them with");
+    }
+    for (int b = 0; b < c.batch; ++b) {
+        if (plan->counts[b] == 0) continue;
+        const int64_t start = plan->starts[b], end = start + plan->counts[b];
+        const int64_t len = h->len[b] > 0 ? h->len[b] : 0;
+        if (start > len)
+            return fail(KVQ_ERR_STATE, "slot %d holds %lld tokens, the chunk starts at %lld", b,
+                        static_cast<long long>(len), static_cast<long long>(start));
+        if (start < len / c.residual * c.residual && start % c.residual != 0)
+            return fail(KVQ_ERR_STATE, "slot %d: tokens from %lld cannot be dropped, their block is quantized", b,
+                        static_cast<long long>(start));
+        if (end / c.residual * c.residual > c.capacity)
+            return fail(KVQ_ERR_CAPACITY, "slot %d: %lld tokens exceed capacity %lld", b, static_cast<long long>(end),
+                        static_cast<long long>(c.capacity));
+        if (rope && end > rope->positions)
+            return fail(KVQ_ERR_INVALID_ARG, "slot %d ends at position %lld, the angles at %lld", b,
+                        static_cast<long long>(end), static_cast<long long>(rope->positions));
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    kvq::QuantizeArgs a = paged_quantize_args(h);
+    a.chunk.t = chunk_table(plan);
+    a.chunk.k = rows_of(k);
+    a.chunk.v = rows_of(v);
+    a.chunk.rope = r;
+    a.chunk.kr = static_cast<const uint16_t *>(h->base.buf.k_residual);
+    a.chunk.vr = static_cast<const uint16_t *>(h->base.buf.v_residual);
+    a.chunk.R = c.residual;
+    cudaError_t e = kvq::launch_quantize_chunk(a, s);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk quantize launch");
+    const kvq::Rows none{};
+    e = kvq::launch_chunk_rows(paged_view(h), a.chunk.t, a.chunk.k, a.chunk.v, r, q ? rows_of(q) : none,
+                               q ? rows_of(q_out) : none, s);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk rows launch");
+    for (int b = 0; b < c.batch; ++b)
+        if (plan->counts[b] > 0) h->len[b] = static_cast<int64_t>(plan->starts[b]) + plan->counts[b];
+    return ok();
+}
+
+kvq_status kvq_paged_read_chunk(kvq_paged *h, const kvq_chunk *plan, const kvq_rows *k, const kvq_rows *v,
+                                void *stream) {
+    kvq_status st = check_chunk_for(h, plan);
+    if (st != KVQ_OK) return st;
+    if (plan->tokens == 0) return ok();
+    st = check_rows(k, "k");
+    if (st == KVQ_OK) st = check_rows(v, "v");
+    if (st == KVQ_OK) st = check_held(h, plan);
+    if (st != KVQ_OK) return st;
+    const cudaError_t e = kvq::launch_chunk_read(paged_view(h), chunk_table(plan), rows_of(k), rows_of(v),
+                                                 static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "chunk read launch");
+    return ok();
+}
+
+kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const kvq_rows *q, const kvq_rows *o,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
+    kvq_status st = check_chunk_for(h, plan);
+    if (st != KVQ_OK) return st;
+    if (plan->tokens == 0) return ok();
+    st = check_rows(q, "q");
+    if (st == KVQ_OK) st = check_rows(o, "o");
+    if (st == KVQ_OK) st = check_held(h, plan);
+    if (st != KVQ_OK) return st;
+    (void)workspace;
+    (void)workspace_bytes;
+    kvq::AttendArgs a = attend_args(plan, q, o, h->base.cfg.dtype == KVQ_BF16);
+    a.cache = paged_view(h);
+    a.status = a.cache.status;
+    const cudaError_t e = kvq::launch_attend(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+    return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // LogQuant retention ("Resumo Técnico: LogQuant", section 2, Estratégia de
 // Filtragem Baseada em Logaritmos; section 4): a cache whose full-precision
 // store holds up to 3W tokens and, whenever it fills, quantizes every other one

@@ -40,6 +40,41 @@ void count_launches(int n);
 // cudaError_t of the launch.
 // ---------------------------------------------------------------------------
 
+// Packed rows of e elements: row i of head h at p + i * ts + h * hs.
+struct Rows {
+    uint16_t *p;
+    int64_t ts, hs;
+};
+
+// A chunk's tables on the device (see kvq_chunk): slot b's new tokens are packed rows
+// offsets[b] .. offsets[b + 1] - 1 and tokens starts[b] ... of its sequence.
+struct ChunkTable {
+    const int32_t *offsets;      // [B + 1]
+    const int32_t *starts;       // [B]
+    const int32_t *tiles;        // [B + 1]: 16-token tiles of the slots before
+    const int32_t *blocks;       // [n_blocks][2]: slot, block of R tokens
+    int n_blocks, n_tiles;
+    int64_t tokens;
+    int B;
+};
+
+struct RopeArgs {
+    const float *cos, *sin;      // [positions][rot / 2]; NULL: no rotation
+    int64_t positions;
+    int rot;
+    bool pairs;                  // channels (2i, 2i + 1) instead of (i, i + rot / 2)
+};
+
+// The rows a chunk's block is made of: tokens before starts[b] are residual rows, the others
+// packed rows, the keys' rotated.
+struct ChunkSource {
+    ChunkTable t;
+    Rows k, v;
+    RopeArgs rope;
+    const uint16_t *kr, *vr;     // residual [B * Hkv][R][d]
+    int R;
+};
+
 struct QuantizeArgs {
     const uint16_t *xk, *xv;     // e [BH][*][d]; slice stride in elements below
     int64_t in_bh_stride;        // elements between consecutive (b,h) slices
@@ -71,8 +106,11 @@ struct QuantizeArgs {
     uint32_t *k_out;
     int n_out;
     int gpc;                     // key groups per CTA (1, or 2 for short groups: set by the launch)
+    ChunkSource chunk;           // launch_quantize_chunk: where the rows come from
 };
 cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t s);
+// The blocks of a chunk (a.chunk), into the paged pool of `a`.
+cudaError_t launch_quantize_chunk(const QuantizeArgs &a, cudaStream_t s);
 
 // For both (src, dst) pairs: dst[bh][dst_row0 + i][:] = src[bh][src_row0 + i][:],
 // i < rows (e elements); one launch.
@@ -175,6 +213,43 @@ cudaError_t launch_paged_residual(const uint16_t *xk, const uint16_t *xv, int64_
 // t_O [rows][d] from n partials o_all [n][rows][d], m_all / l_all [n][rows] (log2 units).
 cudaError_t launch_merge_partials(const float *o_all, const float *m_all, const float *l_all, int n,
                                   int64_t rows, int d, float *out, cudaStream_t s);
+// ---------------------------------------------------------------------------
+// chunks (chunk.cu)
+// ---------------------------------------------------------------------------
+
+// The paged cache as the chunk kernels read it.
+struct PagedView {
+    const uint32_t *kc, *vc;
+    const float *ks, *vs;
+    const int16_t *kz, *vz;      // unused when sym
+    uint16_t *kr, *vr;           // residual [B][Hkv][R][d]
+    const int32_t *page_table;   // [B][max_pages]
+    int32_t *seq_len;            // [B]
+    unsigned int *status;
+    int max_pages, num_pages, P;
+    int B, Hq, Hkv, d, G, Gv, R, bits;
+    bool sym, bf16;
+};
+
+// Rows of the new tokens that stay in the residual (keys rotated), the queries rotated from q
+// to q_out (q.p NULL: none), and seq_len of every slot with new tokens.  One launch.
+cudaError_t launch_chunk_rows(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v,
+                              const RopeArgs &rope, const Rows &q, const Rows &q_out, cudaStream_t s);
+// The new tokens as the cache holds them, widened to e.  One launch.
+cudaError_t launch_chunk_read(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v, cudaStream_t s);
+
+struct AttendArgs {
+    ChunkTable t;
+    Rows q, o;
+    Rows k, v;                   // a prompt's keys and values (cache.kc NULL)
+    PagedView cache;             // or the paged cache
+    int B, Hq, Hkv, d;
+    bool bf16;
+    float scale;                 // log2(e) / sqrt(d)
+    unsigned int *status;        // or NULL
+};
+cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s);
+
 // The compute capability the library's kernels were compiled for (major * 10 + minor, as
 // the CUDA runtime reports it for a loaded kernel), or -1 when it cannot be read.
 int binary_version();

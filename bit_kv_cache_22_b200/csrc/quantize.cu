@@ -29,6 +29,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "chunk_rows.cuh"
 #include "kvq_internal.cuh"
 
 namespace kvq {
@@ -304,11 +305,41 @@ __device__ void load_group(const uint16_t *slice, int64_t tok0, const int32_t *r
     }
 }
 
+// The rows of one group of a chunk's block, tokens tok0 .. tok0+G-1 of slot b: those before the
+// chunk's start from the residual (rotated when they were new), the others from the packed rows,
+// rotated as `rope` says.
+template <bool BF16>
+__device__ void load_chunk_group(const ChunkSource &c, const Rows &rows, const RopeArgs &rope, const uint16_t *res,
+                                 int b, int h, int Hkv, int64_t tok0, unsigned int *status, uint16_t *dst, int G,
+                                 int d) {
+    const int64_t start = c.t.starts[b], row0 = static_cast<int64_t>(c.t.offsets[b]) - start;
+    const uint16_t *res_h = res + (static_cast<int64_t>(b) * Hkv + h) * c.R * d;
+    uint4 *d4 = reinterpret_cast<uint4 *>(dst);
+    const RowUnits ru = row_units(d, rope);
+    for (int i = threadIdx.x; i < G * ru.n; i += blockDim.x) {
+        const int t = i / ru.n, u = i - t * ru.n;
+        const int64_t tok = tok0 + t, row = row0 + tok;
+        const uint16_t *src = tok < start ? res_h + tok % c.R * d : rows.p + row * rows.ts + h * rows.hs;
+        int va = u < ru.pairs ? u : u + ru.pairs, vb = u < ru.pairs ? u + ru.pairs : -1;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+        if (tok >= start && (row < 0 || row >= c.t.tokens)) {
+            atomicOr(status, 8u);
+        } else if (tok < start) {
+            x = read_once(src, va);
+            if (vb >= 0) y = read_once(src, vb);
+        } else {
+            rotated_unit<BF16>(src, u, ru, tok, rope, va, vb, x, y);
+        }
+        d4[t * (d / 8) + va] = x;
+        if (vb >= 0) d4[t * (d / 8) + vb] = y;
+    }
+}
+
 // BATCH: the value parameters batched per warp (groups of 64 tokens or more, four or more
 // token pairs per warp); else computed per token pair.  UNROLL: the value phase's token-pair
 // loops unrolled by two (eight or more token pairs per warp).  BF16: the inputs are bf16, else
-// fp16.
-template <int D, int N, bool BATCH, bool UNROLL, bool BF16>
+// fp16.  CHUNK: a chunk's blocks (a.chunk), CTA x = block * (CTAs per block) + part, y = kv head.
+template <int D, int N, bool BATCH, bool UNROLL, bool BF16, bool CHUNK>
 __global__ void __launch_bounds__(kQuantThreads, 4) quantize_pack_kernel(const QuantizeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int d = D, bits = N;
@@ -329,10 +360,22 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quantize_pack_kernel(const Q
     const int64_t in_tok = a.in_tok0 + grp * G;
     int64_t out_tok = a.out_tok0 + grp * G;
     int64_t slice = bh, cap = a.cap;               // output slice and its token capacity
-    if (a.page_table) {
+    int slot = 0;
+    if constexpr (CHUNK) {
+        const int parts = a.chunk.R / G;
+        const int32_t *blk = a.chunk.t.blocks + 2 * (grp / parts);
+        slot = blk[0];
+        if (slot < 0 || slot >= a.chunk.t.B || blk[1] < 0) {
+            if (threadIdx.x == 0) atomicOr(a.status, 8u);
+            return;
+        }
+        out_tok = static_cast<int64_t>(blk[1]) * a.chunk.R + grp % parts * G;
+    }
+    const int64_t tok0 = out_tok;                  // first token in its sequence
+    if (CHUNK || a.page_table) {
         // paged pool: the group's page of its sequence (groups never straddle pages)
-        const int64_t b = a.seq0 + bh / a.Hkv;
-        if (a.seq_len) {                           // flush: only sequences whose residual just filled
+        const int64_t b = CHUNK ? slot : a.seq0 + bh / a.Hkv;
+        if (!CHUNK && a.seq_len) {                           // flush: only sequences whose residual just filled
             const int64_t len = a.seq_len[b], R = a.n_groups * GK;
             if (len <= 0 || len % R != 0) return;
             out_tok = len - R + grp * G;
@@ -352,9 +395,13 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quantize_pack_kernel(const Q
 
     // ------------------------------ keys ------------------------------
     const int32_t *rows = a.in_rows ? a.in_rows + grp * G : nullptr;
-    load_group(a.xk + bh * a.in_bh_stride, in_tok, rows, a.in_rows_limit, a.status, xs, G, d);
+    if constexpr (CHUNK) {
+        load_chunk_group<BF16>(a.chunk, a.chunk.k, a.chunk.rope, a.chunk.kr, slot, bh, a.Hkv, tok0, a.status, xs, G, d);
+    } else {
+        load_group(a.xk + bh * a.in_bh_stride, in_tok, rows, a.in_rows_limit, a.status, xs, G, d);
+    }
     __syncthreads();
-    if (a.n_out > 0) {
+    if (!CHUNK && a.n_out > 0) {
         // dense-and-sparse keys: per token, the n_out entries of largest magnitude (ties: the
         // lower channel) are written as outlier words and set to +0 in the dense part
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -454,7 +501,10 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quantize_pack_kernel(const Q
     __syncthreads();
 
     // ------------------------------ values ----------------------------
-    load_group(a.xv + bh * a.in_bh_stride, in_tok, rows, a.in_rows_limit, a.status, xs, G, d);
+    if constexpr (CHUNK)
+        load_chunk_group<BF16>(a.chunk, a.chunk.v, RopeArgs{}, a.chunk.vr, slot, bh, a.Hkv, tok0, a.status, xs, G, d);
+    else
+        load_group(a.xv + bh * a.in_bh_stride, in_tok, rows, a.in_rows_limit, a.status, xs, G, d);
     __syncthreads();
     {
         // one token per half-warp (two per warp).  With four or more token pairs per warp, a warp
@@ -728,33 +778,34 @@ size_t quantize_smem_bytes(int d, int G, int Gv) {
            static_cast<size_t>(d) * 16 + static_cast<size_t>(G) * (d / Gv) * 16;
 }
 
+namespace {
+
 using QuantizeKernel = void (*)(const QuantizeArgs);
-template <int D, int N>
+template <int D, int N, bool CHUNK>
 QuantizeKernel quantize_instance(bool batch, bool unroll, bool bf16) {
     if (bf16) {
-        if (!batch) return quantize_pack_kernel<D, N, false, false, true>;
-        return unroll ? quantize_pack_kernel<D, N, true, true, true> : quantize_pack_kernel<D, N, true, false, true>;
+        if (!batch) return quantize_pack_kernel<D, N, false, false, true, CHUNK>;
+        return unroll ? quantize_pack_kernel<D, N, true, true, true, CHUNK>
+                      : quantize_pack_kernel<D, N, true, false, true, CHUNK>;
     }
-    if (!batch) return quantize_pack_kernel<D, N, false, false, false>;
-    return unroll ? quantize_pack_kernel<D, N, true, true, false> : quantize_pack_kernel<D, N, true, false, false>;
+    if (!batch) return quantize_pack_kernel<D, N, false, false, false, CHUNK>;
+    return unroll ? quantize_pack_kernel<D, N, true, true, false, CHUNK>
+                  : quantize_pack_kernel<D, N, true, false, false, CHUNK>;
 }
 
-cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t s) {
-    if (a.n_groups == 0 || a.BH == 0) return cudaSuccess;
-    // short key groups of a contiguous cache go two to a CTA, so a CTA streams 64 tokens and
-    // the value parameters are batched (paged pools and row lists keep one group per CTA)
-    QuantizeArgs b = a;
-    b.gpc = (a.G / 2 < 4 * (kQuantThreads / 32) && a.n_groups % 2 == 0 && !a.page_table && !a.in_rows) ? 2 : 1;
+template <bool CHUNK>
+cudaError_t launch_instance(const QuantizeArgs &b, dim3 grid, cudaStream_t s) {
+    const QuantizeArgs &a = b;
     const int tokens = b.gpc * a.G;
     const size_t smem = quantize_smem_bytes(a.d, tokens, a.Gv);
     void (*kernel)(const QuantizeArgs) = nullptr;
     int variant = -1;
     const bool batch = tokens / 2 >= 4 * (kQuantThreads / 32);
     const bool unroll = tokens / 2 >= 8 * (kQuantThreads / 32);
-    if (a.d == 64 && a.bits == 2) kernel = quantize_instance<64, 2>(batch, unroll, a.bf16), variant = 0;
-    else if (a.d == 64 && a.bits == 4) kernel = quantize_instance<64, 4>(batch, unroll, a.bf16), variant = 1;
-    else if (a.d == 128 && a.bits == 2) kernel = quantize_instance<128, 2>(batch, unroll, a.bf16), variant = 2;
-    else if (a.d == 128 && a.bits == 4) kernel = quantize_instance<128, 4>(batch, unroll, a.bf16), variant = 3;
+    if (a.d == 64 && a.bits == 2) kernel = quantize_instance<64, 2, CHUNK>(batch, unroll, a.bf16), variant = 0;
+    else if (a.d == 64 && a.bits == 4) kernel = quantize_instance<64, 4, CHUNK>(batch, unroll, a.bf16), variant = 1;
+    else if (a.d == 128 && a.bits == 2) kernel = quantize_instance<128, 2, CHUNK>(batch, unroll, a.bf16), variant = 2;
+    else if (a.d == 128 && a.bits == 4) kernel = quantize_instance<128, 4, CHUNK>(batch, unroll, a.bf16), variant = 3;
     if (!kernel) return cudaErrorInvalidValue;
     variant = 6 * variant + (a.bf16 ? 3 : 0) + (batch ? (unroll ? 2 : 1) : 0);
     // opt in to the largest dynamic shared memory any configuration needs, once per device and variant
@@ -768,10 +819,33 @@ cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev][variant] = true;
     }
-    dim3 grid(static_cast<unsigned>(a.n_groups / b.gpc), static_cast<unsigned>(a.BH));
     kernel<<<grid, kQuantThreads, smem, s>>>(b);
     count_launches(1);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t s) {
+    if (a.n_groups == 0 || a.BH == 0) return cudaSuccess;
+    // short key groups of a contiguous cache go two to a CTA, so a CTA streams 64 tokens and
+    // the value parameters are batched (paged pools and row lists keep one group per CTA)
+    QuantizeArgs b = a;
+    b.gpc = (a.G / 2 < 4 * (kQuantThreads / 32) && a.n_groups % 2 == 0 && !a.page_table && !a.in_rows) ? 2 : 1;
+    const dim3 grid(static_cast<unsigned>(a.n_groups / b.gpc), static_cast<unsigned>(a.BH));
+    return launch_instance<false>(b, grid, s);
+}
+
+cudaError_t launch_quantize_chunk(const QuantizeArgs &a, cudaStream_t s) {
+    if (a.chunk.t.n_blocks == 0) return cudaSuccess;
+    // two short key groups to a CTA where a block holds an even number of them: pages hold whole
+    // blocks, so the pair lies in one page
+    QuantizeArgs b = a;
+    const int groups = a.chunk.R / a.G;
+    b.gpc = (a.G / 2 < 4 * (kQuantThreads / 32) && groups % 2 == 0) ? 2 : 1;
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.chunk.t.n_blocks) * (groups / b.gpc)),
+                    static_cast<unsigned>(a.Hkv));
+    return launch_instance<true>(b, grid, s);
 }
 
 cudaError_t launch_copy_rows(const uint16_t *src0, const uint16_t *src1, int64_t src_bh_stride,

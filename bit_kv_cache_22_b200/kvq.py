@@ -39,7 +39,9 @@ EXPORTED = ("kvq_get_sizes", "kvq_create", "kvq_destroy", "kvq_reset", "kvq_pref
             "kvq_paged_decode_attention", "kvq_paged_release", "kvq_paged_seq_len",
             "kvq_paged_decode_splits", "kvq_paged_check_device", "kvq_logquant_get_sizes",
             "kvq_logquant_create", "kvq_logquant_retained", "kvq_set_key_outliers", "kvq_plan_decode",
-            "kvq_binary_arch", "kvq_set_decode_kernel")
+            "kvq_binary_arch", "kvq_set_decode_kernel", "kvq_plan_chunk", "kvq_plan_prompt",
+            "kvq_prompt_attention", "kvq_paged_append_chunk", "kvq_paged_read_chunk",
+            "kvq_paged_chunk_attention")
 
 
 class KVQError(RuntimeError):
@@ -77,6 +79,23 @@ class PagedSizes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("k_codes", "k_scales", "k_zeros", "v_codes", "v_scales", "v_zeros",
                  "k_residual", "v_residual", "page_table", "workspace", "state")]
+
+
+class Chunk(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("residual", ctypes.c_int32), ("blocks", ctypes.c_int32),
+                ("read_tiles", ctypes.c_int32), ("reserved", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("table_bytes", ctypes.c_size_t), ("counts", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("table", ctypes.c_void_p)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 def check_build() -> bool:
@@ -158,6 +177,16 @@ def load() -> ctypes.CDLL:
         lib.kvq_plan_decode.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(i64), i32, i32,
                                         ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)]
         lib.kvq_plan_decode.restype = ctypes.c_int
+        RP = ctypes.POINTER(Rows)
+        lib.kvq_plan_chunk.argtypes = [ctypes.POINTER(PagedConfig), P, P, ctypes.POINTER(Chunk), P, sz]
+        lib.kvq_plan_prompt.argtypes = [i32, i32, i32, i32, P, ctypes.POINTER(Chunk), P, sz]
+        lib.kvq_prompt_attention.argtypes = [ctypes.POINTER(Chunk), i32, RP, RP, RP, RP, P, P]
+        lib.kvq_paged_append_chunk.argtypes = [P, ctypes.POINTER(Chunk), RP, RP, ctypes.POINTER(RopeArgs), RP, RP, P]
+        lib.kvq_paged_read_chunk.argtypes = [P, ctypes.POINTER(Chunk), RP, RP, P]
+        lib.kvq_paged_chunk_attention.argtypes = [P, ctypes.POINTER(Chunk), RP, RP, P, sz, P]
+        for name in ("kvq_plan_chunk", "kvq_plan_prompt", "kvq_prompt_attention", "kvq_paged_append_chunk",
+                     "kvq_paged_read_chunk", "kvq_paged_chunk_attention"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("kvq_logquant_get_sizes", "kvq_logquant_create", "kvq_logquant_retained",
                      "kvq_set_key_outliers"):
             getattr(lib, name).restype = ctypes.c_int
@@ -396,6 +425,132 @@ class KVQCache:
         return dev_out
 
 
+class _Call:
+    """One call's device and stream: the device is current and its stream is torch's current one,
+    so what the call allocates belongs to the stream its kernels run on."""
+
+    def __init__(self, device: torch.device, stream=None):
+        self.device, self.stream, self.guards = device, stream, ()
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.guards = (torch.cuda.device(self.device),)
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError(f"the stream must be one of {self.device}")
+            self.guards += (torch.cuda.stream(self.stream),)
+        for g in self.guards:
+            g.__enter__()
+        return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _packed(t: torch.Tensor, name: str, tokens: int, heads: int, d: int, dtype, device) -> torch.Tensor:
+    """Packed rows as a kernel takes them: checked, on the device, channels contiguous, rows on 16
+    bytes (copied where they are not)."""
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        t = t.to(device, non_blocking=True)
+    a, b, c = t.stride()
+    if t.numel() and (c != 1 or a % 8 or b % 8 or t.data_ptr() % 16):
+        t = t.contiguous()
+        if t.data_ptr() % 16:
+            t = t.clone()
+    return t
+
+
+def _output(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != shape or out.dtype != dtype or out.device != device:
+        raise ValueError(f"out must be {dtype} {list(shape)} on {device}")
+    a, b, c = out.stride()
+    if out.numel() and (c != 1 or a % 8 or b % 8 or out.data_ptr() % 16):
+        raise ValueError("out's channels must be contiguous and its rows start on 16 bytes")
+    return out
+
+
+def _rows(t: torch.Tensor):
+    return ctypes.byref(Rows(t.data_ptr(), t.stride(0), t.stride(1)))
+
+
+class Rope:
+    """Rotary angles cos, sin (float32 [positions, rot_dim / 2], CUDA): row p turns token p."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32 or \
+                not cos.is_cuda or cos.device != sin.device:
+            raise ValueError("cos and sin must be float32 CUDA tensors [positions, rot_dim / 2]")
+        self.cos, self.sin = cos.contiguous(), sin.contiguous()
+        self.args = RopeArgs(self.cos.data_ptr(), self.sin.data_ptr(), cos.shape[0], 2 * cos.shape[1],
+                             int(bool(interleaved)))
+        self.ref = ctypes.byref(self.args)
+
+
+class ChunkPlan:
+    """counts[b] new tokens of each slot from position starts[b] on, planned once on the host and
+    used for the chunk calls of every layer (kvq_chunk).  `tokens` packed rows in all; slot b's are
+    rows offsets[b] .. offsets[b + 1] - 1.  Made by PagedKVQCache.plan_chunk and plan_prompt."""
+
+    def __init__(self, counts, starts, device, cfg=None, heads=None):
+        counts = [int(n) for n in counts]
+        batch = cfg.geom.batch if cfg is not None else len(counts)
+        if len(counts) != batch or (starts is not None and len(starts) != batch):
+            raise ValueError(f"counts and starts must have {batch} entries")
+        dev = torch.device(device if device is not None else "cuda")
+        if dev.type != "cuda":
+            raise ValueError("a plan's table lives on a CUDA device")
+        self.device = dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
+        self.counts, self.starts = counts, [int(s) for s in starts] if starts is not None else [0] * batch
+        if any(not 0 <= n < 1 << 31 for n in self.counts + self.starts):
+            raise ValueError("counts and starts must be in 0 .. 2^31 - 1")
+        self._counts = (ctypes.c_int32 * batch)(*self.counts)
+        self._starts = (ctypes.c_int32 * batch)(*self.starts)
+        self.chunk = Chunk()
+        self.ref = ctypes.byref(self.chunk)
+        lib = load()
+
+        def fill(table, room):
+            if cfg is not None:
+                return lib.kvq_plan_chunk(ctypes.byref(cfg), self._counts, self._starts, self.ref, table, room)
+            return lib.kvq_plan_prompt(batch, *heads, self._counts, self.ref, table, room)
+
+        _check(fill(None, 0))
+        host = torch.empty(self.chunk.table_bytes // 4, dtype=torch.int32)
+        _check(fill(host.data_ptr(), self.chunk.table_bytes))
+        self.tokens = self.chunk.tokens
+        self.offsets = host[:batch + 1].tolist()
+        self.table = host.to(self.device)
+        self.chunk.table = self.table.data_ptr()
+
+
+def plan_prompt(counts, q_heads: int, kv_heads: int, head_dim: int, device=None) -> ChunkPlan:
+    """Plan for prompts of counts[b] tokens each (prompt_attention)."""
+    return ChunkPlan(counts, None, device, heads=(q_heads, kv_heads, head_dim))
+
+
+def prompt_attention(plan: ChunkPlan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts (kvq_prompt_attention): q [tokens, Hq, d], k, v
+    [tokens, Hkv, d] (fp16 or bf16, strided views welcome) -> e [tokens, Hq, d]."""
+    c = plan.chunk
+    code = _dtype_code(q.dtype)
+    with _Call(plan.device, stream) as s:
+        q = _packed(q, "q", plan.tokens, c.q_heads, c.head_dim, q.dtype, plan.device)
+        k = _packed(k, "k", plan.tokens, c.kv_heads, c.head_dim, q.dtype, plan.device)
+        v = _packed(v, "v", plan.tokens, c.kv_heads, c.head_dim, q.dtype, plan.device)
+        out = _output(out, q.shape, q.dtype, plan.device)
+        _check(load().kvq_prompt_attention(plan.ref, code, _rows(q), _rows(k), _rows(v), _rows(out), None,
+                                           s.cuda_stream))
+        return out
+
+
 class PagedKVQCache:
     """A paged, ragged cache: `slots` sequences of their own lengths whose quantized tokens
     live in pages of `page_tokens` tokens of one pool (torch tensors), with a page table
@@ -552,6 +707,76 @@ class PagedKVQCache:
                                                     self.workspace.data_ptr(), self.workspace.numel() * 4,
                                                     _stream_ptr(stream)))
         return out
+
+    def reserve(self, seq: int, tokens: int, stream=None):
+        """Give slot `seq` the pages its first `tokens` tokens need, so that a later call (one that is
+        captured into a graph, say) finds them in the page table."""
+        g = self.geom
+        if not 0 <= seq < g.batch:
+            raise ValueError(f"seq must be in 0..{g.batch - 1}")
+        whole = tokens // g.residual * g.residual
+        if whole > g.capacity:
+            raise KVQError(KVQ_ERR_CAPACITY, f"{tokens} tokens exceed capacity {g.capacity}")
+        self._grow({seq: -(-whole // self.page_tokens)}, stream)
+        return self
+
+    def plan_chunk(self, counts, starts=None) -> ChunkPlan:
+        """Plan for counts[b] new tokens of each slot from position starts[b] on (default: behind
+        what the slot holds; an inactive slot holds nothing)."""
+        if starts is None:
+            starts = [max(n, 0) for n in self.lens]
+        return ChunkPlan(counts, starts, self.device, cfg=self.cfg)
+
+    def append_chunk(self, plan: ChunkPlan, t_K: torch.Tensor, t_V: torch.Tensor, rope: Rope | None = None,
+                     t_Q: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+        """Append the planned tokens t_K, t_V [tokens, Hkv, d] (kvq_paged_append_chunk), keys
+        rotated when `rope` is given; with t_Q [tokens, Hq, d], returns the rotated queries (in
+        `out` when given), else None."""
+        g = self.geom
+        with _Call(self.device, stream) as s:
+            t_K = _packed(t_K, "t_K", plan.tokens, g.kv_heads, g.head_dim, self.dtype, self.device)
+            t_V = _packed(t_V, "t_V", plan.tokens, g.kv_heads, g.head_dim, self.dtype, self.device)
+            if t_Q is not None:
+                t_Q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
+                out = _output(out, t_Q.shape, self.dtype, self.device)
+            if rope is not None and rope.cos.device != self.device:
+                raise ValueError(f"the angles must be on {self.device}")
+            need = {}
+            for b, (start, n) in enumerate(zip(plan.starts, plan.counts)):
+                held = max(self.lens[b], 0)
+                whole = (start + n) // g.residual * g.residual
+                if n and start <= held and whole <= g.capacity:
+                    need[b] = -(-whole // self.page_tokens)
+            if sum(max(0, n - len(self.pages[b])) for b, n in need.items()) > len(self.free_pages):
+                raise KVQError(KVQ_ERR_CAPACITY, "the page pool is exhausted")
+            self._grow(need, s)
+            _check(self._lib.kvq_paged_append_chunk(
+                self._h, plan.ref, _rows(t_K), _rows(t_V), None if rope is None else rope.ref,
+                None if t_Q is None else _rows(t_Q), None if t_Q is None else _rows(out), s.cuda_stream))
+            for b, (start, n) in enumerate(zip(plan.starts, plan.counts)):
+                if n:
+                    self.lens[b] = start + n
+            return out if t_Q is not None else None
+
+    def read_chunk(self, plan: ChunkPlan, stream=None):
+        """(k, v) [tokens, Hkv, d]: the planned tokens as the cache holds them."""
+        g = self.geom
+        with _Call(self.device, stream) as s:
+            k = torch.empty((plan.tokens, g.kv_heads, g.head_dim), dtype=self.dtype, device=self.device)
+            v = torch.empty_like(k)
+            _check(self._lib.kvq_paged_read_chunk(self._h, plan.ref, _rows(k), _rows(v), s.cuda_stream))
+            return k, v
+
+    def chunk_attention(self, plan: ChunkPlan, t_Q: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        """Attention of the planned tokens' queries t_Q [tokens, Hq, d] over the cache, which holds
+        them: the token at position p sees tokens 0 .. p.  Returns e [tokens, Hq, d]."""
+        g = self.geom
+        with _Call(self.device, stream) as s:
+            t_Q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
+            out = _output(out, t_Q.shape, self.dtype, self.device)
+            _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, _rows(t_Q), _rows(out), None, 0,
+                                                       s.cuda_stream))
+            return out
 
     def release(self, seq: int, stream=None):
         """End slot `seq`: it becomes inactive and its pages return to the free list (reused by

@@ -436,6 +436,129 @@ KVQ_API kvq_status kvq_paged_check_device(kvq_paged *cache);
 
 /*
  * ---------------------------------------------------------------------------
+ * Chunks: several new tokens of each of several sequences in one call (the pages have no
+ * counterpart beyond KIVI's per-token step; a serving engine prefills prompts in chunks,
+ * mixes them with decode steps and verifies drafted tokens this way).
+ *
+ * Slot b brings counts[b] >= 0 new tokens, the tokens starts[b] .. starts[b] + counts[b] - 1
+ * of its sequence.  All new tokens are packed: the rows of slot 0, then slot 1, ... (a slot
+ * with counts[b] = 0 has none and is left alone by every call).  A kvq_chunk plans the calls:
+ * made on the host once per step and used for every layer's cache of that step.  The caller
+ * uploads its table (table_bytes of host memory the plan call fills) to the device and sets
+ * `table` to the copy; counts and starts stay the caller's host arrays and must outlive the
+ * plan's calls.
+ *
+ * Packed rows: row i of head h starts at data + i * token_stride + h * head_stride (elements;
+ * channels are contiguous).  data 16-byte aligned, strides multiples of 8; e elements.
+ * Negative strides are not served.  Rows of inputs may overlap (stride 0 broadcasts a head);
+ * rows of outputs must not.
+ *
+ * The calls follow the conventions above: asynchronous on `stream`, nothing allocated, an
+ * error launches nothing and changes no state.  They may be captured into a CUDA graph: a
+ * replay repeats the captured chunk at its captured positions (host lengths advance once, at
+ * the capture), reading what the table and the tensors then hold.  It takes the slots to hold
+ * the tokens before starts[b] as at the capture: an append that completes a half-filled block
+ * reads the block's first tokens from the residual, whose rows it then reuses.  A kernel that meets a table
+ * entry or a page outside its buffers skips the access and raises a bit of the cache's status
+ * word (kvq_paged_check_device; kvq_prompt_attention has a status word of its own).
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+    int32_t batch, q_heads, kv_heads, head_dim;
+    int32_t residual;        /* R of the paged caches the plan serves; 0: a prompt plan     */
+    int32_t blocks;          /* blocks of R tokens that kvq_paged_append_chunk quantizes    */
+    int32_t read_tiles;      /* 16-token tiles that kvq_paged_read_chunk visits             */
+    int32_t reserved;
+    int64_t tokens;          /* packed rows: the sum of counts                              */
+    size_t table_bytes;      /* size of the table                                           */
+    const int32_t *counts;   /* host [batch]                                                */
+    const int32_t *starts;   /* host [batch]; NULL for a prompt plan (all 0)                */
+    const int32_t *table;    /* device copy of the table, 16-byte aligned: set by the caller */
+} kvq_chunk;
+
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;   /* elements */
+} kvq_rows;
+
+/*
+ * Rotary position angles: cos, sin: device float [positions][rot_dim / 2], row p the angles of
+ * token p.  A rotated head's channels (x, y) = (i, i + rot_dim/2) -- or (2i, 2i + 1) when
+ * interleaved -- become (x cos - y sin, y cos + x sin), each product and sum one fp32 operation,
+ * the result rounded once to e.  Channels from rot_dim on stay.  rot_dim: a multiple of 16, at
+ * most head_dim.
+ */
+typedef struct {
+    const float *cos, *sin;
+    int64_t positions;
+    int32_t rot_dim;
+    int32_t interleaved;
+} kvq_rope;
+
+/*
+ * Plans for `counts` new tokens per slot (host arrays of cfg->geom.batch / `batch` entries).
+ * Fill `out` but its `table`; write the table to `table` (host, `table_bytes` bytes of room),
+ * or only the sizes when `table` is NULL.  Host only, no device needed.  KVQ_ERR_INVALID_ARG
+ * for a negative count or start, too little room, or sums past 2^31 - 1; KVQ_ERR_UNSUPPORTED
+ * for more than 128 query heads per kv head.  A prompt plan needs no cache: head_dim 64 or 128,
+ * q_heads a multiple of kv_heads.
+ */
+KVQ_API kvq_status kvq_plan_chunk(const kvq_paged_config *cfg, const int32_t *counts, const int32_t *starts,
+                                  kvq_chunk *out, void *table, size_t table_bytes);
+KVQ_API kvq_status kvq_plan_prompt(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                   const int32_t *counts, kvq_chunk *out, void *table, size_t table_bytes);
+
+/*
+ * Causal attention over whole prompts: o_i = sum_{j <= i} p_ij v_j within each sequence,
+ * p_i = softmax_j(q_i . k_j / sqrt(d)).  q, o: [tokens][q_heads][d]; k, v: [tokens][kv_heads][d],
+ * packed as planned (a prompt plan); all of element type `dtype` (kvq_dtype); o must overlap no
+ * input.  Logits, softmax statistics and sums are fp32; the weights are rounded to e before
+ * they meet v, the output once.  Finite inputs: a NaN or infinity reaches rows of its own
+ * sequence only.  `status`: device word (4 bytes, or NULL) whose bits the kernel raises (bit 0:
+ * a bounded wait gave up; bit 3: a table entry outside the tensors).
+ */
+KVQ_API kvq_status kvq_prompt_attention(const kvq_chunk *plan, int32_t dtype, const kvq_rows *q, const kvq_rows *k,
+                                        const kvq_rows *v, const kvq_rows *o, uint32_t *status, void *stream);
+
+/*
+ * Appends the planned tokens: k, v e [tokens][kv_heads][d].  Keys are rotated by their
+ * token's position when `rope` is given.  Each slot's tokens behind starts[b] are dropped first
+ * (rejected drafts): starts[b] is at most the slot's length, and below it only where the kept
+ * tokens need nothing restored -- starts[b] at least its quantized tokens, or a multiple of R
+ * (KVQ_ERR_STATE otherwise).  An inactive slot with starts[b] = 0 becomes active.  Then the
+ * slot holds starts[b] + counts[b] tokens, whole blocks of R quantized (with the residual rows
+ * they start with) and the rest kept in the residual: the state that appending one by one
+ * leaves.  The caller has filled the page-table entries of the new blocks.
+ * q (or NULL): queries e [tokens][q_heads][d] of the same tokens, rotated into q_out (may be the
+ * same rows as q; needs rope).  KVQ_ERR_CAPACITY when a block would pass capacity,
+ * KVQ_ERR_INVALID_ARG when a position has no angles.  One launch, two when a block fills.
+ */
+KVQ_API kvq_status kvq_paged_append_chunk(kvq_paged *cache, const kvq_chunk *plan, const kvq_rows *k,
+                                          const kvq_rows *v, const kvq_rope *rope, const kvq_rows *q,
+                                          const kvq_rows *q_out, void *stream);
+
+/*
+ * What the cache holds for the planned tokens, as e: k, v [tokens][kv_heads][d] receive the
+ * residual rows as they are and (code - z) s of quantized tokens, computed in fp32 and rounded
+ * once.  starts[b] + counts[b] must not pass the slot's length (KVQ_ERR_STATE).  One launch.
+ */
+KVQ_API kvq_status kvq_paged_read_chunk(kvq_paged *cache, const kvq_chunk *plan, const kvq_rows *k,
+                                        const kvq_rows *v, void *stream);
+
+/*
+ * Attention of the planned tokens over the cache, which already holds them: query row i of
+ * slot b, at position p = starts[b] + i, sees tokens 0 .. p (quantized ones as (code - z) s,
+ * residual rows as they are; a token's neighbours in its chunk are read from the cache too).
+ * q, o: e [tokens][q_heads][d]; o must not overlap q.  starts[b] + counts[b] must not pass the
+ * slot's length (KVQ_ERR_STATE); rows of which the device length leaves nothing to see give
+ * zeros.  Logits, softmax statistics and sums are fp32.
+ */
+KVQ_API kvq_status kvq_paged_chunk_attention(kvq_paged *cache, const kvq_chunk *plan, const kvq_rows *q,
+                                             const kvq_rows *o, void *workspace, size_t workspace_bytes,
+                                             void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * LogQuant retention ("Resumo Técnico: LogQuant", section 2, Estratégia de
  * Filtragem Baseada em Logaritmos, and section 4).  Instead of KIVI's residual of
  * the newest < R tokens, a full-precision store keeps up to 3W tokens: every new

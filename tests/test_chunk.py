@@ -1,0 +1,101 @@
+"""The chunk planner and its refusals on the host, without a device."""
+import ctypes
+import random
+
+import pytest
+
+from bit_kv_cache_22_b200 import kvq
+
+
+def config(batch=3, hq=8, hkv=2, R=128, page=128, capacity=1024):
+    geom = kvq.make_config(batch, hq, hkv, 128, 32, 32, R, 2, False, kvq.KVQ_BF16, capacity)
+    return kvq.PagedConfig(geom, page, 16)
+
+
+def plan(cfg, counts, starts, room=None):
+    n = len(counts)
+    c, s = (ctypes.c_int32 * n)(*counts), (ctypes.c_int32 * n)(*starts)
+    out = kvq.Chunk()
+    lib = kvq.load()
+    st = lib.kvq_plan_chunk(ctypes.byref(cfg), c, s, ctypes.byref(out), None, 0)
+    if st != kvq.KVQ_OK:
+        return st, None, None
+    words = out.table_bytes // 4
+    table = (ctypes.c_int32 * (words + 1))(*([77] * (words + 1)))
+    st = lib.kvq_plan_chunk(ctypes.byref(cfg), c, s, ctypes.byref(out), table,
+                            out.table_bytes if room is None else room)
+    assert table[words] == 77                       # nothing past the end
+    return st, out, list(table)
+
+
+def test_table_of_random_plans():
+    rng = random.Random(1)
+    for _ in range(200):
+        B, R = rng.randint(1, 9), rng.choice([32, 128, 256])
+        cfg = config(batch=B, R=R, page=256, capacity=1024)
+        counts = [rng.choice([0, 1, rng.randint(0, 700)]) for _ in range(B)]
+        starts = [rng.randint(0, 500) for _ in range(B)]
+        st, out, t = plan(cfg, counts, starts)
+        assert st == kvq.KVQ_OK and out.tokens == sum(counts)
+        assert t[:B + 1] == [sum(counts[:b]) for b in range(B + 1)]
+        assert t[B + 1:2 * B + 1] == starts
+        tiles = [(s + n + 15) // 16 - s // 16 if n else 0 for s, n in zip(starts, counts)]
+        assert t[2 * B + 1:3 * B + 2] == [sum(tiles[:b]) for b in range(B + 1)] and out.read_tiles == sum(tiles)
+        blocks = [(b, i) for b in range(B) if counts[b]
+                  for i in range(starts[b] // R, (starts[b] + counts[b]) // R)]
+        at = 3 * B + 2
+        assert [tuple(t[at + 2 * i:at + 2 * i + 2]) for i in range(out.blocks)] == blocks and out.blocks == len(blocks)
+
+
+@pytest.mark.parametrize("counts,starts", [([-1, 0, 0], [0, 0, 0]), ([1, 0, 0], [-1, 0, 0]),
+                                           ([2, 0, 0], [2 ** 31 - 2, 0, 0]), ([2 ** 30] * 3, [0] * 3)])
+def test_refused_plans(counts, starts):
+    assert plan(config(), counts, starts)[0] == kvq.KVQ_ERR_INVALID_ARG
+    assert kvq.load().kvq_last_error()
+
+
+def test_a_short_table_is_refused():
+    assert plan(config(), [5, 1, 300], [0, 0, 0], room=8)[0] == kvq.KVQ_ERR_INVALID_ARG
+
+
+def test_prompt_plans():
+    lib = kvq.load()
+    out = kvq.Chunk()
+    c = (ctypes.c_int32 * 2)(5, 7)
+    ok = [2, 8, 2, 128]
+    assert lib.kvq_plan_prompt(*ok, c, ctypes.byref(out), None, 0) == kvq.KVQ_OK
+    assert out.tokens == 12 and out.residual == 0 and out.blocks == 0
+    for bad, status in (([0, 8, 2, 128], kvq.KVQ_ERR_INVALID_ARG), ([2, 8, 3, 128], kvq.KVQ_ERR_INVALID_ARG),
+                        ([2, 8, 2, 96], kvq.KVQ_ERR_UNSUPPORTED), ([2, 129, 1, 128], kvq.KVQ_ERR_UNSUPPORTED)):
+        assert lib.kvq_plan_prompt(*bad, c, ctypes.byref(out), None, 0) == status, bad
+    assert lib.kvq_plan_prompt(*ok, None, ctypes.byref(out), None, 0) == kvq.KVQ_ERR_INVALID_ARG
+    assert lib.kvq_plan_chunk(None, c, c, ctypes.byref(out), None, 0) == kvq.KVQ_ERR_INVALID_ARG
+
+
+def test_calls_refuse_bad_arguments_before_any_launch():
+    lib = kvq.load()
+    c = (ctypes.c_int32 * 1)(4)
+    out = kvq.Chunk()
+    assert lib.kvq_plan_prompt(1, 4, 2, 128, c, ctypes.byref(out), None, 0) == kvq.KVQ_OK
+    fake = 1 << 20                                  # aligned, never followed: every call below is refused
+    good = kvq.Rows(fake, 512, 128)
+    r = ctypes.byref
+
+    def attend(p, dtype=kvq.KVQ_BF16, q=good, o=good):
+        return lib.kvq_prompt_attention(r(p), dtype, r(q), r(good), r(good), r(o), None, None)
+
+    assert attend(out) == kvq.KVQ_ERR_INVALID_ARG and b"table" in lib.kvq_last_error()
+    out.table = fake
+    assert attend(out, dtype=9) == kvq.KVQ_ERR_INVALID_ARG
+    for bad in (kvq.Rows(None, 512, 128), kvq.Rows(fake + 2, 512, 128), kvq.Rows(fake, 500, 128),
+                kvq.Rows(fake, 512, -128), kvq.Rows(fake, 512, 4)):
+        assert attend(out, q=bad) == kvq.KVQ_ERR_INVALID_ARG
+        assert attend(out, o=bad) == kvq.KVQ_ERR_INVALID_ARG
+    assert lib.kvq_prompt_attention(None, 0, r(good), r(good), r(good), r(good), None, None) == kvq.KVQ_ERR_INVALID_ARG
+    assert lib.kvq_paged_append_chunk(None, r(out), r(good), r(good), None, None, None, None) == kvq.KVQ_ERR_INVALID_ARG
+    assert lib.kvq_paged_read_chunk(None, r(out), r(good), r(good), None) == kvq.KVQ_ERR_INVALID_ARG
+    assert lib.kvq_paged_chunk_attention(None, r(out), r(good), r(good), None, 0, None) == kvq.KVQ_ERR_INVALID_ARG
+    none = (ctypes.c_int32 * 1)(0)                  # nothing to do: no launch, no device
+    assert lib.kvq_plan_prompt(1, 4, 2, 128, none, r(out), None, 0) == kvq.KVQ_OK
+    out.table = fake
+    assert attend(out) == kvq.KVQ_OK
