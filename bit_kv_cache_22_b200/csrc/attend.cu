@@ -101,7 +101,7 @@ void rows_launch(const AttendArgs &a, unsigned grid, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s) {
+cudaError_t launch_attend_cache(const AttendArgs &a, cudaStream_t s) {
     if (a.t.tokens == 0) return cudaSuccess;
     const unsigned grid = static_cast<unsigned>((a.t.tokens * a.Hq + kRowWarps - 1) / kRowWarps);
     if (a.d == 64) rows_launch<64>(a, grid, s);

@@ -1,0 +1,389 @@
+// attend_prompt.cu -- causal attention over packed prompts on the tensor cores.
+//
+// o_i = sum_{j <= i} p_ij v_j, p_i = softmax_j(q_i . k_j / sqrt(d)), one pass over the keys with a
+// running maximum m and sum l per row: with y = log2(e) q.k / sqrt(d), weights 2^(y - m) meet the
+// values as they come, and the sums are rescaled when m rises.
+//
+// A CTA serves one kv head and two tiles of 128 query rows; the rows of a tile are tokens x the
+// query heads of that kv head, so keys and values are fetched once for all of them.  Key and value
+// tiles of 128 tokens stream through shared memory by TMA; S = Q K^T and O += P V run on tcgen05
+// with both accumulators in tensor memory, and P never leaves tensor memory: a row's thread reads
+// its logits there, and writes its weights, as e, over them.  While one tile's threads take the
+// exponentials the tensor core works for the other tile.
+//
+//   warps 0-3, 4-7   softmax of tile 0, 1: thread = row
+//   warp 8           issues the MMAs
+//   warp 9           TMA loads (warps 10, 11 fill the warpgroup, which gives its registers to the
+//                    softmax: 2 x 128 x 208 + 128 x 80 <= 384 x 168)
+//
+// Tensor memory (512 columns): S0 | S1 | O0 | O1, P over the first half of its S.
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "chunk_rows.cuh"
+#include "kvq_internal.cuh"
+#include "tensor_core.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128;                 // rows of a query tile, tokens of a key tile
+constexpr int kStages = 2;                 // key and value tiles in flight, each
+
+template <int D>
+struct PromptSmem {
+    static constexpr int kTileBytes = kRows * D * 2;
+    static constexpr int q = 0;                                  // two tiles
+    static constexpr int k = q + 2 * kTileBytes;
+    static constexpr int v = k + kStages * kTileBytes;
+    static constexpr int bars = v + kStages * kTileBytes;
+    // one CTA an SM: it holds all of the tensor memory
+    static constexpr int bytes = (bars + 256 > 120 * 1024 ? bars + 256 : 120 * 1024) + 1024;
+};
+
+// A value above which the running maximum is raised: weights stay below 2^8, which e holds as
+// exactly as weights below 1, and the sums are rescaled rarely.
+constexpr float kLazyMax = 8.0f;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ CUtensorMap map_q,
+                                                                   const __grid_constant__ CUtensorMap map_k,
+                                                                   const __grid_constant__ CUtensorMap map_v,
+                                                                   const AttendArgs a) {
+    using L = PromptSmem<D>;
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    unsigned char *smem = raw + (base - tc::smem_addr(raw));
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int gave_up;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+
+    // the work item: up to 2 * tpt tokens of one slot's prompt from token q0 on
+    const int h = blockIdx.x % a.Hkv;
+    const int4 item = a.t.items[blockIdx.x / a.Hkv];
+    const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
+    const int slot = item.x, q0 = item.y;
+    int first = 0, count = 0;
+    bool good = slot >= 0 && slot < a.t.B && q0 >= 0;
+    if (good) {
+        first = a.t.offsets[slot];
+        count = a.t.offsets[slot + 1] - first;
+        good = first >= 0 && count > q0 && static_cast<int64_t>(first) + count <= a.t.tokens;
+    }
+    if (!good) {                                   // not this library's table
+        if (threadIdx.x == 0 && a.status) atomicOr(a.status, 8u);
+        return;
+    }
+    // key tiles each query tile sees (0: the tile has no tokens)
+    int n_tiles[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int tok = q0 + t * tpt, end = min(tok + tpt, count);
+        n_tiles[t] = tok < count ? (end + kRows - 1) / kRows : 0;
+    }
+    const int n_max = max(n_tiles[0], n_tiles[1]);
+
+    const uint32_t bars = base + L::bars;
+    auto bar = [&](int i) { return bars + 8u * i; };
+    enum { kQFull = 0, kKFull = 2, kKEmpty = 4, kVFull = 6, kVEmpty = 8, kSFull = 10, kPFull = 12, kOFull = 14,
+           kVFixed = 16, kDrain = 17, kBars = 18 };
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < kBars; ++i) tc::bar_init(bar(i), i == kPFull || i == kPFull + 1 ? 4 : 1);
+        tc::fence_barrier_init();
+    }
+    if (warp == 8) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp >= 8) tc::regs_give<80>();
+    else tc::regs_take<208>();
+
+    if (warp == 9) {
+        // ------------------------------ loads ------------------------------
+        int issued = 0;                            // key and value tiles asked for
+        if (lane == 0) {
+            const uint32_t q_bytes = static_cast<uint32_t>(hg * tpt * D * 2);
+            auto load = [&](const CUtensorMap *map, uint32_t dst, int head, int tok, uint32_t b) {
+#pragma unroll
+                for (int p = 0; p < D / 64; ++p) tc::tma_load_3d(dst + p * kRows * 128, map, 64 * p, head, tok, b);
+            };
+            for (int t = 0; t < 2; ++t) {
+                if (n_tiles[t]) {
+                    tc::bar_expect(bar(kQFull + t), q_bytes);
+                    load(&map_q, base + L::q + t * L::kTileBytes, h * hg, first + q0 + t * tpt, bar(kQFull + t));
+                }
+                if (t == 0) {
+                    tc::bar_expect(bar(kKFull), L::kTileBytes);
+                    load(&map_k, base + L::k, h, first, bar(kKFull));
+                }
+            }
+            bool go = true;
+            for (int j = 0; j < n_max && go; ++j) {
+                const int s = j % kStages, phase = (j / kStages) & 1;
+                if (j > 0) {
+                    if (j >= kStages) go = tc::bar_wait(bar(kKEmpty + s), phase ^ 1, &gave_up);
+                    if (!go) break;
+                    tc::bar_expect(bar(kKFull + s), L::kTileBytes);
+                    load(&map_k, base + L::k + s * L::kTileBytes, h, first + j * kRows, bar(kKFull + s));
+                }
+                if (j >= kStages) go = tc::bar_wait(bar(kVEmpty + s), phase ^ 1, &gave_up);
+                if (!go) break;
+                tc::bar_expect(bar(kVFull + s), L::kTileBytes);
+                load(&map_v, base + L::v + s * L::kTileBytes, h, first + j * kRows, bar(kVFull + s));
+                issued = j + 1;
+            }
+        }
+        issued = __shfl_sync(0xffffffffu, issued, 0);
+        // The last value tile may reach past the sequence, into rows that are another's or
+        // anything: their weights are 0, but 0 times an infinity is not, so they are cleared.
+        const int j = n_max - 1, left = count - j * kRows;
+        if (issued == n_max && left < kRows) {
+            const int s = j % kStages;
+            if (tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up)) {
+                unsigned char *v = smem + L::v + s * L::kTileBytes;
+                for (int i = lane; i < (kRows - left) * 8; i += 32)   // whole 128-byte rows: the swizzle stays inside
+#pragma unroll
+                    for (int p = 0; p < D / 64; ++p)
+                        *reinterpret_cast<uint4 *>(v + p * kRows * 128 + left * 128 + 16 * i) = make_uint4(0, 0, 0, 0);
+                tc::fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(bar(kVFixed));
+            }
+        }
+        if (gave_up && lane == 0) {                // copies in flight land before the CTA leaves
+            volatile int never = 0;
+            for (int t = 0; t < 2; ++t)
+                if (n_tiles[t]) tc::bar_wait(bar(kQFull + t), 0, &never);
+            for (int i = max(0, issued - kStages); i < issued; ++i) {
+                tc::bar_wait(bar(kKFull + i % kStages), (i / kStages) & 1, &never);
+                tc::bar_wait(bar(kVFull + i % kStages), (i / kStages) & 1, &never);
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------ MMAs -------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, BF16, false);
+            constexpr uint32_t kDescO = tc::mma_desc(kRows, D, BF16, true);
+            auto issue_s = [&](int t, int s) {
+                const uint64_t qd = tc::desc_k_major(base + L::q + t * L::kTileBytes);
+                const uint64_t kd = tc::desc_k_major(base + L::k + s * L::kTileBytes);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t step = (i / 4) * (kRows * 128 / 16) + (i % 4) * 2;
+                    tc::mma_ss(tmem + t * 128, qd + step, kd + step, kDescS, i > 0);
+                }
+                tc::mma_commit(bar(kSFull + t));
+            };
+            bool go = tc::bar_wait(bar(kKFull), 0, &gave_up);
+            for (int t = 0; t < 2 && go; ++t)
+                if (n_tiles[t]) {
+                    go = tc::bar_wait(bar(kQFull + t), 0, &gave_up);
+                    if (go) issue_s(t, 0);
+                }
+            if (go) tc::mma_commit(bar(kKEmpty));
+            for (int j = 0; j < n_max && go; ++j) {
+                const int s = j % kStages, s1 = (j + 1) % kStages;
+                go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
+                if (go && j == n_max - 1 && count - j * kRows < kRows) go = tc::bar_wait(bar(kVFixed), 0, &gave_up);
+                for (int t = 0; t < 2 && go; ++t) {
+                    if (j >= n_tiles[t]) continue;
+                    go = tc::bar_wait(bar(kPFull + t), j & 1, &gave_up);
+                    if (!go) break;
+                    tc::fence_after_sync();
+                    const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
+#pragma unroll
+                    for (int i = 0; i < kRows / 16; ++i)
+                        tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
+                                   j > 0 || i > 0);
+                    if (j + 1 < n_tiles[t]) {
+                        go = tc::bar_wait(bar(kKFull + s1), ((j + 1) / kStages) & 1, &gave_up);
+                        if (go) issue_s(t, s1);
+                    } else {
+                        tc::mma_commit(bar(kOFull + t));
+                    }
+                }
+                if (go) {
+                    tc::mma_commit(bar(kVEmpty + s));
+                    if (j + 1 < n_max) tc::mma_commit(bar(kKEmpty + s1));
+                }
+            }
+            if (gave_up) {                         // MMAs in flight end before tensor memory is freed
+                volatile int never = 0;
+                tc::mma_commit(bar(kDrain));
+                tc::bar_wait(bar(kDrain), 0, &never);
+            }
+        }
+    } else if (warp < 8) {
+        // ------------------------------ softmax ----------------------------
+        const int t = warp >> 2, r = threadIdx.x & 127;
+        const int tok0 = q0 + t * tpt, tok = tok0 + r / hg;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+        float m = 0.0f, l = 0.0f;
+        bool go = true;
+        for (int j = 0; j < n_tiles[t] && go; ++j) {
+            go = tc::bar_wait(bar(kSFull + t), j & 1, &gave_up);
+            if (!go) break;
+            tc::fence_after_sync();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::tmem_load(ts + 32 * c, s[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::tmem_arrived(s[c]);
+            if ((j + 1) * kRows > tok0 + 1) {      // tokens ahead of some row
+                const int seen = tok + 1 - j * kRows;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i >= seen) s[c][i] = 0xff800000u;
+            }
+            float mx = __uint_as_float(s[0][0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[c][i]));
+            mx *= a.scale;
+            if (j == 0) {
+                m = mx;
+            } else if (__any_sync(0xffffffffu, mx > m + kLazyMax)) {
+                // O holds every tile before j: S_j was committed after its last MMA
+                const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
+                m = mn;
+                l *= alpha;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tc::tmem_load(to + 32 * c, o);
+                    tc::tmem_arrived(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                    tc::tmem_store(to + 32 * c, o);
+                }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t *src = &s[2 * half + i / 16][2 * (i % 16)];
+                    const float p0 = tc::ex2(fmaf(__uint_as_float(src[0]), a.scale, -m));
+                    const float p1 = tc::ex2(fmaf(__uint_as_float(src[1]), a.scale, -m));
+                    l += p0 + p1;
+                    p[i] = narrow2<BF16>(p0, p1);
+                }
+                tc::tmem_store(ts + 32 * half, p);
+            }
+            tc::tmem_stored();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(bar(kPFull + t));
+        }
+        if (go && n_tiles[t]) go = tc::bar_wait(bar(kOFull + t), 0, &gave_up);
+        if (go && n_tiles[t]) {
+            tc::fence_after_sync();
+            const float inv = 1.0f / l;
+            const bool mine = r < hg * tpt && tok < count;
+            uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
+                            static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tc::tmem_load(to + 32 * c, o);
+                tc::tmem_arrived(o);
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = narrow2<BF16>(__uint_as_float(o[8 * i + 2 * k]) * inv,
+                                                 __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                        reinterpret_cast<uint4 *>(out + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0 && gave_up && a.status) atomicOr(a.status, 1u);
+    if (warp == 8) {
+        tc::fence_after_sync();
+        tc::tmem_free(tmem, 512);
+    }
+}
+
+// The tensor map of packed rows [tokens][heads][d], boxes of 64 channels x box_heads x box_tokens
+// in 128-byte rows with the 128-byte swizzle; rows outside the tensor read as zeros.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+bool rows_map(CUtensorMap *map, const Rows &r, int64_t tokens, int heads, int d, bool bf16, int box_heads,
+              int box_tokens) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    // the stride of a dimension of one entry is never followed: any valid one
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? r.hs : d) * 2,
+                                   static_cast<cuuint64_t>(tokens > 1 ? r.ts : d) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, r.p, dims, strides,
+                  box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_instance(const AttendArgs &a, cudaStream_t s) {
+    const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
+    CUtensorMap mq, mk, mv;
+    if (!rows_map(&mq, a.q, a.t.tokens, a.Hq, D, BF16, hg, tpt) ||
+        !rows_map(&mk, a.k, a.t.tokens, a.Hkv, D, BF16, 1, kRows) ||
+        !rows_map(&mv, a.v, a.t.tokens, a.Hkv, D, BF16, 1, kRows))
+        return cudaErrorInvalidValue;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(attend_prompt_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PromptSmem<D>::bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = true;
+    }
+    attend_prompt_kernel<D, BF16><<<static_cast<unsigned>(a.t.n_items) * a.Hkv, kThreads, PromptSmem<D>::bytes, s>>>(
+        mq, mk, mv, a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_prompt(const AttendArgs &a, cudaStream_t s) {
+    if (a.t.n_items == 0) return cudaSuccess;
+    if (a.d == 64) return a.bf16 ? launch_instance<64, true>(a, s) : launch_instance<64, false>(a, s);
+    return a.bf16 ? launch_instance<128, true>(a, s) : launch_instance<128, false>(a, s);
+}
+
+}  // namespace kvq

@@ -13,10 +13,12 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <new>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/kvq.h"
@@ -1102,27 +1104,32 @@ kvq_status kvq_paged_check_device(kvq_paged *h) {
 namespace {
 
 // The table, as int32: offsets [B + 1], starts [B], read tiles before each slot [B + 1], blocks
-// [n_blocks][2] = (slot, block).
+// [n_blocks][2] = (slot, block), and from a multiple of 4 on the attention's items [n_items][4] =
+// (slot, first query token, 0, 0).
 struct ChunkLayout {
-    int64_t starts, tiles, blocks, end;
+    int64_t starts, tiles, blocks, items, end;
 };
-ChunkLayout chunk_layout(int64_t B, int64_t n_blocks) {
+ChunkLayout chunk_layout(int64_t B, int64_t n_blocks, int64_t n_items) {
     ChunkLayout l;
     l.starts = B + 1;
     l.tiles = l.starts + B;
     l.blocks = l.tiles + B + 1;
-    l.end = l.blocks + 2 * n_blocks;
+    l.items = (l.blocks + 2 * n_blocks + 3) / 4 * 4;
+    l.end = l.items + 4 * n_items;
     return l;
 }
 
 constexpr int64_t kMaxInt = 0x7fffffff;
+constexpr int64_t kMaxStride = int64_t{1} << 38;   // elements: a tensor map's strides end at 2^40 bytes
 
 kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t R, const int32_t *counts,
                       const int32_t *starts, kvq_chunk *out, void *table, size_t table_bytes) {
     if (!counts || !out) return fail(KVQ_ERR_INVALID_ARG, "counts and out must be non-NULL");
     if (q_heads / kv_heads > 128)
         return fail(KVQ_ERR_UNSUPPORTED, "at most 128 query heads per kv head (got %d)", q_heads / kv_heads);
-    int64_t tokens = 0, blocks = 0, tiles = 0;
+    // a CTA's two query tiles of 128 rows: tokens x the query heads of one kv head
+    const int64_t per_item = 2 * (128 / (q_heads / kv_heads));
+    int64_t tokens = 0, blocks = 0, tiles = 0, items = 0;
     for (int b = 0; b < batch; ++b) {
         const int64_t n = counts[b], s = starts ? starts[b] : 0;
         if (n < 0 || s < 0 || s + n > kMaxInt)
@@ -1130,13 +1137,14 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
                         static_cast<long long>(s));
         if (n == 0) continue;
         tokens += n;
+        items += (n + per_item - 1) / per_item;
         if (R > 0) {
             blocks += (s + n) / R - s / R;
             tiles += (s + n + 15) / 16 - s / 16;
         }
     }
-    const ChunkLayout l = chunk_layout(batch, blocks);
-    if (tokens * q_heads > kMaxInt || tiles * kv_heads > kMaxInt || l.end > kMaxInt)
+    const ChunkLayout l = chunk_layout(batch, blocks, items);
+    if (tokens * q_heads > kMaxInt || items * kv_heads > kMaxInt || tiles * kv_heads > kMaxInt || l.end > kMaxInt)
         return fail(KVQ_ERR_INVALID_ARG, "too many tokens for one chunk (%lld)", static_cast<long long>(tokens));
     std::memset(out, 0, sizeof *out);
     out->batch = batch;
@@ -1146,6 +1154,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     out->residual = R;
     out->blocks = static_cast<int32_t>(blocks);
     out->read_tiles = static_cast<int32_t>(tiles);
+    out->items = static_cast<int32_t>(items);
     out->tokens = tokens;
     out->table_bytes = static_cast<size_t>(l.end) * sizeof(int32_t);
     out->counts = counts;
@@ -1170,16 +1179,36 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     }
     t[batch] = row;
     t[l.tiles + batch] = tile;
+    while (blk < t + l.items) *blk++ = 0;
+    // the items that see the most tokens first, so that the last CTAs to start are short
+    std::vector<std::pair<int32_t, int32_t>> order;
+    order.reserve(static_cast<size_t>(items));
+    for (int b = 0; b < batch; ++b)
+        for (int64_t i = 0; i < counts[b]; i += per_item) order.emplace_back(b, static_cast<int32_t>(i));
+    auto seen = [&](const std::pair<int32_t, int32_t> &i) {
+        const int64_t n = counts[i.first], last = i.second + per_item;
+        return (starts ? starts[i.first] : 0) + (last < n ? last : n);
+    };
+    std::stable_sort(order.begin(), order.end(), [&](const auto &x, const auto &y) { return seen(x) > seen(y); });
+    int32_t *it = t + l.items;
+    for (const auto &i : order) {
+        *it++ = i.first;
+        *it++ = i.second;
+        *it++ = 0;
+        *it++ = 0;
+    }
     return ok();
 }
 
 kvq::ChunkTable chunk_table(const kvq_chunk *p) {
-    const ChunkLayout l = chunk_layout(p->batch, p->blocks);
+    const ChunkLayout l = chunk_layout(p->batch, p->blocks, p->items);
     kvq::ChunkTable t{};
     t.offsets = p->table;
     t.starts = p->table + l.starts;
     t.tiles = p->table + l.tiles;
     t.blocks = p->table + l.blocks;
+    t.items = reinterpret_cast<const int4 *>(p->table + l.items);
+    t.n_items = p->items;
     t.n_blocks = p->blocks;
     t.n_tiles = p->read_tiles;
     t.tokens = p->tokens;
@@ -1187,11 +1216,13 @@ kvq::ChunkTable chunk_table(const kvq_chunk *p) {
     return t;
 }
 
-kvq_status check_rows(const kvq_rows *r, const char *name) {
+kvq_status check_rows(const kvq_rows *r, const char *name, int64_t tokens, int heads) {
     if (!r || !r->data || !aligned16(r->data))
         return fail(KVQ_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", name);
-    if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride % 8 != 0 || r->head_stride % 8 != 0)
-        return fail(KVQ_ERR_INVALID_ARG, "the strides of %s must be non-negative multiples of 8 elements", name);
+    const bool token = tokens < 2 || (r->token_stride > 0 && r->token_stride % 8 == 0 && r->token_stride < kMaxStride);
+    const bool head = heads < 2 || (r->head_stride > 0 && r->head_stride % 8 == 0 && r->head_stride < kMaxStride);
+    if (!token || !head)
+        return fail(KVQ_ERR_INVALID_ARG, "the strides of %s must be positive multiples of 8 elements, below 2^38", name);
     return KVQ_OK;
 }
 
@@ -1304,13 +1335,14 @@ kvq_status kvq_prompt_attention(const kvq_chunk *plan, int32_t dtype, const kvq_
     if (plan->tokens == 0) return ok();
     const kvq_rows *rows[] = {q, k, v, o};
     const char *names[] = {"q", "k", "v", "o"};
-    for (int i = 0; i < 4 && st == KVQ_OK; ++i) st = check_rows(rows[i], names[i]);
+    for (int i = 0; i < 4 && st == KVQ_OK; ++i)
+        st = check_rows(rows[i], names[i], plan->tokens, i == 1 || i == 2 ? plan->kv_heads : plan->q_heads);
     if (st != KVQ_OK) return st;
     kvq::AttendArgs a = attend_args(plan, q, o, dtype == KVQ_BF16);
     a.k = rows_of(k);
     a.v = rows_of(v);
     a.status = status;
-    const cudaError_t e = kvq::launch_attend(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = kvq::launch_attend_prompt(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
     return ok();
 }
@@ -1320,10 +1352,10 @@ kvq_status kvq_paged_append_chunk(kvq_paged *h, const kvq_chunk *plan, const kvq
     kvq_status st = check_chunk_for(h, plan);
     if (st != KVQ_OK) return st;
     if (plan->tokens == 0) return ok();
-    st = check_rows(k, "k");
-    if (st == KVQ_OK) st = check_rows(v, "v");
-    if (st == KVQ_OK && q) st = check_rows(q, "q");
-    if (st == KVQ_OK && q) st = check_rows(q_out, "q_out");
+    st = check_rows(k, "k", plan->tokens, plan->kv_heads);
+    if (st == KVQ_OK) st = check_rows(v, "v", plan->tokens, plan->kv_heads);
+    if (st == KVQ_OK && q) st = check_rows(q, "q", plan->tokens, plan->q_heads);
+    if (st == KVQ_OK && q) st = check_rows(q_out, "q_out", plan->tokens, plan->q_heads);
     if (st != KVQ_OK) return st;
     const kvq_config &c = h->base.cfg;
     kvq::RopeArgs r{};
@@ -1378,8 +1410,8 @@ kvq_status kvq_paged_read_chunk(kvq_paged *h, const kvq_chunk *plan, const kvq_r
     kvq_status st = check_chunk_for(h, plan);
     if (st != KVQ_OK) return st;
     if (plan->tokens == 0) return ok();
-    st = check_rows(k, "k");
-    if (st == KVQ_OK) st = check_rows(v, "v");
+    st = check_rows(k, "k", plan->tokens, plan->kv_heads);
+    if (st == KVQ_OK) st = check_rows(v, "v", plan->tokens, plan->kv_heads);
     if (st == KVQ_OK) st = check_held(h, plan);
     if (st != KVQ_OK) return st;
     const cudaError_t e = kvq::launch_chunk_read(paged_view(h), chunk_table(plan), rows_of(k), rows_of(v),
@@ -1393,8 +1425,8 @@ kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const 
     kvq_status st = check_chunk_for(h, plan);
     if (st != KVQ_OK) return st;
     if (plan->tokens == 0) return ok();
-    st = check_rows(q, "q");
-    if (st == KVQ_OK) st = check_rows(o, "o");
+    st = check_rows(q, "q", plan->tokens, plan->q_heads);
+    if (st == KVQ_OK) st = check_rows(o, "o", plan->tokens, plan->q_heads);
     if (st == KVQ_OK) st = check_held(h, plan);
     if (st != KVQ_OK) return st;
     (void)workspace;
@@ -1402,7 +1434,7 @@ kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const 
     kvq::AttendArgs a = attend_args(plan, q, o, h->base.cfg.dtype == KVQ_BF16);
     a.cache = paged_view(h);
     a.status = a.cache.status;
-    const cudaError_t e = kvq::launch_attend(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = kvq::launch_attend_cache(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
     return ok();
 }

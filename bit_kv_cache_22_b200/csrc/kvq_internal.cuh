@@ -53,7 +53,8 @@ struct ChunkTable {
     const int32_t *starts;       // [B]
     const int32_t *tiles;        // [B + 1]: 16-token tiles of the slots before
     const int32_t *blocks;       // [n_blocks][2]: slot, block of R tokens
-    int n_blocks, n_tiles;
+    const int4 *items;           // [n_items] attention work: slot, first query token, ...
+    int n_blocks, n_tiles, n_items;
     int64_t tokens;
     int B;
 };
@@ -248,7 +249,8 @@ struct AttendArgs {
     float scale;                 // log2(e) / sqrt(d)
     unsigned int *status;        // or NULL
 };
-cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_attend_cache(const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_attend_prompt(const AttendArgs &a, cudaStream_t s);
 
 // The compute capability the library's kernels were compiled for (major * 10 + minor, as
 // the CUDA runtime reports it for a loaded kernel), or -1 when it cannot be read.

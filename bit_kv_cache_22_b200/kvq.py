@@ -84,7 +84,7 @@ class PagedSizes(ctypes.Structure):
 class Chunk(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("residual", ctypes.c_int32), ("blocks", ctypes.c_int32),
-                ("read_tiles", ctypes.c_int32), ("reserved", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("read_tiles", ctypes.c_int32), ("items", ctypes.c_int32), ("tokens", ctypes.c_int64),
                 ("table_bytes", ctypes.c_size_t), ("counts", ctypes.c_void_p), ("starts", ctypes.c_void_p),
                 ("table", ctypes.c_void_p)]
 
@@ -448,6 +448,14 @@ class _Call:
             g.__exit__(*exc)
 
 
+def _servable(t: torch.Tensor) -> bool:
+    """Packed rows the kernels take as they are: channels contiguous, rows on 16 bytes, strides positive."""
+    a, b, c = t.stride()
+    n, h, _ = t.shape
+    return c == 1 and t.data_ptr() % 16 == 0 and (n < 2 or (a > 0 and a % 8 == 0)) and \
+        (h < 2 or (b > 0 and b % 8 == 0))
+
+
 def _packed(t: torch.Tensor, name: str, tokens: int, heads: int, d: int, dtype, device) -> torch.Tensor:
     """Packed rows as a kernel takes them: checked, on the device, channels contiguous, rows on 16
     bytes (copied where they are not)."""
@@ -457,10 +465,9 @@ def _packed(t: torch.Tensor, name: str, tokens: int, heads: int, d: int, dtype, 
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         t = t.to(device, non_blocking=True)
-    a, b, c = t.stride()
-    if t.numel() and (c != 1 or a % 8 or b % 8 or t.data_ptr() % 16):
+    if t.numel() and not _servable(t):
         t = t.contiguous()
-        if t.data_ptr() % 16:
+        if not _servable(t):
             t = t.clone()
     return t
 
@@ -470,8 +477,7 @@ def _output(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
     if out.shape != shape or out.dtype != dtype or out.device != device:
         raise ValueError(f"out must be {dtype} {list(shape)} on {device}")
-    a, b, c = out.stride()
-    if out.numel() and (c != 1 or a % 8 or b % 8 or out.data_ptr() % 16):
+    if out.numel() and not _servable(out):
         raise ValueError("out's channels must be contiguous and its rows start on 16 bytes")
     return out
 

@@ -449,9 +449,8 @@ KVQ_API kvq_status kvq_paged_check_device(kvq_paged *cache);
  * plan's calls.
  *
  * Packed rows: row i of head h starts at data + i * token_stride + h * head_stride (elements;
- * channels are contiguous).  data 16-byte aligned, strides multiples of 8; e elements.
- * Negative strides are not served.  Rows of inputs may overlap (stride 0 broadcasts a head);
- * rows of outputs must not.
+ * channels are contiguous).  data 16-byte aligned; strides positive multiples of 8 (free where
+ * there is one token or one head); e elements.  Rows of outputs must not overlap.
  *
  * The calls follow the conventions above: asynchronous on `stream`, nothing allocated, an
  * error launches nothing and changes no state.  They may be captured into a CUDA graph: a
@@ -468,7 +467,7 @@ typedef struct {
     int32_t residual;        /* R of the paged caches the plan serves; 0: a prompt plan     */
     int32_t blocks;          /* blocks of R tokens that kvq_paged_append_chunk quantizes    */
     int32_t read_tiles;      /* 16-token tiles that kvq_paged_read_chunk visits             */
-    int32_t reserved;
+    int32_t items;           /* pieces of work of the attention calls                       */
     int64_t tokens;          /* packed rows: the sum of counts                              */
     size_t table_bytes;      /* size of the table                                           */
     const int32_t *counts;   /* host [batch]                                                */

@@ -45,6 +45,11 @@ def test_table_of_random_plans():
                   for i in range(starts[b] // R, (starts[b] + counts[b]) // R)]
         at = 3 * B + 2
         assert [tuple(t[at + 2 * i:at + 2 * i + 2]) for i in range(out.blocks)] == blocks and out.blocks == len(blocks)
+        at = -(-(at + 2 * out.blocks) // 4) * 4
+        items = [tuple(t[i:i + 2]) for i in range(at, len(t) - 1, 4)]
+        assert sorted(items) == [(b, i) for b in range(B) for i in range(0, counts[b], 64)] and len(items) == out.items
+        seen = [starts[b] + min(i + 64, counts[b]) for b, i in items]
+        assert seen == sorted(seen, reverse=True)
 
 
 @pytest.mark.parametrize("counts,starts", [([-1, 0, 0], [0, 0, 0]), ([1, 0, 0], [-1, 0, 0]),
@@ -88,7 +93,7 @@ def test_calls_refuse_bad_arguments_before_any_launch():
     out.table = fake
     assert attend(out, dtype=9) == kvq.KVQ_ERR_INVALID_ARG
     for bad in (kvq.Rows(None, 512, 128), kvq.Rows(fake + 2, 512, 128), kvq.Rows(fake, 500, 128),
-                kvq.Rows(fake, 512, -128), kvq.Rows(fake, 512, 4)):
+                kvq.Rows(fake, 512, -128), kvq.Rows(fake, 512, 4), kvq.Rows(fake, 0, 128), kvq.Rows(fake, 512, 0)):
         assert attend(out, q=bad) == kvq.KVQ_ERR_INVALID_ARG
         assert attend(out, o=bad) == kvq.KVQ_ERR_INVALID_ARG
     assert lib.kvq_prompt_attention(None, 0, r(good), r(good), r(good), r(good), None, None) == kvq.KVQ_ERR_INVALID_ARG
