@@ -100,130 +100,132 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
-    if (warp >= 8) tc::regs_give<80>();
-    else tc::regs_take<208>();
-
-    if (warp == 9) {
-        // ------------------------------ loads ------------------------------
-        int issued = 0;                            // key and value tiles asked for
-        if (lane == 0) {
-            const uint32_t q_bytes = static_cast<uint32_t>(hg * tpt * D * 2);
-            auto load = [&](const CUtensorMap *map, uint32_t dst, int head, int tok, uint32_t b) {
+    if (warp >= 8) {
+        tc::regs_give<80>();
+        if (warp == 9) {
+            // ------------------------------ loads ------------------------------
+            int issued_k = 0, issued = 0;          // key and value tiles asked for
+            if (lane == 0) {
+                const uint32_t q_bytes = static_cast<uint32_t>(hg * tpt * D * 2);
+                auto load = [&](const CUtensorMap *map, uint32_t dst, int head, int tok, uint32_t b) {
 #pragma unroll
-                for (int p = 0; p < D / 64; ++p) tc::tma_load_3d(dst + p * kRows * 128, map, 64 * p, head, tok, b);
-            };
-            for (int t = 0; t < 2; ++t) {
-                if (n_tiles[t]) {
-                    tc::bar_expect(bar(kQFull + t), q_bytes);
-                    load(&map_q, base + L::q + t * L::kTileBytes, h * hg, first + q0 + t * tpt, bar(kQFull + t));
-                }
-                if (t == 0) {
-                    tc::bar_expect(bar(kKFull), L::kTileBytes);
-                    load(&map_k, base + L::k, h, first, bar(kKFull));
-                }
-            }
-            bool go = true;
-            for (int j = 0; j < n_max && go; ++j) {
-                const int s = j % kStages, phase = (j / kStages) & 1;
-                if (j > 0) {
-                    if (j >= kStages) go = tc::bar_wait(bar(kKEmpty + s), phase ^ 1, &gave_up);
-                    if (!go) break;
-                    tc::bar_expect(bar(kKFull + s), L::kTileBytes);
-                    load(&map_k, base + L::k + s * L::kTileBytes, h, first + j * kRows, bar(kKFull + s));
-                }
-                if (j >= kStages) go = tc::bar_wait(bar(kVEmpty + s), phase ^ 1, &gave_up);
-                if (!go) break;
-                tc::bar_expect(bar(kVFull + s), L::kTileBytes);
-                load(&map_v, base + L::v + s * L::kTileBytes, h, first + j * kRows, bar(kVFull + s));
-                issued = j + 1;
-            }
-        }
-        issued = __shfl_sync(0xffffffffu, issued, 0);
-        // The last value tile may reach past the sequence, into rows that are another's or
-        // anything: their weights are 0, but 0 times an infinity is not, so they are cleared.
-        const int j = n_max - 1, left = count - j * kRows;
-        if (issued == n_max && left < kRows) {
-            const int s = j % kStages;
-            if (tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up)) {
-                unsigned char *v = smem + L::v + s * L::kTileBytes;
-                for (int i = lane; i < (kRows - left) * 8; i += 32)   // whole 128-byte rows: the swizzle stays inside
-#pragma unroll
-                    for (int p = 0; p < D / 64; ++p)
-                        *reinterpret_cast<uint4 *>(v + p * kRows * 128 + left * 128 + 16 * i) = make_uint4(0, 0, 0, 0);
-                tc::fence_async_proxy();
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(bar(kVFixed));
-            }
-        }
-        if (gave_up && lane == 0) {                // copies in flight land before the CTA leaves
-            volatile int never = 0;
-            for (int t = 0; t < 2; ++t)
-                if (n_tiles[t]) tc::bar_wait(bar(kQFull + t), 0, &never);
-            for (int i = max(0, issued - kStages); i < issued; ++i) {
-                tc::bar_wait(bar(kKFull + i % kStages), (i / kStages) & 1, &never);
-                tc::bar_wait(bar(kVFull + i % kStages), (i / kStages) & 1, &never);
-            }
-        }
-    } else if (warp == 8) {
-        // ------------------------------ MMAs -------------------------------
-        if (lane == 0) {
-            constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, BF16, false);
-            constexpr uint32_t kDescO = tc::mma_desc(kRows, D, BF16, true);
-            auto issue_s = [&](int t, int s) {
-                const uint64_t qd = tc::desc_k_major(base + L::q + t * L::kTileBytes);
-                const uint64_t kd = tc::desc_k_major(base + L::k + s * L::kTileBytes);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t step = (i / 4) * (kRows * 128 / 16) + (i % 4) * 2;
-                    tc::mma_ss(tmem + t * 128, qd + step, kd + step, kDescS, i > 0);
-                }
-                tc::mma_commit(bar(kSFull + t));
-            };
-            bool go = tc::bar_wait(bar(kKFull), 0, &gave_up);
-            for (int t = 0; t < 2 && go; ++t)
-                if (n_tiles[t]) {
-                    go = tc::bar_wait(bar(kQFull + t), 0, &gave_up);
-                    if (go) issue_s(t, 0);
-                }
-            if (go) tc::mma_commit(bar(kKEmpty));
-            for (int j = 0; j < n_max && go; ++j) {
-                const int s = j % kStages, s1 = (j + 1) % kStages;
-                go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
-                if (go && j == n_max - 1 && count - j * kRows < kRows) go = tc::bar_wait(bar(kVFixed), 0, &gave_up);
-                for (int t = 0; t < 2 && go; ++t) {
-                    if (j >= n_tiles[t]) continue;
-                    go = tc::bar_wait(bar(kPFull + t), j & 1, &gave_up);
-                    if (!go) break;
-                    tc::fence_after_sync();
-                    const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
-#pragma unroll
-                    for (int i = 0; i < kRows / 16; ++i)
-                        tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
-                                   j > 0 || i > 0);
-                    if (j + 1 < n_tiles[t]) {
-                        go = tc::bar_wait(bar(kKFull + s1), ((j + 1) / kStages) & 1, &gave_up);
-                        if (go) issue_s(t, s1);
-                    } else {
-                        tc::mma_commit(bar(kOFull + t));
+                    for (int p = 0; p < D / 64; ++p) tc::tma_load_3d(dst + p * kRows * 128, map, 64 * p, head, tok, b);
+                };
+                for (int t = 0; t < 2; ++t) {
+                    if (n_tiles[t]) {
+                        tc::bar_expect(bar(kQFull + t), q_bytes);
+                        load(&map_q, base + L::q + t * L::kTileBytes, h * hg, first + q0 + t * tpt, bar(kQFull + t));
+                    }
+                    if (t == 0) {
+                        tc::bar_expect(bar(kKFull), L::kTileBytes);
+                        load(&map_k, base + L::k, h, first, bar(kKFull));
+                        issued_k = 1;
                     }
                 }
-                if (go) {
-                    tc::mma_commit(bar(kVEmpty + s));
-                    if (j + 1 < n_max) tc::mma_commit(bar(kKEmpty + s1));
+                bool go = true;
+                for (int j = 0; j < n_max && go; ++j) {
+                    const int s = j % kStages, phase = (j / kStages) & 1;
+                    if (j > 0) {
+                        if (j >= kStages) go = tc::bar_wait(bar(kKEmpty + s), phase ^ 1, &gave_up);
+                        if (!go) break;
+                        tc::bar_expect(bar(kKFull + s), L::kTileBytes);
+                        load(&map_k, base + L::k + s * L::kTileBytes, h, first + j * kRows, bar(kKFull + s));
+                        issued_k = j + 1;
+                    }
+                    if (j >= kStages) go = tc::bar_wait(bar(kVEmpty + s), phase ^ 1, &gave_up);
+                    if (!go) break;
+                    tc::bar_expect(bar(kVFull + s), L::kTileBytes);
+                    load(&map_v, base + L::v + s * L::kTileBytes, h, first + j * kRows, bar(kVFull + s));
+                    issued = j + 1;
                 }
             }
-            if (gave_up) {                         // MMAs in flight end before tensor memory is freed
+            issued = __shfl_sync(0xffffffffu, issued, 0);
+            // The last value tile may reach past the sequence, into rows that are another's or
+            // anything: their weights are 0, but 0 times an infinity is not, so they are cleared.
+            const int j = n_max - 1, left = count - j * kRows;
+            if (issued == n_max && left < kRows) {
+                const int s = j % kStages;
+                if (tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up)) {
+                    unsigned char *v = smem + L::v + s * L::kTileBytes;
+                    for (int i = lane; i < (kRows - left) * 8; i += 32)   // whole 128-byte rows: the swizzle stays inside
+#pragma unroll
+                        for (int p = 0; p < D / 64; ++p)
+                            *reinterpret_cast<uint4 *>(v + p * kRows * 128 + left * 128 + 16 * i) = make_uint4(0, 0, 0, 0);
+                    tc::fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(bar(kVFixed));
+                }
+            }
+            if (lane == 0) {                       // copies in flight land before the CTA leaves
                 volatile int never = 0;
+                for (int t = 0; t < 2; ++t)
+                    if (n_tiles[t]) tc::bar_wait(bar(kQFull + t), 0, &never);
+                for (int i = max(0, issued_k - kStages); i < issued_k; ++i)
+                    tc::bar_wait(bar(kKFull + i % kStages), (i / kStages) & 1, &never);
+                for (int i = max(0, issued - kStages); i < issued; ++i)
+                    tc::bar_wait(bar(kVFull + i % kStages), (i / kStages) & 1, &never);
+            }
+        } else if (warp == 8) {
+            // ------------------------------ MMAs -------------------------------
+            if (lane == 0) {
+                constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, BF16, false);
+                constexpr uint32_t kDescO = tc::mma_desc(kRows, D, BF16, true);
+                auto issue_s = [&](int t, int s) {
+                    const uint64_t qd = tc::desc_k_major(base + L::q + t * L::kTileBytes);
+                    const uint64_t kd = tc::desc_k_major(base + L::k + s * L::kTileBytes);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint64_t step = (i / 4) * (kRows * 128 / 16) + (i % 4) * 2;
+                        tc::mma_ss(tmem + t * 128, qd + step, kd + step, kDescS, i > 0);
+                    }
+                    tc::mma_commit(bar(kSFull + t));
+                };
+                bool go = tc::bar_wait(bar(kKFull), 0, &gave_up);
+                for (int t = 0; t < 2 && go; ++t)
+                    if (n_tiles[t]) {
+                        go = tc::bar_wait(bar(kQFull + t), 0, &gave_up);
+                        if (go) issue_s(t, 0);
+                    }
+                if (go) tc::mma_commit(bar(kKEmpty));
+                for (int j = 0; j < n_max && go; ++j) {
+                    const int s = j % kStages, s1 = (j + 1) % kStages;
+                    go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
+                    if (go && j == n_max - 1 && count - j * kRows < kRows) go = tc::bar_wait(bar(kVFixed), 0, &gave_up);
+                    for (int t = 0; t < 2 && go; ++t) {
+                        if (j >= n_tiles[t]) continue;
+                        go = tc::bar_wait(bar(kPFull + t), j & 1, &gave_up);
+                        if (!go) break;
+                        tc::fence_after_sync();
+                        const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
+#pragma unroll
+                        for (int i = 0; i < kRows / 16; ++i)
+                            tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
+                                       j > 0 || i > 0);
+                        if (j + 1 < n_tiles[t]) {
+                            go = tc::bar_wait(bar(kKFull + s1), ((j + 1) / kStages) & 1, &gave_up);
+                            if (go) issue_s(t, s1);
+                        } else {
+                            tc::mma_commit(bar(kOFull + t));
+                        }
+                    }
+                    if (go) {
+                        tc::mma_commit(bar(kVEmpty + s));
+                        if (j + 1 < n_max) tc::mma_commit(bar(kKEmpty + s1));
+                    }
+                }
+                volatile int never = 0;            // MMAs in flight end before tensor memory is freed
                 tc::mma_commit(bar(kDrain));
                 tc::bar_wait(bar(kDrain), 0, &never);
             }
         }
-    } else if (warp < 8) {
+    } else {
+        tc::regs_take<208>();
         // ------------------------------ softmax ----------------------------
         const int t = warp >> 2, r = threadIdx.x & 127;
         const int tok0 = q0 + t * tpt, tok = tok0 + r / hg;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+        const float scale = a.scale;
         float m = 0.0f, l = 0.0f;
         bool go = true;
         for (int j = 0; j < n_tiles[t] && go; ++j) {
@@ -243,12 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                     for (int i = 0; i < 32; ++i)
                         if (32 * c + i >= seen) s[c][i] = 0xff800000u;
             }
-            float mx = __uint_as_float(s[0][0]);
+            float mxs[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
+                mxs[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[c][i]));
-            mx *= a.scale;
+                for (int i = 1; i < 32; ++i) mxs[c] = fmaxf(mxs[c], __uint_as_float(s[c][i]));
+            }
+            const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * scale;
             if (j == 0) {
                 m = mx;
             } else if (__any_sync(0xffffffffu, mx > m + kLazyMax)) {
@@ -266,16 +270,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                     tc::tmem_store(to + 32 * c, o);
                 }
             }
+            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                uint32_t p[32];
+                uint32_t(&p)[32] = s[2 * half];    // a weight takes the place of a logit read before
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const uint32_t *src = &s[2 * half + i / 16][2 * (i % 16)];
-                    const float p0 = tc::ex2(fmaf(__uint_as_float(src[0]), a.scale, -m));
-                    const float p1 = tc::ex2(fmaf(__uint_as_float(src[1]), a.scale, -m));
-                    l += p0 + p1;
-                    p[i] = narrow2<BF16>(p0, p1);
+                    const float2 y = tc::fma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])),
+                                              make_float2(scale, scale), make_float2(-m, -m));
+                    const float2 w = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+                    l2[i % 2] = tc::add2(l2[i % 2], w);
+                    p[i] = narrow2<BF16>(w.x, w.y);
                 }
                 tc::tmem_store(ts + 32 * half, p);
             }
@@ -283,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(bar(kPFull + t));
+            l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         }
         if (go && n_tiles[t]) go = tc::bar_wait(bar(kOFull + t), 0, &gave_up);
         if (go && n_tiles[t]) {
