@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
             const int j = n_max - 1, left = count - j * kRows;
             if (issued == n_max && left < kRows) {
                 const int s = j % kStages;
-                if (tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up)) {
+                if (tc::bar_wait_warp(bar(kVFull + s), (j / kStages) & 1, &gave_up)) {
                     unsigned char *v = smem + L::v + s * L::kTileBytes;
                     for (int i = lane; i < (kRows - left) * 8; i += 32)   // whole 128-byte rows: the swizzle stays inside
 #pragma unroll
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         float m = 0.0f, l = 0.0f;
         bool go = true;
         for (int j = 0; j < n_tiles[t] && go; ++j) {
-            go = tc::bar_wait(bar(kSFull + t), j & 1, &gave_up);
+            go = tc::bar_wait_warp(bar(kSFull + t), j & 1, &gave_up);
             if (!go) break;
             tc::fence_after_sync();
             uint32_t s[4][32];
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
             if (lane == 0) tc::bar_arrive(bar(kPFull + t));
             l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         }
-        if (go && n_tiles[t]) go = tc::bar_wait(bar(kOFull + t), 0, &gave_up);
+        if (go && n_tiles[t]) go = tc::bar_wait_warp(bar(kOFull + t), 0, &gave_up);
         if (go && n_tiles[t]) {
             tc::fence_after_sync();
             const float inv = 1.0f / l;
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
+                __syncwarp();
                 tc::tmem_load(to + 32 * c, o);
                 tc::tmem_arrived(o);
                 if (mine) {

@@ -1105,31 +1105,58 @@ namespace {
 
 // The table, as int32: offsets [B + 1], starts [B], read tiles before each slot [B + 1], blocks
 // [n_blocks][2] = (slot, block), and from a multiple of 4 on the attention's items [n_items][4] =
-// (slot, first query token, 0, 0).
+// (slot, first query token, splits << 16 | split, first partial tile) and merges [n_merges][4] =
+// (slot, first query token, splits, first partial tile).
 struct ChunkLayout {
-    int64_t starts, tiles, blocks, items, end;
+    int64_t starts, tiles, blocks, items, merges, end;
 };
-ChunkLayout chunk_layout(int64_t B, int64_t n_blocks, int64_t n_items) {
+ChunkLayout chunk_layout(int64_t B, int64_t n_blocks, int64_t n_items, int64_t n_merges) {
     ChunkLayout l;
     l.starts = B + 1;
     l.tiles = l.starts + B;
     l.blocks = l.tiles + B + 1;
     l.items = (l.blocks + 2 * n_blocks + 3) / 4 * 4;
-    l.end = l.items + 4 * n_items;
+    l.merges = l.items + 4 * n_items;
+    l.end = l.merges + 4 * n_merges;
     return l;
 }
 
 constexpr int64_t kMaxInt = 0x7fffffff;
 constexpr int64_t kMaxStride = int64_t{1} << 38;   // elements: a tensor map's strides end at 2^40 bytes
 
+// One piece of attention work before it is split: tokens q0 .. of a slot's chunk, whose last row
+// sees `tiles` tiles of 128 tokens.
+struct Piece {
+    int32_t slot, q0;
+    int64_t tiles;
+    bool one_tile;               // its rows fill at most one query tile
+    int32_t splits;
+};
+
+// Splits of the pieces over their keys: a CTA's share is at most `share` key tiles.  The shares
+// of all SMs even out when each SM gets several; a CTA's start and end cost a few tiles' time, so a
+// share is not below kMinShare.
+constexpr int64_t kMinShare = 16, kSharesPerSm = 4;
+
+void split_pieces(std::vector<Piece> &pieces, int32_t kv_heads, int32_t num_sms) {
+    int64_t total = 0;
+    for (const Piece &p : pieces) total += p.tiles * kv_heads;
+    int64_t share = (total + num_sms * kSharesPerSm - 1) / (num_sms * kSharesPerSm);
+    if (share < kMinShare) share = kMinShare;
+    for (Piece &p : pieces) {
+        int64_t n = (p.tiles + share - 1) / share;
+        p.splits = static_cast<int32_t>(n < 1 ? 1 : n > 1024 ? 1024 : n);
+    }
+}
+
 kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t R, const int32_t *counts,
-                      const int32_t *starts, kvq_chunk *out, void *table, size_t table_bytes) {
+                      const int32_t *starts, int32_t num_sms, kvq_chunk *out, void *table, size_t table_bytes) {
     if (!counts || !out) return fail(KVQ_ERR_INVALID_ARG, "counts and out must be non-NULL");
     if (q_heads / kv_heads > 128)
         return fail(KVQ_ERR_UNSUPPORTED, "at most 128 query heads per kv head (got %d)", q_heads / kv_heads);
     // a CTA's two query tiles of 128 rows: tokens x the query heads of one kv head
-    const int64_t per_item = 2 * (128 / (q_heads / kv_heads));
-    int64_t tokens = 0, blocks = 0, tiles = 0, items = 0;
+    const int64_t tile_tokens = 128 / (q_heads / kv_heads);
+    int64_t tokens = 0, blocks = 0, tiles = 0, n_pieces = 0;
     for (int b = 0; b < batch; ++b) {
         const int64_t n = counts[b], s = starts ? starts[b] : 0;
         if (n < 0 || s < 0 || s + n > kMaxInt)
@@ -1137,14 +1164,36 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
                         static_cast<long long>(s));
         if (n == 0) continue;
         tokens += n;
-        items += (n + per_item - 1) / per_item;
+        n_pieces += (n + 2 * tile_tokens - 1) / (2 * tile_tokens);
         if (R > 0) {
             blocks += (s + n) / R - s / R;
             tiles += (s + n + 15) / 16 - s / 16;
         }
     }
-    const ChunkLayout l = chunk_layout(batch, blocks, items);
-    if (tokens * q_heads > kMaxInt || items * kv_heads > kMaxInt || tiles * kv_heads > kMaxInt || l.end > kMaxInt)
+    if (tokens * q_heads > kMaxInt || n_pieces * kv_heads > kMaxInt || tiles * kv_heads > kMaxInt || blocks > kMaxInt / 4)
+        return fail(KVQ_ERR_INVALID_ARG, "too many tokens for one chunk (%lld)", static_cast<long long>(tokens));
+    std::vector<Piece> pieces;
+    pieces.reserve(static_cast<size_t>(n_pieces));
+    for (int b = 0; b < batch; ++b) {
+        const int64_t n = counts[b], s = starts ? starts[b] : 0;
+        for (int64_t i = 0; i < n; i += 2 * tile_tokens) {
+            const int64_t last = i + 2 * tile_tokens < n ? i + 2 * tile_tokens : n;
+            pieces.push_back({b, static_cast<int32_t>(i), (s + last + 127) / 128, last - i <= tile_tokens, 1});
+        }
+    }
+    if (R > 0) split_pieces(pieces, kv_heads, num_sms);
+    // the longest first, so that the last CTAs to start are short
+    std::stable_sort(pieces.begin(), pieces.end(), [](const Piece &x, const Piece &y) {
+        return x.tiles * y.splits > y.tiles * x.splits;
+    });
+    int64_t items = 0, merges = 0, parts = 0;
+    for (const Piece &p : pieces) {
+        items += p.splits;
+        merges += p.splits > 1;
+        parts += p.splits > 1 ? p.splits * (p.one_tile ? 1 : 2) : 0;
+    }
+    const ChunkLayout l = chunk_layout(batch, blocks, items, merges);
+    if (items * kv_heads > kMaxInt || merges > 65535 || l.end > kMaxInt)
         return fail(KVQ_ERR_INVALID_ARG, "too many tokens for one chunk (%lld)", static_cast<long long>(tokens));
     std::memset(out, 0, sizeof *out);
     out->batch = batch;
@@ -1155,8 +1204,11 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     out->blocks = static_cast<int32_t>(blocks);
     out->read_tiles = static_cast<int32_t>(tiles);
     out->items = static_cast<int32_t>(items);
+    out->merges = static_cast<int32_t>(merges);
+    out->part_tiles = static_cast<int32_t>(parts);
     out->tokens = tokens;
     out->table_bytes = static_cast<size_t>(l.end) * sizeof(int32_t);
+    out->workspace = static_cast<size_t>(parts) * kv_heads * 128 * (d + 2) * sizeof(float);
     out->counts = counts;
     out->starts = starts;
     if (!table) return ok();
@@ -1180,28 +1232,22 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     t[batch] = row;
     t[l.tiles + batch] = tile;
     while (blk < t + l.items) *blk++ = 0;
-    // the items that see the most tokens first, so that the last CTAs to start are short
-    std::vector<std::pair<int32_t, int32_t>> order;
-    order.reserve(static_cast<size_t>(items));
-    for (int b = 0; b < batch; ++b)
-        for (int64_t i = 0; i < counts[b]; i += per_item) order.emplace_back(b, static_cast<int32_t>(i));
-    auto seen = [&](const std::pair<int32_t, int32_t> &i) {
-        const int64_t n = counts[i.first], last = i.second + per_item;
-        return (starts ? starts[i.first] : 0) + (last < n ? last : n);
-    };
-    std::stable_sort(order.begin(), order.end(), [&](const auto &x, const auto &y) { return seen(x) > seen(y); });
-    int32_t *it = t + l.items;
-    for (const auto &i : order) {
-        *it++ = i.first;
-        *it++ = i.second;
-        *it++ = 0;
-        *it++ = 0;
+    int32_t *it = t + l.items, *mg = t + l.merges, part = 0;
+    for (const Piece &p : pieces) {
+        for (int32_t i = 0; i < p.splits; ++i) {
+            const int32_t e[4] = {p.slot, p.q0, p.splits << 16 | i, part};
+            it = std::copy(e, e + 4, it);
+        }
+        if (p.splits == 1) continue;
+        const int32_t e[4] = {p.slot, p.q0, p.splits, part};
+        mg = std::copy(e, e + 4, mg);
+        part += p.splits * (p.one_tile ? 1 : 2);
     }
     return ok();
 }
 
 kvq::ChunkTable chunk_table(const kvq_chunk *p) {
-    const ChunkLayout l = chunk_layout(p->batch, p->blocks, p->items);
+    const ChunkLayout l = chunk_layout(p->batch, p->blocks, p->items, p->merges);
     kvq::ChunkTable t{};
     t.offsets = p->table;
     t.starts = p->table + l.starts;
@@ -1209,6 +1255,8 @@ kvq::ChunkTable chunk_table(const kvq_chunk *p) {
     t.blocks = p->table + l.blocks;
     t.items = reinterpret_cast<const int4 *>(p->table + l.items);
     t.n_items = p->items;
+    t.merges = reinterpret_cast<const int4 *>(p->table + l.merges);
+    t.n_merges = p->merges;
     t.n_blocks = p->blocks;
     t.n_tiles = p->read_tiles;
     t.tokens = p->tokens;
@@ -1306,13 +1354,15 @@ kvq::AttendArgs attend_args(const kvq_chunk *p, const kvq_rows *q, const kvq_row
 
 extern "C" {
 
-kvq_status kvq_plan_chunk(const kvq_paged_config *cfg, const int32_t *counts, const int32_t *starts, kvq_chunk *out,
-                          void *table, size_t table_bytes) {
+kvq_status kvq_plan_chunk(const kvq_paged_config *cfg, const int32_t *counts, const int32_t *starts, int32_t num_sms,
+                          kvq_chunk *out, void *table, size_t table_bytes) {
     const kvq_status st = validate_paged(cfg);
     if (st != KVQ_OK) return st;
     if (!starts) return fail(KVQ_ERR_INVALID_ARG, "starts is NULL");
+    if (num_sms < 1) return fail(KVQ_ERR_INVALID_ARG, "num_sms must be >= 1");
     const kvq_config &g = cfg->geom;
-    return plan_chunk(g.batch, g.q_heads, g.kv_heads, g.head_dim, g.residual, counts, starts, out, table, table_bytes);
+    return plan_chunk(g.batch, g.q_heads, g.kv_heads, g.head_dim, g.residual, counts, starts, num_sms, out, table,
+                      table_bytes);
 }
 
 kvq_status kvq_plan_prompt(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, const int32_t *counts,
@@ -1322,7 +1372,7 @@ kvq_status kvq_plan_prompt(int32_t batch, int32_t q_heads, int32_t kv_heads, int
     if (batch > 65535 || q_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "batch and q_heads must be <= 65535");
     if (head_dim != 64 && head_dim != 128)
         return fail(KVQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
-    return plan_chunk(batch, q_heads, kv_heads, head_dim, 0, counts, nullptr, out, table, table_bytes);
+    return plan_chunk(batch, q_heads, kv_heads, head_dim, 0, counts, nullptr, 1, out, table, table_bytes);
 }
 
 kvq_status kvq_prompt_attention(const kvq_chunk *plan, int32_t dtype, const kvq_rows *q, const kvq_rows *k,
@@ -1429,10 +1479,15 @@ kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const 
     if (st == KVQ_OK) st = check_rows(o, "o", plan->tokens, plan->q_heads);
     if (st == KVQ_OK) st = check_held(h, plan);
     if (st != KVQ_OK) return st;
-    (void)workspace;
-    (void)workspace_bytes;
+    if (plan->workspace > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < plan->workspace))
+        return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold %zu bytes", plan->workspace);
     kvq::AttendArgs a = attend_args(plan, q, o, h->base.cfg.dtype == KVQ_BF16);
     a.cache = paged_view(h);
+    a.part_tiles = plan->part_tiles;
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = a.part_o + static_cast<int64_t>(plan->part_tiles) * plan->kv_heads * 128 * plan->head_dim;
+    for (int b = 0; b < plan->batch; ++b)
+        if (plan->counts[b] > a.most_tokens) a.most_tokens = plan->counts[b];
     a.status = a.cache.status;
     const cudaError_t e = kvq::launch_attend_cache(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");

@@ -53,8 +53,10 @@ struct ChunkTable {
     const int32_t *starts;       // [B]
     const int32_t *tiles;        // [B + 1]: 16-token tiles of the slots before
     const int32_t *blocks;       // [n_blocks][2]: slot, block of R tokens
-    const int4 *items;           // [n_items] attention work: slot, first query token, ...
-    int n_blocks, n_tiles, n_items;
+    const int4 *items;           // [n_items] attention work: slot, first query token, splits << 16 | split,
+                                 // first partial tile of the item's splits
+    const int4 *merges;          // [n_merges] items in splits: slot, first query token, splits, first partial tile
+    int n_blocks, n_tiles, n_items, n_merges;
     int64_t tokens;
     int B;
 };
@@ -247,6 +249,11 @@ struct AttendArgs {
     int B, Hq, Hkv, d;
     bool bf16;
     float scale;                 // log2(e) / sqrt(d)
+    int64_t most_tokens;         // of any slot's chunk
+    // splits' partial results, tiles of 128 query rows: [part_tiles][Hkv][128][d], and maxima and sums
+    // [part_tiles][Hkv][2][128]
+    float *part_o, *part_ml;
+    int64_t part_tiles;
     unsigned int *status;        // or NULL
 };
 cudaError_t launch_attend_cache(const AttendArgs &a, cudaStream_t s);

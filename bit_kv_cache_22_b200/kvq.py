@@ -84,8 +84,9 @@ class PagedSizes(ctypes.Structure):
 class Chunk(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("residual", ctypes.c_int32), ("blocks", ctypes.c_int32),
-                ("read_tiles", ctypes.c_int32), ("items", ctypes.c_int32), ("tokens", ctypes.c_int64),
-                ("table_bytes", ctypes.c_size_t), ("counts", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("read_tiles", ctypes.c_int32), ("items", ctypes.c_int32), ("merges", ctypes.c_int32),
+                ("part_tiles", ctypes.c_int32), ("tokens", ctypes.c_int64), ("table_bytes", ctypes.c_size_t),
+                ("workspace", ctypes.c_size_t), ("counts", ctypes.c_void_p), ("starts", ctypes.c_void_p),
                 ("table", ctypes.c_void_p)]
 
 
@@ -178,7 +179,7 @@ def load() -> ctypes.CDLL:
                                         ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)]
         lib.kvq_plan_decode.restype = ctypes.c_int
         RP = ctypes.POINTER(Rows)
-        lib.kvq_plan_chunk.argtypes = [ctypes.POINTER(PagedConfig), P, P, ctypes.POINTER(Chunk), P, sz]
+        lib.kvq_plan_chunk.argtypes = [ctypes.POINTER(PagedConfig), P, P, i32, ctypes.POINTER(Chunk), P, sz]
         lib.kvq_plan_prompt.argtypes = [i32, i32, i32, i32, P, ctypes.POINTER(Chunk), P, sz]
         lib.kvq_prompt_attention.argtypes = [ctypes.POINTER(Chunk), i32, RP, RP, RP, RP, P, P]
         lib.kvq_paged_append_chunk.argtypes = [P, ctypes.POINTER(Chunk), RP, RP, ctypes.POINTER(RopeArgs), RP, RP, P]
@@ -521,10 +522,11 @@ class ChunkPlan:
         self.chunk = Chunk()
         self.ref = ctypes.byref(self.chunk)
         lib = load()
+        sms = torch.cuda.get_device_properties(self.device).multi_processor_count if cfg is not None else 0
 
         def fill(table, room):
             if cfg is not None:
-                return lib.kvq_plan_chunk(ctypes.byref(cfg), self._counts, self._starts, self.ref, table, room)
+                return lib.kvq_plan_chunk(ctypes.byref(cfg), self._counts, self._starts, sms, self.ref, table, room)
             return lib.kvq_plan_prompt(batch, *heads, self._counts, self.ref, table, room)
 
         _check(fill(None, 0))
@@ -780,8 +782,11 @@ class PagedKVQCache:
         with _Call(self.device, stream) as s:
             t_Q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
             out = _output(out, t_Q.shape, self.dtype, self.device)
-            _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, _rows(t_Q), _rows(out), None, 0,
-                                                       s.cuda_stream))
+            # scratch of the call's own, from torch's pool of its stream (or graph)
+            room = plan.chunk.workspace
+            work = torch.empty(room, dtype=torch.uint8, device=self.device) if room else None
+            _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, _rows(t_Q), _rows(out),
+                                                       work.data_ptr() if room else None, room, s.cuda_stream))
             return out
 
     def release(self, seq: int, stream=None):

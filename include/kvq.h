@@ -468,8 +468,11 @@ typedef struct {
     int32_t blocks;          /* blocks of R tokens that kvq_paged_append_chunk quantizes    */
     int32_t read_tiles;      /* 16-token tiles that kvq_paged_read_chunk visits             */
     int32_t items;           /* pieces of work of the attention calls                       */
+    int32_t merges;          /* ... of which these many are joined from splits              */
+    int32_t part_tiles;      /* partial results of the splits                               */
     int64_t tokens;          /* packed rows: the sum of counts                              */
     size_t table_bytes;      /* size of the table                                           */
+    size_t workspace;        /* scratch of kvq_paged_chunk_attention (may be 0)             */
     const int32_t *counts;   /* host [batch]                                                */
     const int32_t *starts;   /* host [batch]; NULL for a prompt plan (all 0)                */
     const int32_t *table;    /* device copy of the table, 16-byte aligned: set by the caller */
@@ -499,11 +502,12 @@ typedef struct {
  * Fill `out` but its `table`; write the table to `table` (host, `table_bytes` bytes of room),
  * or only the sizes when `table` is NULL.  Host only, no device needed.  KVQ_ERR_INVALID_ARG
  * for a negative count or start, too little room, or sums past 2^31 - 1; KVQ_ERR_UNSUPPORTED
- * for more than 128 query heads per kv head.  A prompt plan needs no cache: head_dim 64 or 128,
+ * for more than 128 query heads per kv head.  The attention over the cache is cut into pieces for a
+ * GPU of num_sms SMs.  A prompt plan needs no cache: head_dim 64 or 128,
  * q_heads a multiple of kv_heads.
  */
 KVQ_API kvq_status kvq_plan_chunk(const kvq_paged_config *cfg, const int32_t *counts, const int32_t *starts,
-                                  kvq_chunk *out, void *table, size_t table_bytes);
+                                  int32_t num_sms, kvq_chunk *out, void *table, size_t table_bytes);
 KVQ_API kvq_status kvq_plan_prompt(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                    const int32_t *counts, kvq_chunk *out, void *table, size_t table_bytes);
 
@@ -550,7 +554,10 @@ KVQ_API kvq_status kvq_paged_read_chunk(kvq_paged *cache, const kvq_chunk *plan,
  * residual rows as they are; a token's neighbours in its chunk are read from the cache too).
  * q, o: e [tokens][q_heads][d]; o must not overlap q.  starts[b] + counts[b] must not pass the
  * slot's length (KVQ_ERR_STATE); rows of which the device length leaves nothing to see give
- * zeros.  Logits, softmax statistics and sums are fp32.
+ * zeros.  Logits, softmax statistics and sums are fp32; what meets in a product -- queries, keys,
+ * weights, values -- is rounded to fp16 (11 bits) under powers of two that keep it in range, the
+ * output once to e.  `workspace`: plan->workspace bytes of device scratch, 16-byte aligned (NULL
+ * where that is 0); calls that may overlap on the GPU need workspaces of their own.
  */
 KVQ_API kvq_status kvq_paged_chunk_attention(kvq_paged *cache, const kvq_chunk *plan, const kvq_rows *q,
                                              const kvq_rows *o, void *workspace, size_t workspace_bytes,

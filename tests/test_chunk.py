@@ -12,17 +12,17 @@ def config(batch=3, hq=8, hkv=2, R=128, page=128, capacity=1024):
     return kvq.PagedConfig(geom, page, 16)
 
 
-def plan(cfg, counts, starts, room=None):
+def plan(cfg, counts, starts, room=None, sms=148):
     n = len(counts)
     c, s = (ctypes.c_int32 * n)(*counts), (ctypes.c_int32 * n)(*starts)
     out = kvq.Chunk()
     lib = kvq.load()
-    st = lib.kvq_plan_chunk(ctypes.byref(cfg), c, s, ctypes.byref(out), None, 0)
+    st = lib.kvq_plan_chunk(ctypes.byref(cfg), c, s, sms, ctypes.byref(out), None, 0)
     if st != kvq.KVQ_OK:
         return st, None, None
     words = out.table_bytes // 4
     table = (ctypes.c_int32 * (words + 1))(*([77] * (words + 1)))
-    st = lib.kvq_plan_chunk(ctypes.byref(cfg), c, s, ctypes.byref(out), table,
+    st = lib.kvq_plan_chunk(ctypes.byref(cfg), c, s, sms, ctypes.byref(out), table,
                             out.table_bytes if room is None else room)
     assert table[words] == 77                       # nothing past the end
     return st, out, list(table)
@@ -46,10 +46,31 @@ def test_table_of_random_plans():
         at = 3 * B + 2
         assert [tuple(t[at + 2 * i:at + 2 * i + 2]) for i in range(out.blocks)] == blocks and out.blocks == len(blocks)
         at = -(-(at + 2 * out.blocks) // 4) * 4
-        items = [tuple(t[i:i + 2]) for i in range(at, len(t) - 1, 4)]
-        assert sorted(items) == [(b, i) for b in range(B) for i in range(0, counts[b], 64)] and len(items) == out.items
-        seen = [starts[b] + min(i + 64, counts[b]) for b, i in items]
-        assert seen == sorted(seen, reverse=True)
+        items = [tuple(t[i:i + 4]) for i in range(at, at + 4 * out.items, 4)]
+        merges = [tuple(t[i:i + 4]) for i in range(at + 4 * out.items, len(t) - 1, 4)]
+        pieces = {}
+        for b, i, z, part in items:                 # every piece whole, its splits numbered from 0
+            assert z >> 16 >= 1 and z & 0xffff == len(pieces.setdefault((b, i, z >> 16, part), []))
+            pieces[b, i, z >> 16, part].append(z & 0xffff)
+        assert sorted(k[:2] for k in pieces) == [(b, i) for b in range(B) for i in range(0, counts[b], 64)]
+        assert all(len(v) == k[2] for k, v in pieces.items())
+        assert merges == [k for k in pieces if k[2] > 1] and len(merges) == out.merges
+        part = 0                                    # partial results laid end to end
+        for b, i, n, at_part in merges:
+            assert at_part == part
+            part += n * (1 if counts[b] - i <= 32 else 2)
+        assert part == out.part_tiles and out.workspace == part * 2 * 128 * 130 * 4
+        share = [-(-(starts[b] + min(i + 64, counts[b])) // 128) / n for b, i, n, _ in pieces]
+        assert share == sorted(share, reverse=True)
+
+
+def test_a_long_sequence_is_split_over_the_gpu():
+    cfg = config(batch=1, hq=8, hkv=2, capacity=131072)
+    st, out, _ = plan(cfg, [1], [130000])
+    assert st == kvq.KVQ_OK and out.merges == 1 and out.items * 2 > 100
+    st, out, _ = plan(cfg, [1], [130000], sms=1)
+    assert st == kvq.KVQ_OK and out.items * 2 <= 4 * 2
+    assert plan(cfg, [1], [5], sms=0)[0] == kvq.KVQ_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("counts,starts", [([-1, 0, 0], [0, 0, 0]), ([1, 0, 0], [-1, 0, 0]),
@@ -74,7 +95,7 @@ def test_prompt_plans():
                         ([2, 8, 2, 96], kvq.KVQ_ERR_UNSUPPORTED), ([2, 129, 1, 128], kvq.KVQ_ERR_UNSUPPORTED)):
         assert lib.kvq_plan_prompt(*bad, c, ctypes.byref(out), None, 0) == status, bad
     assert lib.kvq_plan_prompt(*ok, None, ctypes.byref(out), None, 0) == kvq.KVQ_ERR_INVALID_ARG
-    assert lib.kvq_plan_chunk(None, c, c, ctypes.byref(out), None, 0) == kvq.KVQ_ERR_INVALID_ARG
+    assert lib.kvq_plan_chunk(None, c, c, 148, ctypes.byref(out), None, 0) == kvq.KVQ_ERR_INVALID_ARG
 
 
 def test_calls_refuse_bad_arguments_before_any_launch():
