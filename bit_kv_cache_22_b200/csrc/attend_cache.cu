@@ -14,8 +14,7 @@
 //
 //   warps 0-3, 4-7   softmax of stream 0, 1: thread = row
 //   warps 8-15       operands: warp w the tokens 16w .. 16w+15 of each key tile
-//   warp 16          issues the MMAs (warps 17-19 fill the warpgroup, which gives its registers to the
-//                    others: 2 x 128 x 112 + 2 x 128 x 104 + 128 x 40 <= 640 x 96)
+//   warp 16          issues the MMAs
 //
 // Operands in fp16 for caches of either type: (code - z) s is computed in fp32 and rounded once to
 // 11 bits (bf16 would leave 8, a rounding as large as the output's own).  What fp16 lacks is range,
@@ -34,13 +33,14 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 544;
 constexpr int kRows = 128;                 // rows of a query tile, tokens of a key tile
 constexpr int kStages = 2;                 // key and value operand tiles, each
 constexpr int kUnpackWarps = 8;
 constexpr int kExps = 8;                   // key tiles whose exponents are kept (at most kStages + 1 are live)
 constexpr float kLazyMax = 8.0f;           // the running maximum is raised when a logit passes it by this
 constexpr float kNoMax = -1e30f;           // the maximum of no logits: finite, so differences stay numbers
+constexpr int kMaxTokens = 0x7fffffff - 1024;   // of a sequence (the planner refuses more)
 constexpr int kMinExp = -112;              // exponents of operand scales: 2^e and 2^-e stay normal
 
 template <int D>
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
         first = a.t.offsets[slot];
         count = a.t.offsets[slot + 1] - first;
         start = a.t.starts[slot];
-        good = first >= 0 && count > q0 && start >= 0 && static_cast<int64_t>(first) + count <= a.t.tokens;
+        good = first >= 0 && count > q0 && start >= 0 && start <= kMaxTokens - count && static_cast<int64_t>(first) + count <= a.t.tokens;
         if (n_splits > 1 &&
             item.w + static_cast<int64_t>(n_splits) * (count - q0 <= tpt ? 1 : 2) > a.part_tiles)
             good = false;
@@ -121,14 +121,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
         if (threadIdx.x == 0) atomicOr(a.status, 8u);
         return;
     }
-    const int len = max(c.seq_len[slot], 0), tq = len / c.R * c.R;
+    // (positions stay below 2^31 - 1024, so a tile's tokens are 32-bit numbers)
+    const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
     const int n_tok = min(2 * tpt, count - q0);
     const bool alternate = n_tok <= tpt;           // one query tile, alternate key tiles
     // key tiles: those the item's last row sees, this split's share [tile0, tile0 + n)
-    const int all = static_cast<int>((min(static_cast<int64_t>(start) + q0 + n_tok, static_cast<int64_t>(len)) +
-                                      kRows - 1) / kRows);
-    const int tile0 = static_cast<int>(static_cast<int64_t>(all) * split / n_splits);
-    const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / n_splits) - tile0;
+    const int all = (min(start + q0 + n_tok, len) + kRows - 1) / kRows;
+    const int share = all / n_splits, extra = all % n_splits;      // the first splits take a tile more
+    const int tile0 = share * split + min(split, extra), n = share + (split < extra);
     // stream t takes tiles first_of(t), + stride, ... below end_of(t)
     const int stride = alternate ? 2 : 1;
     int ends[2];
@@ -136,18 +136,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
     if (alternate) {
         ends[0] = n;
     } else {
-        const int64_t seen = min(static_cast<int64_t>(start) + q0 + tpt, static_cast<int64_t>(len));
-        ends[0] = max(0, min(n, static_cast<int>((seen + kRows - 1) / kRows) - tile0));
+        ends[0] = max(0, min(n, (min(start + q0 + tpt, len) + kRows - 1) / kRows - tile0));
     }
 
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
-    enum { kQFull = 0, kKFull = 1, kKEmpty = 3, kVFull = 5, kVEmpty = 7, kSFull = 9, kPFull = 11, kOFull = 13,
-           kDrain = 15, kBars = 16 };
+    enum { kQFull = 0, kKFull = 1, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages, kVEmpty = kKEmpty + kStages,
+           kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kOFull = kPFull + 2, kDrain = kOFull + 2, kBars };
     if (threadIdx.x == 0) {
         gave_up = 0;
         for (int i = 0; i < kBars; ++i) {
-            const bool unpacked = i == kQFull || i == kKFull || i == kKFull + 1 || i == kVFull || i == kVFull + 1;
+            const bool unpacked = i < kKEmpty;     // kQFull, kKFull, kVFull
             tc::bar_init(bar(i), unpacked ? kUnpackWarps : i == kPFull || i == kPFull + 1 ? 4 : 1);
         }
         tc::fence_barrier_init();
@@ -160,7 +159,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
     float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
 
     if (warp >= 8 && warp < 16) {
-        tc::regs_take<104>();
         // ------------------------------ operands ---------------------------
         const int w = warp - 8;
         // queries: a warp turns a row at a time, four (d = 128) or two channels a lane
@@ -199,20 +197,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
 
         float *meta = reinterpret_cast<float *>(smem + L::meta) + w * L::kMetaFloats;
         float *ks_s = meta, *kz_s = meta + D, *vs_s = meta + 2 * D, *vz_s = vs_s + 128;
-        const int ngv = D / c.Gv;
+        const int gv_shift = __ffs(c.Gv) - 1, g_shift = __ffs(c.G) - 1;      // powers of two
+        const int ngv = D >> gv_shift, ngv_shift = __ffs(ngv) - 1;
         constexpr int B = 4 / N, W = D * N / 64, TW = D * N / 2;
         constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
         constexpr float kTop = static_cast<float>((1 << N) - 1);
 
-        auto page_of = [&](int j) -> int {         // the page of this warp's tokens of tile j
-            const int64_t tok = static_cast<int64_t>(tile0 + j) * kRows + 16 * w;
-            if (j >= n || tok >= tq) return 0;
-            const int64_t pi = tok / c.P;
-            return pi < c.max_pages ? c.page_table[static_cast<int64_t>(slot) * c.max_pages + pi] : -1;
+        const int32_t *pages = c.page_table + static_cast<int64_t>(slot) * c.max_pages;
+        // this warp's place in the pages: of the tile to fetch (page index and token in it), whose page
+        // number is loaded a tile ahead
+        int at_page = ((tile0 * kRows) + 16 * w) / c.P, at_tok = ((tile0 * kRows) + 16 * w) % c.P;
+        auto page_at = [&](int j, int pi) -> int {
+            return j < n && (tile0 + j) * kRows + 16 * w < tq && pi < c.max_pages ? pages[pi] : -1;
+        };
+        auto advance = [&] {
+            at_tok += kRows;
+            while (at_tok >= c.P) {
+                at_tok -= c.P;
+                ++at_page;
+            }
         };
         Fetched<D, N> f;
         auto fetch = [&](int j, int page) {
-            const int64_t tok = static_cast<int64_t>(tile0 + j) * kRows + 16 * w;
+            const int tok = (tile0 + j) * kRows + 16 * w;
             f.kind = j >= n || tok >= len ? 0 : tok < tq ? 1 : 2;
             if (f.kind != 1) return;
             if (page < 0 || page >= c.num_pages) {
@@ -220,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 page = 0;
             }
             const int64_t slice = static_cast<int64_t>(page) * a.Hkv + h;
-            const int pt = static_cast<int>(tok % c.P);
-            const int64_t words = (slice * (c.P / 16) + pt / 16) * TW + lane * W;
+            const int pt = at_tok;
+            const int64_t words = (slice * (c.P >> 4) + (pt >> 4)) * TW + lane * W;
 #pragma unroll
             for (int i = 0; i < W; i += W >= 4 ? 4 : 2) {
                 if constexpr (W >= 4) {
@@ -236,12 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     f.vw[0] = y.x; f.vw[1] = y.y;
                 }
             }
-            const int64_t km = (slice * (c.P / c.G) + pt / c.G) * D + 4 * lane;
+            const int64_t km = (slice * (c.P >> g_shift) + (pt >> g_shift)) * D + 4 * lane;
             if (4 * lane < D) {
                 f.ks = *reinterpret_cast<const float4 *>(c.ks + km);
                 if (!c.sym) f.kz = *reinterpret_cast<const uint2 *>(c.kz + km);
             }
-            const int64_t vm = (slice * c.P + pt) * ngv;
+            const int64_t vm = (slice * c.P + pt) << ngv_shift;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (lane + 32 * i < 16 * ngv) {
@@ -277,11 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                         bv = fmaxf(bv, f.vs[i] * fmaxf(fabsf(zf), fabsf(kTop - zf)));
                     }
             } else if (f.kind == 2) {
-                const int64_t tok = static_cast<int64_t>(tile0 + j) * kRows + 16 * w;
+                const int tok = (tile0 + j) * kRows + 16 * w;
                 for (int i = lane; i < 16 * D / 2; i += 32) {
-                    const int64_t tk = tok + i / (D / 2);
+                    const int tk = tok + i / (D / 2);
                     if (tk < len) {
-                        const int64_t at = tk % c.R * (D / 2) + i % (D / 2);
+                        const int64_t at = static_cast<int64_t>(tk - tq) * (D / 2) + i % (D / 2);
                         const float2 x = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(res_k)[at]);
                         const float2 y = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(res_v)[at]);
                         bk = fmaxf(bk, fmaxf(fabsf(x.x), fabsf(x.y)));
@@ -301,8 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
         // lane's place in an operand tile: row l / 4 (+ 8), 8 bytes l % 4 of a 32-byte step, swizzled
         const uint32_t place = (lane >> 2) * 128 + ((((lane & 3) >> 1) ^ (lane >> 2)) << 4) + (lane & 1) * 8;
 
-        fetch(0, page_of(0));
-        int page = page_of(1);
+        fetch(0, page_at(0, at_page));
+        advance();
+        int page = page_at(1, at_page);
         bound(0);
         for (int j = 0; j < n; ++j) {
             asm volatile("bar.sync 1, %0;" ::"r"(32 * kUnpackWarps) : "memory");
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (lane + 32 * i < 16 * ngv) {
-                        const int tk = (lane + 32 * i) / ngv, g = (lane + 32 * i) % ngv;
+                        const int tk = (lane + 32 * i) >> ngv_shift, g = (lane + 32 * i) & (ngv - 1);
                         vs_s[g * 16 + tk] = f.vs[i] * down_v;
                         vz_s[g * 16 + tk] = -8388608.0f - static_cast<float>(f.vz[i]);
                     }
@@ -347,38 +355,47 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 __syncwarp();
             }
             fetch(j + 1, page);
-            page = page_of(j + 2);
+            advance();
+            page = page_at(j + 2, at_page);
 
             const int s = j % kStages, phase = (j / kStages) & 1;
-            const int64_t tok = static_cast<int64_t>(tile0 + j) * kRows + 16 * w;
+            const int tok = (tile0 + j) * kRows + 16 * w;
+            // four codes at a time: bytes to fp32, minus z, times s, rounded to fp16
+            auto four = [&](uint32_t b, const float4 &sc, const float4 &zr, uint32_t dst) {
+                const float2 x = tc::mul2(tc::add2(make_float2(byte_plus_2_23<0>(b), byte_plus_2_23<1>(b)),
+                                                   make_float2(zr.x, zr.y)), make_float2(sc.x, sc.y));
+                const float2 y = tc::mul2(tc::add2(make_float2(byte_plus_2_23<2>(b), byte_plus_2_23<3>(b)),
+                                                   make_float2(zr.z, zr.w)), make_float2(sc.z, sc.w));
+                tc::store_shared(dst, half2_bits(x.x, x.y), half2_bits(y.x, y.y));
+            };
             // ---- keys: rows = tokens, channels along a row
             // (a warp whose wait gave up keeps step with the others, which meet at the barrier above)
             if (j >= kStages) go = go && tc::bar_wait_warp(bar(kKEmpty + s), phase ^ 1, &gave_up);
-            unsigned char *kt = smem + L::k + s * L::kTileBytes + 16 * w * 128;
+            const uint32_t kt = base + L::k + s * L::kTileBytes + 16 * w * 128;
             if (!go) {
             } else if (kind == 1) {
+                const float4 *s4 = reinterpret_cast<const float4 *>(ks_s) + (lane & 3);
+                const float4 *r4 = reinterpret_cast<const float4 *>(kz_s) + (lane & 3);
+                float4 sc = s4[0], zr = r4[0];
 #pragma unroll
-                for (int ch = 0; ch < D / 16; ++ch) {
-                    const float4 sc = reinterpret_cast<const float4 *>(ks_s)[4 * ch + (lane & 3)];
-                    const float4 zr = reinterpret_cast<const float4 *>(kz_s)[4 * ch + (lane & 3)];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t b = (kw[ch / B] >> (N * (2 * (ch % B) + half))) & kMask;
-                        const float2 x = tc::mul2(tc::add2(make_float2(byte_plus_2_23<0>(b), byte_plus_2_23<1>(b)),
-                                                           make_float2(zr.x, zr.y)), make_float2(sc.x, sc.y));
-                        const float2 y = tc::mul2(tc::add2(make_float2(byte_plus_2_23<2>(b), byte_plus_2_23<3>(b)),
-                                                           make_float2(zr.z, zr.w)), make_float2(sc.z, sc.w));
-                        *reinterpret_cast<uint2 *>(kt + (ch / 4) * (kRows * 128) + half * 1024 +
-                                                   (place ^ ((ch % 4) << 5))) =
-                            make_uint2(half2_bits(x.x, x.y), half2_bits(y.x, y.y));
+                for (int ch = 0; ch < D / 16; ++ch) {      // the next chunk's scales before this one's stores
+                    float4 sc1 = sc, zr1 = zr;
+                    if (ch + 1 < D / 16) {
+                        sc1 = s4[4 * (ch + 1)];
+                        zr1 = r4[4 * (ch + 1)];
                     }
+                    const uint32_t dst = kt + (ch / 4) * (kRows * 128) + (place ^ ((ch % 4) << 5));
+                    four((kw[ch / B] >> (N * 2 * (ch % B))) & kMask, sc, zr, dst);
+                    four((kw[ch / B] >> (N * 2 * (ch % B) + N)) & kMask, sc, zr, dst + 1024);
+                    sc = sc1;
+                    zr = zr1;
                 }
             } else {
                 for (int i = lane; i < 16 * (D / 8); i += 32) {
                     const int r = i / (D / 8), v = i % (D / 8);
                     uint32_t o[4] = {0u, 0u, 0u, 0u};
                     if (kind == 2 && tok + r < len) {
-                        const uint4 x = reinterpret_cast<const uint4 *>(res_k + (tok + r) % c.R * D)[v];
+                        const uint4 x = reinterpret_cast<const uint4 *>(res_k + static_cast<int64_t>(tok + r - tq) * D)[v];
                         const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -386,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                             o[e] = half2_bits(p.x * down_k, p.y * down_k);
                         }
                     }
-                    *reinterpret_cast<uint4 *>(kt + (v / 8) * (kRows * 128) + r * 128 + (((v % 8) ^ (r & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                    tc::store_shared(kt + (v / 8) * (kRows * 128) + r * 128 + (((v % 8) ^ (r & 7)) << 4), o);
                 }
             }
             tc::fence_async_proxy();
@@ -395,51 +411,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
             if (lane == 0) tc::bar_arrive(bar(kKFull + s));
             // ---- values: rows = channels, tokens along a row
             if (j >= kStages) go = go && tc::bar_wait_warp(bar(kVEmpty + s), phase ^ 1, &gave_up);
-            unsigned char *vt = smem + L::v + s * L::kTileBytes + (w / 4) * (D * 128);
+            const uint32_t vt = base + L::v + s * L::kTileBytes + (w / 4) * (D * 128);
             if (!go) {
             } else if (kind == 1) {
-                float4 sc, zr;
+                const float4 *s4 = reinterpret_cast<const float4 *>(vs_s) + (lane & 3);
+                const float4 *r4 = reinterpret_cast<const float4 *>(vz_s) + (lane & 3);
+                float4 sc = s4[0], zr = r4[0];
 #pragma unroll
                 for (int ch = 0; ch < D / 16; ++ch) {
-                    if (ch == 0 || (16 * ch) % c.Gv == 0) {
-                        const int g = 16 * ch / c.Gv;
-                        sc = reinterpret_cast<const float4 *>(vs_s)[4 * g + (lane & 3)];
-                        zr = reinterpret_cast<const float4 *>(vz_s)[4 * g + (lane & 3)];
+                    float4 sc1 = sc, zr1 = zr;
+                    if (ch + 1 < D / 16) {
+                        const int g = (16 * (ch + 1)) >> gv_shift;
+                        sc1 = s4[4 * g];
+                        zr1 = r4[4 * g];
                     }
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t b = (vw[ch / B] >> (N * (2 * (ch % B) + half))) & kMask;
-                        const float2 x = tc::mul2(tc::add2(make_float2(byte_plus_2_23<0>(b), byte_plus_2_23<1>(b)),
-                                                           make_float2(zr.x, zr.y)), make_float2(sc.x, sc.y));
-                        const float2 y = tc::mul2(tc::add2(make_float2(byte_plus_2_23<2>(b), byte_plus_2_23<3>(b)),
-                                                           make_float2(zr.z, zr.w)), make_float2(sc.z, sc.w));
-                        *reinterpret_cast<uint2 *>(vt + (16 * ch + 8 * half) * 128 + (place ^ ((w % 4) << 5))) =
-                            make_uint2(half2_bits(x.x, x.y), half2_bits(y.x, y.y));
-                    }
+                    const uint32_t dst = vt + 16 * ch * 128 + (place ^ ((w % 4) << 5));
+                    four((vw[ch / B] >> (N * 2 * (ch % B))) & kMask, sc, zr, dst);
+                    four((vw[ch / B] >> (N * 2 * (ch % B) + N)) & kMask, sc, zr, dst + 1024);
+                    sc = sc1;
+                    zr = zr1;
                 }
             } else {
                 for (int cp = lane; cp < D / 2; cp += 32) {           // channels 2 cp, 2 cp + 1: 16 tokens each
-                    uint32_t o[2][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 p[2];
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t o[2][4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float2 p[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int tk = tok + 8 * i + 2 * k + e;
+                                p[e] = make_float2(0.0f, 0.0f);
+                                if (kind == 2 && tk < len)
+                                    p[e] = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(
+                                        res_v + static_cast<int64_t>(tk - tq) * D)[cp]);
+                            }
+                            o[0][k] = half2_bits(p[0].x * down_v, p[1].x * down_v);
+                            o[1][k] = half2_bits(p[0].y * down_v, p[1].y * down_v);
+                        }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int64_t tk = tok + 2 * i + e;
-                            p[e] = kind == 2 && tk < len
-                                       ? widen_pair<BF16>(reinterpret_cast<const uint32_t *>(res_v + tk % c.R * D)[cp])
-                                       : make_float2(0.0f, 0.0f);
+                            const int r = 2 * cp + e;
+                            tc::store_shared(vt + r * 128 + (((2 * (w % 4) + i) ^ (r & 7)) << 4), o[e]);
                         }
-                        o[0][i] = half2_bits(p[0].x * down_v, p[1].x * down_v);
-                        o[1][i] = half2_bits(p[0].y * down_v, p[1].y * down_v);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = 2 * cp + e;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint4 *>(vt + r * 128 + (((2 * (w % 4) + i) ^ (r & 7)) << 4)) =
-                                make_uint4(o[e][4 * i], o[e][4 * i + 1], o[e][4 * i + 2], o[e][4 * i + 3]);
                     }
                 }
             }
@@ -448,10 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
             if (lane == 0) tc::bar_arrive(bar(kVFull + s));
             bound(j + 1);
         }
-    } else if (warp >= 16) {
-        tc::regs_give<40>();
+    } else if (warp == 16) {
         // ------------------------------ MMAs -------------------------------
-        if (warp == 16 && lane == 0 && n > 0) {
+        if (lane == 0 && n > 0) {
             constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, false, false);
             constexpr uint32_t kDescO = tc::mma_desc(kRows, D, false, false);
             auto issue_s = [&](int t, int s) {
@@ -503,8 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
             tc::mma_commit(bar(kDrain));
             tc::bar_wait(bar(kDrain), 0, &never);
         }
-    } else {
-        tc::regs_take<112>();
+    } else if (warp < 8) {
         // ------------------------------ softmax ----------------------------
         const int t = warp >> 2, r = threadIdx.x & 127;
         const int qt = alternate ? 0 : t;          // the query tile
@@ -512,8 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
         const bool mine = r < hg * tpt && tok < count;
         const bool any = __any_sync(0xffffffffu, mine);      // a warp without rows only keeps step
         // tokens row r sees, from tile0 on
-        const int64_t seen_all = min(static_cast<int64_t>(start) + tok + 1, static_cast<int64_t>(len));
-        const int seen0 = static_cast<int>(seen_all - static_cast<int64_t>(tile0) * kRows);
+        const int seen0 = min(start + tok + 1, len) - tile0 * kRows;
         const int seen_least = __reduce_min_sync(0xffffffffu, mine ? seen0 : 0x7fffffff);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
@@ -541,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     }
                 };
                 float mx = kNoMax;
-#pragma unroll
+#pragma unroll 1
                 for (int cc = 0; cc < 4; ++cc) {
                     uint32_t x[32];
                     logits(cc, x);
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     m = mn;
                     l *= alpha;
                     e_ref = ev;
-#pragma unroll
+#pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t o[32];
                         tc::tmem_load(to + 32 * cc, o);
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     }
                 }
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
                 for (int cc = 0; cc < 4; ++cc) {
                     uint32_t x[32], p[16];
                     logits(cc, x);
@@ -607,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     ml[r] = m;
                     ml[kRows + r] = l;
                     const float up = pow2(e_ref);
-#pragma unroll
+#pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t o[32];
                         if (had) {
@@ -625,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 tc::fence_after_sync();
                 const float m1 = ml[r], l1 = ml[kRows + r];
                 const float mn = fmaxf(m, m1), w0 = tc::ex2(m - mn), w1 = tc::ex2(m1 - mn);
-                const float sum = l * w0 + l1 * w1, inv = n_splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
+                const float sum = l * w0 + l1 * w1, inv = n_splits > 1 ? 1.0f : sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
                 const float f0 = w0 * inv * pow2(e_ref), f1 = w1 * inv;
                 uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                                 static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     a.part_ml[tile * 2 * kRows + r] = mn;
                     a.part_ml[(tile * 2 + 1) * kRows + r] = sum;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
                     __syncwarp();
@@ -663,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
             }
         } else if (any && go) {
             tc::fence_after_sync();
-            const float f0 = (n_splits > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f) * pow2(e_ref);
+            const float f0 = (n_splits > 1 ? 1.0f : l > 0.0f ? __fdividef(1.0f, l) : 0.0f) * pow2(e_ref);
             uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                             static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
             const int64_t tile = (static_cast<int64_t>(item.w) + 2 * split + t) * a.Hkv + h;
@@ -672,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 a.part_ml[tile * 2 * kRows + r] = m;
                 a.part_ml[(tile * 2 + 1) * kRows + r] = l;
             }
-#pragma unroll
+#pragma unroll 1
             for (int cc = 0; cc < D / 32; ++cc) {
                 uint32_t o[32];
                 __syncwarp();
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_splits_kernel(const At
             o[e + 1] = fmaf(w, x.y, o[e + 1]);
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f;
     uint16_t *out = a.o.p + static_cast<int64_t>(first + q0 + tok) * a.o.ts + static_cast<int64_t>(hq) * a.o.hs + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)

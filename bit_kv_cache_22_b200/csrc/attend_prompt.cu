@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         if (go && n_tiles[t]) go = tc::bar_wait_warp(bar(kOFull + t), 0, &gave_up);
         if (go && n_tiles[t]) {
             tc::fence_after_sync();
-            const float inv = 1.0f / l;
+            const float inv = __fdividef(1.0f, l);
             const bool mine = r < hg * tpt && tok < count;
             uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                             static_cast<int64_t>(h * hg + r % hg) * a.o.hs;

@@ -1122,6 +1122,7 @@ ChunkLayout chunk_layout(int64_t B, int64_t n_blocks, int64_t n_items, int64_t n
 }
 
 constexpr int64_t kMaxInt = 0x7fffffff;
+constexpr int64_t kMaxTokens = kMaxInt - 1024;     // of a sequence: the kernels' token numbers are 32-bit
 constexpr int64_t kMaxStride = int64_t{1} << 38;   // elements: a tensor map's strides end at 2^40 bytes
 
 // One piece of attention work before it is split: tokens q0 .. of a slot's chunk, whose last row
@@ -1159,7 +1160,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     int64_t tokens = 0, blocks = 0, tiles = 0, n_pieces = 0;
     for (int b = 0; b < batch; ++b) {
         const int64_t n = counts[b], s = starts ? starts[b] : 0;
-        if (n < 0 || s < 0 || s + n > kMaxInt)
+        if (n < 0 || s < 0 || s + n > kMaxTokens)
             return fail(KVQ_ERR_INVALID_ARG, "slot %d: %lld tokens from %lld", b, static_cast<long long>(n),
                         static_cast<long long>(s));
         if (n == 0) continue;
