@@ -87,11 +87,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
 
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
-    enum { kQFull = 0, kKFull = 2, kKEmpty = 4, kVFull = 6, kVEmpty = 8, kSFull = 10, kPFull = 12, kOFull = 14,
-           kVFixed = 16, kDrain = 17, kBars = 18 };
+    // kPFull: [half of the tile's tokens][stream]
+    enum { kQFull = 0, kKFull = 2, kKEmpty = 4, kVFull = 6, kVEmpty = 8, kSFull = 10, kPFull = 12, kOFull = 16,
+           kVFixed = 18, kDrain = 19, kBars = 20 };
     if (threadIdx.x == 0) {
         gave_up = 0;
-        for (int i = 0; i < kBars; ++i) tc::bar_init(bar(i), i == kPFull || i == kPFull + 1 ? 4 : 1);
+        for (int i = 0; i < kBars; ++i) tc::bar_init(bar(i), i >= kPFull && i < kPFull + 4 ? 4 : 1);
         tc::fence_barrier_init();
     }
     if (warp == 8) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
@@ -193,14 +194,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                     if (go && j == n_max - 1 && count - j * kRows < kRows) go = tc::bar_wait(bar(kVFixed), 0, &gave_up);
                     for (int t = 0; t < 2 && go; ++t) {
                         if (j >= n_tiles[t]) continue;
-                        go = tc::bar_wait(bar(kPFull + t), j & 1, &gave_up);
-                        if (!go) break;
-                        tc::fence_after_sync();
                         const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
 #pragma unroll
-                        for (int i = 0; i < kRows / 16; ++i)
-                            tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
-                                       j > 0 || i > 0);
+                        for (int half = 0; half < 2; ++half) {     // the first weights while the others are taken
+                            go = go && tc::bar_wait(bar(kPFull + 2 * half + t), j & 1, &gave_up);
+                            if (!go) break;
+                            tc::fence_after_sync();
+#pragma unroll
+                            for (int i = 4 * half; i < 4 * half + 4; ++i)
+                                tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
+                                           j > 0 || i > 0);
+                        }
+                        if (!go) break;
                         if (j + 1 < n_tiles[t]) {
                             go = tc::bar_wait(bar(kKFull + s1), ((j + 1) / kStages) & 1, &gave_up);
                             if (go) issue_s(t, s1);
@@ -284,11 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                     p[i] = narrow2<BF16>(w.x, w.y);
                 }
                 tc::tmem_store(ts + 32 * half, p);
+                tc::tmem_stored();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(bar(kPFull + 2 * half + t));
             }
-            tc::tmem_stored();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(bar(kPFull + t));
             l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         }
         if (go && n_tiles[t]) go = tc::bar_wait_warp(bar(kOFull + t), 0, &gave_up);
