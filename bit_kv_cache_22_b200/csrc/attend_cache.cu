@@ -14,15 +14,21 @@
 //
 //   warps 0-3, 4-7   softmax of stream 0, 1: thread = row
 //   warps 8-15       operands: warp w the tokens 16w .. 16w+15 of each key tile
-//   warp 16          issues the MMAs
+//   warp 16          issues the MMAs (warps 17-19 fill the warpgroup, which gives its registers to the
+//                    softmax: 2 x 128 x 120 + 2 x 128 x 88 + 128 x 64 <= 640 x 96)
 //
-// Operands in fp16 for caches of either type: (code - z) s is computed in fp32 and rounded once to
-// 11 bits (bf16 would leave 8, a rounding as large as the output's own).  What fp16 lacks is range,
-// so operands carry powers of two of their own: a query row that of its largest channel, a key
-// tile that of a bound on its elements, 2^14 <= largest < 2^15, undone in the logits' scale; value
-// tiles the largest such exponent so far in the CTA's pass, undone at the end (the sums in tensor
-// memory are rescaled when it grows).  An element far below its tile's largest loses bits under
-// 2^-40 of that largest.
+// Operands in fp16 for caches of either type: (code - z) s is rounded to 11 bits (bf16 would leave 8,
+// a rounding as large as the output's own).  What fp16 lacks is range, so operands carry powers of
+// two of their own: a query row that of its largest channel, 16 tokens' keys that of a bound on
+// their elements, so that the largest lies in [2^14, 2^15), undone in the logits' scale; 16 tokens'
+// values a power that only grows along the pass, in steps of 2^4, undone at the end (weights that
+// meet smaller powers than the largest so far are scaled down, and the sums in tensor memory when
+// the largest grows).  An element far below the largest loses bits under 2^-36 of it.
+//
+// Unpacking is bound by the integer pipe, so codes stay in 16-bit pairs: bytes 0 and 2 (1 and 3) of a
+// word's slot, OR 0x6400, are the fp16 numbers 1024 + code; minus (1024 + z), exact for |z| <= 1024,
+// times s in two fp16 parts.  Within each four channels of keys (and queries) and each four
+// tokens the order in the operands is 0, 2, 1, 3, as the pairs come.
 #include <algorithm>
 #include <cstdint>
 
@@ -33,15 +39,18 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 544;
+constexpr int kThreads = 640;
 constexpr int kRows = 128;                 // rows of a query tile, tokens of a key tile
 constexpr int kStages = 2;                 // key and value operand tiles, each
 constexpr int kUnpackWarps = 8;
 constexpr int kExps = 8;                   // key tiles whose exponents are kept (at most kStages + 1 are live)
+constexpr int kValueStep = 4;              // values' exponents are multiples of this: they rarely differ
 constexpr float kLazyMax = 8.0f;           // the running maximum is raised when a logit passes it by this
 constexpr float kNoMax = -1e30f;           // the maximum of no logits: finite, so differences stay numbers
 constexpr int kMaxTokens = 0x7fffffff - 1024;   // of a sequence (the planner refuses more)
-constexpr int kMinExp = -112;              // exponents of operand scales: 2^e and 2^-e stay normal
+// Least exponents of operands: values' 2^e and 2^-e stay normal; those of queries and keys keep
+// their product, the logits' scale, above 0 (what they cost a logit is below 2^-60 of the other).
+constexpr int kMinExp = -112, kMinLogitExp = -56;
 
 template <int D>
 struct CacheSmem {
@@ -50,8 +59,8 @@ struct CacheSmem {
     static constexpr int k = q + 2 * kTileBytes;
     static constexpr int v = k + kStages * kTileBytes;
     static constexpr int meta = v + kStages * kTileBytes;         // per unpacking warp: s, z of keys and values
-    static constexpr int kMetaFloats = 2 * D + 2 * 128;
-    static constexpr int row_scale = meta + kUnpackWarps * kMetaFloats * 4;   // [2][128]
+    static constexpr int kMetaBytes = (2 * D + 2 * 128) * 4;
+    static constexpr int row_scale = meta + kUnpackWarps * kMetaBytes;        // [2][128]
     static constexpr int bars = row_scale + 2 * kRows * 4;
     // one CTA an SM: it holds all of the tensor memory
     static constexpr int bytes = (bars + 256 > 120 * 1024 ? bars + 256 : 120 * 1024) + 1024;
@@ -59,9 +68,9 @@ struct CacheSmem {
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// the exponent e with bound 2^-e in [2^14, 2^15), as far as kMinExp allows
-__device__ __forceinline__ int operand_exp(uint32_t bound_bits) {
-    return max(static_cast<int>(bound_bits >> 23) - 127 - 14, kMinExp);
+// the exponent e with bound 2^-e in [2^14, 2^15), as far as `least` allows
+__device__ __forceinline__ int operand_exp(uint32_t bound_bits, int least) {
+    return max(static_cast<int>(bound_bits >> 23) - 127 - 14, least);
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -75,18 +84,101 @@ __device__ __forceinline__ float byte_plus_2_23(uint32_t w) {
     return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + E));
 }
 
-// What one unpacking warp needs of a tile's 16 tokens: the code words of its lanes, and the scales
-// and zeros it spreads over shared memory.
+// place of element i of four in an operand: 0, 2, 1, 3
+__host__ __device__ constexpr int mixed(int i) { return (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1); }
+
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
+__device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+
+// The parameters of four elements, in pairs (0, 2) and (1, 3): -(1024 + z), and s in two parts.
+struct Quad {
+    uint2 z, hi, lo;
+};
+
+// Four codes of N bits in the bytes of b (above them anything): (code - z) s.
+template <int N>
+__device__ __forceinline__ uint2 unpack_four(uint32_t b, const Quad &q) {
+    constexpr uint32_t kMask = 0x00010001u * ((1u << N) - 1);
+    const __half2 x = __hadd2(as_half2((b & kMask) | 0x64006400u), as_half2(q.z.x));
+    const __half2 y = __hadd2(as_half2(((b >> 8) & kMask) | 0x64006400u), as_half2(q.z.y));
+    return make_uint2(as_bits(__hfma2(x, as_half2(q.hi.x), __hmul2(x, as_half2(q.lo.x)))),
+                      as_bits(__hfma2(y, as_half2(q.hi.y), __hmul2(y, as_half2(q.lo.y)))));
+}
+// The same in fp32, for zeros that 1024 + z does not hold.
+__device__ __forceinline__ uint2 unpack_four_wide(uint32_t b, const float4 &s, const float4 &z) {
+    const float2 x = tc::mul2(tc::add2(make_float2(byte_plus_2_23<0>(b), byte_plus_2_23<2>(b)), make_float2(z.x, z.z)),
+                              make_float2(s.x, s.z));
+    const float2 y = tc::mul2(tc::add2(make_float2(byte_plus_2_23<1>(b), byte_plus_2_23<3>(b)), make_float2(z.y, z.w)),
+                              make_float2(s.y, s.w));
+    return make_uint2(half2_bits(x.x, x.y), half2_bits(y.x, y.y));
+}
+
+// What one unpacking warp needs of a tile's 16 tokens: the code words of its lanes, and four
+// scales and zeros a lane, which it spreads over shared memory.
 template <int D, int N>
 struct Fetched {
     static constexpr int W = D * N / 64;   // words per lane
     uint32_t kw[W], vw[W];
-    float4 ks;                             // keys: channels 4 lane .. 4 lane + 3 (lanes below D / 4)
-    uint2 kz;
-    float vs[4];                           // values: entries lane + 32 i of [16 tokens][D / Gv]
-    int vz[4];
+    float4 ks, vs;                         // keys: channels 4 lane ...; values: entries 4 lane ... of
+    uint2 kz, vz;                          // [16 tokens][D / Gv], as far as there are any
     int kind;                              // 0: no tokens, 1: quantized, 2: residual
 };
+
+__device__ __forceinline__ void widen_zeros(uint2 z, bool sym, int half_levels, float (&f)[4]) {
+    f[0] = static_cast<float>(sym ? half_levels : static_cast<int>(static_cast<int16_t>(z.x & 0xffffu)));
+    f[1] = static_cast<float>(sym ? half_levels : static_cast<int>(z.x) >> 16);
+    f[2] = static_cast<float>(sym ? half_levels : static_cast<int>(static_cast<int16_t>(z.y & 0xffffu)));
+    f[3] = static_cast<float>(sym ? half_levels : static_cast<int>(z.y) >> 16);
+}
+
+// A CTA's work: up to 2 * tpt tokens of one slot's chunk from q0 on, for kv head h, over split
+// `split` of n_splits of the key tiles their last token sees: tiles tile0 .. tile0 + n - 1.
+struct CacheItem {
+    int slot, h, q0, count, first, start;          // the slot's chunk: tokens, first row, first position
+    int hg, tpt;                                   // query heads of the kv head, tokens of a query tile
+    int len, tq;                                   // tokens of the slot, quantized ones
+    int tile0, n;
+    int end0;                                      // tiles below it concern stream 0 (stream 1: n)
+    int split, n_splits, part;                     // first partial tile
+    bool alternate;                                // one query tile, alternate key tiles
+    bool good;
+};
+
+__device__ __forceinline__ CacheItem cache_item(const AttendArgs &a) {
+    CacheItem w{};
+    const int4 item = a.t.items[blockIdx.x / a.Hkv];
+    w.h = blockIdx.x % a.Hkv;
+    w.hg = a.Hq / a.Hkv;
+    w.tpt = kRows / w.hg;
+    w.slot = item.x;
+    w.q0 = item.y;
+    w.split = item.z & 0xffff;
+    w.n_splits = item.z >> 16;
+    w.part = item.w;
+    w.good = w.slot >= 0 && w.slot < a.t.B && w.q0 >= 0 && w.split < w.n_splits && w.part >= 0;
+    if (!w.good) return w;
+    w.first = a.t.offsets[w.slot];
+    w.count = a.t.offsets[w.slot + 1] - w.first;
+    w.start = a.t.starts[w.slot];
+    w.alternate = w.count - w.q0 <= w.tpt;
+    w.good = w.first >= 0 && w.count > w.q0 && w.start >= 0 && w.start <= kMaxTokens - w.count &&
+             static_cast<int64_t>(w.first) + w.count <= a.t.tokens &&
+             (w.n_splits == 1 ||
+              w.part + static_cast<int64_t>(w.n_splits) * (w.alternate ? 1 : 2) <= a.part_tiles);
+    if (!w.good) return w;
+    // (positions stay below 2^31 - 1024, so a tile's tokens are 32-bit numbers)
+    w.len = min(max(a.cache.seq_len[w.slot], 0), kMaxTokens);
+    w.tq = w.len / a.cache.R * a.cache.R;
+    const int last = min(w.q0 + 2 * w.tpt, w.count);
+    const int all = (min(w.start + last, w.len) + kRows - 1) / kRows;
+    const int share = all / w.n_splits, extra = all % w.n_splits;      // the first splits take a tile more
+    w.tile0 = share * w.split + min(w.split, extra);
+    w.n = share + (w.split < extra);
+    w.end0 = w.n;
+    if (!w.alternate)
+        w.end0 = max(0, min(w.n, (min(w.start + w.q0 + w.tpt, w.len) + kRows - 1) / kRows - w.tile0));
+    return w;
+}
 
 template <int D, int N, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendArgs a) {
@@ -96,60 +188,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
     unsigned char *smem = raw + (base - tc::smem_addr(raw));
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
-    __shared__ int exp_k[kExps], exp_v[kExps];
-    __shared__ uint32_t bounds[2][2][kUnpackWarps];   // [tile parity][keys, values][warp]
+    __shared__ CacheItem work;                     // in shared memory: each role keeps what it needs of it
+    __shared__ __align__(16) float scale_k[kExps][kUnpackWarps];   // 2^e of each 16 tokens' keys
+    __shared__ __align__(16) int exp_v[kExps][kUnpackWarps];       // e of each 16 tokens' values
     const PagedView &c = a.cache;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
-    // the work item: up to 2 * tpt tokens of one slot's chunk from q0 on, split s of n over their keys
-    const int h = blockIdx.x % a.Hkv;
-    const int4 item = a.t.items[blockIdx.x / a.Hkv];
-    const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
-    const int slot = item.x, q0 = item.y, split = item.z & 0xffff, n_splits = item.z >> 16;
-    int first = 0, count = 0, start = 0;
-    bool good = slot >= 0 && slot < a.t.B && q0 >= 0 && split < n_splits && item.w >= 0;
-    if (good) {
-        first = a.t.offsets[slot];
-        count = a.t.offsets[slot + 1] - first;
-        start = a.t.starts[slot];
-        good = first >= 0 && count > q0 && start >= 0 && start <= kMaxTokens - count && static_cast<int64_t>(first) + count <= a.t.tokens;
-        if (n_splits > 1 &&
-            item.w + static_cast<int64_t>(n_splits) * (count - q0 <= tpt ? 1 : 2) > a.part_tiles)
-            good = false;
-    }
-    if (!good) {                                   // not this library's table
-        if (threadIdx.x == 0) atomicOr(a.status, 8u);
-        return;
-    }
-    // (positions stay below 2^31 - 1024, so a tile's tokens are 32-bit numbers)
-    const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
-    const int n_tok = min(2 * tpt, count - q0);
-    const bool alternate = n_tok <= tpt;           // one query tile, alternate key tiles
-    // key tiles: those the item's last row sees, this split's share [tile0, tile0 + n)
-    const int all = (min(start + q0 + n_tok, len) + kRows - 1) / kRows;
-    const int share = all / n_splits, extra = all % n_splits;      // the first splits take a tile more
-    const int tile0 = share * split + min(split, extra), n = share + (split < extra);
-    // stream t takes tiles first_of(t), + stride, ... below end_of(t)
-    const int stride = alternate ? 2 : 1;
-    int ends[2];
-    ends[1] = n;
-    if (alternate) {
-        ends[0] = n;
-    } else {
-        ends[0] = max(0, min(n, (min(start + q0 + tpt, len) + kRows - 1) / kRows - tile0));
-    }
-
+    if (threadIdx.x == 0) work = cache_item(a);
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
     enum { kQFull = 0, kKFull = 1, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages, kVEmpty = kKEmpty + kStages,
-           kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kOFull = kPFull + 2, kDrain = kOFull + 2, kBars };
+           kSFull = kVEmpty + kStages, kPFull = kSFull + 2 /* [half of the tile's tokens][stream] */,
+           kOFull = kPFull + 4, kDrain = kOFull + 2, kBars };
     if (threadIdx.x == 0) {
         gave_up = 0;
         for (int i = 0; i < kBars; ++i) {
             const bool unpacked = i < kKEmpty;     // kQFull, kKFull, kVFull
-            tc::bar_init(bar(i), unpacked ? kUnpackWarps : i == kPFull || i == kPFull + 1 ? 4 : 1);
+            tc::bar_init(bar(i), unpacked ? kUnpackWarps : i >= kPFull && i < kPFull + 4 ? 4 : 1);
         }
         tc::fence_barrier_init();
+    }
+    __syncthreads();
+    if (!work.good) {                              // not this library's table
+        if (threadIdx.x == 0) atomicOr(a.status, 8u);
+        return;
     }
     if (warp == 16) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
     tc::fence_before_sync();
@@ -159,54 +221,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
     float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
 
     if (warp >= 8 && warp < 16) {
+        tc::regs_give<88>();
+        const int tile0 = work.tile0, n = work.n, len = work.len, tq = work.tq;
         // ------------------------------ operands ---------------------------
         const int w = warp - 8;
-        // queries: a warp turns a row at a time, four (d = 128) or two channels a lane
-        for (int r = w; r < (alternate ? kRows : 2 * kRows); r += kUnpackWarps) {
-            const int t = r / kRows, rr = r % kRows, tok = q0 + t * tpt + rr / hg;
-            constexpr int E = D / 32;
-            float x[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = 0.0f;
-            if (rr < hg * tpt && tok < count) {
-                const uint16_t *src = a.q.p + static_cast<int64_t>(first + tok) * a.q.ts +
-                                      static_cast<int64_t>(h * hg + rr % hg) * a.q.hs + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 p = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(src)[e / 2]);
-                    x[e] = p.x;
-                    x[e + 1] = p.y;
-                }
-            }
-            float big = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(x[e]));
-            const int ex = operand_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-            const float down = pow2(-ex);
-            if (lane == 0) row_scale[r] = pow2(ex) * a.scale;
-            const int col = lane * E;              // channel: 128-byte rows of 64 channels, swizzled
-            unsigned char *dst = smem + L::q + t * L::kTileBytes + (col / 64) * (kRows * 128) + rr * 128 +
-                                 ((((col % 64) / 8) ^ (rr & 7)) << 4) + (col % 8) * 2;
-#pragma unroll
-            for (int e = 0; e < E; e += 2)
-                reinterpret_cast<uint32_t *>(dst)[e / 2] = half2_bits(x[e] * down, x[e + 1] * down);
-        }
-        tc::fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(bar(kQFull));
-
-        float *meta = reinterpret_cast<float *>(smem + L::meta) + w * L::kMetaFloats;
-        float *ks_s = meta, *kz_s = meta + D, *vs_s = meta + 2 * D, *vz_s = vs_s + 128;
+        unsigned char *meta = smem + L::meta + w * L::kMetaBytes;
         const int gv_shift = __ffs(c.Gv) - 1, g_shift = __ffs(c.G) - 1;      // powers of two
         const int ngv = D >> gv_shift, ngv_shift = __ffs(ngv) - 1;
         constexpr int B = 4 / N, W = D * N / 64, TW = D * N / 2;
-        constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
         constexpr float kTop = static_cast<float>((1 << N) - 1);
 
-        const int32_t *pages = c.page_table + static_cast<int64_t>(slot) * c.max_pages;
         // this warp's place in the pages: of the tile to fetch (page index and token in it), whose page
         // number is loaded a tile ahead
-        int at_page = ((tile0 * kRows) + 16 * w) / c.P, at_tok = ((tile0 * kRows) + 16 * w) % c.P;
+        const int32_t *pages = c.page_table + static_cast<int64_t>(work.slot) * c.max_pages;
+        int at_page = (tile0 * kRows + 16 * w) / c.P, at_tok = (tile0 * kRows + 16 * w) % c.P;
         auto page_at = [&](int j, int pi) -> int {
             return j < n && (tile0 + j) * kRows + 16 * w < tq && pi < c.max_pages ? pages[pi] : -1;
         };
@@ -226,65 +254,103 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 if (lane == 0) atomicOr(a.status, 2u);
                 page = 0;
             }
-            const int64_t slice = static_cast<int64_t>(page) * a.Hkv + h;
-            const int pt = at_tok;
-            const int64_t words = (slice * (c.P >> 4) + (pt >> 4)) * TW + lane * W;
+            const int64_t slice = static_cast<int64_t>(page) * a.Hkv + work.h;
+            const int64_t words = (slice * (c.P >> 4) + (at_tok >> 4)) * TW + lane * W;
+            if constexpr (W >= 4) {
 #pragma unroll
-            for (int i = 0; i < W; i += W >= 4 ? 4 : 2) {
-                if constexpr (W >= 4) {
+                for (int i = 0; i < W; i += 4) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(c.kc + words + i);
                     const uint4 y = *reinterpret_cast<const uint4 *>(c.vc + words + i);
                     f.kw[i] = x.x; f.kw[i + 1] = x.y; f.kw[i + 2] = x.z; f.kw[i + 3] = x.w;
                     f.vw[i] = y.x; f.vw[i + 1] = y.y; f.vw[i + 2] = y.z; f.vw[i + 3] = y.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(c.kc + words);
-                    const uint2 y = *reinterpret_cast<const uint2 *>(c.vc + words);
-                    f.kw[0] = x.x; f.kw[1] = x.y;
-                    f.vw[0] = y.x; f.vw[1] = y.y;
                 }
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(c.kc + words);
+                const uint2 y = *reinterpret_cast<const uint2 *>(c.vc + words);
+                f.kw[0] = x.x; f.kw[1] = x.y;
+                f.vw[0] = y.x; f.vw[1] = y.y;
             }
-            const int64_t km = (slice * (c.P >> g_shift) + (pt >> g_shift)) * D + 4 * lane;
             if (4 * lane < D) {
+                const int64_t km = (slice * (c.P >> g_shift) + (at_tok >> g_shift)) * D + 4 * lane;
                 f.ks = *reinterpret_cast<const float4 *>(c.ks + km);
                 if (!c.sym) f.kz = *reinterpret_cast<const uint2 *>(c.kz + km);
             }
-            const int64_t vm = (slice * c.P + pt) << ngv_shift;
+            if (4 * lane < 16 << ngv_shift) {
+                const int64_t vm = ((slice * c.P + at_tok) << ngv_shift) + 4 * lane;
+                f.vs = *reinterpret_cast<const float4 *>(c.vs + vm);
+                if (!c.sym) f.vz = *reinterpret_cast<const uint2 *>(c.vz + vm);
+            }
+        };
+        fetch(0, page_at(0, at_page));
+        advance();
+        int page = page_at(1, at_page);
+
+        // queries: four channels a lane, kBatch rows of loads in flight
+        {
+            constexpr int kLanes = D / 4, kPer = 32 / kLanes, kBatch = 4;   // lanes a row, rows at a time
+            const int hg = work.hg, tpt = work.tpt, q0 = work.q0, count = work.count, first = work.first;
+            const int rows = work.alternate ? kRows : 2 * kRows, col = (lane % kLanes) * 4;
+#pragma unroll 1
+            for (int r0 = w * kPer + lane / kLanes; r0 < rows; r0 += kBatch * kUnpackWarps * kPer) {
+                uint2 x[kBatch];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (lane + 32 * i < 16 * ngv) {
-                    f.vs[i] = c.vs[vm + lane + 32 * i];
-                    f.vz[i] = c.sym ? 1 << (N - 1) : c.vz[vm + lane + 32 * i];
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = r0 + k * kUnpackWarps * kPer, rr = r % kRows, tok = q0 + r / kRows * tpt + rr / hg;
+                    x[k] = make_uint2(0u, 0u);
+                    if (rr < hg * tpt && tok < count)
+                        x[k] = *reinterpret_cast<const uint2 *>(a.q.p + static_cast<int64_t>(first + tok) * a.q.ts +
+                                                                static_cast<int64_t>(work.h * hg + rr % hg) * a.q.hs + col);
                 }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = r0 + k * kUnpackWarps * kPer, rr = r % kRows;
+                    const float2 p = widen_pair<BF16>(x[k].x), q = widen_pair<BF16>(x[k].y);
+                    float big = fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(q.x), fabsf(q.y)));
+#pragma unroll
+                    for (int off = kLanes / 2; off > 0; off >>= 1)
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                    const int ex = operand_exp(__float_as_uint(big), kMinLogitExp);
+                    const float down = pow2(-ex);
+                    if (col == 0) row_scale[r] = pow2(ex) * a.scale;
+                    tc::store_shared(base + L::q + r / kRows * L::kTileBytes + (col / 64) * (kRows * 128) + rr * 128 +
+                                         ((((col % 64) / 8) ^ (rr & 7)) << 4) + (col % 8) * 2,
+                                     half2_bits(p.x * down, q.x * down), half2_bits(p.y * down, q.y * down));
+                }
+            }
+            tc::fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(bar(kQFull));
+        }
+
+        // the slot's residual rows: token tq's first
+        auto residual = [&](const uint16_t *rows) {
+            return rows + (static_cast<int64_t>(work.slot) * a.Hkv + work.h) * c.R * D;
         };
-        const uint16_t *res_k = c.kr + (static_cast<int64_t>(slot) * a.Hkv + h) * c.R * D;
-        const uint16_t *res_v = c.vr + (static_cast<int64_t>(slot) * a.Hkv + h) * c.R * D;
-        auto z4 = [&](int (&z)[4]) {
-            z[0] = static_cast<int16_t>(f.kz.x & 0xffffu); z[1] = static_cast<int>(f.kz.x) >> 16;
-            z[2] = static_cast<int16_t>(f.kz.y & 0xffffu); z[3] = static_cast<int>(f.kz.y) >> 16;
-            if (c.sym) z[0] = z[1] = z[2] = z[3] = 1 << (N - 1);
-        };
-        // bounds on the magnitude of this warp's tokens of tile j, left for all unpacking warps
-        auto bound = [&](int j) {
+        int ev = kMinExp;
+        bool go = true;
+        // lane's row in an operand tile (+ 8 in a second store): a key's is its token, in mixed order, a
+        // value's its channel
+        const int row_k = mixed(lane >> 2), row_v = lane >> 2;
+
+        for (int j = 0; j < n && go; ++j) {
+            const int s = j % kStages, phase = (j / kStages) & 1, kind = f.kind;
+            const int tok = (tile0 + j) * kRows + 16 * w;
+            // bounds on the 16 tokens' magnitudes, and from them the powers of two
             float bk = 0.0f, bv = 0.0f;
-            if (f.kind == 1) {
-                if (4 * lane < D) {
-                    int z[4];
-                    z4(z);
-                    const float s[4] = {f.ks.x, f.ks.y, f.ks.z, f.ks.w};
+            float zk[4], zv[4];
+            const bool has_k = kind == 1 && 4 * lane < D, has_v = kind == 1 && 4 * lane < 16 << ngv_shift;
+            if (kind == 1) {
+                widen_zeros(f.kz, c.sym, 1 << (N - 1), zk);
+                widen_zeros(f.vz, c.sym, 1 << (N - 1), zv);
+                const float sk[4] = {f.ks.x, f.ks.y, f.ks.z, f.ks.w}, sv[4] = {f.vs.x, f.vs.y, f.vs.z, f.vs.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float zf = static_cast<float>(z[e]);
-                        bk = fmaxf(bk, s[e] * fmaxf(fabsf(zf), fabsf(kTop - zf)));
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    if (has_k) bk = fmaxf(bk, sk[e] * fmaxf(fabsf(zk[e]), fabsf(kTop - zk[e])));
+                    if (has_v) bv = fmaxf(bv, sv[e] * fmaxf(fabsf(zv[e]), fabsf(kTop - zv[e])));
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (lane + 32 * i < 16 * ngv) {
-                        const float zf = static_cast<float>(f.vz[i]);
-                        bv = fmaxf(bv, f.vs[i] * fmaxf(fabsf(zf), fabsf(kTop - zf)));
-                    }
-            } else if (f.kind == 2) {
-                const int tok = (tile0 + j) * kRows + 16 * w;
+            } else if (kind == 2) {
+                const uint16_t *res_k = residual(c.kr), *res_v = residual(c.vr);
+#pragma unroll 1
                 for (int i = lane; i < 16 * D / 2; i += 32) {
                     const int tk = tok + i / (D / 2);
                     if (tk < len) {
@@ -296,57 +362,63 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     }
                 }
             }
-            const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(bk));
-            const uint32_t mv = __reduce_max_sync(0xffffffffu, __float_as_uint(bv));
-            if (lane == 0) {
-                bounds[j & 1][0][w] = mk;
-                bounds[j & 1][1][w] = mv;
-            }
-        };
-        int ev = kMinExp;
-        bool go = true;
-        // lane's place in an operand tile: row l / 4 (+ 8), 8 bytes l % 4 of a 32-byte step, swizzled
-        const uint32_t place = (lane >> 2) * 128 + ((((lane & 3) >> 1) ^ (lane >> 2)) << 4) + (lane & 1) * 8;
-
-        fetch(0, page_at(0, at_page));
-        advance();
-        int page = page_at(1, at_page);
-        bound(0);
-        for (int j = 0; j < n; ++j) {
-            asm volatile("bar.sync 1, %0;" ::"r"(32 * kUnpackWarps) : "memory");
-            uint32_t mk = 0, mv = 0;
-#pragma unroll
-            for (int i = 0; i < kUnpackWarps; ++i) {
-                mk = max(mk, bounds[j & 1][0][i]);
-                mv = max(mv, bounds[j & 1][1][i]);
-            }
-            const int ek = operand_exp(mk);
-            ev = max(ev, operand_exp(mv));
+            const int ek = operand_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(bk)), kMinLogitExp);
+            ev = max(ev, (operand_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(bv)), kMinExp) + kValueStep - 1) &
+                             ~(kValueStep - 1));
             const float down_k = pow2(-ek), down_v = pow2(-ev);
-            if (w == 0 && lane == 0) {
-                exp_k[j % kExps] = ek;
-                exp_v[j % kExps] = ev;
-            }
-            const int kind = f.kind;
+            // the parameters, spread over shared memory for the lanes that use them
+            bool wide = false;
             uint32_t kw[W], vw[W];
             if (kind == 1) {
-                __syncwarp();                      // the tile before is unpacked
-                if (4 * lane < D) {
-                    int z[4];
-                    z4(z);
-                    reinterpret_cast<float4 *>(ks_s)[lane] =
-                        make_float4(f.ks.x * down_k, f.ks.y * down_k, f.ks.z * down_k, f.ks.w * down_k);
-                    reinterpret_cast<float4 *>(kz_s)[lane] =
-                        make_float4(-8388608.0f - static_cast<float>(z[0]), -8388608.0f - static_cast<float>(z[1]),
-                                    -8388608.0f - static_cast<float>(z[2]), -8388608.0f - static_cast<float>(z[3]));
-                }
+                bool over = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (lane + 32 * i < 16 * ngv) {
-                        const int tk = (lane + 32 * i) >> ngv_shift, g = (lane + 32 * i) & (ngv - 1);
-                        vs_s[g * 16 + tk] = f.vs[i] * down_v;
-                        vz_s[g * 16 + tk] = -8388608.0f - static_cast<float>(f.vz[i]);
+                for (int e = 0; e < 4; ++e)
+                    over = over || (has_k && fabsf(zk[e]) > 1024.0f) || (has_v && fabsf(zv[e]) > 1024.0f);
+                wide = __any_sync(0xffffffffu, over);          // (and the tile before is unpacked)
+                const float sk[4] = {f.ks.x * down_k, f.ks.y * down_k, f.ks.z * down_k, f.ks.w * down_k};
+                const float sv[4] = {f.vs.x * down_v, f.vs.y * down_v, f.vs.z * down_v, f.vs.w * down_v};
+                if (!wide) {
+                    // keys: [z, hi, lo][D / 4] pairs of pairs; values: [z, hi, lo][D / Gv][16] in mixed order
+                    uint2 *km = reinterpret_cast<uint2 *>(meta);
+                    uint16_t *vm = reinterpret_cast<uint16_t *>(meta + 3 * D * 2);
+                    if (has_k) {
+                        float hi[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) hi[e] = __half2float(__float2half_rn(sk[e]));
+                        km[lane] = make_uint2(half2_bits(-1024.0f - zk[0], -1024.0f - zk[2]),
+                                              half2_bits(-1024.0f - zk[1], -1024.0f - zk[3]));
+                        km[D / 4 + lane] = make_uint2(half2_bits(hi[0], hi[2]), half2_bits(hi[1], hi[3]));
+                        km[D / 2 + lane] = make_uint2(half2_bits(sk[0] - hi[0], sk[2] - hi[2]),
+                                                      half2_bits(sk[1] - hi[1], sk[3] - hi[3]));
                     }
+                    if (has_v) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = 4 * lane + e;
+                            const int at = (i & (ngv - 1)) * 16 + mixed(i >> ngv_shift);
+                            const __half hi = __float2half_rn(sv[e]);
+                            vm[at] = __half_as_ushort(__float2half_rn(-1024.0f - zv[e]));
+                            vm[128 + at] = __half_as_ushort(hi);
+                            vm[256 + at] = __half_as_ushort(__float2half_rn(sv[e] - __half2float(hi)));
+                        }
+                    }
+                } else {
+                    // fp32 [s, z] of keys [D] and values [D / Gv][16]
+                    float *km = reinterpret_cast<float *>(meta), *vm = km + 2 * D;
+                    if (has_k) {
+                        reinterpret_cast<float4 *>(km)[lane] = make_float4(sk[0], sk[1], sk[2], sk[3]);
+                        reinterpret_cast<float4 *>(km + D)[lane] =
+                            make_float4(-8388608.0f - zk[0], -8388608.0f - zk[1], -8388608.0f - zk[2], -8388608.0f - zk[3]);
+                    }
+                    if (has_v) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = 4 * lane + e, at = (i & (ngv - 1)) * 16 + (i >> ngv_shift);
+                            vm[at] = sv[e];
+                            vm[128 + at] = -8388608.0f - zv[e];
+                        }
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     kw[i] = f.kw[i];
@@ -358,94 +430,109 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
             advance();
             page = page_at(j + 2, at_page);
 
-            const int s = j % kStages, phase = (j / kStages) & 1;
-            const int tok = (tile0 + j) * kRows + 16 * w;
-            // four codes at a time: bytes to fp32, minus z, times s, rounded to fp16
-            auto four = [&](uint32_t b, const float4 &sc, const float4 &zr, uint32_t dst) {
-                const float2 x = tc::mul2(tc::add2(make_float2(byte_plus_2_23<0>(b), byte_plus_2_23<1>(b)),
-                                                   make_float2(zr.x, zr.y)), make_float2(sc.x, sc.y));
-                const float2 y = tc::mul2(tc::add2(make_float2(byte_plus_2_23<2>(b), byte_plus_2_23<3>(b)),
-                                                   make_float2(zr.z, zr.w)), make_float2(sc.z, sc.w));
-                tc::store_shared(dst, half2_bits(x.x, x.y), half2_bits(y.x, y.y));
-            };
-            // ---- keys: rows = tokens, channels along a row
-            // (a warp whose wait gave up keeps step with the others, which meet at the barrier above)
-            if (j >= kStages) go = go && tc::bar_wait_warp(bar(kKEmpty + s), phase ^ 1, &gave_up);
-            const uint32_t kt = base + L::k + s * L::kTileBytes + 16 * w * 128;
-            if (!go) {
-            } else if (kind == 1) {
-                const float4 *s4 = reinterpret_cast<const float4 *>(ks_s) + (lane & 3);
-                const float4 *r4 = reinterpret_cast<const float4 *>(kz_s) + (lane & 3);
-                float4 sc = s4[0], zr = r4[0];
+            // keys (rows = tokens, channels along a row), then values (rows = channels, tokens along a row),
+            // by the same code: the kernel's instructions have to stay in the SM's cache
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                if (j >= kStages) go = tc::bar_wait_warp(bar((kv ? kVEmpty : kKEmpty) + s), phase ^ 1, &gave_up);
+                if (!go) break;
+                if (kv == 1) {
 #pragma unroll
-                for (int ch = 0; ch < D / 16; ++ch) {      // the next chunk's scales before this one's stores
-                    float4 sc1 = sc, zr1 = zr;
-                    if (ch + 1 < D / 16) {
-                        sc1 = s4[4 * (ch + 1)];
-                        zr1 = r4[4 * (ch + 1)];
-                    }
-                    const uint32_t dst = kt + (ch / 4) * (kRows * 128) + (place ^ ((ch % 4) << 5));
-                    four((kw[ch / B] >> (N * 2 * (ch % B))) & kMask, sc, zr, dst);
-                    four((kw[ch / B] >> (N * 2 * (ch % B) + N)) & kMask, sc, zr, dst + 1024);
-                    sc = sc1;
-                    zr = zr1;
+                    for (int i = 0; i < W; ++i) kw[i] = vw[i];
                 }
-            } else {
-                for (int i = lane; i < 16 * (D / 8); i += 32) {
-                    const int r = i / (D / 8), v = i % (D / 8);
-                    uint32_t o[4] = {0u, 0u, 0u, 0u};
-                    if (kind == 2 && tok + r < len) {
-                        const uint4 x = reinterpret_cast<const uint4 *>(res_k + static_cast<int64_t>(tok + r - tq) * D)[v];
-                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                if (kv == 0 && lane == 0) {
+                    scale_k[j % kExps][w] = pow2(ek);
+                    exp_v[j % kExps][w] = ev;
+                }
+                const uint32_t tile = kv ? base + L::v + s * L::kTileBytes + (w / 4) * (D * 128)
+                                         : base + L::k + s * L::kTileBytes + 16 * w * 128;
+                if (kind == 1) {
+                    // two chunks of 16 channels at a time; their parameters are loaded before the stores
+                    // of the two before
+                    const int shift = kv ? gv_shift - 4 : 0;           // chunk -> group of parameters
+                    const uint32_t place = (kv ? row_v : row_k) * 128 + (lane & 1) * 8;
+                    const uint32_t col = (((lane & 3) >> 1) ^ ((kv ? row_v : row_k) & 7)) << 4;
+                    if (!wide) {
+                        const uint2 *pm = reinterpret_cast<const uint2 *>(meta + (kv ? 3 * D * 2 : 0)) + (lane & 3);
+                        const int next = kv ? 32 : D / 4;              // from z to hi to lo
+                        auto quad = [&](int ch) {
+                            const uint2 *at = pm + 4 * (ch >> shift);
+                            return Quad{at[0], at[next], at[2 * next]};
+                        };
+                        Quad q0 = quad(0), q1 = quad(1);
+#pragma unroll 1
+                        for (int ch = 0; ch < D / 16; ch += 2) {
+                            const int more = ch + 2 < D / 16 ? ch + 2 : 0;
+                            const Quad n0 = quad(more), n1 = quad(more + 1);
+                            const uint32_t b0 = kw[0];
+                            const uint32_t b1 = N == 2 ? b0 >> 4 : kw[2 / B - 1];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 p = widen_pair<BF16>(xw[e]);
-                            o[e] = half2_bits(p.x * down_k, p.y * down_k);
+                            for (int i = 0; i + 2 / B < W; ++i) kw[i] = kw[i + 2 / B];   // the words move up
+                            const uint32_t d0 = kv ? tile + ch * 2048 + place + (col ^ ((w % 4) << 5))
+                                                   : tile + (ch / 4) * (kRows * 128) + place + (col ^ ((ch % 4) << 5));
+                            const uint32_t d1 = kv ? d0 + 2048 : d0 ^ 32;
+                            const uint2 x0 = unpack_four<N>(b0, q0), y0 = unpack_four<N>(b0 >> N, q0);
+                            const uint2 x1 = unpack_four<N>(b1, q1), y1 = unpack_four<N>(b1 >> N, q1);
+                            tc::store_shared(d0, x0.x, x0.y);
+                            tc::store_shared(d0 + 1024, y0.x, y0.y);
+                            tc::store_shared(d1, x1.x, x1.y);
+                            tc::store_shared(d1 + 1024, y1.x, y1.y);
+                            q0 = n0;
+                            q1 = n1;
+                        }
+                    } else {
+                        constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
+                        const float4 *pm = reinterpret_cast<const float4 *>(meta) + (kv ? 2 * D / 4 : 0) + (lane & 3);
+                        const int next = kv ? 32 : D / 4;              // from s to z
+#pragma unroll 1
+                        for (int i = 0; i < D / 8; ++i) {              // chunk i / 2, row half i % 2
+                            const int ch = i / 2;
+                            const uint32_t b = (kw[0] >> (N * (i % (2 * B)))) & kMask;
+                            if (i % (2 * B) == 2 * B - 1)
+#pragma unroll
+                                for (int k = 0; k + 1 < W; ++k) kw[k] = kw[k + 1];
+                            const float4 *at = pm + 4 * (ch >> shift);
+                            const uint2 x = unpack_four_wide(b, at[0], at[next]);
+                            tc::store_shared((kv ? tile + ch * 2048 + place + (col ^ ((w % 4) << 5))
+                                                 : tile + (ch / 4) * (kRows * 128) + place + (col ^ ((ch % 4) << 5))) +
+                                                 1024 * (i % 2),
+                                             x.x, x.y);
                         }
                     }
-                    tc::store_shared(kt + (v / 8) * (kRows * 128) + r * 128 + (((v % 8) ^ (r & 7)) << 4), o);
-                }
-            }
-            tc::fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(bar(kKFull + s));
-            // ---- values: rows = channels, tokens along a row
-            if (j >= kStages) go = go && tc::bar_wait_warp(bar(kVEmpty + s), phase ^ 1, &gave_up);
-            const uint32_t vt = base + L::v + s * L::kTileBytes + (w / 4) * (D * 128);
-            if (!go) {
-            } else if (kind == 1) {
-                const float4 *s4 = reinterpret_cast<const float4 *>(vs_s) + (lane & 3);
-                const float4 *r4 = reinterpret_cast<const float4 *>(vz_s) + (lane & 3);
-                float4 sc = s4[0], zr = r4[0];
+                } else if (kv == 0) {
+                    const uint16_t *res = residual(c.kr);
+#pragma unroll 1
+                    for (int i = lane; i < 16 * (D / 8); i += 32) {
+                        const int r = i / (D / 8), v = i % (D / 8), rm = mixed(r);
+                        uint32_t o[4] = {0u, 0u, 0u, 0u};
+                        if (kind == 2 && tok + r < len) {
+                            const uint4 x = reinterpret_cast<const uint4 *>(res + static_cast<int64_t>(tok + r - tq) * D)[v];
+                            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int ch = 0; ch < D / 16; ++ch) {
-                    float4 sc1 = sc, zr1 = zr;
-                    if (ch + 1 < D / 16) {
-                        const int g = (16 * (ch + 1)) >> gv_shift;
-                        sc1 = s4[4 * g];
-                        zr1 = r4[4 * g];
+                            for (int e = 0; e < 4; e += 2) {
+                                const float2 p = widen_pair<BF16>(xw[e]), q = widen_pair<BF16>(xw[e + 1]);
+                                o[e] = half2_bits(p.x * down_k, q.x * down_k);
+                                o[e + 1] = half2_bits(p.y * down_k, q.y * down_k);
+                            }
+                        }
+                        tc::store_shared(tile + (v / 8) * (kRows * 128) + rm * 128 + (((v % 8) ^ (rm & 7)) << 4), o);
                     }
-                    const uint32_t dst = vt + 16 * ch * 128 + (place ^ ((w % 4) << 5));
-                    four((vw[ch / B] >> (N * 2 * (ch % B))) & kMask, sc, zr, dst);
-                    four((vw[ch / B] >> (N * 2 * (ch % B) + N)) & kMask, sc, zr, dst + 1024);
-                    sc = sc1;
-                    zr = zr1;
-                }
-            } else {
-                for (int cp = lane; cp < D / 2; cp += 32) {           // channels 2 cp, 2 cp + 1: 16 tokens each
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                } else {
+                    const uint16_t *res = residual(c.vr);
+#pragma unroll 1
+                    for (int i = lane; i < D; i += 32) {       // channels 2 cp, 2 cp + 1: 8 of the 16 tokens
+                        const int cp = i >> 1, part = i & 1;
                         uint32_t o[2][4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             float2 p[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int tk = tok + 8 * i + 2 * k + e;
+                                const int tk = tok + 8 * part + mixed(2 * k + e);
                                 p[e] = make_float2(0.0f, 0.0f);
                                 if (kind == 2 && tk < len)
-                                    p[e] = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(
-                                        res_v + static_cast<int64_t>(tk - tq) * D)[cp]);
+                                    p[e] = widen_pair<BF16>(
+                                        reinterpret_cast<const uint32_t *>(res + static_cast<int64_t>(tk - tq) * D)[cp]);
                             }
                             o[0][k] = half2_bits(p[0].x * down_v, p[1].x * down_v);
                             o[1][k] = half2_bits(p[0].y * down_v, p[1].y * down_v);
@@ -453,28 +540,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int r = 2 * cp + e;
-                            tc::store_shared(vt + r * 128 + (((2 * (w % 4) + i) ^ (r & 7)) << 4), o[e]);
+                            tc::store_shared(tile + r * 128 + (((2 * (w % 4) + part) ^ (r & 7)) << 4), o[e]);
                         }
                     }
                 }
+                tc::fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(bar((kv ? kVFull : kKFull) + s));
             }
-            tc::fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(bar(kVFull + s));
-            bound(j + 1);
         }
-    } else if (warp == 16) {
+    } else if (warp >= 16) {
+        tc::regs_give<64>();
+        const int n = work.n, ends[2] = {work.end0, n};
+        const bool alternate = work.alternate;
+        const int stride = alternate ? 2 : 1;      // of a stream's tiles
         // ------------------------------ MMAs -------------------------------
-        if (lane == 0 && n > 0) {
+        if (warp == 16 && lane == 0 && n > 0) {
             constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, false, false);
             constexpr uint32_t kDescO = tc::mma_desc(kRows, D, false, false);
             auto issue_s = [&](int t, int s) {
-                const uint64_t qd = tc::desc_k_major(base + L::q + (alternate ? 0 : t) * L::kTileBytes);
-                const uint64_t kd = tc::desc_k_major(base + L::k + s * L::kTileBytes);
+                const uint32_t qa = base + L::q + (alternate ? 0 : t) * L::kTileBytes, ka = base + L::k + s * L::kTileBytes;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t step = (i / 4) * (kRows * 128 / 16) + (i % 4) * 2;
-                    tc::mma_ss(tmem + t * 128, qd + step, kd + step, kDescS, i > 0);
+                    const uint32_t step = (i / 4) * (kRows * 128) + (i % 4) * 32;
+                    tc::mma_ss(tmem + t * 128, tc::desc_k_major(qa + step), tc::desc_k_major(ka + step), kDescS, i > 0);
                 }
                 tc::mma_commit(bar(kSFull + t));
             };
@@ -493,14 +582,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 for (int t = 0; t < 2 && go; ++t) {
                     if (j >= ends[t] || (alternate && (j & 1) != t)) continue;
                     const int i = alternate ? j / 2 : j;       // how many tiles the stream has had
-                    go = tc::bar_wait(bar(kPFull + t), i & 1, &gave_up);
-                    if (!go) break;
-                    tc::fence_after_sync();
-                    const uint64_t vd = tc::desc_k_major(base + L::v + s * L::kTileBytes);
+                    const uint32_t va = base + L::v + s * L::kTileBytes;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {         // the first weights while the others are taken
+                        go = tc::bar_wait(bar(kPFull + 2 * half + t), i & 1, &gave_up);
+                        if (!go) break;
+                        tc::fence_after_sync();
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                                   vd + (k / 4) * (D * 128 / 16) + (k % 4) * 2, kDescO, i > 0 || k > 0);
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 32 * half + 8 * k,
+                                       tc::desc_k_major(va + half * (D * 128) + k * 32), kDescO, i > 0 || half > 0 || k > 0);
+                    }
+                    if (!go) break;
                     if (next < ends[t]) {
                         go = tc::bar_wait(bar(kKFull + s1), (next / kStages) & 1, &gave_up);
                         if (go) issue_s(t, s1);
@@ -513,67 +606,88 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                     if (next < n) tc::mma_commit(bar(kKEmpty + s1));
                 }
             }
-            volatile int never = 0;                // MMAs in flight end before tensor memory is freed
+            // MMAs in flight end before tensor memory is freed
             tc::mma_commit(bar(kDrain));
-            tc::bar_wait(bar(kDrain), 0, &never);
+            tc::bar_drain(bar(kDrain), 0);
         }
-    } else if (warp < 8) {
+    } else {
+        tc::regs_take<120>();
         // ------------------------------ softmax ----------------------------
         const int t = warp >> 2, r = threadIdx.x & 127;
+        const bool alternate = work.alternate;
         const int qt = alternate ? 0 : t;          // the query tile
-        const int tok = q0 + qt * tpt + r / hg;
-        const bool mine = r < hg * tpt && tok < count;
-        const bool any = __any_sync(0xffffffffu, mine);      // a warp without rows only keeps step
-        // tokens row r sees, from tile0 on
-        const int seen0 = min(start + tok + 1, len) - tile0 * kRows;
+        // tokens row r sees, from tile0 on; a warp without rows only keeps step
+        int seen0;
+        bool mine, any;
+        {
+            const int hg = work.hg, tok = work.q0 + qt * work.tpt + r / hg;
+            mine = r < hg * work.tpt && tok < work.count;
+            any = __any_sync(0xffffffffu, mine);
+            seen0 = min(work.start + tok + 1, work.len) - work.tile0 * kRows;
+        }
         const int seen_least = __reduce_min_sync(0xffffffffu, mine ? seen0 : 0x7fffffff);
+        const int stride = alternate ? 2 : 1, n = work.n;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
         float m = kNoMax, l = 0.0f, row_s = 0.0f;
         int e_ref = kMinExp;
         bool go = n == 0 || tc::bar_wait_warp(bar(kQFull), 0, &gave_up);
         if (go && n > 0) row_s = row_scale[qt * kRows + r];
+        const int end = t == 0 ? work.end0 : n;
         int i = 0;                                 // tiles this stream has had
-        for (int j = alternate ? t : 0; j < ends[t] && go; j += stride, ++i) {
+        for (int j = alternate ? t : 0; j < end && go; j += stride, ++i) {
             go = tc::bar_wait_warp(bar(kSFull + t), i & 1, &gave_up);
             if (!go) break;
             tc::fence_after_sync();
             if (any) {
-                const float scale = row_s * pow2(exp_k[j % kExps]);
-                const int ev = exp_v[j % kExps];
+                const float *scales = scale_k[j % kExps];
+                const int *evs = exp_v[j % kExps];
+                int top = e_ref;
+                bool even = true;
+#pragma unroll
+                for (int g = 0; g < kUnpackWarps; ++g) top = max(top, evs[g]);
+#pragma unroll
+                for (int g = 0; g < kUnpackWarps; ++g) even = even && evs[g] == top;
                 const int seen = seen0 - j * kRows;
                 const bool masked = seen_least < (j + 1) * kRows;
-                auto logits = [&](int cc, uint32_t(&x)[32]) {
-                    tc::tmem_load(ts + 32 * cc, x);
-                    tc::tmem_arrived(x);
+                // 64 of the tile's columns; column e is token mixed(e)
+                auto logits = [&](int half, uint32_t(&x)[2][32]) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) tc::tmem_load(ts + 64 * half + 32 * k, x[k]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) tc::tmem_arrived(x[k]);
                     if (masked) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * cc + e >= seen) x[e] = 0xff800000u;
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (64 * half + 32 * k + mixed(e) >= seen) x[k][e] = 0xff800000u;
                     }
                 };
+                uint32_t x[2][32];
                 float mx = kNoMax;
 #pragma unroll 1
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t x[32];
-                    logits(cc, x);
-                    float m4[4];
+                for (int half = 1; half >= 0; --half) {        // the first half stays for its weights
+                    logits(half, x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(x[e]);
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t *y = &x[g / 2][16 * (g % 2)];
+                        float m2[2] = {__uint_as_float(y[0]), __uint_as_float(y[1])};
 #pragma unroll
-                    for (int e = 4; e < 32; ++e) m4[e % 4] = fmaxf(m4[e % 4], __uint_as_float(x[e]));
-                    mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale);
+                        for (int e = 2; e < 16; ++e) m2[e % 2] = fmaxf(m2[e % 2], __uint_as_float(y[e]));
+                        mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * (row_s * scales[4 * half + g]));
+                    }
                 }
                 if (i == 0) {
                     m = mx;
-                    e_ref = ev;
-                } else if (ev != e_ref || __any_sync(0xffffffffu, mx > m + kLazyMax)) {
+                    e_ref = top;
+                } else if (top != e_ref || __any_sync(0xffffffffu, mx > m + kLazyMax)) {
                     // O holds every tile of the stream before j: S_j was committed after its last MMA
                     const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
-                    const float alpha_o = alpha * tc::ex2(static_cast<float>(e_ref - ev));
+                    const float alpha_o = alpha * tc::ex2(static_cast<float>(e_ref - top));
                     m = mn;
                     l *= alpha;
-                    e_ref = ev;
+                    e_ref = top;
 #pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t o[32];
@@ -586,27 +700,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 }
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t x[32], p[16];
-                    logits(cc, x);
+                for (int half = 0; half < 2; ++half) {
+                    if (half == 1) logits(1, x);
+                    uint32_t(&p)[32] = x[0];       // a weight takes the place of a logit read before
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 y = tc::fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                                  make_float2(scale, scale), make_float2(-m, -m));
-                        const float2 wt = make_float2(tc::ex2(y.x), tc::ex2(y.y));
-                        l2[e % 2] = tc::add2(l2[e % 2], wt);
-                        p[e] = half2_bits(wt.x, wt.y);
+                    for (int g = 0; g < 4; ++g) {
+                        const float sc = row_s * scales[4 * half + g];
+                        const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[4 * half + g] - top));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t *y = &x[g / 2][16 * (g % 2) + 2 * e];
+                            const float2 z = tc::fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                                      make_float2(sc, sc), make_float2(-m, -m));
+                            float2 wt = make_float2(tc::ex2(z.x), tc::ex2(z.y));
+                            l2[e % 2] = tc::add2(l2[e % 2], wt);
+                            if (!even) wt = tc::mul2(wt, make_float2(down, down));
+                            p[8 * g + e] = half2_bits(wt.x, wt.y);
+                        }
                     }
-                    tc::tmem_store16(ts + 16 * cc, p);   // over logits that both passes have read
+                    tc::tmem_store(ts + 32 * half, p);         // over logits that have been read
+                    tc::tmem_stored();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(bar(kPFull + 2 * half + t));
                 }
-                tc::tmem_stored();
                 l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+            } else {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::bar_arrive(bar(kPFull + t));
+                    tc::bar_arrive(bar(kPFull + 2 + t));
+                }
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(bar(kPFull + t));
         }
         const bool had = i > 0;                    // O holds something
+        const int h = work.h, first = work.first, split = work.split, n_splits = work.n_splits, hg = work.hg;
+        const int tok = work.q0 + qt * work.tpt + r / hg;
         if (go && had) go = tc::bar_wait_warp(bar(kOFull + t), 0, &gave_up);
         if (alternate) {
             // stream 1 hands its sums over through the key tiles' shared memory, which the tensor
@@ -641,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
                 const float f0 = w0 * inv * pow2(e_ref), f1 = w1 * inv;
                 uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                                 static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
-                const int64_t tile = (static_cast<int64_t>(item.w) + split) * a.Hkv + h;
+                const int64_t tile = (static_cast<int64_t>(work.part) + split) * a.Hkv + h;
                 float *part = a.part_o + (tile * kRows + r) * D;
                 if (n_splits > 1 && mine) {
                     a.part_ml[tile * 2 * kRows + r] = mn;
@@ -678,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_cache_kernel(const AttendA
             const float f0 = (n_splits > 1 ? 1.0f : l > 0.0f ? __fdividef(1.0f, l) : 0.0f) * pow2(e_ref);
             uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                             static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
-            const int64_t tile = (static_cast<int64_t>(item.w) + 2 * split + t) * a.Hkv + h;
+            const int64_t tile = (static_cast<int64_t>(work.part) + 2 * split + t) * a.Hkv + h;
             float *part = a.part_o + (tile * kRows + r) * D;
             if (n_splits > 1 && mine) {
                 a.part_ml[tile * 2 * kRows + r] = m;

@@ -158,13 +158,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                 }
             }
             if (lane == 0) {                       // copies in flight land before the CTA leaves
-                volatile int never = 0;
                 for (int t = 0; t < 2; ++t)
-                    if (n_tiles[t]) tc::bar_wait(bar(kQFull + t), 0, &never);
+                    if (n_tiles[t]) tc::bar_drain(bar(kQFull + t), 0);
                 for (int i = max(0, issued_k - kStages); i < issued_k; ++i)
-                    tc::bar_wait(bar(kKFull + i % kStages), (i / kStages) & 1, &never);
+                    tc::bar_drain(bar(kKFull + i % kStages), (i / kStages) & 1);
                 for (int i = max(0, issued - kStages); i < issued; ++i)
-                    tc::bar_wait(bar(kVFull + i % kStages), (i / kStages) & 1, &never);
+                    tc::bar_drain(bar(kVFull + i % kStages), (i / kStages) & 1);
             }
         } else if (warp == 8) {
             // ------------------------------ MMAs -------------------------------
@@ -218,9 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                         if (j + 1 < n_max) tc::mma_commit(bar(kKEmpty + s1));
                     }
                 }
-                volatile int never = 0;            // MMAs in flight end before tensor memory is freed
+                // MMAs in flight end before tensor memory is freed
                 tc::mma_commit(bar(kDrain));
-                tc::bar_wait(bar(kDrain), 0, &never);
+                tc::bar_drain(bar(kDrain), 0);
             }
         }
     } else {

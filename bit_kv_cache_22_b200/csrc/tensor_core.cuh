@@ -22,33 +22,36 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// One poll, suspended for at most about a microsecond.
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
         "selp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
         : "r"(bar), "r"(parity)
         : "memory");
     return done != 0;
 }
-// Waits for the barrier's phase `parity`; gives up after about two seconds, or as soon as
+// Waits for the barrier's phase `parity`; gives up after about two seconds of polls, or as soon as
 // another role of the CTA gave up, and then raises *gave_up (shared).
-constexpr long long kWaitCycles = 4000000000LL;
+constexpr int kPolls = 1 << 21;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-    if (bar_test(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!bar_test(bar, parity)) {
+#pragma unroll 1
+    for (int polls = 0; !bar_test(bar, parity); ++polls) {
+        if (polls == kPolls) *gave_up = 1;
         if (*gave_up) return false;
-        if (clock64() - t0 > kWaitCycles) {
-            *gave_up = 1;
-            return false;
-        }
     }
     return true;
 }
-// The same for a whole warp: every lane gets the answer all lanes agree on.
+// The same on the way out, whatever gave up before.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (int polls = 0; polls < kPolls && !bar_test(bar, parity); ++polls) {
+    }
+}
+// bar_wait for a whole warp: every lane gets the answer all lanes agree on.
 __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
 }
