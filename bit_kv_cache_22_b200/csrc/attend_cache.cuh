@@ -1,0 +1,762 @@
+// attend_cache.cuh -- what the two kernels that attend a chunk over the paged low-bit cache share
+// (attend_narrow.cu: few query rows a slot, attend_wide.cu: many): the operands' form, their
+// unpacking, the MMA and softmax roles.
+//
+// Query row i of a slot, at position p, sees tokens 0 .. p of its sequence: o_i = sum_{j <= p}
+// p_ij v_j with p_i = softmax_j(q_i . k_j / sqrt(d)), k_j and v_j as the cache holds them: (code - z) s
+// for tokens below Tq, the residual rows behind.  One pass with a running maximum and sum per row.
+//
+// A CTA serves one kv head and up to two tiles of 128 query rows (tokens x the query heads of that
+// kv head).  Key and value tiles of 128 tokens lie in shared memory as fp16 operands; S = Q K^T and
+// O += P V run on tcgen05 with both accumulators and P in tensor memory, and four warps per query
+// tile take the softmax (thread = row).  Where one query tile holds all rows the two halves of the
+// CTA take alternate key tiles of it and meet at the end.
+//
+// Operands in fp16 for caches of either type: (code - z) s is rounded to 11 bits (bf16 would leave 8,
+// a rounding as large as the output's own).  What fp16 lacks is range, so operands carry powers of
+// two of their own: a query row that of its largest channel, 16 tokens' keys and values those of
+// bounds on their elements, so that the largest lies in [2^14, 2^15) -- values' in steps of 2^4.
+// They are undone in the logits' scale and at the end: weights that meet a smaller power of values
+// than the largest so far are scaled down, and the sums in tensor memory when the largest grows.
+// An element far below the largest of its 16 tokens loses bits under 2^-36 of it.
+//
+// Unpacking is bound by the integer pipe, so codes stay in 16-bit pairs: bytes 0 and 2 (1 and 3) of a
+// word's slot, OR 0x6400, are the fp16 numbers 1024 + code; minus (1024 + z), exact for |z| <= 1024,
+// times s in two fp16 parts.  Within each four channels of keys (and queries) and each four
+// tokens the order in the operands is 0, 2, 1, 3, as the pairs come.
+#pragma once
+
+#include <cstdint>
+
+#include "chunk_rows.cuh"
+#include "kvq_internal.cuh"
+#include "tensor_core.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kRows = 128;                 // rows of a query tile, tokens of a key tile
+constexpr int kStages = 2;                 // key and value operand tiles, each
+constexpr int kUnpackWarps = 8;            // of 16 tokens each in a key tile
+constexpr int kExps = 8;                   // key tiles whose exponents are kept (at most kStages + 1 are live)
+constexpr int kValueStep = 4;              // values' exponents are multiples of this: they rarely differ
+constexpr float kLazyMax = 8.0f;           // the running maximum is raised when a logit passes it by this
+constexpr float kNoMax = -1e30f;           // the maximum of no logits: finite, so differences stay numbers
+constexpr int kMaxTokens = 0x7fffffff - 1024;   // of a sequence (the planner refuses more)
+// Least exponents of operands: values' 2^e and 2^-e stay normal; those of queries and keys keep
+// their product, the logits' scale, above 0 (what they cost a logit is below 2^-60 of the other).
+constexpr int kMinExp = -112, kMinLogitExp = -56;
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// the exponent e with bound 2^-e in [2^14, 2^15), as far as `least` allows
+__device__ __forceinline__ int operand_exp(uint32_t bound_bits, int least) {
+    return max(static_cast<int>(bound_bits >> 23) - 127 - 14, least);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// byte e of w as 2^23 + byte
+template <int E>
+__device__ __forceinline__ float byte_plus_2_23(uint32_t w) {
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + E));
+}
+
+// place of element i of four in an operand: 0, 2, 1, 3
+__host__ __device__ constexpr int mixed(int i) { return (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1); }
+
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
+__device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+
+// The parameters of four elements, in pairs (0, 2) and (1, 3): -(1024 + z), and s in two parts.
+struct Quad {
+    uint2 z, hi, lo;
+};
+
+// Four codes of N bits in the bytes of b (above them anything): (code - z) s.
+template <int N>
+__device__ __forceinline__ uint2 unpack_four(uint32_t b, const Quad &q) {
+    constexpr uint32_t kMask = 0x00010001u * ((1u << N) - 1);
+    const __half2 x = __hadd2(as_half2((b & kMask) | 0x64006400u), as_half2(q.z.x));
+    const __half2 y = __hadd2(as_half2(((b >> 8) & kMask) | 0x64006400u), as_half2(q.z.y));
+    return make_uint2(as_bits(__hfma2(x, as_half2(q.hi.x), __hmul2(x, as_half2(q.lo.x)))),
+                      as_bits(__hfma2(y, as_half2(q.hi.y), __hmul2(y, as_half2(q.lo.y)))));
+}
+// The same in fp32, for zeros that 1024 + z does not hold.
+__device__ __forceinline__ uint2 unpack_four_wide(uint32_t b, const float4 &s, const float4 &z) {
+    const float2 x = tc::mul2(tc::add2(make_float2(byte_plus_2_23<0>(b), byte_plus_2_23<2>(b)), make_float2(z.x, z.z)),
+                              make_float2(s.x, s.z));
+    const float2 y = tc::mul2(tc::add2(make_float2(byte_plus_2_23<1>(b), byte_plus_2_23<3>(b)), make_float2(z.y, z.w)),
+                              make_float2(s.y, s.w));
+    return make_uint2(half2_bits(x.x, x.y), half2_bits(y.x, y.y));
+}
+
+// What one unpacking warp needs of a tile's 16 tokens: the code words of its lanes, and four
+// scales and zeros a lane, which it spreads over shared memory.
+template <int D, int N>
+struct Fetched {
+    static constexpr int W = D * N / 64;   // words per lane
+    uint32_t kw[W], vw[W];
+    float4 ks, vs;                         // keys: channels 4 lane ...; values: entries 4 lane ... of
+    uint2 kz, vz;                          // [16 tokens][D / Gv], as far as there are any
+    int kind;                              // 0: no tokens, 1: quantized, 2: residual
+};
+
+__device__ __forceinline__ void widen_zeros(uint2 z, bool sym, int half_levels, float (&f)[4]) {
+    f[0] = static_cast<float>(sym ? half_levels : static_cast<int>(static_cast<int16_t>(z.x & 0xffffu)));
+    f[1] = static_cast<float>(sym ? half_levels : static_cast<int>(z.x) >> 16);
+    f[2] = static_cast<float>(sym ? half_levels : static_cast<int>(static_cast<int16_t>(z.y & 0xffffu)));
+    f[3] = static_cast<float>(sym ? half_levels : static_cast<int>(z.y) >> 16);
+}
+
+// The powers of two of a key tile, per 16 tokens: 2^e of the keys, then e of the values.
+struct TileExps {
+    float scale_k[kUnpackWarps];
+    int exp_v[kUnpackWarps];
+};
+
+// Fetches the 16 tokens tok .. of a slot for kv head h; at_tok: the first one's place in its page.
+template <int D, int N>
+__device__ __forceinline__ void fetch16(Fetched<D, N> &f, const PagedView &c, int h, int page, int at_tok, int tok,
+                                        int len, int tq, bool on, int lane) {
+    constexpr int W = D * N / 64, TW = D * N / 2;
+    f.kind = !on || tok >= len ? 0 : tok < tq ? 1 : 2;
+    if (f.kind != 1) return;
+    if (page < 0 || page >= c.num_pages) {
+        if (lane == 0) atomicOr(c.status, 2u);
+        page = 0;
+    }
+    const int64_t slice = static_cast<int64_t>(page) * c.Hkv + h;
+    const int64_t words = (slice * (c.P >> 4) + (at_tok >> 4)) * TW + lane * W;
+    if constexpr (W >= 4) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(c.kc + words + i);
+            const uint4 y = *reinterpret_cast<const uint4 *>(c.vc + words + i);
+            f.kw[i] = x.x; f.kw[i + 1] = x.y; f.kw[i + 2] = x.z; f.kw[i + 3] = x.w;
+            f.vw[i] = y.x; f.vw[i + 1] = y.y; f.vw[i + 2] = y.z; f.vw[i + 3] = y.w;
+        }
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(c.kc + words);
+        const uint2 y = *reinterpret_cast<const uint2 *>(c.vc + words);
+        f.kw[0] = x.x; f.kw[1] = x.y;
+        f.vw[0] = y.x; f.vw[1] = y.y;
+    }
+    const int g_shift = __ffs(c.G) - 1, ngv_shift = __ffs(D) - __ffs(c.Gv);      // powers of two
+    if (4 * lane < D) {
+        const int64_t km = (slice * (c.P >> g_shift) + (at_tok >> g_shift)) * D + 4 * lane;
+        f.ks = *reinterpret_cast<const float4 *>(c.ks + km);
+        if (!c.sym) f.kz = *reinterpret_cast<const uint2 *>(c.kz + km);
+    }
+    if (4 * lane < 16 << ngv_shift) {
+        const int64_t vm = ((slice * c.P + at_tok) << ngv_shift) + 4 * lane;
+        f.vs = *reinterpret_cast<const float4 *>(c.vs + vm);
+        if (!c.sym) f.vz = *reinterpret_cast<const uint2 *>(c.vz + vm);
+    }
+}
+
+// A warp's 512 floats of shared memory for the parameters of its 16 tokens.
+template <int D>
+constexpr int kMetaBytes = (2 * D + 2 * 128) * 4;
+
+// The 16 tokens' powers of two (ek, and ev at least what it was), and their parameters spread over
+// shared memory for the lanes that use them; false: in fp32, for zeros that 1024 + z does not hold.
+// res_k, res_v: the slot's residual rows (token tq's first).
+template <int D, int N, bool BF16>
+__device__ __forceinline__ bool prepare16(const Fetched<D, N> &f, const PagedView &c, const uint16_t *res_k,
+                                          const uint16_t *res_v, int tok, int len, int tq, int lane,
+                                          unsigned char *meta, int &ek, int &ev) {
+    constexpr float kTop = static_cast<float>((1 << N) - 1);
+    const int ngv_shift = __ffs(D) - __ffs(c.Gv), ngv = 1 << ngv_shift;
+    float bk = 0.0f, bv = 0.0f;
+    float zk[4], zv[4];
+    const bool has_k = f.kind == 1 && 4 * lane < D, has_v = f.kind == 1 && 4 * lane < 16 << ngv_shift;
+    if (f.kind == 1) {
+        widen_zeros(f.kz, c.sym, 1 << (N - 1), zk);
+        widen_zeros(f.vz, c.sym, 1 << (N - 1), zv);
+        const float sk[4] = {f.ks.x, f.ks.y, f.ks.z, f.ks.w}, sv[4] = {f.vs.x, f.vs.y, f.vs.z, f.vs.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (has_k) bk = fmaxf(bk, sk[e] * fmaxf(fabsf(zk[e]), fabsf(kTop - zk[e])));
+            if (has_v) bv = fmaxf(bv, sv[e] * fmaxf(fabsf(zv[e]), fabsf(kTop - zv[e])));
+        }
+    } else if (f.kind == 2) {
+#pragma unroll 1
+        for (int i = lane; i < 16 * D / 2; i += 32) {
+            const int tk = tok + i / (D / 2);
+            if (tk < len) {
+                const int64_t at = static_cast<int64_t>(tk - tq) * (D / 2) + i % (D / 2);
+                const float2 x = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(res_k)[at]);
+                const float2 y = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(res_v)[at]);
+                bk = fmaxf(bk, fmaxf(fabsf(x.x), fabsf(x.y)));
+                bv = fmaxf(bv, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+        }
+    }
+    ek = operand_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(bk)), kMinLogitExp);
+    ev = max(ev, (operand_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(bv)), kMinExp) + kValueStep - 1) &
+                     ~(kValueStep - 1));
+    if (f.kind != 1) return true;
+    const float down_k = pow2(-ek), down_v = pow2(-ev);
+    bool over = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        over = over || (has_k && fabsf(zk[e]) > 1024.0f) || (has_v && fabsf(zv[e]) > 1024.0f);
+    const bool wide = __any_sync(0xffffffffu, over);       // (and the tokens before are unpacked)
+    const float sk[4] = {f.ks.x * down_k, f.ks.y * down_k, f.ks.z * down_k, f.ks.w * down_k};
+    const float sv[4] = {f.vs.x * down_v, f.vs.y * down_v, f.vs.z * down_v, f.vs.w * down_v};
+    if (!wide) {
+        // keys: [z, hi, lo][D / 4] pairs of pairs; values: [z, hi, lo][D / Gv][16] in mixed order
+        uint2 *km = reinterpret_cast<uint2 *>(meta);
+        uint16_t *vm = reinterpret_cast<uint16_t *>(meta + 3 * D * 2);
+        if (has_k) {
+            float hi[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hi[e] = __half2float(__float2half_rn(sk[e]));
+            km[lane] = make_uint2(half2_bits(-1024.0f - zk[0], -1024.0f - zk[2]),
+                                  half2_bits(-1024.0f - zk[1], -1024.0f - zk[3]));
+            km[D / 4 + lane] = make_uint2(half2_bits(hi[0], hi[2]), half2_bits(hi[1], hi[3]));
+            km[D / 2 + lane] = make_uint2(half2_bits(sk[0] - hi[0], sk[2] - hi[2]), half2_bits(sk[1] - hi[1], sk[3] - hi[3]));
+        }
+        if (has_v) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * lane + e, at = (i & (ngv - 1)) * 16 + mixed(i >> ngv_shift);
+                const __half hi = __float2half_rn(sv[e]);
+                vm[at] = __half_as_ushort(__float2half_rn(-1024.0f - zv[e]));
+                vm[128 + at] = __half_as_ushort(hi);
+                vm[256 + at] = __half_as_ushort(__float2half_rn(sv[e] - __half2float(hi)));
+            }
+        }
+    } else {
+        // fp32 [s, z] of keys [D] and values [D / Gv][16]
+        float *km = reinterpret_cast<float *>(meta), *vm = km + 2 * D;
+        if (has_k) {
+            reinterpret_cast<float4 *>(km)[lane] = make_float4(sk[0], sk[1], sk[2], sk[3]);
+            reinterpret_cast<float4 *>(km + D)[lane] =
+                make_float4(-8388608.0f - zk[0], -8388608.0f - zk[1], -8388608.0f - zk[2], -8388608.0f - zk[3]);
+        }
+        if (has_v) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * lane + e, at = (i & (ngv - 1)) * 16 + (i >> ngv_shift);
+                vm[at] = sv[e];
+                vm[128 + at] = -8388608.0f - zv[e];
+            }
+        }
+    }
+    __syncwarp();
+    return !wide;
+}
+
+// The 16 tokens (warp w of a key tile's eight) as operands.  kv 0: keys, rows = tokens, channels along
+// a row; kv 1: values, rows = channels, tokens along a row.  put(offset, a, b) stores 8 bytes of the
+// tile, put(offset, v) 16.  words: the tokens' code words, used up.
+template <int D, int N, bool BF16, class Put>
+__device__ __forceinline__ void emit16(int kv, uint32_t (&words)[D * N / 64], int kind, bool narrow, const PagedView &c,
+                                       const uint16_t *res, int tok, int len, int tq, float down, int w, int lane,
+                                       const unsigned char *meta, const Put &put) {
+    constexpr int B = 4 / N, W = D * N / 64;
+    const int tile = kv ? (w / 4) * (D * 128) : 16 * w * 128;
+    // lane's row (+ 8 in a second store): a key's is its token, in mixed order, a value's its channel;
+    // 8 bytes of a 32-byte step along it, swizzled
+    const int row = kv ? lane >> 2 : mixed(lane >> 2);
+    const int place = row * 128 + (lane & 1) * 8, col = (((lane & 3) >> 1) ^ (row & 7)) << 4;
+    auto offset = [&](int ch) {                    // of chunk ch (16 channels)
+        return kv ? tile + ch * 2048 + place + (col ^ ((w % 4) << 5))
+                  : tile + (ch / 4) * (kRows * 128) + place + (col ^ ((ch % 4) << 5));
+    };
+    const int shift = kv ? __ffs(c.Gv) - 5 : 0;    // chunk -> group of parameters
+    if (kind == 1 && narrow) {
+        // two chunks at a time; the parameters of the next two are loaded before their stores
+        const uint2 *pm = reinterpret_cast<const uint2 *>(meta + (kv ? 3 * D * 2 : 0)) + (lane & 3);
+        const int next = kv ? 32 : D / 4;          // from z to hi to lo
+        auto quad = [&](int ch) {
+            const uint2 *at = pm + 4 * (ch >> shift);
+            return Quad{at[0], at[next], at[2 * next]};
+        };
+        Quad q0 = quad(0), q1 = quad(1);
+#pragma unroll 1
+        for (int ch = 0; ch < D / 16; ch += 2) {
+            const int more = ch + 2 < D / 16 ? ch + 2 : 0;
+            const Quad n0 = quad(more), n1 = quad(more + 1);
+            const uint32_t b0 = words[0], b1 = N == 2 ? b0 >> 4 : words[2 / B - 1];
+#pragma unroll
+            for (int i = 0; i + 2 / B < W; ++i) words[i] = words[i + 2 / B];   // the words move up
+            const int d0 = offset(ch), d1 = kv ? d0 + 2048 : d0 ^ 32;
+            const uint2 x0 = unpack_four<N>(b0, q0), y0 = unpack_four<N>(b0 >> N, q0);
+            const uint2 x1 = unpack_four<N>(b1, q1), y1 = unpack_four<N>(b1 >> N, q1);
+            put(d0, x0.x, x0.y);
+            put(d0 + 1024, y0.x, y0.y);
+            put(d1, x1.x, x1.y);
+            put(d1 + 1024, y1.x, y1.y);
+            q0 = n0;
+            q1 = n1;
+        }
+    } else if (kind == 1) {
+        constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
+        const float4 *pm = reinterpret_cast<const float4 *>(meta) + (kv ? 2 * D / 4 : 0) + (lane & 3);
+        const int next = kv ? 32 : D / 4;          // from s to z
+#pragma unroll 1
+        for (int i = 0; i < D / 8; ++i) {          // chunk i / 2, row half i % 2
+            const uint32_t b = (words[0] >> (N * (i % (2 * B)))) & kMask;
+            if (i % (2 * B) == 2 * B - 1)
+#pragma unroll
+                for (int k = 0; k + 1 < W; ++k) words[k] = words[k + 1];
+            const float4 *at = pm + 4 * ((i / 2) >> shift);
+            const uint2 x = unpack_four_wide(b, at[0], at[next]);
+            put(offset(i / 2) + 1024 * (i % 2), x.x, x.y);
+        }
+    } else if (kv == 0) {
+#pragma unroll 1
+        for (int i = lane; i < 16 * (D / 8); i += 32) {
+            const int r = i / (D / 8), v = i % (D / 8), rm = mixed(r);
+            uint32_t o[4] = {0u, 0u, 0u, 0u};
+            if (kind == 2 && tok + r < len) {
+                const uint4 x = reinterpret_cast<const uint4 *>(res + static_cast<int64_t>(tok + r - tq) * D)[v];
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 p = widen_pair<BF16>(xw[e]), q = widen_pair<BF16>(xw[e + 1]);
+                    o[e] = half2_bits(p.x * down, q.x * down);
+                    o[e + 1] = half2_bits(p.y * down, q.y * down);
+                }
+            }
+            put(tile + (v / 8) * (kRows * 128) + rm * 128 + (((v % 8) ^ (rm & 7)) << 4), o);
+        }
+    } else {
+#pragma unroll 1
+        for (int i = lane; i < D; i += 32) {       // channels 2 cp, 2 cp + 1: 8 of the 16 tokens
+            const int cp = i >> 1, part = i & 1;
+            uint32_t o[2][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float2 p[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tk = tok + 8 * part + mixed(2 * k + e);
+                    p[e] = make_float2(0.0f, 0.0f);
+                    if (kind == 2 && tk < len)
+                        p[e] = widen_pair<BF16>(
+                            reinterpret_cast<const uint32_t *>(res + static_cast<int64_t>(tk - tq) * D)[cp]);
+                }
+                o[0][k] = half2_bits(p[0].x * down, p[1].x * down);
+                o[1][k] = half2_bits(p[0].y * down, p[1].y * down);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * cp + e;
+                put(tile + r * 128 + (((2 * (w % 4) + part) ^ (r & 7)) << 4), o[e]);
+            }
+        }
+    }
+}
+
+// Query rows r (tokens x heads) of a tile as operands, by warp w of n_warps: four channels a lane,
+// kBatch rows of loads in flight.  row(r) is a row's elements, or NULL; put(offset, a, b) as above;
+// put_scale(r, 2^e).
+template <int D, bool BF16, class Row, class Put, class PutScale>
+__device__ __forceinline__ void emit_queries(int rows, int w, int n_warps, int lane, const Row &row, const Put &put,
+                                             const PutScale &put_scale) {
+    constexpr int kLanes = D / 4, kPer = 32 / kLanes, kBatch = 4;      // lanes a row, rows at a time
+    const int col = (lane % kLanes) * 4, step = n_warps * kPer;
+#pragma unroll 1
+    for (int r0 = w * kPer + lane / kLanes; r0 < rows; r0 += kBatch * step) {
+        uint2 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = r0 + k * step;
+            const uint16_t *src = r < rows ? row(r) : nullptr;
+            x[k] = src ? *reinterpret_cast<const uint2 *>(src + col) : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = r0 + k * step;
+            const float2 p = widen_pair<BF16>(x[k].x), q = widen_pair<BF16>(x[k].y);
+            float big = fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(q.x), fabsf(q.y)));
+#pragma unroll
+            for (int off = kLanes / 2; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+            const int ex = operand_exp(__float_as_uint(big), kMinLogitExp);
+            const float down = pow2(-ex);
+            if (r >= rows) continue;
+            if (col == 0) put_scale(r, pow2(ex));
+            put((col / 64) * (kRows * 128) + r * 128 + ((((col % 64) / 8) ^ (r & 7)) << 4) + (col % 8) * 2,
+                half2_bits(p.x * down, q.x * down), half2_bits(p.y * down, q.y * down));
+        }
+    }
+}
+
+// A CTA's work: up to 2 * tpt tokens of one slot's chunk from q0 on, for kv head h, over split
+// `split` of n_splits of the key tiles their last token sees: tiles tile0 .. tile0 + n - 1.
+struct CacheItem {
+    int slot, h, q0, count, first, start;          // the slot's chunk: tokens, first row, first position
+    int hg, tpt;                                   // query heads of the kv head, tokens of a query tile
+    int len, tq;                                   // tokens of the slot, quantized ones
+    int tile0, n;
+    int end0;                                      // tiles below it concern stream 0 (stream 1: n)
+    int split, n_splits, part;                     // first partial tile
+    bool alternate;                                // one query tile, alternate key tiles
+    bool good;
+};
+
+__device__ __forceinline__ CacheItem cache_item(const AttendArgs &a, const int4 item, int h) {
+    CacheItem w{};
+    w.h = h;
+    w.hg = a.Hq / a.Hkv;
+    w.tpt = kRows / w.hg;
+    w.slot = item.x;
+    w.q0 = item.y;
+    w.split = item.z & 0xffff;
+    w.n_splits = item.z >> 16;
+    w.part = item.w;
+    w.good = w.slot >= 0 && w.slot < a.t.B && w.q0 >= 0 && w.split < w.n_splits && w.part >= 0;
+    if (!w.good) return w;
+    w.first = a.t.offsets[w.slot];
+    w.count = a.t.offsets[w.slot + 1] - w.first;
+    w.start = a.t.starts[w.slot];
+    w.alternate = w.count - w.q0 <= w.tpt;
+    w.good = w.first >= 0 && w.count > w.q0 && w.start >= 0 && w.start <= kMaxTokens - w.count &&
+             static_cast<int64_t>(w.first) + w.count <= a.t.tokens &&
+             (w.n_splits == 1 ||
+              w.part + static_cast<int64_t>(w.n_splits) * (w.alternate ? 1 : 2) <= a.part_tiles);
+    if (!w.good) return w;
+    // (positions stay below 2^31 - 1024, so a tile's tokens are 32-bit numbers)
+    w.len = min(max(a.cache.seq_len[w.slot], 0), kMaxTokens);
+    w.tq = w.len / a.cache.R * a.cache.R;
+    const int last = min(w.q0 + 2 * w.tpt, w.count);
+    const int all = (min(w.start + last, w.len) + kRows - 1) / kRows;
+    const int share = all / w.n_splits, extra = all % w.n_splits;      // the first splits take a tile more
+    w.tile0 = share * w.split + min(w.split, extra);
+    w.n = share + (w.split < extra);
+    w.end0 = w.n;
+    if (!w.alternate)
+        w.end0 = max(0, min(w.n, (min(w.start + w.q0 + w.tpt, w.len) + kRows - 1) / kRows - w.tile0));
+    return w;
+}
+
+// The CTA's barriers; kPFull: [half of the tile's tokens][stream].
+enum { kQFull = 0, kKFull = 1, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages, kVEmpty = kKEmpty + kStages,
+       kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kOFull = kPFull + 4, kDrain = kOFull + 2, kBars };
+
+// filled: arrivals that fill the queries or a tile's operands
+__device__ __forceinline__ void init_bars(uint32_t bars, int filled) {
+    for (int i = 0; i < kBars; ++i) tc::bar_init(bars + 8u * i, i < kKEmpty ? filled : i >= kPFull && i < kPFull + 4 ? 4 : 1);
+    tc::fence_barrier_init();
+}
+
+// Tensor memory (512 columns): S0 | S1 | O0 | O1, P over the first half of its S.
+
+// Issues the CTA's MMAs (one thread).
+template <int D, class L>
+__device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, uint32_t tmem, volatile int &gave_up) {
+    const uint32_t bars = base + L::bars;
+    auto bar = [&](int i) { return bars + 8u * i; };
+    const int n = work.n, ends[2] = {work.end0, n};
+    const bool alternate = work.alternate;
+    const int stride = alternate ? 2 : 1;          // of a stream's tiles
+    constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, false, false);
+    constexpr uint32_t kDescO = tc::mma_desc(kRows, D, false, false);
+    auto issue_s = [&](int t, int s) {
+        const uint32_t qa = base + L::q + (alternate ? 0 : t) * L::kTileBytes, ka = base + L::k + s * L::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint32_t step = (i / 4) * (kRows * 128) + (i % 4) * 32;
+            tc::mma_ss(tmem + t * 128, tc::desc_k_major(qa + step), tc::desc_k_major(ka + step), kDescS, i > 0);
+        }
+        tc::mma_commit(bar(kSFull + t));
+    };
+    bool go = tc::bar_wait(bar(kQFull), 0, &gave_up);
+    for (int t = 0; t < 2 && go; ++t) {
+        const int j = alternate ? t : 0;   // the stream's first tile
+        if (j < ends[t]) {
+            go = tc::bar_wait(bar(kKFull + j % kStages), (j / kStages) & 1, &gave_up);
+            if (go) issue_s(t, j % kStages);
+        }
+        if (go && (alternate ? j < n : t == 1)) tc::mma_commit(bar(kKEmpty + j % kStages));
+    }
+    for (int j = 0; j < n && go; ++j) {
+        const int s = j % kStages, next = j + stride, s1 = next % kStages;
+        go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
+        for (int t = 0; t < 2 && go; ++t) {
+            if (j >= ends[t] || (alternate && (j & 1) != t)) continue;
+            const int i = alternate ? j / 2 : j;       // how many tiles the stream has had
+            const uint32_t va = base + L::v + s * L::kTileBytes;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {         // the first weights while the others are taken
+                go = tc::bar_wait(bar(kPFull + 2 * half + t), i & 1, &gave_up);
+                if (!go) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 32 * half + 8 * k,
+                               tc::desc_k_major(va + half * (D * 128) + k * 32), kDescO, i > 0 || half > 0 || k > 0);
+            }
+            if (!go) break;
+            if (next < ends[t]) {
+                go = tc::bar_wait(bar(kKFull + s1), (next / kStages) & 1, &gave_up);
+                if (go) issue_s(t, s1);
+            } else {
+                tc::mma_commit(bar(kOFull + t));
+            }
+        }
+        if (go) {
+            tc::mma_commit(bar(kVEmpty + s));
+            if (next < n) tc::mma_commit(bar(kKEmpty + s1));
+        }
+    }
+    // MMAs in flight end before tensor memory is freed
+    tc::mma_commit(bar(kDrain));
+    tc::bar_drain(bar(kDrain), 0);
+}
+
+// The softmax of one query row a thread, warps 0-3 for stream 0, 4-7 for stream 1; then the row's
+// output, or its part of it.  WHOLE: a row's 128 logits are held in registers at once; else 64, read twice.
+template <int D, bool BF16, bool WHOLE, class L>
+__device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheItem &work, const TileExps *exps,
+                                             unsigned char *smem, uint32_t base, uint32_t tmem, int warp, int lane,
+                                             volatile int &gave_up) {
+    const uint32_t bars = base + L::bars;
+    auto bar = [&](int i) { return bars + 8u * i; };
+    const float *row_scale = reinterpret_cast<const float *>(smem + L::row_scale);
+    const int t = warp >> 2, r = threadIdx.x & 127;
+    const bool alternate = work.alternate;
+    const int qt = alternate ? 0 : t;          // the query tile
+    // tokens row r sees, from tile0 on; a warp without rows only keeps step
+    int seen0;
+    bool mine, any;
+    {
+        const int hg = work.hg, tok = work.q0 + qt * work.tpt + r / hg;
+        mine = r < hg * work.tpt && tok < work.count;
+        any = __any_sync(0xffffffffu, mine);
+        seen0 = min(work.start + tok + 1, work.len) - work.tile0 * kRows;
+    }
+    const int seen_least = __reduce_min_sync(0xffffffffu, mine ? seen0 : 0x7fffffff);
+    const int stride = alternate ? 2 : 1, n = work.n;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+    float m = kNoMax, l = 0.0f, row_s = 0.0f;
+    int e_ref = kMinExp;
+    bool go = n == 0 || tc::bar_wait_warp(bar(kQFull), 0, &gave_up);
+    if (go && n > 0) row_s = row_scale[qt * kRows + r] * a.scale;
+    const int end = t == 0 ? work.end0 : n;
+    int i = 0;                                 // tiles this stream has had
+    for (int j = alternate ? t : 0; j < end && go; j += stride, ++i) {
+        go = tc::bar_wait_warp(bar(kSFull + t), i & 1, &gave_up);
+        if (!go) break;
+        tc::fence_after_sync();
+        if (any) {
+            const float *scales = exps[j % kExps].scale_k;
+            const int *evs = exps[j % kExps].exp_v;
+            int top = e_ref;
+            bool even = true;
+#pragma unroll
+            for (int g = 0; g < kUnpackWarps; ++g) top = max(top, evs[g]);
+#pragma unroll
+            for (int g = 0; g < kUnpackWarps; ++g) even = even && evs[g] == top;
+            const int seen = seen0 - j * kRows;
+            const bool masked = seen_least < (j + 1) * kRows;
+            // kHeld / 32 registers' worth of the tile's columns from column 64 half on; column e is token mixed(e)
+            constexpr int kHeld = WHOLE ? 4 : 2;
+            uint32_t x[kHeld][32];
+            auto logits = [&](int half) {
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) tc::tmem_load(ts + 64 * half + 32 * k, x[k]);
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) tc::tmem_arrived(x[k]);
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < kHeld; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (64 * half + 32 * k + mixed(e) >= seen) x[k][e] = 0xff800000u;
+                }
+            };
+            float mx = kNoMax;
+#pragma unroll 1
+            for (int half = WHOLE ? 0 : 1; half >= 0; --half) {    // the first half stays for its weights
+                logits(half);
+#pragma unroll
+                for (int g = 0; g < 2 * kHeld; ++g) {
+                    const uint32_t *y = &x[g / 2][16 * (g % 2)];
+                    float m2[2] = {__uint_as_float(y[0]), __uint_as_float(y[1])};
+#pragma unroll
+                    for (int e = 2; e < 16; ++e) m2[e % 2] = fmaxf(m2[e % 2], __uint_as_float(y[e]));
+                    mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * (row_s * scales[4 * half + g]));
+                }
+            }
+            if (i == 0) {
+                m = mx;
+                e_ref = top;
+            } else if (top != e_ref || __any_sync(0xffffffffu, mx > m + kLazyMax)) {
+                // O holds every tile of the stream before j: S_j was committed after its last MMA
+                const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
+                const float alpha_o = alpha * tc::ex2(static_cast<float>(e_ref - top));
+                m = mn;
+                l *= alpha;
+                e_ref = top;
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[32];
+                    tc::tmem_load(to + 32 * cc, o);
+                    tc::tmem_arrived(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_o);
+                    tc::tmem_store(to + 32 * cc, o);
+                }
+            }
+            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto weights = [&](int half, int from) {           // from x[from], x[from + 1]
+                uint32_t(&p)[32] = x[from];        // a weight takes the place of a logit read before
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float sc = row_s * scales[4 * half + g];
+                    const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[4 * half + g] - top));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t *y = &x[from + g / 2][16 * (g % 2) + 2 * e];
+                        const float2 z = tc::fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                                  make_float2(sc, sc), make_float2(-m, -m));
+                        float2 wt = make_float2(tc::ex2(z.x), tc::ex2(z.y));
+                        l2[e % 2] = tc::add2(l2[e % 2], wt);
+                        if (!even) wt = tc::mul2(wt, make_float2(down, down));
+                        p[8 * g + e] = half2_bits(wt.x, wt.y);
+                    }
+                }
+                tc::tmem_store(ts + 32 * half, p);             // over logits that have been read
+                tc::tmem_stored();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(bar(kPFull + 2 * half + t));
+            };
+            if constexpr (WHOLE) {
+                weights(0, 0);
+                weights(1, 2);
+            } else {
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (half == 1) logits(1);
+                    weights(half, 0);
+                }
+            }
+            l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        } else {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                tc::bar_arrive(bar(kPFull + t));
+                tc::bar_arrive(bar(kPFull + 2 + t));
+            }
+        }
+    }
+    const bool had = i > 0;                    // O holds something
+    const int h = work.h, first = work.first, split = work.split, n_splits = work.n_splits, hg = work.hg;
+    const int tok = work.q0 + qt * work.tpt + r / hg;
+    if (go && had) go = tc::bar_wait_warp(bar(kOFull + t), 0, &gave_up);
+    if (alternate) {
+        // stream 1 hands its sums over through the key tiles' shared memory, which the tensor
+        // core is done with once stream 0's last MMA is
+        float *ml = reinterpret_cast<float *>(smem + L::v), *ox = reinterpret_cast<float *>(smem + L::k);
+        if (t == 1) {
+            if (go && n > 0) go = tc::bar_wait_warp(bar(kOFull), 0, &gave_up);
+            tc::fence_after_sync();
+            if (any && go) {
+                ml[r] = m;
+                ml[kRows + r] = l;
+                const float up = pow2(e_ref);
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[32];
+                    if (had) {
+                        tc::tmem_load(to + 32 * cc, o);
+                        tc::tmem_arrived(o);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        ox[(32 * cc + e) * kRows + r] = had ? __uint_as_float(o[e]) * up : 0.0f;
+                }
+            }
+        }
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (t == 0 && any && go) {
+            tc::fence_after_sync();
+            const float m1 = ml[r], l1 = ml[kRows + r];
+            const float mn = fmaxf(m, m1), w0 = tc::ex2(m - mn), w1 = tc::ex2(m1 - mn);
+            const float sum = l * w0 + l1 * w1, inv = n_splits > 1 ? 1.0f : sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
+            const float f0 = w0 * inv * pow2(e_ref), f1 = w1 * inv;
+            uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
+                            static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
+            const int64_t tile = (static_cast<int64_t>(work.part) + split) * a.Hkv + h;
+            float *part = a.part_o + (tile * kRows + r) * D;
+            if (n_splits > 1 && mine) {
+                a.part_ml[tile * 2 * kRows + r] = mn;
+                a.part_ml[(tile * 2 + 1) * kRows + r] = sum;
+            }
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t o[32];
+                __syncwarp();
+                if (had) {
+                    tc::tmem_load(to + 32 * cc, o);
+                    tc::tmem_arrived(o);
+                }
+                if (!mine) continue;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        y[k] = (had ? __uint_as_float(o[e + k]) * f0 : 0.0f) + ox[(32 * cc + e + k) * kRows + r] * f1;
+                    if (n_splits > 1) {
+                        reinterpret_cast<float4 *>(part + 32 * cc + e)[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        reinterpret_cast<float4 *>(part + 32 * cc + e)[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(out + 32 * cc + e) =
+                            make_uint4(narrow2<BF16>(y[0], y[1]), narrow2<BF16>(y[2], y[3]),
+                                       narrow2<BF16>(y[4], y[5]), narrow2<BF16>(y[6], y[7]));
+                    }
+                }
+            }
+        }
+    } else if (any && go) {
+        tc::fence_after_sync();
+        const float f0 = (n_splits > 1 ? 1.0f : l > 0.0f ? __fdividef(1.0f, l) : 0.0f) * pow2(e_ref);
+        uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
+                        static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
+        const int64_t tile = (static_cast<int64_t>(work.part) + 2 * split + t) * a.Hkv + h;
+        float *part = a.part_o + (tile * kRows + r) * D;
+        if (n_splits > 1 && mine) {
+            a.part_ml[tile * 2 * kRows + r] = m;
+            a.part_ml[(tile * 2 + 1) * kRows + r] = l;
+        }
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            __syncwarp();
+            if (had) {
+                tc::tmem_load(to + 32 * cc, o);
+                tc::tmem_arrived(o);
+            }
+            if (!mine) continue;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = had ? __uint_as_float(o[e + k]) * f0 : 0.0f;
+                if (n_splits > 1) {
+                    reinterpret_cast<float4 *>(part + 32 * cc + e)[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    reinterpret_cast<float4 *>(part + 32 * cc + e)[1] = make_float4(y[4], y[5], y[6], y[7]);
+                } else {
+                    *reinterpret_cast<uint4 *>(out + 32 * cc + e) =
+                        make_uint4(narrow2<BF16>(y[0], y[1]), narrow2<BF16>(y[2], y[3]), narrow2<BF16>(y[4], y[5]),
+                                   narrow2<BF16>(y[6], y[7]));
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+}  // namespace kvq

@@ -1,0 +1,264 @@
+// attend_narrow.cu -- attention over the paged low-bit cache for slots with few new tokens (decode
+// steps, drafts): one query tile of 128 rows holds all of a slot's rows, so each code is used by one
+// tile only and is unpacked where it is used.
+//
+//   warps 0-3, 4-7   softmax of stream 0, 1: alternate key tiles
+//   warps 8-15       operands: warp w the tokens 16w .. 16w+15 of each key tile, its values' power of two
+//                    growing along the pass
+//   warp 16          issues the MMAs (warps 17-19 fill the warpgroup, which gives its registers to the
+//                    softmax: 2 x 128 x 120 + 2 x 128 x 88 + 128 x 64 <= 640 x 96)
+#include <algorithm>
+#include <cstdint>
+
+#include "attend_cache.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 640;
+
+struct SharedPut {
+    uint32_t tile;
+    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
+        tc::store_shared(tile + offset, x, y);
+    }
+    __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const { tc::store_shared(tile + offset, v); }
+};
+
+template <int D>
+struct NarrowSmem {
+    static constexpr int kTileBytes = kRows * D * 2;
+    static constexpr int q = 0;
+    static constexpr int k = q + kTileBytes;
+    static constexpr int v = k + kStages * kTileBytes;
+    static constexpr int meta = v + kStages * kTileBytes;
+    static constexpr int row_scale = meta + kUnpackWarps * kMetaBytes<D>;     // [128]
+    static constexpr int bars = row_scale + kRows * 4;
+    // one CTA an SM: it holds all of the tensor memory
+    static constexpr int bytes = (bars + 256 > 120 * 1024 ? bars + 256 : 120 * 1024) + 1024;
+};
+
+template <int D, int N, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const AttendArgs a) {
+    using L = NarrowSmem<D>;
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    unsigned char *smem = raw + (base - tc::smem_addr(raw));
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int gave_up;
+    __shared__ CacheItem work;                     // in shared memory: each role keeps what it needs of it
+    __shared__ TileExps exps[kExps];
+    const PagedView &c = a.cache;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        work = cache_item(a, a.t.items[a.t.n_wide + blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
+        gave_up = 0;
+        init_bars(base + L::bars, kUnpackWarps);
+    }
+    __syncthreads();
+    if (!work.good || !work.alternate) {           // not this library's table
+        if (threadIdx.x == 0) atomicOr(a.status, 8u);
+        return;
+    }
+    if (warp == 16) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    auto bar = [&](int i) { return base + L::bars + 8u * i; };
+
+    if (warp >= 8 && warp < 16) {
+        tc::regs_give<88>();
+        // ------------------------------ operands ---------------------------
+        const int w = warp - 8;
+        unsigned char *meta = smem + L::meta + w * kMetaBytes<D>;
+        const int tile0 = work.tile0, n = work.n, len = work.len, tq = work.tq;
+        constexpr int W = D * N / 64;
+        // this warp's place in the pages: of the tile to fetch (page index and token in it), whose page
+        // number is loaded a tile ahead
+        const int32_t *pages = c.page_table + static_cast<int64_t>(work.slot) * c.max_pages;
+        int at_page = (tile0 * kRows + 16 * w) / c.P, at_tok = (tile0 * kRows + 16 * w) % c.P;
+        auto page_at = [&](int j, int pi) -> int {
+            return j < n && (tile0 + j) * kRows + 16 * w < tq && pi < c.max_pages ? pages[pi] : -1;
+        };
+        auto advance = [&] {
+            at_tok += kRows;
+            while (at_tok >= c.P) {
+                at_tok -= c.P;
+                ++at_page;
+            }
+        };
+        // the slot's residual rows: token tq's first
+        auto residual = [&](const uint16_t *rows) {
+            return rows + (static_cast<int64_t>(work.slot) * a.Hkv + work.h) * c.R * D;
+        };
+        Fetched<D, N> f;
+        fetch16<D, N>(f, c, work.h, page_at(0, at_page), at_tok, tile0 * kRows + 16 * w, len, tq, n > 0, lane);
+        advance();
+        int page = page_at(1, at_page);
+        {
+            const int hg = work.hg, tpt = work.tpt, q0 = work.q0, count = work.count, first = work.first, h = work.h;
+            emit_queries<D, BF16>(
+                kRows, w, kUnpackWarps, lane,
+                [&](int r) -> const uint16_t * {
+                    const int tok = q0 + r / hg;
+                    if (r >= hg * tpt || tok >= count) return nullptr;
+                    return a.q.p + static_cast<int64_t>(first + tok) * a.q.ts + static_cast<int64_t>(h * hg + r % hg) * a.q.hs;
+                },
+                [&](int offset, uint32_t x, uint32_t y) { tc::store_shared(base + L::q + offset, x, y); },
+                [&](int r, float scale) { reinterpret_cast<float *>(smem + L::row_scale)[r] = scale; });
+            tc::fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(bar(kQFull));
+        }
+        int ev = kMinExp;
+        bool go = true;
+        for (int j = 0; j < n && go; ++j) {
+            const int s = j % kStages, phase = (j / kStages) & 1, kind = f.kind;
+            const int tok = (tile0 + j) * kRows + 16 * w;
+            int ek;
+            const bool narrow =
+                prepare16<D, N, BF16>(f, c, residual(c.kr), residual(c.vr), tok, len, tq, lane, meta, ek, ev);
+            uint32_t words[2][W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                words[0][i] = f.kw[i];
+                words[1][i] = f.vw[i];
+            }
+            fetch16<D, N>(f, c, work.h, page, at_tok, tok + kRows, len, tq, j + 1 < n, lane);
+            advance();
+            page = page_at(j + 2, at_page);
+            // keys, then values, by the same code: the kernel's instructions have to stay in the SM's cache
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                if (j >= kStages) go = tc::bar_wait_warp(bar((kv ? kVEmpty : kKEmpty) + s), phase ^ 1, &gave_up);
+                if (!go) break;
+                if (kv == 0 && lane == 0) {
+                    exps[j % kExps].scale_k[w] = pow2(ek);
+                    exps[j % kExps].exp_v[w] = ev;
+                }
+                const uint32_t tile = base + (kv ? L::v : L::k) + s * L::kTileBytes;
+                emit16<D, N, BF16>(kv, words[0], kind, narrow, c, residual(kv ? c.vr : c.kr), tok, len, tq,
+                                   pow2(kv ? -ev : -ek), w, lane, meta, SharedPut{tile});
+#pragma unroll
+                for (int i = 0; i < W; ++i) words[0][i] = words[1][i];
+                tc::fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(bar((kv ? kVFull : kKFull) + s));
+            }
+        }
+    } else if (warp >= 16) {
+        tc::regs_give<64>();
+        if (warp == 16 && lane == 0 && work.n > 0) mma_role<D, L>(work, base, tmem, gave_up);
+    } else {
+        tc::regs_take<120>();
+        softmax_role<D, BF16, false, L>(a, work, exps, smem, base, tmem, warp, lane, gave_up);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0 && gave_up) atomicOr(a.status, 1u);
+    if (warp == 16) {
+        tc::fence_after_sync();
+        tc::tmem_free(tmem, 512);
+    }
+}
+
+// Joins an item's splits: one warp per (query token, query head) of its rows, o = sum_s 2^(m_s - M)
+// o_s / sum_s 2^(m_s - M) l_s, in the splits' order.  merges: [n][4] = (slot, first query token, splits,
+// first partial tile).
+constexpr int kMergeWarps = 8;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_splits_kernel(const AttendArgs a) {
+    const int4 item = a.t.merges[blockIdx.y];
+    const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
+    const int slot = item.x, q0 = item.y, n_splits = item.z;
+    if (slot < 0 || slot >= a.t.B || q0 < 0 || n_splits < 1 || item.w < 0) {
+        if (threadIdx.x == 0) atomicOr(a.status, 8u);
+        return;
+    }
+    const int first = a.t.offsets[slot], count = a.t.offsets[slot + 1] - first;
+    const int n_tok = min(2 * tpt, count - q0), nt = n_tok <= tpt ? 1 : 2;
+    if (first < 0 || n_tok < 1 || static_cast<int64_t>(first) + count > a.t.tokens ||
+        static_cast<int64_t>(item.w) + static_cast<int64_t>(n_splits) * nt > a.part_tiles) {
+        if (threadIdx.x == 0) atomicOr(a.status, 8u);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int u = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (u >= n_tok * a.Hq) return;
+    const int tok = u / a.Hq, hq = u % a.Hq, h = hq / hg;
+    const int t = tok / tpt, r = (tok % tpt) * hg + hq % hg;
+    auto tile = [&](int s) { return (static_cast<int64_t>(item.w) + s * nt + t) * a.Hkv + h; };
+    float M = kNoMax;
+    for (int s = lane; s < n_splits; s += 32) M = fmaxf(M, a.part_ml[tile(s) * 2 * kRows + r]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    constexpr int E = D / 32;
+    float o[E] = {}, l = 0.0f;
+    for (int s = 0; s < n_splits; ++s) {
+        const float w = tc::ex2(a.part_ml[tile(s) * 2 * kRows + r] - M);
+        l = fmaf(w, a.part_ml[(tile(s) * 2 + 1) * kRows + r], l);
+        const float *p = a.part_o + (tile(s) * kRows + r) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(p + e);
+            o[e] = fmaf(w, x.x, o[e]);
+            o[e + 1] = fmaf(w, x.y, o[e + 1]);
+        }
+    }
+    const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f;
+    uint16_t *out = a.o.p + static_cast<int64_t>(first + q0 + tok) * a.o.ts + static_cast<int64_t>(hq) * a.o.hs + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        reinterpret_cast<uint32_t *>(out)[e / 2] = narrow2<BF16>(o[e] * inv, o[e + 1] * inv);
+}
+
+template <int D, int N, bool BF16>
+cudaError_t launch_instance(const AttendArgs &a, cudaStream_t s) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(attend_narrow_kernel<D, N, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 NarrowSmem<D>::bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = true;
+    }
+    const unsigned grid = static_cast<unsigned>(a.t.n_items - a.t.n_wide) * a.Hkv;
+    attend_narrow_kernel<D, N, BF16><<<grid, kThreads, NarrowSmem<D>::bytes, s>>>(a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_narrow(const AttendArgs &a, cudaStream_t s) {
+    if (a.t.n_items == a.t.n_wide) return cudaSuccess;
+    if (a.d == 64) {
+        if (a.cache.bits == 2) return a.bf16 ? launch_instance<64, 2, true>(a, s) : launch_instance<64, 2, false>(a, s);
+        return a.bf16 ? launch_instance<64, 4, true>(a, s) : launch_instance<64, 4, false>(a, s);
+    }
+    if (a.cache.bits == 2) return a.bf16 ? launch_instance<128, 2, true>(a, s) : launch_instance<128, 2, false>(a, s);
+    return a.bf16 ? launch_instance<128, 4, true>(a, s) : launch_instance<128, 4, false>(a, s);
+}
+
+cudaError_t launch_merge_splits(const AttendArgs &a, cudaStream_t s) {
+    if (a.t.n_merges == 0) return cudaSuccess;
+    // the grid covers the largest item's rows; smaller items leave warps idle
+    const int hg = a.Hq / a.Hkv;
+    const int64_t rows = std::min<int64_t>(2 * (kRows / hg), a.most_tokens) * a.Hq;
+    const dim3 grid(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps), static_cast<unsigned>(a.t.n_merges));
+    if (a.d == 64) {
+        if (a.bf16) merge_splits_kernel<64, true><<<grid, 32 * kMergeWarps, 0, s>>>(a);
+        else merge_splits_kernel<64, false><<<grid, 32 * kMergeWarps, 0, s>>>(a);
+    } else {
+        if (a.bf16) merge_splits_kernel<128, true><<<grid, 32 * kMergeWarps, 0, s>>>(a);
+        else merge_splits_kernel<128, false><<<grid, 32 * kMergeWarps, 0, s>>>(a);
+    }
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace kvq

@@ -1,0 +1,231 @@
+// attend_wide.cu -- attention over the paged low-bit cache for slots with many new tokens (chunked
+// prefill): several query tiles use each code, so a first kernel unpacks every slot's keys and values
+// once, as the operand tiles themselves (swizzled, 64 KB per 128 tokens and kv head at d = 128), and
+// the queries, into the workspace; the attention kernel copies whole tiles.
+//
+//   warps 0-3, 4-7   softmax of query tile 0, 1 (a slot's last CTA may have one: alternate key tiles)
+//   warp 8           issues the MMAs
+//   warp 9           copies (warps 10, 11 fill the warpgroup, which gives its registers to the
+//                    softmax: 2 x 128 x 208 + 128 x 80 <= 384 x 168)
+#include <cstdint>
+
+#include "attend_cache.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kStageThreads = 32 * kUnpackWarps;
+
+template <int D>
+struct WideSmem {
+    static constexpr int kTileBytes = kRows * D * 2;
+    static constexpr int q = 0;                                   // two tiles
+    static constexpr int k = q + 2 * kTileBytes;
+    static constexpr int v = k + kStages * kTileBytes;
+    static constexpr int exps = v + kStages * kTileBytes;
+    static constexpr int row_scale = exps + kExps * static_cast<int>(sizeof(TileExps));       // [2][128]
+    static constexpr int bars = row_scale + 2 * kRows * 4;
+    // one CTA an SM: it holds all of the tensor memory
+    static constexpr int bytes = (bars + 256 > 120 * 1024 ? bars + 256 : 120 * 1024) + 1024;
+};
+
+// The workspace: operand tiles [key tile][kv head][keys, values], [query tile][kv head], then the key
+// tiles' powers of two and the query rows' [..][128].
+template <int D>
+struct Staged {
+    static constexpr int64_t kTileBytes = kRows * D * 2;
+    unsigned char *kv, *q;
+    TileExps *exps;
+    float *row_scale;
+    __device__ explicit Staged(const AttendArgs &a) {
+        kv = a.staged;
+        q = kv + a.t.n_kv_tiles * a.Hkv * 2 * kTileBytes;
+        exps = reinterpret_cast<TileExps *>(q + a.t.n_q_tiles * a.Hkv * kTileBytes);
+        row_scale = reinterpret_cast<float *>(exps + a.t.n_kv_tiles * a.Hkv);
+    }
+};
+
+struct GlobalPut {
+    unsigned char *tile;
+    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
+        *reinterpret_cast<uint2 *>(tile + offset) = make_uint2(x, y);
+    }
+    __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const {
+        *reinterpret_cast<uint4 *>(tile + offset) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+};
+
+// CTA (x, h): key tile x of the wide slots, or query tile x - n_kv_tiles.
+template <int D, int N, bool BF16>
+__global__ void __launch_bounds__(kStageThreads) stage_kernel(const AttendArgs a) {
+    __shared__ __align__(16) unsigned char meta_s[kUnpackWarps][kMetaBytes<D>];
+    const PagedView &c = a.cache;
+    const Staged<D> st(a);
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
+    if (blockIdx.x < static_cast<unsigned>(a.t.n_kv_tiles)) {
+        const int x = blockIdx.x, slot = slot_of(a.t.kv_tiles, a.t.B, x);
+        const int tok = (x - a.t.kv_tiles[slot]) * kRows + 16 * w;
+        const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
+        if (tok < 0) return;
+        const int pi = tok / c.P;
+        const int page = tok < tq && pi < c.max_pages ? c.page_table[static_cast<int64_t>(slot) * c.max_pages + pi] : -1;
+        Fetched<D, N> f;
+        fetch16<D, N>(f, c, h, page, tok % c.P, tok, len, tq, true, lane);
+        const int64_t rows = (static_cast<int64_t>(slot) * a.Hkv + h) * c.R * D;
+        int ek, ev = kMinExp;
+        const bool narrow =
+            prepare16<D, N, BF16>(f, c, c.kr + rows, c.vr + rows, tok, len, tq, lane, meta_s[w], ek, ev);
+        const int64_t at = static_cast<int64_t>(x) * a.Hkv + h;
+        if (lane == 0) {
+            st.exps[at].scale_k[w] = pow2(ek);
+            st.exps[at].exp_v[w] = ev;
+        }
+        unsigned char *tile = st.kv + at * 2 * Staged<D>::kTileBytes;
+        emit16<D, N, BF16>(0, f.kw, f.kind, narrow, c, c.kr + rows, tok, len, tq, pow2(-ek), w, lane, meta_s[w],
+                           GlobalPut{tile});
+        emit16<D, N, BF16>(1, f.vw, f.kind, narrow, c, c.vr + rows, tok, len, tq, pow2(-ev), w, lane, meta_s[w],
+                           GlobalPut{tile + Staged<D>::kTileBytes});
+    } else {
+        const int x = blockIdx.x - a.t.n_kv_tiles, slot = slot_of(a.t.q_tiles, a.t.B, x);
+        const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
+        const int first = a.t.offsets[slot], count = a.t.offsets[slot + 1] - first;
+        const int q0 = (x - a.t.q_tiles[slot]) * tpt;
+        if (first < 0 || q0 < 0 || static_cast<int64_t>(first) + count > a.t.tokens) return;
+        const int64_t at = static_cast<int64_t>(x) * a.Hkv + h;
+        const GlobalPut put{st.q + at * Staged<D>::kTileBytes};
+        emit_queries<D, BF16>(
+            kRows, w, kUnpackWarps, lane,
+            [&](int r) -> const uint16_t * {
+                const int tok = q0 + r / hg;
+                if (r >= hg * tpt || tok >= count) return nullptr;
+                return a.q.p + static_cast<int64_t>(first + tok) * a.q.ts + static_cast<int64_t>(h * hg + r % hg) * a.q.hs;
+            },
+            put, [&](int r, float scale) { st.row_scale[at * kRows + r] = scale; });
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const AttendArgs a) {
+    using L = WideSmem<D>;
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    unsigned char *smem = raw + (base - tc::smem_addr(raw));
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int gave_up;
+    __shared__ CacheItem work;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        work = cache_item(a, a.t.items[blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
+        if (work.good) {                           // its tiles have been staged
+            const int kv = a.t.kv_tiles[work.slot], q = a.t.q_tiles[work.slot];
+            if (kv < 0 || kv + work.tile0 + work.n > a.t.kv_tiles[work.slot + 1] || q < 0 ||
+                a.t.kv_tiles[work.slot + 1] > a.t.n_kv_tiles || a.t.q_tiles[work.slot + 1] > a.t.n_q_tiles ||
+                q + (work.count + work.tpt - 1) / work.tpt > a.t.q_tiles[work.slot + 1])
+                work.good = false;
+        }
+        gave_up = 0;
+        init_bars(base + L::bars, 1);
+    }
+    __syncthreads();
+    if (!work.good) {                              // not this library's table
+        if (threadIdx.x == 0) atomicOr(a.status, 8u);
+        return;
+    }
+    if (warp == 8) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    auto bar = [&](int i) { return base + L::bars + 8u * i; };
+
+    if (warp >= 8) {
+        tc::regs_give<80>();
+        if (warp == 9 && lane == 0 && work.n > 0) {
+            // ------------------------------ copies -------------------------
+            const Staged<D> st(a);
+            const int n = work.n, h = work.h, q_tiles = work.alternate ? 1 : 2;
+            const int64_t q_at = static_cast<int64_t>(a.t.q_tiles[work.slot] + work.q0 / work.tpt);
+            tc::bar_expect(bar(kQFull), q_tiles * (L::kTileBytes + kRows * 4));
+            for (int t = 0; t < q_tiles; ++t) {
+                const int64_t at = (q_at + t) * a.Hkv + h;
+                tc::bulk_load(base + L::q + t * L::kTileBytes, st.q + at * L::kTileBytes, L::kTileBytes, bar(kQFull));
+                tc::bulk_load(base + L::row_scale + t * kRows * 4, st.row_scale + at * kRows, kRows * 4, bar(kQFull));
+            }
+            int64_t at = static_cast<int64_t>(a.t.kv_tiles[work.slot] + work.tile0) * a.Hkv + h;
+            int keys = 0, values = 0;
+            for (int j = 0; j < n; ++j, at += a.Hkv) {
+                const int s = j % kStages, phase = (j / kStages) & 1;
+                const unsigned char *tile = st.kv + at * 2 * L::kTileBytes;
+                if (j >= kStages && !tc::bar_wait(bar(kKEmpty + s), phase ^ 1, &gave_up)) break;
+                tc::bar_expect(bar(kKFull + s), L::kTileBytes + static_cast<int>(sizeof(TileExps)));
+                tc::bulk_load(base + L::k + s * L::kTileBytes, tile, L::kTileBytes, bar(kKFull + s));
+                tc::bulk_load(base + L::exps + (j % kExps) * static_cast<int>(sizeof(TileExps)), st.exps + at,
+                              sizeof(TileExps), bar(kKFull + s));
+                keys = j + 1;
+                if (j >= kStages && !tc::bar_wait(bar(kVEmpty + s), phase ^ 1, &gave_up)) break;
+                tc::bar_expect(bar(kVFull + s), L::kTileBytes);
+                tc::bulk_load(base + L::v + s * L::kTileBytes, tile + L::kTileBytes, L::kTileBytes, bar(kVFull + s));
+                values = j + 1;
+            }
+            tc::bar_drain(bar(kQFull), 0);         // copies in flight land before the CTA leaves
+            for (int j = max(0, keys - kStages); j < keys; ++j) tc::bar_drain(bar(kKFull + j % kStages), (j / kStages) & 1);
+            for (int j = max(0, values - kStages); j < values; ++j)
+                tc::bar_drain(bar(kVFull + j % kStages), (j / kStages) & 1);
+        } else if (warp == 8 && lane == 0 && work.n > 0) {
+            mma_role<D, L>(work, base, tmem, gave_up);
+        }
+    } else {
+        tc::regs_take<208>();
+        softmax_role<D, BF16, true, L>(a, work, reinterpret_cast<const TileExps *>(smem + L::exps), smem, base, tmem, warp,
+                                       lane, gave_up);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0 && gave_up) atomicOr(a.status, 1u);
+    if (warp == 8) {
+        tc::fence_after_sync();
+        tc::tmem_free(tmem, 512);
+    }
+}
+
+template <int D, int N, bool BF16>
+cudaError_t launch_instance(const AttendArgs &a, cudaStream_t s) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(attend_wide_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 WideSmem<D>::bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = true;
+    }
+    const dim3 grid(static_cast<unsigned>(a.t.n_kv_tiles + a.t.n_q_tiles), static_cast<unsigned>(a.Hkv));
+    stage_kernel<D, N, BF16><<<grid, kStageThreads, 0, s>>>(a);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    attend_wide_kernel<D, BF16><<<static_cast<unsigned>(a.t.n_wide) * a.Hkv, kThreads, WideSmem<D>::bytes, s>>>(a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t staged_bytes(int64_t kv_tiles, int64_t q_tiles, int kv_heads, int d) {
+    const int64_t tile = static_cast<int64_t>(kRows) * d * 2;
+    return kv_heads * (kv_tiles * (2 * tile + static_cast<int64_t>(sizeof(TileExps))) + q_tiles * (tile + kRows * 4));
+}
+
+cudaError_t launch_attend_wide(const AttendArgs &a, cudaStream_t s) {
+    if (a.t.n_wide == 0) return cudaSuccess;
+    if (a.d == 64) {
+        if (a.cache.bits == 2) return a.bf16 ? launch_instance<64, 2, true>(a, s) : launch_instance<64, 2, false>(a, s);
+        return a.bf16 ? launch_instance<64, 4, true>(a, s) : launch_instance<64, 4, false>(a, s);
+    }
+    if (a.cache.bits == 2) return a.bf16 ? launch_instance<128, 2, true>(a, s) : launch_instance<128, 2, false>(a, s);
+    return a.bf16 ? launch_instance<128, 4, true>(a, s) : launch_instance<128, 4, false>(a, s);
+}
+
+}  // namespace kvq

@@ -1103,18 +1103,21 @@ kvq_status kvq_paged_check_device(kvq_paged *h) {
 // ---------------------------------------------------------------------------
 namespace {
 
-// The table, as int32: offsets [B + 1], starts [B], read tiles before each slot [B + 1], blocks
+// The table, as int32: offsets [B + 1], starts [B], read tiles before each slot [B + 1], staged key and
+// query tiles before each slot [B + 1] each, blocks
 // [n_blocks][2] = (slot, block), and from a multiple of 4 on the attention's items [n_items][4] =
 // (slot, first query token, splits << 16 | split, first partial tile) and merges [n_merges][4] =
 // (slot, first query token, splits, first partial tile).
 struct ChunkLayout {
-    int64_t starts, tiles, blocks, items, merges, end;
+    int64_t starts, tiles, kv_tiles, q_tiles, blocks, items, merges, end;
 };
 ChunkLayout chunk_layout(int64_t B, int64_t n_blocks, int64_t n_items, int64_t n_merges) {
     ChunkLayout l;
     l.starts = B + 1;
     l.tiles = l.starts + B;
-    l.blocks = l.tiles + B + 1;
+    l.kv_tiles = l.tiles + B + 1;
+    l.q_tiles = l.kv_tiles + B + 1;
+    l.blocks = l.q_tiles + B + 1;
     l.items = (l.blocks + 2 * n_blocks + 3) / 4 * 4;
     l.merges = l.items + 4 * n_items;
     l.end = l.merges + 4 * n_merges;
@@ -1131,6 +1134,7 @@ struct Piece {
     int32_t slot, q0;
     int64_t tiles;
     bool one_tile;               // its rows fill at most one query tile
+    bool wide;                   // of a slot whose tiles are staged
     int32_t splits;
 };
 
@@ -1157,7 +1161,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         return fail(KVQ_ERR_UNSUPPORTED, "at most 128 query heads per kv head (got %d)", q_heads / kv_heads);
     // a CTA's two query tiles of 128 rows: tokens x the query heads of one kv head
     const int64_t tile_tokens = 128 / (q_heads / kv_heads);
-    int64_t tokens = 0, blocks = 0, tiles = 0, n_pieces = 0;
+    int64_t tokens = 0, blocks = 0, tiles = 0, n_pieces = 0, kv_tiles = 0, q_tiles = 0;
     for (int b = 0; b < batch; ++b) {
         const int64_t n = counts[b], s = starts ? starts[b] : 0;
         if (n < 0 || s < 0 || s + n > kMaxTokens)
@@ -1169,8 +1173,14 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         if (R > 0) {
             blocks += (s + n) / R - s / R;
             tiles += (s + n + 15) / 16 - s / 16;
+            if (n > tile_tokens) {
+                kv_tiles += (s + n + 127) / 128;
+                q_tiles += (n + tile_tokens - 1) / tile_tokens;
+            }
         }
     }
+    if ((kv_tiles + q_tiles) * kv_heads > kMaxInt)
+        return fail(KVQ_ERR_INVALID_ARG, "too many tokens for one chunk (%lld)", static_cast<long long>(tokens));
     if (tokens * q_heads > kMaxInt || n_pieces * kv_heads > kMaxInt || tiles * kv_heads > kMaxInt || blocks > kMaxInt / 4)
         return fail(KVQ_ERR_INVALID_ARG, "too many tokens for one chunk (%lld)", static_cast<long long>(tokens));
     std::vector<Piece> pieces;
@@ -1179,17 +1189,20 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         const int64_t n = counts[b], s = starts ? starts[b] : 0;
         for (int64_t i = 0; i < n; i += 2 * tile_tokens) {
             const int64_t last = i + 2 * tile_tokens < n ? i + 2 * tile_tokens : n;
-            pieces.push_back({b, static_cast<int32_t>(i), (s + last + 127) / 128, last - i <= tile_tokens, 1});
+            pieces.push_back({b, static_cast<int32_t>(i), (s + last + 127) / 128, last - i <= tile_tokens,
+                              R > 0 && n > tile_tokens, 1});
         }
     }
     if (R > 0) split_pieces(pieces, kv_heads, num_sms);
     // the longest first, so that the last CTAs to start are short
     std::stable_sort(pieces.begin(), pieces.end(), [](const Piece &x, const Piece &y) {
+        if (x.wide != y.wide) return x.wide;
         return x.tiles * y.splits > y.tiles * x.splits;
     });
-    int64_t items = 0, merges = 0, parts = 0;
+    int64_t items = 0, wide = 0, merges = 0, parts = 0;
     for (const Piece &p : pieces) {
         items += p.splits;
+        wide += p.wide ? p.splits : 0;
         merges += p.splits > 1;
         parts += p.splits > 1 ? p.splits * (p.one_tile ? 1 : 2) : 0;
     }
@@ -1207,21 +1220,31 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     out->items = static_cast<int32_t>(items);
     out->merges = static_cast<int32_t>(merges);
     out->part_tiles = static_cast<int32_t>(parts);
+    out->wide_items = static_cast<int32_t>(wide);
+    out->kv_tiles = static_cast<int32_t>(kv_tiles);
+    out->q_tiles = static_cast<int32_t>(q_tiles);
     out->tokens = tokens;
     out->table_bytes = static_cast<size_t>(l.end) * sizeof(int32_t);
-    out->workspace = static_cast<size_t>(parts) * kv_heads * 128 * (d + 2) * sizeof(float);
+    out->workspace = static_cast<size_t>(parts) * kv_heads * 128 * (d + 2) * sizeof(float) +
+                     static_cast<size_t>(kvq::staged_bytes(kv_tiles, q_tiles, kv_heads, d));
     out->counts = counts;
     out->starts = starts;
     if (!table) return ok();
     if (table_bytes < out->table_bytes)
         return fail(KVQ_ERR_INVALID_ARG, "the table needs %zu bytes, got %zu", out->table_bytes, table_bytes);
     int32_t *t = static_cast<int32_t *>(table), *blk = t + l.blocks;
-    int32_t row = 0, tile = 0;
+    int32_t row = 0, tile = 0, kv = 0, qt = 0;
     for (int b = 0; b < batch; ++b) {
         const int64_t n = counts[b], s = starts ? starts[b] : 0;
         t[b] = row;
         t[l.starts + b] = static_cast<int32_t>(s);
         t[l.tiles + b] = tile;
+        t[l.kv_tiles + b] = kv;
+        t[l.q_tiles + b] = qt;
+        if (R > 0 && n > tile_tokens) {
+            kv += static_cast<int32_t>((s + n + 127) / 128);
+            qt += static_cast<int32_t>((n + tile_tokens - 1) / tile_tokens);
+        }
         row += static_cast<int32_t>(n);
         if (R == 0 || n == 0) continue;
         tile += static_cast<int32_t>((s + n + 15) / 16 - s / 16);
@@ -1232,6 +1255,8 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     }
     t[batch] = row;
     t[l.tiles + batch] = tile;
+    t[l.kv_tiles + batch] = kv;
+    t[l.q_tiles + batch] = qt;
     while (blk < t + l.items) *blk++ = 0;
     int32_t *it = t + l.items, *mg = t + l.merges, part = 0;
     for (const Piece &p : pieces) {
@@ -1258,6 +1283,11 @@ kvq::ChunkTable chunk_table(const kvq_chunk *p) {
     t.n_items = p->items;
     t.merges = reinterpret_cast<const int4 *>(p->table + l.merges);
     t.n_merges = p->merges;
+    t.kv_tiles = p->table + l.kv_tiles;
+    t.q_tiles = p->table + l.q_tiles;
+    t.n_wide = p->wide_items;
+    t.n_kv_tiles = p->kv_tiles;
+    t.n_q_tiles = p->q_tiles;
     t.n_blocks = p->blocks;
     t.n_tiles = p->read_tiles;
     t.tokens = p->tokens;
@@ -1485,12 +1515,17 @@ kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const 
     kvq::AttendArgs a = attend_args(plan, q, o, h->base.cfg.dtype == KVQ_BF16);
     a.cache = paged_view(h);
     a.part_tiles = plan->part_tiles;
-    a.part_o = static_cast<float *>(workspace);
+    a.staged = static_cast<unsigned char *>(workspace);
+    a.part_o = reinterpret_cast<float *>(
+        a.staged + kvq::staged_bytes(plan->kv_tiles, plan->q_tiles, plan->kv_heads, plan->head_dim));
     a.part_ml = a.part_o + static_cast<int64_t>(plan->part_tiles) * plan->kv_heads * 128 * plan->head_dim;
     for (int b = 0; b < plan->batch; ++b)
         if (plan->counts[b] > a.most_tokens) a.most_tokens = plan->counts[b];
     a.status = a.cache.status;
-    const cudaError_t e = kvq::launch_attend_cache(a, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = kvq::launch_attend_wide(a, s);
+    if (e == cudaSuccess) e = kvq::launch_attend_narrow(a, s);
+    if (e == cudaSuccess) e = kvq::launch_merge_splits(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
     return ok();
 }

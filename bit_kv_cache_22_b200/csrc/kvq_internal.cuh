@@ -56,7 +56,9 @@ struct ChunkTable {
     const int4 *items;           // [n_items] attention work: slot, first query token, splits << 16 | split,
                                  // first partial tile of the item's splits
     const int4 *merges;          // [n_merges] items in splits: slot, first query token, splits, first partial tile
+    const int32_t *kv_tiles, *q_tiles;   // [B + 1]: staged key and query tiles of the slots before
     int n_blocks, n_tiles, n_items, n_merges;
+    int n_wide, n_kv_tiles, n_q_tiles;   // the first n_wide items have their tiles staged
     int64_t tokens;
     int B;
 };
@@ -254,9 +256,14 @@ struct AttendArgs {
     // [part_tiles][Hkv][2][128]
     float *part_o, *part_ml;
     int64_t part_tiles;
+    unsigned char *staged;       // staged_bytes: operand tiles of the wide slots
     unsigned int *status;        // or NULL
 };
-cudaError_t launch_attend_cache(const AttendArgs &a, cudaStream_t s);
+// Over the cache: slots of at most one query tile, slots of more, and the joining of splits.
+cudaError_t launch_attend_narrow(const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_attend_wide(const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_merge_splits(const AttendArgs &a, cudaStream_t s);
+int64_t staged_bytes(int64_t kv_tiles, int64_t q_tiles, int kv_heads, int d);
 cudaError_t launch_attend_prompt(const AttendArgs &a, cudaStream_t s);
 
 // The compute capability the library's kernels were compiled for (major * 10 + minor, as

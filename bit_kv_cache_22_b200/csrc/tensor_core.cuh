@@ -81,6 +81,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x
         : "memory");
 }
 
+// size: a multiple of 16, both addresses on 16 bytes
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t size, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(size), "r"(bar)
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ tensor memory
 
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns) {   // one warp

@@ -85,7 +85,8 @@ class Chunk(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("residual", ctypes.c_int32), ("blocks", ctypes.c_int32),
                 ("read_tiles", ctypes.c_int32), ("items", ctypes.c_int32), ("merges", ctypes.c_int32),
-                ("part_tiles", ctypes.c_int32), ("tokens", ctypes.c_int64), ("table_bytes", ctypes.c_size_t),
+                ("part_tiles", ctypes.c_int32), ("wide_items", ctypes.c_int32), ("kv_tiles", ctypes.c_int32),
+                ("q_tiles", ctypes.c_int32), ("reserved", ctypes.c_int32), ("tokens", ctypes.c_int64), ("table_bytes", ctypes.c_size_t),
                 ("workspace", ctypes.c_size_t), ("counts", ctypes.c_void_p), ("starts", ctypes.c_void_p),
                 ("table", ctypes.c_void_p)]
 

@@ -470,6 +470,10 @@ typedef struct {
     int32_t items;           /* pieces of work of the attention calls                       */
     int32_t merges;          /* ... of which these many are joined from splits              */
     int32_t part_tiles;      /* partial results of the splits                               */
+    int32_t wide_items;      /* items whose slots' tiles are unpacked first, ...            */
+    int32_t kv_tiles;        /* ... key tiles of 128 tokens                                 */
+    int32_t q_tiles;         /* ... and query tiles                                         */
+    int32_t reserved;
     int64_t tokens;          /* packed rows: the sum of counts                              */
     size_t table_bytes;      /* size of the table                                           */
     size_t workspace;        /* scratch of kvq_paged_chunk_attention (may be 0)             */

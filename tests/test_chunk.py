@@ -43,7 +43,12 @@ def test_table_of_random_plans():
         assert t[2 * B + 1:3 * B + 2] == [sum(tiles[:b]) for b in range(B + 1)] and out.read_tiles == sum(tiles)
         blocks = [(b, i) for b in range(B) if counts[b]
                   for i in range(starts[b] // R, (starts[b] + counts[b]) // R)]
-        at = 3 * B + 2
+        wide = [n > 32 for n in counts]             # more than one query tile of 128 rows: 4 heads a token
+        kv = [-(-(s + n) // 128) * w for s, n, w in zip(starts, counts, wide)]
+        q = [-(-n // 32) * w for n, w in zip(counts, wide)]
+        assert t[3 * B + 2:4 * B + 3] == [sum(kv[:b]) for b in range(B + 1)] and out.kv_tiles == sum(kv)
+        assert t[4 * B + 3:5 * B + 4] == [sum(q[:b]) for b in range(B + 1)] and out.q_tiles == sum(q)
+        at = 5 * B + 4
         assert [tuple(t[at + 2 * i:at + 2 * i + 2]) for i in range(out.blocks)] == blocks and out.blocks == len(blocks)
         at = -(-(at + 2 * out.blocks) // 4) * 4
         items = [tuple(t[i:i + 4]) for i in range(at, at + 4 * out.items, 4)]
@@ -59,9 +64,15 @@ def test_table_of_random_plans():
         for b, i, n, at_part in merges:
             assert at_part == part
             part += n * (1 if counts[b] - i <= 32 else 2)
-        assert part == out.part_tiles and out.workspace == part * 2 * 128 * 130 * 4
+        assert part == out.part_tiles
+        assert out.workspace == 2 * (part * 128 * 130 * 4 + sum(kv) * (2 * 32768 + 64) + sum(q) * (32768 + 512))
+        n_wide = sum(n for b, _, n, _ in pieces if wide[b])
+        assert out.wide_items == n_wide and all(wide[i[0]] == (k < n_wide) for k, i in enumerate(items))
         share = [-(-(starts[b] + min(i + 64, counts[b])) // 128) / n for b, i, n, _ in pieces]
-        assert share == sorted(share, reverse=True)
+        of_wide = [wide[b] for b, _, _, _ in pieces]
+        for w in (True, False):                     # the longest first, the wide slots' before the others
+            part = [x for x, y in zip(share, of_wide) if y == w]
+            assert part == sorted(part, reverse=True)
 
 
 def test_a_long_sequence_is_split_over_the_gpu():
