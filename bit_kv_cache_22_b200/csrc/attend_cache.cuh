@@ -184,15 +184,18 @@ __device__ __forceinline__ bool prepare16(const Fetched<D, N> &f, const PagedVie
             if (has_v) bv = fmaxf(bv, sv[e] * fmaxf(fabsf(zv[e]), fabsf(kTop - zv[e])));
         }
     } else if (f.kind == 2) {
-#pragma unroll 1
-        for (int i = lane; i < 16 * D / 2; i += 32) {
-            const int tk = tok + i / (D / 2);
-            if (tk < len) {
-                const int64_t at = static_cast<int64_t>(tk - tq) * (D / 2) + i % (D / 2);
-                const float2 x = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(res_k)[at]);
-                const float2 y = widen_pair<BF16>(reinterpret_cast<const uint32_t *>(res_v)[at]);
-                bk = fmaxf(bk, fmaxf(fabsf(x.x), fabsf(x.y)));
-                bv = fmaxf(bv, fmaxf(fabsf(y.x), fabsf(y.y)));
+#pragma unroll 4
+        for (int i = lane; i < 16 * (D / 8); i += 32) {    // rows of one token are D / 8 vectors
+            const bool on = tok + i / (D / 8) < len;
+            const int64_t at = static_cast<int64_t>(tok - tq) * (D / 8) + i;
+            const uint4 x = on ? reinterpret_cast<const uint4 *>(res_k)[at] : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 y = on ? reinterpret_cast<const uint4 *>(res_v)[at] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 p = widen_pair<BF16>(xw[e]), q = widen_pair<BF16>(yw[e]);
+                bk = fmaxf(bk, fmaxf(fabsf(p.x), fabsf(p.y)));
+                bv = fmaxf(bv, fmaxf(fabsf(q.x), fabsf(q.y)));
             }
         }
     }
@@ -311,7 +314,7 @@ __device__ __forceinline__ void emit16(int kv, uint32_t (&words)[D * N / 64], in
             put(offset(i / 2) + 1024 * (i % 2), x.x, x.y);
         }
     } else if (kv == 0) {
-#pragma unroll 1
+#pragma unroll 4
         for (int i = lane; i < 16 * (D / 8); i += 32) {
             const int r = i / (D / 8), v = i % (D / 8), rm = mixed(r);
             uint32_t o[4] = {0u, 0u, 0u, 0u};
@@ -328,7 +331,7 @@ __device__ __forceinline__ void emit16(int kv, uint32_t (&words)[D * N / 64], in
             put(tile + (v / 8) * (kRows * 128) + rm * 128 + (((v % 8) ^ (rm & 7)) << 4), o);
         }
     } else {
-#pragma unroll 1
+#pragma unroll 2
         for (int i = lane; i < D; i += 32) {       // channels 2 cp, 2 cp + 1: 8 of the 16 tokens
             const int cp = i >> 1, part = i & 1;
             uint32_t o[2][4];

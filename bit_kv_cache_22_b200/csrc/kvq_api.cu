@@ -1138,19 +1138,29 @@ struct Piece {
     int32_t splits;
 };
 
-// Splits of the pieces over their keys: a CTA's share is at most `share` key tiles.  The shares
-// of all SMs even out when each SM gets several; a CTA's start and end cost a few tiles' time, so a
-// share is not below kMinShare.
-constexpr int64_t kMinShare = 16, kSharesPerSm = 4;
+// Splits of the pieces over their keys, of the narrow and the wide slots apart (they are launches of
+// their own): a CTA's share is at most `share` key tiles.  A CTA's start and end cost a few tiles'
+// time (and a wide piece's partial results 128 KB a split), so a share is not below its least, and
+// pieces that give every SM a CTA or more are left whole when they are wide.
+constexpr int64_t kMinShare = 16, kSharesPerSm = 4, kMinWideShare = 24;
 
 void split_pieces(std::vector<Piece> &pieces, int32_t kv_heads, int32_t num_sms) {
-    int64_t total = 0;
-    for (const Piece &p : pieces) total += p.tiles * kv_heads;
-    int64_t share = (total + num_sms * kSharesPerSm - 1) / (num_sms * kSharesPerSm);
-    if (share < kMinShare) share = kMinShare;
-    for (Piece &p : pieces) {
-        int64_t n = (p.tiles + share - 1) / share;
-        p.splits = static_cast<int32_t>(n < 1 ? 1 : n > 1024 ? 1024 : n);
+    for (const bool wide : {false, true}) {
+        int64_t total = 0, n = 0;
+        for (const Piece &p : pieces)
+            if (p.wide == wide) {
+                total += p.tiles * kv_heads;
+                n += kv_heads;
+            }
+        if (n == 0 || (wide && n >= num_sms)) continue;
+        const int64_t shares = num_sms * (wide ? 1 : kSharesPerSm), least = wide ? kMinWideShare : kMinShare;
+        int64_t share = (total + shares - 1) / shares;
+        if (share < least) share = least;
+        for (Piece &p : pieces)
+            if (p.wide == wide) {
+                const int64_t k = (p.tiles + share - 1) / share;
+                p.splits = static_cast<int32_t>(k < 1 ? 1 : k > 1024 ? 1024 : k);
+            }
     }
 }
 
