@@ -22,7 +22,8 @@
 //
 // Unpacking is bound by the integer pipe, so codes stay in 16-bit pairs: bytes 0 and 2 (1 and 3) of a
 // word's slot, OR 0x6400, are the fp16 numbers 1024 + code; minus (1024 + z), exact for |z| <= 1024,
-// times s in two fp16 parts.  Within each four channels of keys (and queries) and each four
+// times s -- in fp16 caches in two fp16 parts, lest s's own rounding double the element's; next to a
+// bf16 output it is an eighth of a rounding and s goes as one.  Within each four channels of keys (and queries) and each four
 // tokens the order in the operands is 0, 2, 1, 3, as the pairs come.
 #pragma once
 
@@ -71,17 +72,20 @@ __host__ __device__ constexpr int mixed(int i) { return (i & ~3) | ((i & 1) << 1
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 __device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
 
-// The parameters of four elements, in pairs (0, 2) and (1, 3): -(1024 + z), and s in two parts.
+// The parameters of four elements, in pairs (0, 2) and (1, 3): -(1024 + z), and s in two parts (the
+// second in fp16 caches only).
 struct Quad {
     uint2 z, hi, lo;
 };
 
 // Four codes of N bits in the bytes of b (above them anything): (code - z) s.
-template <int N>
+template <int N, bool BF16>
 __device__ __forceinline__ uint2 unpack_four(uint32_t b, const Quad &q) {
     constexpr uint32_t kMask = 0x00010001u * ((1u << N) - 1);
     const __half2 x = __hadd2(as_half2((b & kMask) | 0x64006400u), as_half2(q.z.x));
     const __half2 y = __hadd2(as_half2(((b >> 8) & kMask) | 0x64006400u), as_half2(q.z.y));
+    if constexpr (BF16)
+        return make_uint2(as_bits(__hmul2(x, as_half2(q.hi.x))), as_bits(__hmul2(y, as_half2(q.hi.y))));
     return make_uint2(as_bits(__hfma2(x, as_half2(q.hi.x), __hmul2(x, as_half2(q.lo.x)))),
                       as_bits(__hfma2(y, as_half2(q.hi.y), __hmul2(y, as_half2(q.lo.y)))));
 }
@@ -92,6 +96,19 @@ __device__ __forceinline__ uint2 unpack_four_wide(uint32_t b, const float4 &s, c
     const float2 y = tc::mul2(tc::add2(make_float2(byte_plus_2_23<1>(b), byte_plus_2_23<3>(b)), make_float2(z.y, z.w)),
                               make_float2(s.y, s.w));
     return make_uint2(half2_bits(x.x, x.y), half2_bits(y.x, y.y));
+}
+
+// f(0) .. f(n - 1), the numbers known when compiling
+template <int I>
+struct Number {
+    static constexpr int value = I;
+};
+template <int Count, int I = 0, class F>
+__device__ __forceinline__ void static_for(const F &f) {
+    if constexpr (I < Count) {
+        f(Number<I>{});
+        static_for<Count, I + 1>(f);
+    }
 }
 
 // What one unpacking warp needs of a tile's 16 tokens: the code words of its lanes, and four
@@ -222,7 +239,9 @@ __device__ __forceinline__ bool prepare16(const Fetched<D, N> &f, const PagedVie
             km[lane] = make_uint2(half2_bits(-1024.0f - zk[0], -1024.0f - zk[2]),
                                   half2_bits(-1024.0f - zk[1], -1024.0f - zk[3]));
             km[D / 4 + lane] = make_uint2(half2_bits(hi[0], hi[2]), half2_bits(hi[1], hi[3]));
-            km[D / 2 + lane] = make_uint2(half2_bits(sk[0] - hi[0], sk[2] - hi[2]), half2_bits(sk[1] - hi[1], sk[3] - hi[3]));
+            if (!BF16)
+                km[D / 2 + lane] =
+                    make_uint2(half2_bits(sk[0] - hi[0], sk[2] - hi[2]), half2_bits(sk[1] - hi[1], sk[3] - hi[3]));
         }
         if (has_v) {
 #pragma unroll
@@ -231,7 +250,7 @@ __device__ __forceinline__ bool prepare16(const Fetched<D, N> &f, const PagedVie
                 const __half hi = __float2half_rn(sv[e]);
                 vm[at] = __half_as_ushort(__float2half_rn(-1024.0f - zv[e]));
                 vm[128 + at] = __half_as_ushort(hi);
-                vm[256 + at] = __half_as_ushort(__float2half_rn(sv[e] - __half2float(hi)));
+                if (!BF16) vm[256 + at] = __half_as_ushort(__float2half_rn(sv[e] - __half2float(hi)));
             }
         }
     } else {
@@ -255,65 +274,58 @@ __device__ __forceinline__ bool prepare16(const Fetched<D, N> &f, const PagedVie
     return !wide;
 }
 
-// The 16 tokens (warp w of a key tile's eight) as operands.  kv 0: keys, rows = tokens, channels along
-// a row; kv 1: values, rows = channels, tokens along a row.  put(offset, a, b) stores 8 bytes of the
-// tile, put(offset, v) 16.  words: the tokens' code words, used up.
-template <int D, int N, bool BF16, class Put>
-__device__ __forceinline__ void emit16(int kv, uint32_t (&words)[D * N / 64], int kind, bool narrow, const PagedView &c,
+// The 16 tokens (warp w of a key tile's eight) as operands.  KV 0: keys, rows = tokens, channels along
+// a row; KV 1: values, rows = channels, tokens along a row.  put.at<I>(offset, a, b) stores 8 bytes of
+// the tile at offset + I, put(offset, v) 16.
+template <int D, int N, bool BF16, int KV, class Put>
+__device__ __forceinline__ void emit16(const uint32_t (&words)[D * N / 64], int kind, bool narrow, const PagedView &c,
                                        const uint16_t *res, int tok, int len, int tq, float down, int w, int lane,
                                        const unsigned char *meta, const Put &put) {
-    constexpr int B = 4 / N, W = D * N / 64;
-    const int tile = kv ? (w / 4) * (D * 128) : 16 * w * 128;
+    constexpr int B = 4 / N;
+    const int tile = KV ? (w / 4) * (D * 128) : 16 * w * 128;
     // lane's row (+ 8 in a second store): a key's is its token, in mixed order, a value's its channel;
     // 8 bytes of a 32-byte step along it, swizzled
-    const int row = kv ? lane >> 2 : mixed(lane >> 2);
+    const int row = KV ? lane >> 2 : mixed(lane >> 2);
     const int place = row * 128 + (lane & 1) * 8, col = (((lane & 3) >> 1) ^ (row & 7)) << 4;
-    auto offset = [&](int ch) {                    // of chunk ch (16 channels)
-        return kv ? tile + ch * 2048 + place + (col ^ ((w % 4) << 5))
-                  : tile + (ch / 4) * (kRows * 128) + place + (col ^ ((ch % 4) << 5));
-    };
-    const int shift = kv ? __ffs(c.Gv) - 5 : 0;    // chunk -> group of parameters
-    if (kind == 1 && narrow) {
-        // two chunks at a time; the parameters of the next two are loaded before their stores
-        const uint2 *pm = reinterpret_cast<const uint2 *>(meta + (kv ? 3 * D * 2 : 0)) + (lane & 3);
-        const int next = kv ? 32 : D / 4;          // from z to hi to lo
-        auto quad = [&](int ch) {
-            const uint2 *at = pm + 4 * (ch >> shift);
-            return Quad{at[0], at[next], at[2 * next]};
-        };
-        Quad q0 = quad(0), q1 = quad(1);
-#pragma unroll 1
-        for (int ch = 0; ch < D / 16; ch += 2) {
-            const int more = ch + 2 < D / 16 ? ch + 2 : 0;
-            const Quad n0 = quad(more), n1 = quad(more + 1);
-            const uint32_t b0 = words[0], b1 = N == 2 ? b0 >> 4 : words[2 / B - 1];
+    // chunk ch (16 channels): a value's rows are its channels; a key's chunk is a step of its rows
+    int at[KV ? 1 : 4];
 #pragma unroll
-            for (int i = 0; i + 2 / B < W; ++i) words[i] = words[i + 2 / B];   // the words move up
-            const int d0 = offset(ch), d1 = kv ? d0 + 2048 : d0 ^ 32;
-            const uint2 x0 = unpack_four<N>(b0, q0), y0 = unpack_four<N>(b0 >> N, q0);
-            const uint2 x1 = unpack_four<N>(b1, q1), y1 = unpack_four<N>(b1 >> N, q1);
-            put(d0, x0.x, x0.y);
-            put(d0 + 1024, y0.x, y0.y);
-            put(d1, x1.x, x1.y);
-            put(d1 + 1024, y1.x, y1.y);
-            q0 = n0;
-            q1 = n1;
-        }
+    for (int x = 0; x < (KV ? 1 : 4); ++x) at[x] = tile + place + (col ^ ((KV ? w % 4 : x) << 5));
+    constexpr int kNext = KV ? 32 : D / 4;         // from z to hi to lo; in fp32 from s to z
+    if (kind == 1 && narrow) {
+        const uint2 *pm = reinterpret_cast<const uint2 *>(meta + (KV ? 3 * D * 2 : 0)) + (lane & 3);
+        const int shift = KV ? __ffs(c.Gv) - 5 : 0;            // chunk -> group of parameters
+        auto quad = [&](int ch) {
+            const uint2 *from = pm + 4 * (ch >> shift);
+            return Quad{from[0], from[kNext], BF16 ? make_uint2(0u, 0u) : from[2 * kNext]};
+        };
+        Quad q = quad(0);
+        static_for<D / 16>([&](auto ci) {          // the next chunk's parameters before this one's stores
+            constexpr int ch = decltype(ci)::value;
+            Quad q1 = q;
+            if constexpr (ch + 1 < D / 16) q1 = quad(ch + 1);
+            const uint32_t b = words[ch / B] >> (N * 2 * (ch % B));
+            const uint2 x = unpack_four<N, BF16>(b, q), y = unpack_four<N, BF16>(b >> N, q);
+            constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128);
+            put.template at<I>(at[KV ? 0 : ch % 4], x.x, x.y);
+            put.template at<I + 1024>(at[KV ? 0 : ch % 4], y.x, y.y);
+            q = q1;
+        });
     } else if (kind == 1) {
         constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
-        const float4 *pm = reinterpret_cast<const float4 *>(meta) + (kv ? 2 * D / 4 : 0) + (lane & 3);
-        const int next = kv ? 32 : D / 4;          // from s to z
-#pragma unroll 1
-        for (int i = 0; i < D / 8; ++i) {          // chunk i / 2, row half i % 2
-            const uint32_t b = (words[0] >> (N * (i % (2 * B)))) & kMask;
-            if (i % (2 * B) == 2 * B - 1)
-#pragma unroll
-                for (int k = 0; k + 1 < W; ++k) words[k] = words[k + 1];
-            const float4 *at = pm + 4 * ((i / 2) >> shift);
-            const uint2 x = unpack_four_wide(b, at[0], at[next]);
-            put(offset(i / 2) + 1024 * (i % 2), x.x, x.y);
-        }
-    } else if (kv == 0) {
+        const float4 *pm = reinterpret_cast<const float4 *>(meta) + (KV ? 2 * D / 4 : 0) + (lane & 3);
+        const int shift = KV ? __ffs(c.Gv) - 5 : 0;
+        static_for<D / 16>([&](auto ci) {
+            constexpr int ch = decltype(ci)::value;
+            constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128);
+            const float4 *from = pm + 4 * (ch >> shift);
+            const float4 sc = from[0], z = from[kNext];
+            const uint32_t b = words[ch / B] >> (N * 2 * (ch % B));
+            const uint2 x = unpack_four_wide(b & kMask, sc, z), y = unpack_four_wide((b >> N) & kMask, sc, z);
+            put.template at<I>(at[KV ? 0 : ch % 4], x.x, x.y);
+            put.template at<I + 1024>(at[KV ? 0 : ch % 4], y.x, y.y);
+        });
+    } else if constexpr (KV == 0) {
 #pragma unroll 4
         for (int i = lane; i < 16 * (D / 8); i += 32) {
             const int r = i / (D / 8), v = i % (D / 8), rm = mixed(r);
@@ -359,7 +371,7 @@ __device__ __forceinline__ void emit16(int kv, uint32_t (&words)[D * N / 64], in
 }
 
 // Query rows r (tokens x heads) of a tile as operands, by warp w of n_warps: four channels a lane,
-// kBatch rows of loads in flight.  row(r) is a row's elements, or NULL; put(offset, a, b) as above;
+// kBatch rows of loads in flight.  row(r) is a row's elements, or NULL; put.at(offset, a, b) as above;
 // put_scale(r, 2^e).
 template <int D, bool BF16, class Row, class Put, class PutScale>
 __device__ __forceinline__ void emit_queries(int rows, int w, int n_warps, int lane, const Row &row, const Put &put,
@@ -386,7 +398,7 @@ __device__ __forceinline__ void emit_queries(int rows, int w, int n_warps, int l
             const float down = pow2(-ex);
             if (r >= rows) continue;
             if (col == 0) put_scale(r, pow2(ex));
-            put((col / 64) * (kRows * 128) + r * 128 + ((((col % 64) / 8) ^ (r & 7)) << 4) + (col % 8) * 2,
+            put.template at<0>((col / 64) * (kRows * 128) + r * 128 + ((((col % 64) / 8) ^ (r & 7)) << 4) + (col % 8) * 2,
                 half2_bits(p.x * down, q.x * down), half2_bits(p.y * down, q.y * down));
         }
     }

@@ -19,8 +19,9 @@ constexpr int kThreads = 640;
 
 struct SharedPut {
     uint32_t tile;
-    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
-        tc::store_shared(tile + offset, x, y);
+    template <int I>
+    __device__ __forceinline__ void at(int offset, uint32_t x, uint32_t y) const {
+        tc::store_shared<I>(tile + offset, x, y);
     }
     __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const { tc::store_shared(tile + offset, v); }
 };
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
                     if (r >= hg * tpt || tok >= count) return nullptr;
                     return a.q.p + static_cast<int64_t>(first + tok) * a.q.ts + static_cast<int64_t>(h * hg + r % hg) * a.q.hs;
                 },
-                [&](int offset, uint32_t x, uint32_t y) { tc::store_shared(base + L::q + offset, x, y); },
+                SharedPut{base + L::q},
                 [&](int r, float scale) { reinterpret_cast<float *>(smem + L::row_scale)[r] = scale; });
             tc::fence_async_proxy();
             __syncwarp();
@@ -119,33 +120,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
             int ek;
             const bool narrow =
                 prepare16<D, N, BF16>(f, c, residual(c.kr), residual(c.vr), tok, len, tq, lane, meta, ek, ev);
-            uint32_t words[2][W];
+            uint32_t kw[W], vw[W];
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                words[0][i] = f.kw[i];
-                words[1][i] = f.vw[i];
+                kw[i] = f.kw[i];
+                vw[i] = f.vw[i];
             }
             fetch16<D, N>(f, c, work.h, page, at_tok, tok + kRows, len, tq, j + 1 < n, lane);
             advance();
             page = page_at(j + 2, at_page);
-            // keys, then values, by the same code: the kernel's instructions have to stay in the SM's cache
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-                if (j >= kStages) go = tc::bar_wait_warp(bar((kv ? kVEmpty : kKEmpty) + s), phase ^ 1, &gave_up);
-                if (!go) break;
-                if (kv == 0 && lane == 0) {
-                    exps[j % kExps].scale_k[w] = pow2(ek);
-                    exps[j % kExps].exp_v[w] = ev;
-                }
-                const uint32_t tile = base + (kv ? L::v : L::k) + s * L::kTileBytes;
-                emit16<D, N, BF16>(kv, words[0], kind, narrow, c, residual(kv ? c.vr : c.kr), tok, len, tq,
-                                   pow2(kv ? -ev : -ek), w, lane, meta, SharedPut{tile});
-#pragma unroll
-                for (int i = 0; i < W; ++i) words[0][i] = words[1][i];
-                tc::fence_async_proxy();
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(bar((kv ? kVFull : kKFull) + s));
+            if (j >= kStages) go = tc::bar_wait_warp(bar(kKEmpty + s), phase ^ 1, &gave_up);
+            if (!go) break;
+            if (lane == 0) {
+                exps[j % kExps].scale_k[w] = pow2(ek);
+                exps[j % kExps].exp_v[w] = ev;
             }
+            emit16<D, N, BF16, 0>(kw, kind, narrow, c, residual(c.kr), tok, len, tq, pow2(-ek), w, lane, meta,
+                                  SharedPut{base + L::k + s * L::kTileBytes});
+            tc::fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(bar(kKFull + s));
+            if (j >= kStages) go = tc::bar_wait_warp(bar(kVEmpty + s), phase ^ 1, &gave_up);
+            if (!go) break;
+            emit16<D, N, BF16, 1>(vw, kind, narrow, c, residual(c.vr), tok, len, tq, pow2(-ev), w, lane, meta,
+                                  SharedPut{base + L::v + s * L::kTileBytes});
+            tc::fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(bar(kVFull + s));
         }
     } else if (warp >= 16) {
         tc::regs_give<64>();

@@ -48,8 +48,9 @@ struct Staged {
 
 struct GlobalPut {
     unsigned char *tile;
-    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
-        *reinterpret_cast<uint2 *>(tile + offset) = make_uint2(x, y);
+    template <int I>
+    __device__ __forceinline__ void at(int offset, uint32_t x, uint32_t y) const {
+        *reinterpret_cast<uint2 *>(tile + offset + I) = make_uint2(x, y);
     }
     __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const {
         *reinterpret_cast<uint4 *>(tile + offset) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -82,9 +83,9 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const AttendArgs a
             st.exps[at].exp_v[w] = ev;
         }
         unsigned char *tile = st.kv + at * 2 * Staged<D>::kTileBytes;
-        emit16<D, N, BF16>(0, f.kw, f.kind, narrow, c, c.kr + rows, tok, len, tq, pow2(-ek), w, lane, meta_s[w],
+        emit16<D, N, BF16, 0>(f.kw, f.kind, narrow, c, c.kr + rows, tok, len, tq, pow2(-ek), w, lane, meta_s[w],
                            GlobalPut{tile});
-        emit16<D, N, BF16>(1, f.vw, f.kind, narrow, c, c.vr + rows, tok, len, tq, pow2(-ev), w, lane, meta_s[w],
+        emit16<D, N, BF16, 1>(f.vw, f.kind, narrow, c, c.vr + rows, tok, len, tq, pow2(-ev), w, lane, meta_s[w],
                            GlobalPut{tile + Staged<D>::kTileBytes});
     } else {
         const int x = blockIdx.x - a.t.n_kv_tiles, slot = slot_of(a.t.q_tiles, a.t.B, x);
