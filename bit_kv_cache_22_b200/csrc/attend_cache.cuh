@@ -23,8 +23,13 @@
 // Unpacking is bound by the integer pipe, so codes stay in 16-bit pairs: bytes 0 and 2 (1 and 3) of a
 // word's slot, OR 0x6400, are the fp16 numbers 1024 + code; minus (1024 + z), exact for |z| <= 1024,
 // times s -- in fp16 caches in two fp16 parts, lest s's own rounding double the element's; next to a
-// bf16 output it is an eighth of a rounding and s goes as one.  Within each four channels of keys (and queries) and each four
-// tokens the order in the operands is 0, 2, 1, 3, as the pairs come.
+// bf16 output it is an eighth of a rounding and s goes as one.
+//
+// The order of channels in keys and queries, and of tokens in keys and values, is free as long as
+// both agree.  A lane unpacks four neighbouring channels (tokens) at a time, which lie in the operand as
+// 0, 2, 1, 3, as the pairs come; and of 64 channels (tokens) c, eight to a 16-byte step of a 128-byte
+// row, step c/16 + 4 ((c/8) mod 2) holds c's eight, so that the stores of a warp -- eight rows, four
+// lanes along each -- meet every bank once (in plain order each bank twice).
 #pragma once
 
 #include <cstdint>
@@ -38,7 +43,8 @@ namespace {
 
 constexpr int kRows = 128;                 // rows of a query tile, tokens of a key tile
 constexpr int kStages = 2;                 // key and value operand tiles, each
-constexpr int kUnpackWarps = 8;            // of 16 tokens each in a key tile
+constexpr int kUnits = 4;                  // of 32 tokens in a key tile: a warp's work for keys or values
+constexpr int kUnpackWarps = 2 * kUnits;
 constexpr int kExps = 8;                   // key tiles whose exponents are kept (at most kStages + 1 are live)
 constexpr int kValueStep = 4;              // values' exponents are multiples of this: they rarely differ
 constexpr float kLazyMax = 8.0f;           // the running maximum is raised when a logit passes it by this
@@ -68,6 +74,15 @@ __device__ __forceinline__ float byte_plus_2_23(uint32_t w) {
 
 // place of element i of four in an operand: 0, 2, 1, 3
 __host__ __device__ constexpr int mixed(int i) { return (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1); }
+// 16-byte step of 64 elements that holds the eight of element c
+__host__ __device__ constexpr int step_of(int c) { return (c / 16) % 4 + 4 * ((c / 8) % 2); }
+// the token of column c of a key tile, and the unit of 32 it is in
+__host__ __device__ constexpr int token_of(int c) {
+    return c / 64 * 64 + (c / 8) % 4 * 16 + (c / 32) % 2 * 8 + mixed(c % 8);
+}
+// 16 columns, number g from column 64 half on, are of one unit of 32 tokens
+__host__ __device__ constexpr int unit_of(int half, int g) { return 2 * (half + g / 4) + g % 2; }
+static_assert(step_of(token_of(77)) == 77 / 8 % 8 && mixed(token_of(77) % 8) == 77 % 8, "token_of inverts the places");
 
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 __device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
@@ -111,15 +126,17 @@ __device__ __forceinline__ void static_for(const F &f) {
     }
 }
 
-// What one unpacking warp needs of a tile's 16 tokens: the code words of its lanes, and four
-// scales and zeros a lane, which it spreads over shared memory.
+// What one unpacking warp needs of a unit's keys or values: the code words of its lanes, and scales
+// and zeros it spreads over shared memory -- keys: channels 4 lane .. of the halves' groups (one
+// group of 32 tokens or more: the first only); values: entries 4 lane .. and 128 + 4 lane .. of [32
+// tokens][D / Gv], as far as there are any.
 template <int D, int N>
 struct Fetched {
-    static constexpr int W = D * N / 64;   // words per lane
-    uint32_t kw[W], vw[W];
-    float4 ks, vs;                         // keys: channels 4 lane ...; values: entries 4 lane ... of
-    uint2 kz, vz;                          // [16 tokens][D / Gv], as far as there are any
-    int kind;                              // 0: no tokens, 1: quantized, 2: residual
+    static constexpr int W = D * N / 64;   // words per lane and half
+    uint32_t w[2][W];
+    float4 s[2];
+    uint2 z[2];
+    int kind[2];                           // of each 16 tokens; 0: none, 1: quantized, 2: residual
 };
 
 __device__ __forceinline__ void widen_zeros(uint2 z, bool sym, int half_levels, float (&f)[4]) {
@@ -129,144 +146,148 @@ __device__ __forceinline__ void widen_zeros(uint2 z, bool sym, int half_levels, 
     f[3] = static_cast<float>(sym ? half_levels : static_cast<int>(z.y) >> 16);
 }
 
-// The powers of two of a key tile, per 16 tokens: 2^e of the keys, then e of the values.
+// The powers of two of a key tile's units: 2^e of the keys, then e of the values.
 struct TileExps {
-    float scale_k[kUnpackWarps];
-    int exp_v[kUnpackWarps];
+    float scale_k[kUnits];
+    int exp_v[kUnits];
 };
 
-// Fetches the 16 tokens tok .. of a slot for kv head h; at_tok: the first one's place in its page.
-template <int D, int N>
-__device__ __forceinline__ void fetch16(Fetched<D, N> &f, const PagedView &c, int h, int page, int at_tok, int tok,
-                                        int len, int tq, bool on, int lane) {
+// Fetches the 32 tokens tok .. of a slot for kv head h (KV 0: keys, 1: values); at_tok: the first
+// one's place in its page.
+template <int D, int N, int KV>
+__device__ __forceinline__ void fetch_unit(Fetched<D, N> &f, const PagedView &c, int h, int page, int at_tok, int tok,
+                                           int len, int tq, bool on, int lane) {
     constexpr int W = D * N / 64, TW = D * N / 2;
-    f.kind = !on || tok >= len ? 0 : tok < tq ? 1 : 2;
-    if (f.kind != 1) return;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) f.kind[p] = !on || tok + 16 * p >= len ? 0 : tok + 16 * p < tq ? 1 : 2;
+    if (f.kind[0] != 1) return;
     if (page < 0 || page >= c.num_pages) {
         if (lane == 0) atomicOr(c.status, 2u);
         page = 0;
     }
     const int64_t slice = static_cast<int64_t>(page) * c.Hkv + h;
-    const int64_t words = (slice * (c.P >> 4) + (at_tok >> 4)) * TW + lane * W;
-    if constexpr (W >= 4) {
+    const uint32_t *words = (KV ? c.vc : c.kc) + (slice * (c.P >> 4) + (at_tok >> 4)) * TW + lane * W;
 #pragma unroll
-        for (int i = 0; i < W; i += 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(c.kc + words + i);
-            const uint4 y = *reinterpret_cast<const uint4 *>(c.vc + words + i);
-            f.kw[i] = x.x; f.kw[i + 1] = x.y; f.kw[i + 2] = x.z; f.kw[i + 3] = x.w;
-            f.vw[i] = y.x; f.vw[i + 1] = y.y; f.vw[i + 2] = y.z; f.vw[i + 3] = y.w;
+    for (int p = 0; p < 2; ++p) {                  // pages hold whole units: a half behind tq is read for nothing
+        if constexpr (W >= 4) {
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(words + p * TW + i);
+                f.w[p][i] = x.x; f.w[p][i + 1] = x.y; f.w[p][i + 2] = x.z; f.w[p][i + 3] = x.w;
+            }
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(words + p * TW);
+            f.w[p][0] = x.x; f.w[p][1] = x.y;
+        }
+    }
+    if constexpr (KV == 0) {
+        const int g_shift = __ffs(c.G) - 1;        // G, Gv: powers of two
+        const int64_t at = (slice * (c.P >> g_shift) + (at_tok >> g_shift)) * D + 4 * lane;
+        if (4 * lane < D) {
+            f.s[0] = *reinterpret_cast<const float4 *>(c.ks + at);
+            if (!c.sym) f.z[0] = *reinterpret_cast<const uint2 *>(c.kz + at);
+            if (c.G == 16) {
+                f.s[1] = *reinterpret_cast<const float4 *>(c.ks + at + D);
+                if (!c.sym) f.z[1] = *reinterpret_cast<const uint2 *>(c.kz + at + D);
+            }
         }
     } else {
-        const uint2 x = *reinterpret_cast<const uint2 *>(c.kc + words);
-        const uint2 y = *reinterpret_cast<const uint2 *>(c.vc + words);
-        f.kw[0] = x.x; f.kw[1] = x.y;
-        f.vw[0] = y.x; f.vw[1] = y.y;
-    }
-    const int g_shift = __ffs(c.G) - 1, ngv_shift = __ffs(D) - __ffs(c.Gv);      // powers of two
-    if (4 * lane < D) {
-        const int64_t km = (slice * (c.P >> g_shift) + (at_tok >> g_shift)) * D + 4 * lane;
-        f.ks = *reinterpret_cast<const float4 *>(c.ks + km);
-        if (!c.sym) f.kz = *reinterpret_cast<const uint2 *>(c.kz + km);
-    }
-    if (4 * lane < 16 << ngv_shift) {
-        const int64_t vm = ((slice * c.P + at_tok) << ngv_shift) + 4 * lane;
-        f.vs = *reinterpret_cast<const float4 *>(c.vs + vm);
-        if (!c.sym) f.vz = *reinterpret_cast<const uint2 *>(c.vz + vm);
+        const int ngv_shift = __ffs(D) - __ffs(c.Gv);
+        const int64_t at = ((slice * c.P + at_tok) << ngv_shift) + 4 * lane;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (4 * lane + 128 * x < 32 << ngv_shift) {
+                f.s[x] = *reinterpret_cast<const float4 *>(c.vs + at + 128 * x);
+                if (!c.sym) f.z[x] = *reinterpret_cast<const uint2 *>(c.vz + at + 128 * x);
+            }
     }
 }
 
-// A warp's 512 floats of shared memory for the parameters of its 16 tokens.
-template <int D>
-constexpr int kMetaBytes = (2 * D + 2 * 128) * 4;
+// A warp's shared memory for the parameters of its unit.
+constexpr int kMetaBytes = 2048;
 
-// The 16 tokens' powers of two (ek, and ev at least what it was), and their parameters spread over
-// shared memory for the lanes that use them; false: in fp32, for zeros that 1024 + z does not hold.
-// res_k, res_v: the slot's residual rows (token tq's first).
-template <int D, int N, bool BF16>
-__device__ __forceinline__ bool prepare16(const Fetched<D, N> &f, const PagedView &c, const uint16_t *res_k,
-                                          const uint16_t *res_v, int tok, int len, int tq, int lane,
-                                          unsigned char *meta, int &ek, int &ev) {
+// The unit's power of two e, and its parameters spread over shared memory for the lanes that use them;
+// false: in fp32, for zeros that 1024 + z does not hold.  res: the slot's residual rows (token
+// tq's first).
+//   keys: [half's group][z, hi, lo][D / 4] pairs of pairs; values: [z, hi, lo][D / Gv][32] halves, in mixed order
+//   in fp32: [s, z], keys [half's group][D], values [D / Gv][32]
+template <int D, int N, bool BF16, int KV>
+__device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const PagedView &c, const uint16_t *res, int tok,
+                                             int len, int tq, int lane, unsigned char *meta, int &ex) {
     constexpr float kTop = static_cast<float>((1 << N) - 1);
     const int ngv_shift = __ffs(D) - __ffs(c.Gv), ngv = 1 << ngv_shift;
-    float bk = 0.0f, bv = 0.0f;
-    float zk[4], zv[4];
-    const bool has_k = f.kind == 1 && 4 * lane < D, has_v = f.kind == 1 && 4 * lane < 16 << ngv_shift;
-    if (f.kind == 1) {
-        widen_zeros(f.kz, c.sym, 1 << (N - 1), zk);
-        widen_zeros(f.vz, c.sym, 1 << (N - 1), zv);
-        const float sk[4] = {f.ks.x, f.ks.y, f.ks.z, f.ks.w}, sv[4] = {f.vs.x, f.vs.y, f.vs.z, f.vs.w};
+    float big = 0.0f, z[2][4];
+    bool on[2], over = false;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        if constexpr (KV == 0) on[x] = 4 * lane < D && f.kind[x] == 1 && (x == 0 || c.G == 16);
+        else
+            on[x] = 4 * lane + 128 * x < 32 << ngv_shift &&
+                    ((4 * lane + 128 * x) >> (ngv_shift + 4) ? f.kind[1] : f.kind[0]) == 1;
+        if (!on[x]) continue;
+        widen_zeros(f.z[x], c.sym, 1 << (N - 1), z[x]);
+        const float s[4] = {f.s[x].x, f.s[x].y, f.s[x].z, f.s[x].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if (has_k) bk = fmaxf(bk, sk[e] * fmaxf(fabsf(zk[e]), fabsf(kTop - zk[e])));
-            if (has_v) bv = fmaxf(bv, sv[e] * fmaxf(fabsf(zv[e]), fabsf(kTop - zv[e])));
+            big = fmaxf(big, s[e] * fmaxf(fabsf(z[x][e]), fabsf(kTop - z[x][e])));
+            over = over || fabsf(z[x][e]) > 1024.0f;
         }
-    } else if (f.kind == 2) {
+    }
+    if (f.kind[0] == 2 || f.kind[1] == 2) {        // rows of one token are D / 8 vectors
+        const int from = max(tok, tq);
 #pragma unroll 4
-        for (int i = lane; i < 16 * (D / 8); i += 32) {    // rows of one token are D / 8 vectors
-            const bool on = tok + i / (D / 8) < len;
-            const int64_t at = static_cast<int64_t>(tok - tq) * (D / 8) + i;
-            const uint4 x = on ? reinterpret_cast<const uint4 *>(res_k)[at] : make_uint4(0u, 0u, 0u, 0u);
-            const uint4 y = on ? reinterpret_cast<const uint4 *>(res_v)[at] : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        for (int i = lane; i < 32 * (D / 8); i += 32) {
+            const int tk = tok + i / (D / 8);
+            if (tk < from || tk >= len) continue;
+            const uint4 v = reinterpret_cast<const uint4 *>(res)[static_cast<int64_t>(tok - tq) * (D / 8) + i];
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 p = widen_pair<BF16>(xw[e]), q = widen_pair<BF16>(yw[e]);
-                bk = fmaxf(bk, fmaxf(fabsf(p.x), fabsf(p.y)));
-                bv = fmaxf(bv, fmaxf(fabsf(q.x), fabsf(q.y)));
+                const float2 y = widen_pair<BF16>(vw[e]);
+                big = fmaxf(big, fmaxf(fabsf(y.x), fabsf(y.y)));
             }
         }
     }
-    ek = operand_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(bk)), kMinLogitExp);
-    ev = max(ev, (operand_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(bv)), kMinExp) + kValueStep - 1) &
-                     ~(kValueStep - 1));
-    if (f.kind != 1) return true;
-    const float down_k = pow2(-ek), down_v = pow2(-ev);
-    bool over = false;
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+    ex = KV ? (operand_exp(bits, kMinExp) + kValueStep - 1) & ~(kValueStep - 1) : operand_exp(bits, kMinLogitExp);
+    if (f.kind[0] != 1) return true;
+    const float down = pow2(-ex);
+    const bool wide = __any_sync(0xffffffffu, over);       // (and the unit before is unpacked)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        over = over || (has_k && fabsf(zk[e]) > 1024.0f) || (has_v && fabsf(zv[e]) > 1024.0f);
-    const bool wide = __any_sync(0xffffffffu, over);       // (and the tokens before are unpacked)
-    const float sk[4] = {f.ks.x * down_k, f.ks.y * down_k, f.ks.z * down_k, f.ks.w * down_k};
-    const float sv[4] = {f.vs.x * down_v, f.vs.y * down_v, f.vs.z * down_v, f.vs.w * down_v};
-    if (!wide) {
-        // keys: [z, hi, lo][D / 4] pairs of pairs; values: [z, hi, lo][D / Gv][16] in mixed order
-        uint2 *km = reinterpret_cast<uint2 *>(meta);
-        uint16_t *vm = reinterpret_cast<uint16_t *>(meta + 3 * D * 2);
-        if (has_k) {
-            float hi[4];
+    for (int x = 0; x < 2; ++x) {
+        if (!on[x]) continue;
+        const float s[4] = {f.s[x].x * down, f.s[x].y * down, f.s[x].z * down, f.s[x].w * down};
+        float hi[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) hi[e] = __half2float(__float2half_rn(sk[e]));
-            km[lane] = make_uint2(half2_bits(-1024.0f - zk[0], -1024.0f - zk[2]),
-                                  half2_bits(-1024.0f - zk[1], -1024.0f - zk[3]));
-            km[D / 4 + lane] = make_uint2(half2_bits(hi[0], hi[2]), half2_bits(hi[1], hi[3]));
-            if (!BF16)
-                km[D / 2 + lane] =
-                    make_uint2(half2_bits(sk[0] - hi[0], sk[2] - hi[2]), half2_bits(sk[1] - hi[1], sk[3] - hi[3]));
-        }
-        if (has_v) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 4 * lane + e, at = (i & (ngv - 1)) * 16 + mixed(i >> ngv_shift);
-                const __half hi = __float2half_rn(sv[e]);
-                vm[at] = __half_as_ushort(__float2half_rn(-1024.0f - zv[e]));
-                vm[128 + at] = __half_as_ushort(hi);
-                if (!BF16) vm[256 + at] = __half_as_ushort(__float2half_rn(sv[e] - __half2float(hi)));
+        for (int e = 0; e < 4; ++e) hi[e] = __half2float(__float2half_rn(s[e]));
+        if constexpr (KV == 0) {
+            if (!wide) {
+                uint2 *m = reinterpret_cast<uint2 *>(meta) + x * (3 * D / 4) + lane;
+                m[0] = make_uint2(half2_bits(-1024.0f - z[x][0], -1024.0f - z[x][2]),
+                                  half2_bits(-1024.0f - z[x][1], -1024.0f - z[x][3]));
+                m[D / 4] = make_uint2(half2_bits(s[0], s[2]), half2_bits(s[1], s[3]));
+                if (!BF16)
+                    m[D / 2] = make_uint2(half2_bits(s[0] - hi[0], s[2] - hi[2]), half2_bits(s[1] - hi[1], s[3] - hi[3]));
+            } else {
+                float4 *m = reinterpret_cast<float4 *>(meta) + x * (2 * D / 4) + lane;
+                m[0] = make_float4(s[0], s[1], s[2], s[3]);
+                m[D / 4] = make_float4(-8388608.0f - z[x][0], -8388608.0f - z[x][1], -8388608.0f - z[x][2],
+                                       -8388608.0f - z[x][3]);
             }
-        }
-    } else {
-        // fp32 [s, z] of keys [D] and values [D / Gv][16]
-        float *km = reinterpret_cast<float *>(meta), *vm = km + 2 * D;
-        if (has_k) {
-            reinterpret_cast<float4 *>(km)[lane] = make_float4(sk[0], sk[1], sk[2], sk[3]);
-            reinterpret_cast<float4 *>(km + D)[lane] =
-                make_float4(-8388608.0f - zk[0], -8388608.0f - zk[1], -8388608.0f - zk[2], -8388608.0f - zk[3]);
-        }
-        if (has_v) {
+        } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = 4 * lane + e, at = (i & (ngv - 1)) * 16 + (i >> ngv_shift);
-                vm[at] = sv[e];
-                vm[128 + at] = -8388608.0f - zv[e];
+                const int i = 4 * lane + 128 * x + e, g = (i & (ngv - 1)) * 32, tk = i >> ngv_shift;
+                if (!wide) {
+                    uint16_t *m = reinterpret_cast<uint16_t *>(meta) + g + mixed(tk);
+                    m[0] = __half_as_ushort(__float2half_rn(-1024.0f - z[x][e]));
+                    m[256] = __half_as_ushort(__float2half_rn(s[e]));
+                    if (!BF16) m[512] = __half_as_ushort(__float2half_rn(s[e] - hi[e]));
+                } else {
+                    float *m = reinterpret_cast<float *>(meta) + g + tk;
+                    m[0] = s[e];
+                    m[256] = -8388608.0f - z[x][e];
+                }
             }
         }
     }
@@ -274,64 +295,86 @@ __device__ __forceinline__ bool prepare16(const Fetched<D, N> &f, const PagedVie
     return !wide;
 }
 
-// The 16 tokens (warp w of a key tile's eight) as operands.  KV 0: keys, rows = tokens, channels along
-// a row; KV 1: values, rows = channels, tokens along a row.  put.at<I>(offset, a, b) stores 8 bytes of
-// the tile at offset + I, put(offset, v) 16.
+// Unit u of a key tile as operands.  KV 0: keys, rows = tokens, channels along a row; KV 1: values,
+// rows = channels, tokens along a row.  put.at<I>(offset, a, b) stores 8 bytes of the tile at
+// offset + I, put(offset, v) 16.
 template <int D, int N, bool BF16, int KV, class Put>
-__device__ __forceinline__ void emit16(const uint32_t (&words)[D * N / 64], int kind, bool narrow, const PagedView &c,
-                                       const uint16_t *res, int tok, int len, int tq, float down, int w, int lane,
-                                       const unsigned char *meta, const Put &put) {
+__device__ __forceinline__ void emit_unit(const uint32_t (&words)[2][D * N / 64], int kind0, int kind1, bool narrow,
+                                          const PagedView &c, const uint16_t *res, int tok, int len, int tq, float down,
+                                          int u, int lane, const unsigned char *meta, const Put &put) {
     constexpr int B = 4 / N;
-    const int tile = KV ? (w / 4) * (D * 128) : 16 * w * 128;
-    // lane's row (+ 8 in a second store): a key's is its token, in mixed order, a value's its channel;
-    // 8 bytes of a 32-byte step along it, swizzled
-    const int row = KV ? lane >> 2 : mixed(lane >> 2);
-    const int place = row * 128 + (lane & 1) * 8, col = (((lane & 3) >> 1) ^ (row & 7)) << 4;
-    // chunk ch (16 channels): a value's rows are its channels; a key's chunk is a step of its rows
-    int at[KV ? 1 : 4];
+    // the lane's place: a row (+ 8 of values, + 32 of keys for the second of a slot's two codes), a step
+    // along it (swizzled), eight bytes of that; the second half's tokens are the next step or eight rows on
+    const int row = KV ? lane >> 2 : 64 * (u / 2) + 16 * (u % 2) + mixed(lane >> 2);
+    const int line = (KV ? (u / 2) * (D * 128) : 0) + row * 128 + (lane & 1) * 8, far = 4 * ((lane >> 1) & 1);
+    int at[KV ? 2 : 4];
 #pragma unroll
-    for (int x = 0; x < (KV ? 1 : 4); ++x) at[x] = tile + place + (col ^ ((KV ? w % 4 : x) << 5));
-    constexpr int kNext = KV ? 32 : D / 4;         // from z to hi to lo; in fp32 from s to z
-    if (kind == 1 && narrow) {
-        const uint2 *pm = reinterpret_cast<const uint2 *>(meta + (KV ? 3 * D * 2 : 0)) + (lane & 3);
+    for (int x = 0; x < (KV ? 2 : 4); ++x) at[x] = line + ((((KV ? 2 * (u % 2) : 0) + x + far) ^ (row & 7)) << 4);
+    if (kind0 == 1) {
+        const bool both = kind1 == 1, two = KV == 0 && c.G == 16;
         const int shift = KV ? __ffs(c.Gv) - 5 : 0;            // chunk -> group of parameters
-        auto quad = [&](int ch) {
-            const uint2 *from = pm + 4 * (ch >> shift);
-            return Quad{from[0], from[kNext], BF16 ? make_uint2(0u, 0u) : from[2 * kNext]};
-        };
-        Quad q = quad(0);
-        static_for<D / 16>([&](auto ci) {          // the next chunk's parameters before this one's stores
-            constexpr int ch = decltype(ci)::value;
-            Quad q1 = q;
-            if constexpr (ch + 1 < D / 16) q1 = quad(ch + 1);
-            const uint32_t b = words[ch / B] >> (N * 2 * (ch % B));
-            const uint2 x = unpack_four<N, BF16>(b, q), y = unpack_four<N, BF16>(b >> N, q);
-            constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128);
-            put.template at<I>(at[KV ? 0 : ch % 4], x.x, x.y);
-            put.template at<I + 1024>(at[KV ? 0 : ch % 4], y.x, y.y);
-            q = q1;
-        });
-    } else if (kind == 1) {
-        constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
-        const float4 *pm = reinterpret_cast<const float4 *>(meta) + (KV ? 2 * D / 4 : 0) + (lane & 3);
-        const int shift = KV ? __ffs(c.Gv) - 5 : 0;
-        static_for<D / 16>([&](auto ci) {
-            constexpr int ch = decltype(ci)::value;
-            constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128);
-            const float4 *from = pm + 4 * (ch >> shift);
-            const float4 sc = from[0], z = from[kNext];
-            const uint32_t b = words[ch / B] >> (N * 2 * (ch % B));
-            const uint2 x = unpack_four_wide(b & kMask, sc, z), y = unpack_four_wide((b >> N) & kMask, sc, z);
-            put.template at<I>(at[KV ? 0 : ch % 4], x.x, x.y);
-            put.template at<I + 1024>(at[KV ? 0 : ch % 4], y.x, y.y);
-        });
-    } else if constexpr (KV == 0) {
+        if (narrow) {
+            constexpr int kNext = KV ? 64 : D / 4;             // from z to hi to lo
+            const uint2 *pm = reinterpret_cast<const uint2 *>(meta) + (lane & 3);
+            auto quad = [&](int ch, int p) {
+                const uint2 *from = pm + (KV ? 8 * (ch >> shift) + 4 * p : 4 * ch + (two ? p * (3 * D / 4) : 0));
+                return Quad{from[0], from[kNext], BF16 ? make_uint2(0u, 0u) : from[2 * kNext]};
+            };
+            Quad q0 = quad(0, 0), q1 = KV || two ? quad(0, 1) : q0;
+            static_for<D / 16>([&](auto ci) {      // the next chunk's parameters before this one's stores
+                constexpr int ch = decltype(ci)::value;
+                Quad n0 = q0, n1 = q1;
+                if constexpr (ch + 1 < D / 16) {
+                    n0 = quad(ch + 1, 0);
+                    n1 = KV || two ? quad(ch + 1, 1) : n0;
+                }
+                constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128), kHalf = KV ? 0 : 1024;
+                constexpr int kSecond = KV ? 1024 : 4096;
+                const int a0 = at[KV ? 0 : ch % 4], a1 = at[KV ? 1 : ch % 4];
+                const uint32_t b0 = words[0][ch / B] >> (N * 2 * (ch % B)), b1 = words[1][ch / B] >> (N * 2 * (ch % B));
+                const uint2 x0 = unpack_four<N, BF16>(b0, q0), y0 = unpack_four<N, BF16>(b0 >> N, q0);
+                put.template at<I>(a0, x0.x, x0.y);
+                put.template at<I + kSecond>(a0, y0.x, y0.y);
+                if (both) {
+                    const uint2 x1 = unpack_four<N, BF16>(b1, q1), y1 = unpack_four<N, BF16>(b1 >> N, q1);
+                    put.template at<I + kHalf>(a1, x1.x, x1.y);
+                    put.template at<I + kHalf + kSecond>(a1, y1.x, y1.y);
+                }
+                q0 = n0;
+                q1 = n1;
+            });
+        } else {
+            constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
+            constexpr int kNext = KV ? 64 : D / 4;             // from s to z
+            const float4 *pm = reinterpret_cast<const float4 *>(meta) + (lane & 3);
+            static_for<D / 16>([&](auto ci) {
+                constexpr int ch = decltype(ci)::value;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    if (p == 1 && !both) break;
+                    const float4 *from = pm + (KV ? 8 * (ch >> shift) + 4 * p : 4 * ch + (two ? p * (2 * D / 4) : 0));
+                    const float4 sc = from[0], z = from[kNext];
+                    const uint32_t b = words[p][ch / B] >> (N * 2 * (ch % B));
+                    const uint2 x = unpack_four_wide(b & kMask, sc, z), y = unpack_four_wide((b >> N) & kMask, sc, z);
+                    constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128), kSecond = KV ? 1024 : 4096;
+                    const int a = at[KV ? p : ch % 4] + (KV ? 0 : 1024 * p);
+                    put.template at<I>(a, x.x, x.y);
+                    put.template at<I + kSecond>(a, y.x, y.y);
+                }
+            });
+        }
+        if (both) return;
+    }
+    // the rest: residual rows, zeros behind the last token
+    const int from = kind0 == 1 ? 16 : 0;
+    if constexpr (KV == 0) {
 #pragma unroll 4
-        for (int i = lane; i < 16 * (D / 8); i += 32) {
-            const int r = i / (D / 8), v = i % (D / 8), rm = mixed(r);
+        for (int i = lane; i < (32 - from) * (D / 8); i += 32) {
+            const int t = from + i / (D / 8), v = i % (D / 8);
+            const int rm = 64 * (u / 2) + 16 * (u % 2) + 8 * (t / 16) + 32 * ((t / 8) % 2) + mixed(t % 8);
             uint32_t o[4] = {0u, 0u, 0u, 0u};
-            if (kind == 2 && tok + r < len) {
-                const uint4 x = reinterpret_cast<const uint4 *>(res + static_cast<int64_t>(tok + r - tq) * D)[v];
+            if (tok + t < len) {
+                const uint4 x = reinterpret_cast<const uint4 *>(res + static_cast<int64_t>(tok + t - tq) * D)[v];
                 const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
@@ -340,21 +383,21 @@ __device__ __forceinline__ void emit16(const uint32_t (&words)[D * N / 64], int 
                     o[e + 1] = half2_bits(p.y * down, q.y * down);
                 }
             }
-            put(tile + (v / 8) * (kRows * 128) + rm * 128 + (((v % 8) ^ (rm & 7)) << 4), o);
+            put((v / 8) * (kRows * 128) + rm * 128 + ((step_of(8 * v) ^ (rm & 7)) << 4), o);
         }
     } else {
 #pragma unroll 2
-        for (int i = lane; i < D; i += 32) {       // channels 2 cp, 2 cp + 1: 8 of the 16 tokens
-            const int cp = i >> 1, part = i & 1;
+        for (int i = lane; i < (4 - from / 8) * (D / 2); i += 32) {    // channels 2 cp, 2 cp + 1: eight tokens
+            const int cp = i % (D / 2), t0 = from + 8 * (i / (D / 2));
             uint32_t o[2][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float2 p[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tk = tok + 8 * part + mixed(2 * k + e);
+                    const int tk = tok + t0 + mixed(2 * k + e);
                     p[e] = make_float2(0.0f, 0.0f);
-                    if (kind == 2 && tk < len)
+                    if (tk < len)
                         p[e] = widen_pair<BF16>(
                             reinterpret_cast<const uint32_t *>(res + static_cast<int64_t>(tk - tq) * D)[cp]);
                 }
@@ -364,7 +407,7 @@ __device__ __forceinline__ void emit16(const uint32_t (&words)[D * N / 64], int 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 2 * cp + e;
-                put(tile + r * 128 + (((2 * (w % 4) + part) ^ (r & 7)) << 4), o[e]);
+                put((u / 2) * (D * 128) + r * 128 + ((step_of(32 * (u % 2) + t0) ^ (r & 7)) << 4), o[e]);
             }
         }
     }
@@ -398,7 +441,7 @@ __device__ __forceinline__ void emit_queries(int rows, int w, int n_warps, int l
             const float down = pow2(-ex);
             if (r >= rows) continue;
             if (col == 0) put_scale(r, pow2(ex));
-            put.template at<0>((col / 64) * (kRows * 128) + r * 128 + ((((col % 64) / 8) ^ (r & 7)) << 4) + (col % 8) * 2,
+            put.template at<0>((col / 64) * (kRows * 128) + r * 128 + ((step_of(col) ^ (r & 7)) << 4) + (col % 8) * 2,
                 half2_bits(p.x * down, q.x * down), half2_bits(p.y * down, q.y * down));
         }
     }
@@ -456,9 +499,10 @@ __device__ __forceinline__ CacheItem cache_item(const AttendArgs &a, const int4 
 enum { kQFull = 0, kKFull = 1, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages, kVEmpty = kKEmpty + kStages,
        kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kOFull = kPFull + 4, kDrain = kOFull + 2, kBars };
 
-// filled: arrivals that fill the queries or a tile's operands
-__device__ __forceinline__ void init_bars(uint32_t bars, int filled) {
-    for (int i = 0; i < kBars; ++i) tc::bar_init(bars + 8u * i, i < kKEmpty ? filled : i >= kPFull && i < kPFull + 4 ? 4 : 1);
+// queries, filled: arrivals that fill the queries, a tile's keys or values
+__device__ __forceinline__ void init_bars(uint32_t bars, int queries, int filled) {
+    for (int i = 0; i < kBars; ++i)
+        tc::bar_init(bars + 8u * i, i == kQFull ? queries : i < kKEmpty ? filled : i >= kPFull && i < kPFull + 4 ? 4 : 1);
     tc::fence_barrier_init();
 }
 
@@ -564,16 +608,9 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
         tc::fence_after_sync();
         if (any) {
             const float *scales = exps[j % kExps].scale_k;
-            const int *evs = exps[j % kExps].exp_v;
-            int top = e_ref;
-            bool even = true;
-#pragma unroll
-            for (int g = 0; g < kUnpackWarps; ++g) top = max(top, evs[g]);
-#pragma unroll
-            for (int g = 0; g < kUnpackWarps; ++g) even = even && evs[g] == top;
             const int seen = seen0 - j * kRows;
             const bool masked = seen_least < (j + 1) * kRows;
-            // kHeld / 32 registers' worth of the tile's columns from column 64 half on; column e is token mixed(e)
+            // kHeld / 32 registers' worth of the tile's columns from column 64 half on; column e is token token_of(e)
             constexpr int kHeld = WHOLE ? 4 : 2;
             uint32_t x[kHeld][32];
             auto logits = [&](int half) {
@@ -586,7 +623,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                     for (int k = 0; k < kHeld; ++k)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (64 * half + 32 * k + mixed(e) >= seen) x[k][e] = 0xff800000u;
+                            if (64 * half + token_of(32 * k + e) >= seen) x[k][e] = 0xff800000u;
                 }
             };
             float mx = kNoMax;
@@ -599,9 +636,20 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                     float m2[2] = {__uint_as_float(y[0]), __uint_as_float(y[1])};
 #pragma unroll
                     for (int e = 2; e < 16; ++e) m2[e % 2] = fmaxf(m2[e % 2], __uint_as_float(y[e]));
-                    mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * (row_s * scales[4 * half + g]));
+                    mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * (row_s * scales[unit_of(half, g)]));
                 }
             }
+            if constexpr (!WHOLE) {                // the values' powers come with the values
+                go = tc::bar_wait_warp(bar(kVFull + j % kStages), (j / kStages) & 1, &gave_up);
+                if (!go) break;
+            }
+            const int *evs = exps[j % kExps].exp_v;
+            int top = e_ref;
+            bool even = true;
+#pragma unroll
+            for (int g = 0; g < kUnits; ++g) top = max(top, evs[g]);
+#pragma unroll
+            for (int g = 0; g < kUnits; ++g) even = even && evs[g] == top;
             if (i == 0) {
                 m = mx;
                 e_ref = top;
@@ -627,8 +675,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                 uint32_t(&p)[32] = x[from];        // a weight takes the place of a logit read before
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const float sc = row_s * scales[4 * half + g];
-                    const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[4 * half + g] - top));
+                    const float sc = row_s * scales[unit_of(half, g)];
+                    const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[unit_of(half, g)] - top));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t *y = &x[from + g / 2][16 * (g % 2) + 2 * e];

@@ -3,8 +3,8 @@
 // tile only and is unpacked where it is used.
 //
 //   warps 0-3, 4-7   softmax of stream 0, 1: alternate key tiles
-//   warps 8-15       operands: warp w the tokens 16w .. 16w+15 of each key tile, its values' power of two
-//                    growing along the pass
+//   warps 8-11       keys' operands: each warp 32 tokens of each key tile
+//   warps 12-15      values'
 //   warp 16          issues the MMAs (warps 17-19 fill the warpgroup, which gives its registers to the
 //                    softmax: 2 x 128 x 120 + 2 x 128 x 88 + 128 x 64 <= 640 x 96)
 #include <algorithm>
@@ -33,11 +33,83 @@ struct NarrowSmem {
     static constexpr int k = q + kTileBytes;
     static constexpr int v = k + kStages * kTileBytes;
     static constexpr int meta = v + kStages * kTileBytes;
-    static constexpr int row_scale = meta + kUnpackWarps * kMetaBytes<D>;     // [128]
+    static constexpr int row_scale = meta + kUnpackWarps * kMetaBytes;     // [128]
     static constexpr int bars = row_scale + kRows * 4;
     // one CTA an SM: it holds all of the tensor memory
     static constexpr int bytes = (bars + 256 > 120 * 1024 ? bars + 256 : 120 * 1024) + 1024;
 };
+
+template <int D, bool BF16, class L>
+__device__ __forceinline__ void emit_queries_of(const AttendArgs &a, const CacheItem &work, unsigned char *smem,
+                                                uint32_t base, int w, int lane) {
+    const int hg = work.hg, rows = hg * min(work.tpt, work.count - work.q0);
+    const uint16_t *src = a.q.p + static_cast<int64_t>(work.first + work.q0) * a.q.ts +
+                          static_cast<int64_t>(work.h) * hg * a.q.hs;
+    emit_queries<D, BF16>(
+        kRows, w, kUnpackWarps, lane,
+        [&](int r) -> const uint16_t * {
+            return r < rows ? src + static_cast<int64_t>(r / hg) * a.q.ts + static_cast<int64_t>(r % hg) * a.q.hs : nullptr;
+        },
+        SharedPut{base + L::q}, [&](int r, float scale) { reinterpret_cast<float *>(smem + L::row_scale)[r] = scale; });
+    tc::fence_async_proxy();
+    __syncwarp();
+    if (lane == 0) tc::bar_arrive(base + L::bars + 8u * kQFull);
+}
+
+// Warp u of the four that unpack keys (KV 0) or values (1): unit u of every key tile, fetched a tile
+// ahead, its page number two.
+template <int D, int N, bool BF16, int KV, class L>
+__device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem &work, TileExps *exps,
+                                            unsigned char *smem, uint32_t base, int u, int lane,
+                                            volatile int &gave_up) {
+    const PagedView &c = a.cache;
+    unsigned char *meta = smem + L::meta + (kUnits * KV + u) * kMetaBytes;
+    const int n = work.n, len = work.len, tq = work.tq;
+    constexpr int W = D * N / 64;
+    const int32_t *pages = c.page_table + static_cast<int64_t>(work.slot) * c.max_pages;
+    int tok = work.tile0 * kRows + 32 * u;         // of the tile in hand
+    int at_page = tok / c.P, at_tok = tok % c.P;   // of the tile to fetch
+    auto page_at = [&](int t) { return t < tq && at_page < c.max_pages ? pages[at_page] : -1; };
+    auto advance = [&] {
+        at_tok += kRows;
+        while (at_tok >= c.P) {
+            at_tok -= c.P;
+            ++at_page;
+        }
+    };
+    const uint16_t *res = (KV ? c.vr : c.kr) + (static_cast<int64_t>(work.slot) * a.Hkv + work.h) * c.R * D;
+    Fetched<D, N> f;
+    fetch_unit<D, N, KV>(f, c, work.h, page_at(tok), at_tok, tok, len, tq, n > 0, lane);
+    advance();
+    int page = page_at(tok + kRows);
+    emit_queries_of<D, BF16, L>(a, work, smem, base, kUnits * KV + u, lane);
+    for (int j = 0; j < n; ++j, tok += kRows) {
+        const int s = j % kStages, kind0 = f.kind[0], kind1 = f.kind[1];
+        int ex;
+        const bool narrow = prepare_unit<D, N, BF16, KV>(f, c, res, tok, len, tq, lane, meta, ex);
+        uint32_t words[2][W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            words[0][i] = f.w[0][i];
+            words[1][i] = f.w[1][i];
+        }
+        fetch_unit<D, N, KV>(f, c, work.h, page, at_tok, tok + kRows, len, tq, j + 1 < n, lane);
+        advance();
+        page = page_at(tok + 2 * kRows);
+        if (j >= kStages &&
+            !tc::bar_wait_warp(base + L::bars + 8u * ((KV ? kVEmpty : kKEmpty) + s), ((j / kStages) & 1) ^ 1, &gave_up))
+            break;
+        if (lane == 0) {
+            if (KV) exps[j % kExps].exp_v[u] = ex;
+            else exps[j % kExps].scale_k[u] = pow2(ex);
+        }
+        emit_unit<D, N, BF16, KV>(words, kind0, kind1, narrow, c, res, tok, len, tq, pow2(-ex), u, lane, meta,
+                                  SharedPut{base + (KV ? L::v : L::k) + s * L::kTileBytes});
+        tc::fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(base + L::bars + 8u * ((KV ? kVFull : kKFull) + s));
+    }
+}
 
 template <int D, int N, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const AttendArgs a) {
@@ -49,12 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     __shared__ volatile int gave_up;
     __shared__ CacheItem work;                     // in shared memory: each role keeps what it needs of it
     __shared__ TileExps exps[kExps];
-    const PagedView &c = a.cache;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         work = cache_item(a, a.t.items[a.t.n_wide + blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
         gave_up = 0;
-        init_bars(base + L::bars, kUnpackWarps);
+        init_bars(base + L::bars, kUnpackWarps, kUnits);
     }
     __syncthreads();
     if (!work.good || !work.alternate) {           // not this library's table
@@ -66,88 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    auto bar = [&](int i) { return base + L::bars + 8u * i; };
 
     if (warp >= 8 && warp < 16) {
         tc::regs_give<88>();
-        // ------------------------------ operands ---------------------------
-        const int w = warp - 8;
-        unsigned char *meta = smem + L::meta + w * kMetaBytes<D>;
-        const int tile0 = work.tile0, n = work.n, len = work.len, tq = work.tq;
-        constexpr int W = D * N / 64;
-        // this warp's place in the pages: of the tile to fetch (page index and token in it), whose page
-        // number is loaded a tile ahead
-        const int32_t *pages = c.page_table + static_cast<int64_t>(work.slot) * c.max_pages;
-        int at_page = (tile0 * kRows + 16 * w) / c.P, at_tok = (tile0 * kRows + 16 * w) % c.P;
-        auto page_at = [&](int j, int pi) -> int {
-            return j < n && (tile0 + j) * kRows + 16 * w < tq && pi < c.max_pages ? pages[pi] : -1;
-        };
-        auto advance = [&] {
-            at_tok += kRows;
-            while (at_tok >= c.P) {
-                at_tok -= c.P;
-                ++at_page;
-            }
-        };
-        // the slot's residual rows: token tq's first
-        auto residual = [&](const uint16_t *rows) {
-            return rows + (static_cast<int64_t>(work.slot) * a.Hkv + work.h) * c.R * D;
-        };
-        Fetched<D, N> f;
-        fetch16<D, N>(f, c, work.h, page_at(0, at_page), at_tok, tile0 * kRows + 16 * w, len, tq, n > 0, lane);
-        advance();
-        int page = page_at(1, at_page);
-        {
-            const int hg = work.hg, tpt = work.tpt, q0 = work.q0, count = work.count, first = work.first, h = work.h;
-            emit_queries<D, BF16>(
-                kRows, w, kUnpackWarps, lane,
-                [&](int r) -> const uint16_t * {
-                    const int tok = q0 + r / hg;
-                    if (r >= hg * tpt || tok >= count) return nullptr;
-                    return a.q.p + static_cast<int64_t>(first + tok) * a.q.ts + static_cast<int64_t>(h * hg + r % hg) * a.q.hs;
-                },
-                SharedPut{base + L::q},
-                [&](int r, float scale) { reinterpret_cast<float *>(smem + L::row_scale)[r] = scale; });
-            tc::fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(bar(kQFull));
-        }
-        int ev = kMinExp;
-        bool go = true;
-        for (int j = 0; j < n && go; ++j) {
-            const int s = j % kStages, phase = (j / kStages) & 1, kind = f.kind;
-            const int tok = (tile0 + j) * kRows + 16 * w;
-            int ek;
-            const bool narrow =
-                prepare16<D, N, BF16>(f, c, residual(c.kr), residual(c.vr), tok, len, tq, lane, meta, ek, ev);
-            uint32_t kw[W], vw[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                kw[i] = f.kw[i];
-                vw[i] = f.vw[i];
-            }
-            fetch16<D, N>(f, c, work.h, page, at_tok, tok + kRows, len, tq, j + 1 < n, lane);
-            advance();
-            page = page_at(j + 2, at_page);
-            if (j >= kStages) go = tc::bar_wait_warp(bar(kKEmpty + s), phase ^ 1, &gave_up);
-            if (!go) break;
-            if (lane == 0) {
-                exps[j % kExps].scale_k[w] = pow2(ek);
-                exps[j % kExps].exp_v[w] = ev;
-            }
-            emit16<D, N, BF16, 0>(kw, kind, narrow, c, residual(c.kr), tok, len, tq, pow2(-ek), w, lane, meta,
-                                  SharedPut{base + L::k + s * L::kTileBytes});
-            tc::fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(bar(kKFull + s));
-            if (j >= kStages) go = tc::bar_wait_warp(bar(kVEmpty + s), phase ^ 1, &gave_up);
-            if (!go) break;
-            emit16<D, N, BF16, 1>(vw, kind, narrow, c, residual(c.vr), tok, len, tq, pow2(-ev), w, lane, meta,
-                                  SharedPut{base + L::v + s * L::kTileBytes});
-            tc::fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(bar(kVFull + s));
-        }
+        if (warp < 12) unpack_role<D, N, BF16, 0, L>(a, work, exps, smem, base, warp - 8, lane, gave_up);
+        else unpack_role<D, N, BF16, 1, L>(a, work, exps, smem, base, warp - 12, lane, gave_up);
     } else if (warp >= 16) {
         tc::regs_give<64>();
         if (warp == 16 && lane == 0 && work.n > 0) mma_role<D, L>(work, base, tmem, gave_up);

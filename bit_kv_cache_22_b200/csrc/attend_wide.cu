@@ -57,36 +57,42 @@ struct GlobalPut {
     }
 };
 
+template <int D, int N, bool BF16, int KV>
+__device__ __forceinline__ void stage_unit(const AttendArgs &a, int slot, int h, int tok0, int u, int lane,
+                                           unsigned char *meta, unsigned char *tile, TileExps &exps) {
+    const PagedView &c = a.cache;
+    const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
+    const int tok = tok0 + 32 * u, pi = tok / c.P;
+    const int page = tok < tq && pi < c.max_pages ? c.page_table[static_cast<int64_t>(slot) * c.max_pages + pi] : -1;
+    Fetched<D, N> f;
+    fetch_unit<D, N, KV>(f, c, h, page, tok % c.P, tok, len, tq, true, lane);
+    const uint16_t *res = (KV ? c.vr : c.kr) + (static_cast<int64_t>(slot) * a.Hkv + h) * c.R * D;
+    int ex;
+    const bool narrow = prepare_unit<D, N, BF16, KV>(f, c, res, tok, len, tq, lane, meta, ex);
+    if (lane == 0) {
+        if (KV) exps.exp_v[u] = ex;
+        else exps.scale_k[u] = pow2(ex);
+    }
+    emit_unit<D, N, BF16, KV>(f.w, f.kind[0], f.kind[1], narrow, c, res, tok, len, tq, pow2(-ex), u, lane, meta,
+                              GlobalPut{tile});
+}
+
 // CTA (x, h): key tile x of the wide slots, or query tile x - n_kv_tiles.
 template <int D, int N, bool BF16>
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(const AttendArgs a) {
-    __shared__ __align__(16) unsigned char meta_s[kUnpackWarps][kMetaBytes<D>];
-    const PagedView &c = a.cache;
+    __shared__ __align__(16) unsigned char meta_s[kUnpackWarps][kMetaBytes];
     const Staged<D> st(a);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
     if (blockIdx.x < static_cast<unsigned>(a.t.n_kv_tiles)) {
         const int x = blockIdx.x, slot = slot_of(a.t.kv_tiles, a.t.B, x);
-        const int tok = (x - a.t.kv_tiles[slot]) * kRows + 16 * w;
-        const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
-        if (tok < 0) return;
-        const int pi = tok / c.P;
-        const int page = tok < tq && pi < c.max_pages ? c.page_table[static_cast<int64_t>(slot) * c.max_pages + pi] : -1;
-        Fetched<D, N> f;
-        fetch16<D, N>(f, c, h, page, tok % c.P, tok, len, tq, true, lane);
-        const int64_t rows = (static_cast<int64_t>(slot) * a.Hkv + h) * c.R * D;
-        int ek, ev = kMinExp;
-        const bool narrow =
-            prepare16<D, N, BF16>(f, c, c.kr + rows, c.vr + rows, tok, len, tq, lane, meta_s[w], ek, ev);
+        const int tok0 = (x - a.t.kv_tiles[slot]) * kRows;
+        if (tok0 < 0) return;
         const int64_t at = static_cast<int64_t>(x) * a.Hkv + h;
-        if (lane == 0) {
-            st.exps[at].scale_k[w] = pow2(ek);
-            st.exps[at].exp_v[w] = ev;
-        }
         unsigned char *tile = st.kv + at * 2 * Staged<D>::kTileBytes;
-        emit16<D, N, BF16, 0>(f.kw, f.kind, narrow, c, c.kr + rows, tok, len, tq, pow2(-ek), w, lane, meta_s[w],
-                           GlobalPut{tile});
-        emit16<D, N, BF16, 1>(f.vw, f.kind, narrow, c, c.vr + rows, tok, len, tq, pow2(-ev), w, lane, meta_s[w],
-                           GlobalPut{tile + Staged<D>::kTileBytes});
+        if (w < kUnits)
+            stage_unit<D, N, BF16, 0>(a, slot, h, tok0, w, lane, meta_s[w], tile, st.exps[at]);
+        else
+            stage_unit<D, N, BF16, 1>(a, slot, h, tok0, w - kUnits, lane, meta_s[w], tile + Staged<D>::kTileBytes, st.exps[at]);
     } else {
         const int x = blockIdx.x - a.t.n_kv_tiles, slot = slot_of(a.t.q_tiles, a.t.B, x);
         const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const AttendAr
                 work.good = false;
         }
         gave_up = 0;
-        init_bars(base + L::bars, 1);
+        init_bars(base + L::bars, 1, 1);
     }
     __syncthreads();
     if (!work.good) {                              // not this library's table
