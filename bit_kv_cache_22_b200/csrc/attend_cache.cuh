@@ -298,11 +298,13 @@ __device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const Paged
 // Unit u of a key tile as operands.  KV 0: keys, rows = tokens, channels along a row; KV 1: values,
 // rows = channels, tokens along a row.  put.at<I>(offset, a, b) stores 8 bytes of the tile at
 // offset + I, put(offset, v) 16.
+// words are used up.  The loops are rolled: the narrow kernel's roles together have to stay in the
+// SM's instruction cache (unrolled twice as far they ran half as fast).
 template <int D, int N, bool BF16, int KV, class Put>
-__device__ __forceinline__ void emit_unit(const uint32_t (&words)[2][D * N / 64], int kind0, int kind1, bool narrow,
+__device__ __forceinline__ void emit_unit(uint32_t (&words)[2][D * N / 64], int kind0, int kind1, bool narrow,
                                           const PagedView &c, const uint16_t *res, int tok, int len, int tq, float down,
                                           int u, int lane, const unsigned char *meta, const Put &put) {
-    constexpr int B = 4 / N;
+    constexpr int B = 4 / N, W = D * N / 64;
     // the lane's place: a row (+ 8 of values, + 32 of keys for the second of a slot's two codes), a step
     // along it (swizzled), eight bytes of that; the second half's tokens are the next step or eight rows on
     const int row = KV ? lane >> 2 : 64 * (u / 2) + 16 * (u % 2) + mixed(lane >> 2);
@@ -321,47 +323,59 @@ __device__ __forceinline__ void emit_unit(const uint32_t (&words)[2][D * N / 64]
                 return Quad{from[0], from[kNext], BF16 ? make_uint2(0u, 0u) : from[2 * kNext]};
             };
             Quad q0 = quad(0, 0), q1 = KV || two ? quad(0, 1) : q0;
-            static_for<D / 16>([&](auto ci) {      // the next chunk's parameters before this one's stores
-                constexpr int ch = decltype(ci)::value;
-                Quad n0 = q0, n1 = q1;
-                if constexpr (ch + 1 < D / 16) {
-                    n0 = quad(ch + 1, 0);
-                    n1 = KV || two ? quad(ch + 1, 1) : n0;
-                }
-                constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128), kHalf = KV ? 0 : 1024;
-                constexpr int kSecond = KV ? 1024 : 4096;
-                const int a0 = at[KV ? 0 : ch % 4], a1 = at[KV ? 1 : ch % 4];
-                const uint32_t b0 = words[0][ch / B] >> (N * 2 * (ch % B)), b1 = words[1][ch / B] >> (N * 2 * (ch % B));
-                const uint2 x0 = unpack_four<N, BF16>(b0, q0), y0 = unpack_four<N, BF16>(b0 >> N, q0);
-                put.template at<I>(a0, x0.x, x0.y);
-                put.template at<I + kSecond>(a0, y0.x, y0.y);
-                if (both) {
+#pragma unroll 1
+            for (int ch0 = 0; ch0 < D / 16; ch0 += 4) {
+                static_for<4>([&](auto xi) {       // the next chunk's parameters before this one's stores
+                    constexpr int x = decltype(xi)::value;
+                    const int more = ch0 + x + 1 < D / 16 ? ch0 + x + 1 : 0;
+                    const Quad n0 = quad(more, 0), n1 = KV || two ? quad(more, 1) : n0;
+                    constexpr int I = KV ? x * 2048 : 0, kHalf = KV ? 0 : 1024, kSecond = KV ? 1024 : 4096;
+                    const int a0 = at[KV ? 0 : x], a1 = at[KV ? 1 : x];
+                    const uint32_t b0 = words[0][x / B] >> (N * 2 * (x % B)), b1 = words[1][x / B] >> (N * 2 * (x % B));
+                    const uint2 x0 = unpack_four<N, BF16>(b0, q0), y0 = unpack_four<N, BF16>(b0 >> N, q0);
                     const uint2 x1 = unpack_four<N, BF16>(b1, q1), y1 = unpack_four<N, BF16>(b1 >> N, q1);
-                    put.template at<I + kHalf>(a1, x1.x, x1.y);
-                    put.template at<I + kHalf + kSecond>(a1, y1.x, y1.y);
+                    put.template at<I>(a0, x0.x, x0.y);
+                    put.template at<I + kSecond>(a0, y0.x, y0.y);
+                    if (both) {
+                        put.template at<I + kHalf>(a1, x1.x, x1.y);
+                        put.template at<I + kHalf + kSecond>(a1, y1.x, y1.y);
+                    }
+                    q0 = n0;
+                    q1 = n1;
+                });
+#pragma unroll
+                for (int x = 0; x < (KV ? 2 : 4); ++x) at[x] += KV ? 4 * 2048 : kRows * 128;
+#pragma unroll
+                for (int i = 0; i + 4 / B < W; ++i) {
+                    words[0][i] = words[0][i + 4 / B];
+                    words[1][i] = words[1][i + 4 / B];
                 }
-                q0 = n0;
-                q1 = n1;
-            });
+            }
         } else {
             constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
             constexpr int kNext = KV ? 64 : D / 4;             // from s to z
             const float4 *pm = reinterpret_cast<const float4 *>(meta) + (lane & 3);
-            static_for<D / 16>([&](auto ci) {
-                constexpr int ch = decltype(ci)::value;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    if (p == 1 && !both) break;
+#pragma unroll 1
+            for (int i = 0; i < D / 8; ++i) {      // chunk i / 2 of half i % 2
+                const int ch = i / 2, p = i % 2;
+                if (p == 0 || both) {
                     const float4 *from = pm + (KV ? 8 * (ch >> shift) + 4 * p : 4 * ch + (two ? p * (2 * D / 4) : 0));
                     const float4 sc = from[0], z = from[kNext];
-                    const uint32_t b = words[p][ch / B] >> (N * 2 * (ch % B));
+                    const uint32_t b = (p ? words[1][0] : words[0][0]) >> (N * 2 * (ch % B));
                     const uint2 x = unpack_four_wide(b & kMask, sc, z), y = unpack_four_wide((b >> N) & kMask, sc, z);
-                    constexpr int I = KV ? ch * 2048 : (ch / 4) * (kRows * 128), kSecond = KV ? 1024 : 4096;
-                    const int a = at[KV ? p : ch % 4] + (KV ? 0 : 1024 * p);
-                    put.template at<I>(a, x.x, x.y);
-                    put.template at<I + kSecond>(a, y.x, y.y);
+                    const int to = KV ? (p ? at[1] : at[0]) + ch * 2048
+                                      : (ch & 2 ? ch & 1 ? at[3] : at[2] : ch & 1 ? at[1] : at[0]) + 1024 * p +
+                                            (ch / 4) * (kRows * 128);
+                    put.template at<0>(to, x.x, x.y);
+                    put.template at<KV ? 1024 : 4096>(to, y.x, y.y);
                 }
-            });
+                if (p == 1 && ch % B == B - 1)
+#pragma unroll
+                    for (int k = 0; k + 1 < W; ++k) {
+                        words[0][k] = words[0][k + 1];
+                        words[1][k] = words[1][k + 1];
+                    }
+            }
         }
         if (both) return;
     }

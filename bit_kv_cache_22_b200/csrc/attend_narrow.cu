@@ -3,8 +3,8 @@
 // tile only and is unpacked where it is used.
 //
 //   warps 0-3, 4-7   softmax of stream 0, 1: alternate key tiles
-//   warps 8-11       keys' operands: each warp 32 tokens of each key tile
-//   warps 12-15      values'
+//   warps 8-15       operands: each warp 32 tokens of each key tile, keys (8, 9, 12, 13) or values, so that
+//                    an SM quarter's two run the same code
 //   warp 16          issues the MMAs (warps 17-19 fill the warpgroup, which gives its registers to the
 //                    softmax: 2 x 128 x 120 + 2 x 128 x 88 + 128 x 64 <= 640 x 96)
 #include <algorithm>
@@ -140,8 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
 
     if (warp >= 8 && warp < 16) {
         tc::regs_give<88>();
-        if (warp < 12) unpack_role<D, N, BF16, 0, L>(a, work, exps, smem, base, warp - 8, lane, gave_up);
-        else unpack_role<D, N, BF16, 1, L>(a, work, exps, smem, base, warp - 12, lane, gave_up);
+        const int u = (warp & 1) + (warp >= 12 ? 2 : 0);
+        if (warp & 2) unpack_role<D, N, BF16, 1, L>(a, work, exps, smem, base, u, lane, gave_up);
+        else unpack_role<D, N, BF16, 0, L>(a, work, exps, smem, base, u, lane, gave_up);
     } else if (warp >= 16) {
         tc::regs_give<64>();
         if (warp == 16 && lane == 0 && work.n > 0) mma_role<D, L>(work, base, tmem, gave_up);
