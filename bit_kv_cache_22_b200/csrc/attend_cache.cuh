@@ -80,8 +80,6 @@ __host__ __device__ constexpr int step_of(int c) { return (c / 16) % 4 + 4 * ((c
 __host__ __device__ constexpr int token_of(int c) {
     return c / 64 * 64 + (c / 8) % 4 * 16 + (c / 32) % 2 * 8 + mixed(c % 8);
 }
-// 16 columns, number g from column 64 half on, are of one unit of 32 tokens
-__host__ __device__ constexpr int unit_of(int half, int g) { return 2 * (half + g / 4) + g % 2; }
 static_assert(step_of(token_of(77)) == 77 / 8 % 8 && mixed(token_of(77) % 8) == 77 % 8, "token_of inverts the places");
 
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
@@ -113,23 +111,10 @@ __device__ __forceinline__ uint2 unpack_four_wide(uint32_t b, const float4 &s, c
     return make_uint2(half2_bits(x.x, x.y), half2_bits(y.x, y.y));
 }
 
-// f(0) .. f(n - 1), the numbers known when compiling
-template <int I>
-struct Number {
-    static constexpr int value = I;
-};
-template <int Count, int I = 0, class F>
-__device__ __forceinline__ void static_for(const F &f) {
-    if constexpr (I < Count) {
-        f(Number<I>{});
-        static_for<Count, I + 1>(f);
-    }
-}
-
-// What one unpacking warp needs of a unit's keys or values: the code words of its lanes, and scales
-// and zeros it spreads over shared memory -- keys: channels 4 lane .. of the halves' groups (one
-// group of 32 tokens or more: the first only); values: entries 4 lane .. and 128 + 4 lane .. of [32
-// tokens][D / Gv], as far as there are any.
+// What one unpacking warp needs of a unit's keys or values: the code words of its lanes, and four
+// scales and zeros a lane twice, which it spreads over shared memory -- keys: channels 4 lane .. of the
+// halves' groups (one group of 32 tokens or more: the first only); values: entries 4 lane .. and 128 +
+// 4 lane .. of [32 tokens][D / Gv].
 template <int D, int N>
 struct Fetched {
     static constexpr int W = D * N / 64;   // words per lane and half
@@ -137,6 +122,32 @@ struct Fetched {
     float4 s[2];
     uint2 z[2];
     int kind[2];                           // of each 16 tokens; 0: none, 1: quantized, 2: residual
+};
+
+// Where a warp unpacks: keys (kv 0) or values (1) of a slot's kv head.  One code serves both: the
+// narrow kernel's roles together have to stay in the SM's instruction cache.
+template <int D>
+struct UnitSource {
+    const uint32_t *words;
+    const float *scales;
+    const int16_t *zeros;
+    const uint16_t *res;                   // the slot's residual rows: token tq's first
+    int kv, h, len, tq;
+    int tokens_shift, entries_shift;       // entries of parameters: (token >> tokens_shift) << entries_shift
+    int first, second, apart;              // a unit's: how many, how many more `apart` on
+    __device__ __forceinline__ UnitSource(const PagedView &c, int kv_, int slot, int h_, int len_, int tq_)
+        : kv(kv_), h(h_), len(len_), tq(tq_) {
+        words = kv ? c.vc : c.kc;
+        scales = kv ? c.vs : c.ks;
+        zeros = kv ? c.vz : c.kz;
+        res = (kv ? c.vr : c.kr) + (static_cast<int64_t>(slot) * c.Hkv + h) * c.R * D;
+        const int ngv_shift = __ffs(D) - __ffs(c.Gv);      // G, Gv, D: powers of two
+        tokens_shift = kv ? 0 : __ffs(c.G) - 1;
+        entries_shift = kv ? ngv_shift : __ffs(D) - 1;
+        first = kv ? min(32 << ngv_shift, 128) : D;
+        second = kv ? (32 << ngv_shift) - first : c.G == 16 ? D : 0;
+        apart = kv ? 128 : D;
+    }
 };
 
 __device__ __forceinline__ void widen_zeros(uint2 z, bool sym, int half_levels, float (&f)[4]) {
@@ -152,21 +163,20 @@ struct TileExps {
     int exp_v[kUnits];
 };
 
-// Fetches the 32 tokens tok .. of a slot for kv head h (KV 0: keys, 1: values); at_tok: the first
-// one's place in its page.
-template <int D, int N, int KV>
-__device__ __forceinline__ void fetch_unit(Fetched<D, N> &f, const PagedView &c, int h, int page, int at_tok, int tok,
-                                           int len, int tq, bool on, int lane) {
+// Fetches the 32 tokens tok .. ; at_tok: the first one's place in its page.
+template <int D, int N>
+__device__ __forceinline__ void fetch_unit(Fetched<D, N> &f, const PagedView &c, const UnitSource<D> &src, int page,
+                                           int at_tok, int tok, bool on, int lane) {
     constexpr int W = D * N / 64, TW = D * N / 2;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) f.kind[p] = !on || tok + 16 * p >= len ? 0 : tok + 16 * p < tq ? 1 : 2;
+    for (int p = 0; p < 2; ++p) f.kind[p] = !on || tok + 16 * p >= src.len ? 0 : tok + 16 * p < src.tq ? 1 : 2;
     if (f.kind[0] != 1) return;
     if (page < 0 || page >= c.num_pages) {
         if (lane == 0) atomicOr(c.status, 2u);
         page = 0;
     }
-    const int64_t slice = static_cast<int64_t>(page) * c.Hkv + h;
-    const uint32_t *words = (KV ? c.vc : c.kc) + (slice * (c.P >> 4) + (at_tok >> 4)) * TW + lane * W;
+    const int64_t slice = static_cast<int64_t>(page) * c.Hkv + src.h;
+    const uint32_t *words = src.words + (slice * (c.P >> 4) + (at_tok >> 4)) * TW + lane * W;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {                  // pages hold whole units: a half behind tq is read for nothing
         if constexpr (W >= 4) {
@@ -180,26 +190,15 @@ __device__ __forceinline__ void fetch_unit(Fetched<D, N> &f, const PagedView &c,
             f.w[p][0] = x.x; f.w[p][1] = x.y;
         }
     }
-    if constexpr (KV == 0) {
-        const int g_shift = __ffs(c.G) - 1;        // G, Gv: powers of two
-        const int64_t at = (slice * (c.P >> g_shift) + (at_tok >> g_shift)) * D + 4 * lane;
-        if (4 * lane < D) {
-            f.s[0] = *reinterpret_cast<const float4 *>(c.ks + at);
-            if (!c.sym) f.z[0] = *reinterpret_cast<const uint2 *>(c.kz + at);
-            if (c.G == 16) {
-                f.s[1] = *reinterpret_cast<const float4 *>(c.ks + at + D);
-                if (!c.sym) f.z[1] = *reinterpret_cast<const uint2 *>(c.kz + at + D);
-            }
-        }
-    } else {
-        const int ngv_shift = __ffs(D) - __ffs(c.Gv);
-        const int64_t at = ((slice * c.P + at_tok) << ngv_shift) + 4 * lane;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            if (4 * lane + 128 * x < 32 << ngv_shift) {
-                f.s[x] = *reinterpret_cast<const float4 *>(c.vs + at + 128 * x);
-                if (!c.sym) f.z[x] = *reinterpret_cast<const uint2 *>(c.vz + at + 128 * x);
-            }
+    const int64_t at =
+        ((slice * (c.P >> src.tokens_shift) + (at_tok >> src.tokens_shift)) << src.entries_shift) + 4 * lane;
+    if (4 * lane < src.first) {
+        f.s[0] = *reinterpret_cast<const float4 *>(src.scales + at);
+        if (!c.sym) f.z[0] = *reinterpret_cast<const uint2 *>(src.zeros + at);
+    }
+    if (4 * lane < src.second) {
+        f.s[1] = *reinterpret_cast<const float4 *>(src.scales + at + src.apart);
+        if (!c.sym) f.z[1] = *reinterpret_cast<const uint2 *>(src.zeros + at + src.apart);
     }
 }
 
@@ -207,23 +206,20 @@ __device__ __forceinline__ void fetch_unit(Fetched<D, N> &f, const PagedView &c,
 constexpr int kMetaBytes = 2048;
 
 // The unit's power of two e, and its parameters spread over shared memory for the lanes that use them;
-// false: in fp32, for zeros that 1024 + z does not hold.  res: the slot's residual rows (token
-// tq's first).
+// false: in fp32, for zeros that 1024 + z does not hold.
 //   keys: [half's group][z, hi, lo][D / 4] pairs of pairs; values: [z, hi, lo][D / Gv][32] halves, in mixed order
 //   in fp32: [s, z], keys [half's group][D], values [D / Gv][32]
-template <int D, int N, bool BF16, int KV>
-__device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const PagedView &c, const uint16_t *res, int tok,
-                                             int len, int tq, int lane, unsigned char *meta, int &ex) {
+template <int D, int N, bool BF16>
+__device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const PagedView &c, const UnitSource<D> &src,
+                                             int tok, int lane, unsigned char *meta, int &ex) {
     constexpr float kTop = static_cast<float>((1 << N) - 1);
-    const int ngv_shift = __ffs(D) - __ffs(c.Gv), ngv = 1 << ngv_shift;
+    const int ngv_shift = src.entries_shift, ngv = 1 << ngv_shift;     // (of values)
     float big = 0.0f, z[2][4];
     bool on[2], over = false;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        if constexpr (KV == 0) on[x] = 4 * lane < D && f.kind[x] == 1 && (x == 0 || c.G == 16);
-        else
-            on[x] = 4 * lane + 128 * x < 32 << ngv_shift &&
-                    ((4 * lane + 128 * x) >> (ngv_shift + 4) ? f.kind[1] : f.kind[0]) == 1;
+        const int half = src.kv ? (4 * lane + 128 * x) >> (ngv_shift + 4) : x;
+        on[x] = 4 * lane < (x ? src.second : src.first) && (half ? f.kind[1] : f.kind[0]) == 1;
         if (!on[x]) continue;
         widen_zeros(f.z[x], c.sym, 1 << (N - 1), z[x]);
         const float s[4] = {f.s[x].x, f.s[x].y, f.s[x].z, f.s[x].w};
@@ -234,12 +230,12 @@ __device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const Paged
         }
     }
     if (f.kind[0] == 2 || f.kind[1] == 2) {        // rows of one token are D / 8 vectors
-        const int from = max(tok, tq);
+        const int from = max(tok, src.tq);
 #pragma unroll 4
         for (int i = lane; i < 32 * (D / 8); i += 32) {
             const int tk = tok + i / (D / 8);
-            if (tk < from || tk >= len) continue;
-            const uint4 v = reinterpret_cast<const uint4 *>(res)[static_cast<int64_t>(tok - tq) * (D / 8) + i];
+            if (tk < from || tk >= src.len) continue;
+            const uint4 v = reinterpret_cast<const uint4 *>(src.res)[static_cast<int64_t>(tok - src.tq) * (D / 8) + i];
             const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -249,7 +245,7 @@ __device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const Paged
         }
     }
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-    ex = KV ? (operand_exp(bits, kMinExp) + kValueStep - 1) & ~(kValueStep - 1) : operand_exp(bits, kMinLogitExp);
+    ex = src.kv ? (operand_exp(bits, kMinExp) + kValueStep - 1) & ~(kValueStep - 1) : operand_exp(bits, kMinLogitExp);
     if (f.kind[0] != 1) return true;
     const float down = pow2(-ex);
     const bool wide = __any_sync(0xffffffffu, over);       // (and the unit before is unpacked)
@@ -257,17 +253,16 @@ __device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const Paged
     for (int x = 0; x < 2; ++x) {
         if (!on[x]) continue;
         const float s[4] = {f.s[x].x * down, f.s[x].y * down, f.s[x].z * down, f.s[x].w * down};
-        float hi[4];
+        float lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) hi[e] = __half2float(__float2half_rn(s[e]));
-        if constexpr (KV == 0) {
+        for (int e = 0; e < 4; ++e) lo[e] = s[e] - __half2float(__float2half_rn(s[e]));
+        if (!src.kv) {
             if (!wide) {
                 uint2 *m = reinterpret_cast<uint2 *>(meta) + x * (3 * D / 4) + lane;
                 m[0] = make_uint2(half2_bits(-1024.0f - z[x][0], -1024.0f - z[x][2]),
                                   half2_bits(-1024.0f - z[x][1], -1024.0f - z[x][3]));
                 m[D / 4] = make_uint2(half2_bits(s[0], s[2]), half2_bits(s[1], s[3]));
-                if (!BF16)
-                    m[D / 2] = make_uint2(half2_bits(s[0] - hi[0], s[2] - hi[2]), half2_bits(s[1] - hi[1], s[3] - hi[3]));
+                if (!BF16) m[D / 2] = make_uint2(half2_bits(lo[0], lo[2]), half2_bits(lo[1], lo[3]));
             } else {
                 float4 *m = reinterpret_cast<float4 *>(meta) + x * (2 * D / 4) + lane;
                 m[0] = make_float4(s[0], s[1], s[2], s[3]);
@@ -282,7 +277,7 @@ __device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const Paged
                     uint16_t *m = reinterpret_cast<uint16_t *>(meta) + g + mixed(tk);
                     m[0] = __half_as_ushort(__float2half_rn(-1024.0f - z[x][e]));
                     m[256] = __half_as_ushort(__float2half_rn(s[e]));
-                    if (!BF16) m[512] = __half_as_ushort(__float2half_rn(s[e] - hi[e]));
+                    if (!BF16) m[512] = __half_as_ushort(__float2half_rn(lo[e]));
                 } else {
                     float *m = reinterpret_cast<float *>(meta) + g + tk;
                     m[0] = s[e];
@@ -295,56 +290,57 @@ __device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const Paged
     return !wide;
 }
 
-// Unit u of a key tile as operands.  KV 0: keys, rows = tokens, channels along a row; KV 1: values,
-// rows = channels, tokens along a row.  put.at<I>(offset, a, b) stores 8 bytes of the tile at
-// offset + I, put(offset, v) 16.
-// words are used up.  The loops are rolled: the narrow kernel's roles together have to stay in the
-// SM's instruction cache (unrolled twice as far they ran half as fast).
-template <int D, int N, bool BF16, int KV, class Put>
+// Unit u of a key tile as operands: keys, rows = tokens, channels along a row; values, rows =
+// channels, tokens along a row.  put(offset, a, b) stores 8 bytes of the tile, put(offset, v) 16.
+// words are used up.
+template <int D, int N, bool BF16, class Put>
 __device__ __forceinline__ void emit_unit(uint32_t (&words)[2][D * N / 64], int kind0, int kind1, bool narrow,
-                                          const PagedView &c, const uint16_t *res, int tok, int len, int tq, float down,
-                                          int u, int lane, const unsigned char *meta, const Put &put) {
+                                          const PagedView &c, const UnitSource<D> &src, int tok, float down, int u,
+                                          int lane, const unsigned char *meta, const Put &put) {
     constexpr int B = 4 / N, W = D * N / 64;
-    // the lane's place: a row (+ 8 of values, + 32 of keys for the second of a slot's two codes), a step
-    // along it (swizzled), eight bytes of that; the second half's tokens are the next step or eight rows on
-    const int row = KV ? lane >> 2 : 64 * (u / 2) + 16 * (u % 2) + mixed(lane >> 2);
-    const int line = (KV ? (u / 2) * (D * 128) : 0) + row * 128 + (lane & 1) * 8, far = 4 * ((lane >> 1) & 1);
-    int at[KV ? 2 : 4];
-#pragma unroll
-    for (int x = 0; x < (KV ? 2 : 4); ++x) at[x] = line + ((((KV ? 2 * (u % 2) : 0) + x + far) ^ (row & 7)) << 4);
+    const int kv = src.kv;
     if (kind0 == 1) {
-        const bool both = kind1 == 1, two = KV == 0 && c.G == 16;
-        const int shift = KV ? __ffs(c.Gv) - 5 : 0;            // chunk -> group of parameters
+        // the lane's place: a row, a step along it (swizzled), eight bytes of that; then the same for the
+        // next chunks of 16 channels, for the second of a slot's two codes (eight channels or tokens
+        // on) and the second half's tokens
+        const int row = kv ? lane >> 2 : 64 * (u / 2) + 16 * (u % 2) + mixed(lane >> 2);
+        const int line = (kv ? (u / 2) * (D * 128) : 0) + row * 128 + (lane & 1) * 8;
+        const int far = 4 * ((lane >> 1) & 1) + (kv ? 2 * (u % 2) : 0);
+        int at[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) at[x] = line + (((far + (kv ? 0 : x)) ^ (row & 7)) << 4) + (kv ? x * 2048 : 0);
+        const int code2 = kv ? 1024 : 4096;
+        const int half2 = kv ? (((far + 1) ^ (row & 7)) - (far ^ (row & 7))) << 4 : 1024;
+        const bool both = kind1 == 1;
+        const int shift = kv ? __ffs(c.Gv) - 5 : 0;            // chunk -> group of parameters
         if (narrow) {
-            constexpr int kNext = KV ? 64 : D / 4;             // from z to hi to lo
+            // per group (kv) or chunk, and half: z, hi, lo `next` apart
+            const int next = kv ? 64 : D / 4, per = kv ? 3 : 2, other = kv ? 4 : c.G == 16 ? 3 * D / 4 : 0;
             const uint2 *pm = reinterpret_cast<const uint2 *>(meta) + (lane & 3);
-            auto quad = [&](int ch, int p) {
-                const uint2 *from = pm + (KV ? 8 * (ch >> shift) + 4 * p : 4 * ch + (two ? p * (3 * D / 4) : 0));
-                return Quad{from[0], from[kNext], BF16 ? make_uint2(0u, 0u) : from[2 * kNext]};
+            auto quad = [&](int ch, int from) {
+                const uint2 *q = pm + ((ch >> shift) << per) + from;
+                return Quad{q[0], q[next], BF16 ? make_uint2(0u, 0u) : q[2 * next]};
             };
-            Quad q0 = quad(0, 0), q1 = KV || two ? quad(0, 1) : q0;
+            Quad q0 = quad(0, 0), q1 = quad(0, other);
 #pragma unroll 1
             for (int ch0 = 0; ch0 < D / 16; ch0 += 4) {
-                static_for<4>([&](auto xi) {       // the next chunk's parameters before this one's stores
-                    constexpr int x = decltype(xi)::value;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {      // the next chunk's parameters before this one's stores
                     const int more = ch0 + x + 1 < D / 16 ? ch0 + x + 1 : 0;
-                    const Quad n0 = quad(more, 0), n1 = KV || two ? quad(more, 1) : n0;
-                    constexpr int I = KV ? x * 2048 : 0, kHalf = KV ? 0 : 1024, kSecond = KV ? 1024 : 4096;
-                    const int a0 = at[KV ? 0 : x], a1 = at[KV ? 1 : x];
+                    const Quad n0 = quad(more, 0), n1 = quad(more, other);
                     const uint32_t b0 = words[0][x / B] >> (N * 2 * (x % B)), b1 = words[1][x / B] >> (N * 2 * (x % B));
                     const uint2 x0 = unpack_four<N, BF16>(b0, q0), y0 = unpack_four<N, BF16>(b0 >> N, q0);
                     const uint2 x1 = unpack_four<N, BF16>(b1, q1), y1 = unpack_four<N, BF16>(b1 >> N, q1);
-                    put.template at<I>(a0, x0.x, x0.y);
-                    put.template at<I + kSecond>(a0, y0.x, y0.y);
+                    put(at[x], x0.x, x0.y);
+                    put(at[x] + code2, y0.x, y0.y);
                     if (both) {
-                        put.template at<I + kHalf>(a1, x1.x, x1.y);
-                        put.template at<I + kHalf + kSecond>(a1, y1.x, y1.y);
+                        put(at[x] + half2, x1.x, x1.y);
+                        put(at[x] + half2 + code2, y1.x, y1.y);
                     }
+                    at[x] += kv ? 4 * 2048 : kRows * 128;
                     q0 = n0;
                     q1 = n1;
-                });
-#pragma unroll
-                for (int x = 0; x < (KV ? 2 : 4); ++x) at[x] += KV ? 4 * 2048 : kRows * 128;
+                }
 #pragma unroll
                 for (int i = 0; i + 4 / B < W; ++i) {
                     words[0][i] = words[0][i + 4 / B];
@@ -353,21 +349,20 @@ __device__ __forceinline__ void emit_unit(uint32_t (&words)[2][D * N / 64], int 
             }
         } else {
             constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
-            constexpr int kNext = KV ? 64 : D / 4;             // from s to z
+            const int next = kv ? 64 : D / 4, per = kv ? 3 : 2, other = kv ? 4 : c.G == 16 ? 2 * D / 4 : 0;
             const float4 *pm = reinterpret_cast<const float4 *>(meta) + (lane & 3);
 #pragma unroll 1
             for (int i = 0; i < D / 8; ++i) {      // chunk i / 2 of half i % 2
                 const int ch = i / 2, p = i % 2;
                 if (p == 0 || both) {
-                    const float4 *from = pm + (KV ? 8 * (ch >> shift) + 4 * p : 4 * ch + (two ? p * (2 * D / 4) : 0));
-                    const float4 sc = from[0], z = from[kNext];
+                    const float4 *from = pm + ((ch >> shift) << per) + (p ? other : 0);
+                    const float4 sc = from[0], z = from[next];
                     const uint32_t b = (p ? words[1][0] : words[0][0]) >> (N * 2 * (ch % B));
                     const uint2 x = unpack_four_wide(b & kMask, sc, z), y = unpack_four_wide((b >> N) & kMask, sc, z);
-                    const int to = KV ? (p ? at[1] : at[0]) + ch * 2048
-                                      : (ch & 2 ? ch & 1 ? at[3] : at[2] : ch & 1 ? at[1] : at[0]) + 1024 * p +
-                                            (ch / 4) * (kRows * 128);
-                    put.template at<0>(to, x.x, x.y);
-                    put.template at<KV ? 1024 : 4096>(to, y.x, y.y);
+                    const int to = (ch & 2 ? ch & 1 ? at[3] : at[2] : ch & 1 ? at[1] : at[0]) + (p ? half2 : 0) +
+                                   (ch / 4) * (kv ? 4 * 2048 : kRows * 128);
+                    put(to, x.x, x.y);
+                    put(to + code2, y.x, y.y);
                 }
                 if (p == 1 && ch % B == B - 1)
 #pragma unroll
@@ -381,14 +376,14 @@ __device__ __forceinline__ void emit_unit(uint32_t (&words)[2][D * N / 64], int 
     }
     // the rest: residual rows, zeros behind the last token
     const int from = kind0 == 1 ? 16 : 0;
-    if constexpr (KV == 0) {
+    if (!kv) {
 #pragma unroll 4
         for (int i = lane; i < (32 - from) * (D / 8); i += 32) {
             const int t = from + i / (D / 8), v = i % (D / 8);
             const int rm = 64 * (u / 2) + 16 * (u % 2) + 8 * (t / 16) + 32 * ((t / 8) % 2) + mixed(t % 8);
             uint32_t o[4] = {0u, 0u, 0u, 0u};
-            if (tok + t < len) {
-                const uint4 x = reinterpret_cast<const uint4 *>(res + static_cast<int64_t>(tok + t - tq) * D)[v];
+            if (tok + t < src.len) {
+                const uint4 x = reinterpret_cast<const uint4 *>(src.res + static_cast<int64_t>(tok + t - src.tq) * D)[v];
                 const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
@@ -411,9 +406,9 @@ __device__ __forceinline__ void emit_unit(uint32_t (&words)[2][D * N / 64], int 
                 for (int e = 0; e < 2; ++e) {
                     const int tk = tok + t0 + mixed(2 * k + e);
                     p[e] = make_float2(0.0f, 0.0f);
-                    if (tk < len)
+                    if (tk < src.len)
                         p[e] = widen_pair<BF16>(
-                            reinterpret_cast<const uint32_t *>(res + static_cast<int64_t>(tk - tq) * D)[cp]);
+                            reinterpret_cast<const uint32_t *>(src.res + static_cast<int64_t>(tk - src.tq) * D)[cp]);
                 }
                 o[0][k] = half2_bits(p[0].x * down, p[1].x * down);
                 o[1][k] = half2_bits(p[0].y * down, p[1].y * down);
@@ -428,7 +423,7 @@ __device__ __forceinline__ void emit_unit(uint32_t (&words)[2][D * N / 64], int 
 }
 
 // Query rows r (tokens x heads) of a tile as operands, by warp w of n_warps: four channels a lane,
-// kBatch rows of loads in flight.  row(r) is a row's elements, or NULL; put.at(offset, a, b) as above;
+// kBatch rows of loads in flight.  row(r) is a row's elements, or NULL; put(offset, a, b) as above;
 // put_scale(r, 2^e).
 template <int D, bool BF16, class Row, class Put, class PutScale>
 __device__ __forceinline__ void emit_queries(int rows, int w, int n_warps, int lane, const Row &row, const Put &put,
@@ -455,7 +450,7 @@ __device__ __forceinline__ void emit_queries(int rows, int w, int n_warps, int l
             const float down = pow2(-ex);
             if (r >= rows) continue;
             if (col == 0) put_scale(r, pow2(ex));
-            put.template at<0>((col / 64) * (kRows * 128) + r * 128 + ((step_of(col) ^ (r & 7)) << 4) + (col % 8) * 2,
+            put((col / 64) * (kRows * 128) + r * 128 + ((step_of(col) ^ (r & 7)) << 4) + (col % 8) * 2,
                 half2_bits(p.x * down, q.x * down), half2_bits(p.y * down, q.y * down));
         }
     }
@@ -527,24 +522,25 @@ template <int D, class L>
 __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, uint32_t tmem, volatile int &gave_up) {
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
-    const int n = work.n, ends[2] = {work.end0, n};
+    const int n = work.n;
     const bool alternate = work.alternate;
     const int stride = alternate ? 2 : 1;          // of a stream's tiles
     constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, false, false);
     constexpr uint32_t kDescO = tc::mma_desc(kRows, D, false, false);
     auto issue_s = [&](int t, int s) {
-        const uint32_t qa = base + L::q + (alternate ? 0 : t) * L::kTileBytes, ka = base + L::k + s * L::kTileBytes;
+        uint32_t qa = base + L::q + (alternate ? 0 : t) * L::kTileBytes, ka = base + L::k + s * L::kTileBytes;
+#pragma unroll 1
+        for (int i = 0; i < D / 64; ++i, qa += kRows * 128, ka += kRows * 128)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint32_t step = (i / 4) * (kRows * 128) + (i % 4) * 32;
-            tc::mma_ss(tmem + t * 128, tc::desc_k_major(qa + step), tc::desc_k_major(ka + step), kDescS, i > 0);
-        }
+            for (int k = 0; k < 4; ++k)
+                tc::mma_ss(tmem + t * 128, tc::desc_k_major(qa + 32 * k), tc::desc_k_major(ka + 32 * k), kDescS, i + k > 0);
         tc::mma_commit(bar(kSFull + t));
     };
     bool go = tc::bar_wait(bar(kQFull), 0, &gave_up);
+#pragma unroll 1
     for (int t = 0; t < 2 && go; ++t) {
         const int j = alternate ? t : 0;   // the stream's first tile
-        if (j < ends[t]) {
+        if (j < (t ? n : work.end0)) {
             go = tc::bar_wait(bar(kKFull + j % kStages), (j / kStages) & 1, &gave_up);
             if (go) issue_s(t, j % kStages);
         }
@@ -553,8 +549,9 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
     for (int j = 0; j < n && go; ++j) {
         const int s = j % kStages, next = j + stride, s1 = next % kStages;
         go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
+#pragma unroll 1
         for (int t = 0; t < 2 && go; ++t) {
-            if (j >= ends[t] || (alternate && (j & 1) != t)) continue;
+            if (j >= (t ? n : work.end0) || (alternate && (j & 1) != t)) continue;
             const int i = alternate ? j / 2 : j;       // how many tiles the stream has had
             const uint32_t va = base + L::v + s * L::kTileBytes;
 #pragma unroll 1
@@ -568,7 +565,7 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
                                tc::desc_k_major(va + half * (D * 128) + k * 32), kDescO, i > 0 || half > 0 || k > 0);
             }
             if (!go) break;
-            if (next < ends[t]) {
+            if (next < (t ? n : work.end0)) {
                 go = tc::bar_wait(bar(kKFull + s1), (next / kStages) & 1, &gave_up);
                 if (go) issue_s(t, s1);
             } else {
@@ -586,7 +583,8 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
 }
 
 // The softmax of one query row a thread, warps 0-3 for stream 0, 4-7 for stream 1; then the row's
-// output, or its part of it.  WHOLE: a row's 128 logits are held in registers at once; else 64, read twice.
+// output, or its part of it.  WHOLE: a row's 128 logits are held in registers at once; else they are
+// read twice, 32 at a time, by rolled loops.
 template <int D, bool BF16, bool WHOLE, class L>
 __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheItem &work, const TileExps *exps,
                                              unsigned char *smem, uint32_t base, uint32_t tmem, int warp, int lane,
@@ -624,33 +622,46 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             const float *scales = exps[j % kExps].scale_k;
             const int seen = seen0 - j * kRows;
             const bool masked = seen_least < (j + 1) * kRows;
-            // kHeld / 32 registers' worth of the tile's columns from column 64 half on; column e is token token_of(e)
-            constexpr int kHeld = WHOLE ? 4 : 2;
-            uint32_t x[kHeld][32];
-            auto logits = [&](int half) {
-#pragma unroll
-                for (int k = 0; k < kHeld; ++k) tc::tmem_load(ts + 64 * half + 32 * k, x[k]);
-#pragma unroll
-                for (int k = 0; k < kHeld; ++k) tc::tmem_arrived(x[k]);
+            // the tile's columns from 32 k on; column e is token token_of(e)
+            auto logits = [&](int k, uint32_t(&x)[32]) {
+                tc::tmem_arrived(x);
                 if (masked) {
+                    const int past = seen - 64 * (k / 2) - 8 * (k % 2);
 #pragma unroll
-                    for (int k = 0; k < kHeld; ++k)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (64 * half + token_of(32 * k + e) >= seen) x[k][e] = 0xff800000u;
+                    for (int e = 0; e < 32; ++e)
+                        if (token_of(e) >= past) x[e] = 0xff800000u;
                 }
             };
+            // 16 columns from 32 k + 16 g on are of one unit
+            auto unit = [&](int k, int g) { return 2 * (k / 2) + g; };
+            auto largest = [&](int k, const uint32_t(&x)[32]) {
+                float big = kNoMax;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float m2[2] = {__uint_as_float(x[16 * g]), __uint_as_float(x[16 * g + 1])};
+#pragma unroll
+                    for (int e = 2; e < 16; ++e) m2[e % 2] = fmaxf(m2[e % 2], __uint_as_float(x[16 * g + e]));
+                    big = fmaxf(big, fmaxf(m2[0], m2[1]) * (row_s * scales[unit(k, g)]));
+                }
+                return big;
+            };
+            constexpr int kHeld = WHOLE ? 4 : 1;
+            uint32_t x[kHeld][32];
             float mx = kNoMax;
+            if constexpr (WHOLE) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc::tmem_load(ts + 32 * k, x[k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    logits(k, x[k]);
+                    mx = fmaxf(mx, largest(k, x[k]));
+                }
+            } else {
 #pragma unroll 1
-            for (int half = WHOLE ? 0 : 1; half >= 0; --half) {    // the first half stays for its weights
-                logits(half);
-#pragma unroll
-                for (int g = 0; g < 2 * kHeld; ++g) {
-                    const uint32_t *y = &x[g / 2][16 * (g % 2)];
-                    float m2[2] = {__uint_as_float(y[0]), __uint_as_float(y[1])};
-#pragma unroll
-                    for (int e = 2; e < 16; ++e) m2[e % 2] = fmaxf(m2[e % 2], __uint_as_float(y[e]));
-                    mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * (row_s * scales[unit_of(half, g)]));
+                for (int k = 0; k < 4; ++k) {
+                    tc::tmem_load(ts + 32 * k, x[0]);
+                    logits(k, x[0]);
+                    mx = fmaxf(mx, largest(k, x[0]));
                 }
             }
             if constexpr (!WHOLE) {                // the values' powers come with the values
@@ -685,15 +696,15 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                 }
             }
             float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            auto weights = [&](int half, int from) {           // from x[from], x[from + 1]
-                uint32_t(&p)[32] = x[from];        // a weight takes the place of a logit read before
+            // the weights of 32 columns, packed, take the place of their first logits
+            auto weights = [&](int k, const uint32_t(&x)[32], uint32_t *p) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float sc = row_s * scales[unit_of(half, g)];
-                    const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[unit_of(half, g)] - top));
+                for (int g = 0; g < 2; ++g) {
+                    const float sc = row_s * scales[unit(k, g)];
+                    const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[unit(k, g)] - top));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const uint32_t *y = &x[from + g / 2][16 * (g % 2) + 2 * e];
+                        const uint32_t *y = &x[16 * g + 2 * e];
                         const float2 z = tc::fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
                                                   make_float2(sc, sc), make_float2(-m, -m));
                         float2 wt = make_float2(tc::ex2(z.x), tc::ex2(z.y));
@@ -702,20 +713,31 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                         p[8 * g + e] = half2_bits(wt.x, wt.y);
                     }
                 }
-                tc::tmem_store(ts + 32 * half, p);             // over logits that have been read
+            };
+            auto handed = [&](int half) {
                 tc::tmem_stored();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(bar(kPFull + 2 * half + t));
             };
             if constexpr (WHOLE) {
-                weights(0, 0);
-                weights(1, 2);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t(&p)[32] = x[2 * half];
+                    weights(2 * half, x[2 * half], p);
+                    weights(2 * half + 1, x[2 * half + 1], p + 16);
+                    tc::tmem_store(ts + 32 * half, p);         // over logits that have been read
+                    handed(half);
+                }
             } else {
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (half == 1) logits(1);
-                    weights(half, 0);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t p[16];
+                    tc::tmem_load(ts + 32 * k, x[0]);
+                    logits(k, x[0]);
+                    weights(k, x[0], p);
+                    tc::tmem_store16(ts + 16 * k, p);
+                    if (k & 1) handed(k / 2);
                 }
             }
             l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);

@@ -3,8 +3,8 @@
 // tile only and is unpacked where it is used.
 //
 //   warps 0-3, 4-7   softmax of stream 0, 1: alternate key tiles
-//   warps 8-15       operands: each warp 32 tokens of each key tile, keys (8, 9, 12, 13) or values, so that
-//                    an SM quarter's two run the same code
+//   warps 8-11       keys' operands: each warp 32 tokens of each key tile
+//   warps 12-15      values'
 //   warp 16          issues the MMAs (warps 17-19 fill the warpgroup, which gives its registers to the
 //                    softmax: 2 x 128 x 120 + 2 x 128 x 88 + 128 x 64 <= 640 x 96)
 #include <algorithm>
@@ -19,9 +19,8 @@ constexpr int kThreads = 640;
 
 struct SharedPut {
     uint32_t tile;
-    template <int I>
-    __device__ __forceinline__ void at(int offset, uint32_t x, uint32_t y) const {
-        tc::store_shared<I>(tile + offset, x, y);
+    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
+        tc::store_shared(tile + offset, x, y);
     }
     __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const { tc::store_shared(tile + offset, v); }
 };
@@ -56,20 +55,21 @@ __device__ __forceinline__ void emit_queries_of(const AttendArgs &a, const Cache
     if (lane == 0) tc::bar_arrive(base + L::bars + 8u * kQFull);
 }
 
-// Warp u of the four that unpack keys (KV 0) or values (1): unit u of every key tile, fetched a tile
+// Warp u of the four that unpack keys (kv 0) or values (1): unit u of every key tile, fetched a tile
 // ahead, its page number two.
-template <int D, int N, bool BF16, int KV, class L>
+template <int D, int N, bool BF16, class L>
 __device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem &work, TileExps *exps,
-                                            unsigned char *smem, uint32_t base, int u, int lane,
+                                            unsigned char *smem, uint32_t base, int kv, int u, int lane,
                                             volatile int &gave_up) {
     const PagedView &c = a.cache;
-    unsigned char *meta = smem + L::meta + (kUnits * KV + u) * kMetaBytes;
-    const int n = work.n, len = work.len, tq = work.tq;
+    unsigned char *meta = smem + L::meta + (kUnits * kv + u) * kMetaBytes;
+    const int n = work.n;
     constexpr int W = D * N / 64;
+    const UnitSource<D> src(c, kv, work.slot, work.h, work.len, work.tq);
     const int32_t *pages = c.page_table + static_cast<int64_t>(work.slot) * c.max_pages;
     int tok = work.tile0 * kRows + 32 * u;         // of the tile in hand
     int at_page = tok / c.P, at_tok = tok % c.P;   // of the tile to fetch
-    auto page_at = [&](int t) { return t < tq && at_page < c.max_pages ? pages[at_page] : -1; };
+    auto page_at = [&](int t) { return t < src.tq && at_page < c.max_pages ? pages[at_page] : -1; };
     auto advance = [&] {
         at_tok += kRows;
         while (at_tok >= c.P) {
@@ -77,37 +77,36 @@ __device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem
             ++at_page;
         }
     };
-    const uint16_t *res = (KV ? c.vr : c.kr) + (static_cast<int64_t>(work.slot) * a.Hkv + work.h) * c.R * D;
     Fetched<D, N> f;
-    fetch_unit<D, N, KV>(f, c, work.h, page_at(tok), at_tok, tok, len, tq, n > 0, lane);
+    fetch_unit<D, N>(f, c, src, page_at(tok), at_tok, tok, n > 0, lane);
     advance();
     int page = page_at(tok + kRows);
-    emit_queries_of<D, BF16, L>(a, work, smem, base, kUnits * KV + u, lane);
+    emit_queries_of<D, BF16, L>(a, work, smem, base, kUnits * kv + u, lane);
     for (int j = 0; j < n; ++j, tok += kRows) {
         const int s = j % kStages, kind0 = f.kind[0], kind1 = f.kind[1];
         int ex;
-        const bool narrow = prepare_unit<D, N, BF16, KV>(f, c, res, tok, len, tq, lane, meta, ex);
+        const bool narrow = prepare_unit<D, N, BF16>(f, c, src, tok, lane, meta, ex);
         uint32_t words[2][W];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             words[0][i] = f.w[0][i];
             words[1][i] = f.w[1][i];
         }
-        fetch_unit<D, N, KV>(f, c, work.h, page, at_tok, tok + kRows, len, tq, j + 1 < n, lane);
+        fetch_unit<D, N>(f, c, src, page, at_tok, tok + kRows, j + 1 < n, lane);
         advance();
         page = page_at(tok + 2 * kRows);
         if (j >= kStages &&
-            !tc::bar_wait_warp(base + L::bars + 8u * ((KV ? kVEmpty : kKEmpty) + s), ((j / kStages) & 1) ^ 1, &gave_up))
+            !tc::bar_wait_warp(base + L::bars + 8u * ((kv ? kVEmpty : kKEmpty) + s), ((j / kStages) & 1) ^ 1, &gave_up))
             break;
         if (lane == 0) {
-            if (KV) exps[j % kExps].exp_v[u] = ex;
+            if (kv) exps[j % kExps].exp_v[u] = ex;
             else exps[j % kExps].scale_k[u] = pow2(ex);
         }
-        emit_unit<D, N, BF16, KV>(words, kind0, kind1, narrow, c, res, tok, len, tq, pow2(-ex), u, lane, meta,
-                                  SharedPut{base + (KV ? L::v : L::k) + s * L::kTileBytes});
+        emit_unit<D, N, BF16>(words, kind0, kind1, narrow, c, src, tok, pow2(-ex), u, lane, meta,
+                              SharedPut{base + (kv ? L::v : L::k) + s * L::kTileBytes});
         tc::fence_async_proxy();
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(base + L::bars + 8u * ((KV ? kVFull : kKFull) + s));
+        if (lane == 0) tc::bar_arrive(base + L::bars + 8u * ((kv ? kVFull : kKFull) + s));
     }
 }
 
@@ -140,9 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
 
     if (warp >= 8 && warp < 16) {
         tc::regs_give<88>();
-        const int u = (warp & 1) + (warp >= 12 ? 2 : 0);
-        if (warp & 2) unpack_role<D, N, BF16, 1, L>(a, work, exps, smem, base, u, lane, gave_up);
-        else unpack_role<D, N, BF16, 0, L>(a, work, exps, smem, base, u, lane, gave_up);
+        unpack_role<D, N, BF16, L>(a, work, exps, smem, base, warp >= 12, warp % 4, lane, gave_up);
     } else if (warp >= 16) {
         tc::regs_give<64>();
         if (warp == 16 && lane == 0 && work.n > 0) mma_role<D, L>(work, base, tmem, gave_up);

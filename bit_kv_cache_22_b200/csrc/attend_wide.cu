@@ -48,34 +48,13 @@ struct Staged {
 
 struct GlobalPut {
     unsigned char *tile;
-    template <int I>
-    __device__ __forceinline__ void at(int offset, uint32_t x, uint32_t y) const {
-        *reinterpret_cast<uint2 *>(tile + offset + I) = make_uint2(x, y);
+    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
+        *reinterpret_cast<uint2 *>(tile + offset) = make_uint2(x, y);
     }
     __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const {
         *reinterpret_cast<uint4 *>(tile + offset) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 };
-
-template <int D, int N, bool BF16, int KV>
-__device__ __forceinline__ void stage_unit(const AttendArgs &a, int slot, int h, int tok0, int u, int lane,
-                                           unsigned char *meta, unsigned char *tile, TileExps &exps) {
-    const PagedView &c = a.cache;
-    const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
-    const int tok = tok0 + 32 * u, pi = tok / c.P;
-    const int page = tok < tq && pi < c.max_pages ? c.page_table[static_cast<int64_t>(slot) * c.max_pages + pi] : -1;
-    Fetched<D, N> f;
-    fetch_unit<D, N, KV>(f, c, h, page, tok % c.P, tok, len, tq, true, lane);
-    const uint16_t *res = (KV ? c.vr : c.kr) + (static_cast<int64_t>(slot) * a.Hkv + h) * c.R * D;
-    int ex;
-    const bool narrow = prepare_unit<D, N, BF16, KV>(f, c, res, tok, len, tq, lane, meta, ex);
-    if (lane == 0) {
-        if (KV) exps.exp_v[u] = ex;
-        else exps.scale_k[u] = pow2(ex);
-    }
-    emit_unit<D, N, BF16, KV>(f.w, f.kind[0], f.kind[1], narrow, c, res, tok, len, tq, pow2(-ex), u, lane, meta,
-                              GlobalPut{tile});
-}
 
 // CTA (x, h): key tile x of the wide slots, or query tile x - n_kv_tiles.
 template <int D, int N, bool BF16>
@@ -89,10 +68,21 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const AttendArgs a
         if (tok0 < 0) return;
         const int64_t at = static_cast<int64_t>(x) * a.Hkv + h;
         unsigned char *tile = st.kv + at * 2 * Staged<D>::kTileBytes;
-        if (w < kUnits)
-            stage_unit<D, N, BF16, 0>(a, slot, h, tok0, w, lane, meta_s[w], tile, st.exps[at]);
-        else
-            stage_unit<D, N, BF16, 1>(a, slot, h, tok0, w - kUnits, lane, meta_s[w], tile + Staged<D>::kTileBytes, st.exps[at]);
+        const PagedView &c = a.cache;
+        const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
+        const int kv = w / kUnits, u = w % kUnits, tok = tok0 + 32 * u, pi = tok / c.P;
+        const int page = tok < tq && pi < c.max_pages ? c.page_table[static_cast<int64_t>(slot) * c.max_pages + pi] : -1;
+        const UnitSource<D> src(c, kv, slot, h, len, tq);
+        Fetched<D, N> f;
+        fetch_unit<D, N>(f, c, src, page, tok % c.P, tok, true, lane);
+        int ex;
+        const bool narrow = prepare_unit<D, N, BF16>(f, c, src, tok, lane, meta_s[w], ex);
+        if (lane == 0) {
+            if (kv) st.exps[at].exp_v[u] = ex;
+            else st.exps[at].scale_k[u] = pow2(ex);
+        }
+        emit_unit<D, N, BF16>(f.w, f.kind[0], f.kind[1], narrow, c, src, tok, pow2(-ex), u, lane, meta_s[w],
+                              GlobalPut{tile + kv * Staged<D>::kTileBytes});
     } else {
         const int x = blockIdx.x - a.t.n_kv_tiles, slot = slot_of(a.t.q_tiles, a.t.B, x);
         const int hg = a.Hq / a.Hkv, tpt = kRows / hg;

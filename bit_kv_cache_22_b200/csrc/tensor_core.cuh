@@ -64,9 +64,8 @@ __device__ __forceinline__ void fence_async_proxy() {
 }
 
 // Stores that loads of other shared memory may move across (no clobber); fences order them.
-template <int I>
 __device__ __forceinline__ void store_shared(uint32_t at, uint32_t a, uint32_t b) {
-    asm volatile("st.shared.v2.b32 [%0+%3], {%1, %2};" ::"r"(at), "r"(a), "r"(b), "n"(I));
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(a), "r"(b));
 }
 __device__ __forceinline__ void store_shared(uint32_t at, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]));
