@@ -517,8 +517,8 @@ __device__ __forceinline__ void init_bars(uint32_t bars, int queries, int filled
 
 // Tensor memory (512 columns): S0 | S1 | O0 | O1, P over the first half of its S.
 
-// Issues the CTA's MMAs (one thread).
-template <int D, class L>
+// Issues the CTA's MMAs (one thread).  WIDE: unrolled, for the kernel whose other code is small.
+template <int D, bool WIDE, class L>
 __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, uint32_t tmem, volatile int &gave_up) {
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
@@ -529,7 +529,7 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
     constexpr uint32_t kDescO = tc::mma_desc(kRows, D, false, false);
     auto issue_s = [&](int t, int s) {
         uint32_t qa = base + L::q + (alternate ? 0 : t) * L::kTileBytes, ka = base + L::k + s * L::kTileBytes;
-#pragma unroll 1
+#pragma unroll(WIDE ? D / 64 : 1)
         for (int i = 0; i < D / 64; ++i, qa += kRows * 128, ka += kRows * 128)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -549,12 +549,12 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
     for (int j = 0; j < n && go; ++j) {
         const int s = j % kStages, next = j + stride, s1 = next % kStages;
         go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
-#pragma unroll 1
+#pragma unroll(WIDE ? 2 : 1)
         for (int t = 0; t < 2 && go; ++t) {
             if (j >= (t ? n : work.end0) || (alternate && (j & 1) != t)) continue;
             const int i = alternate ? j / 2 : j;       // how many tiles the stream has had
             const uint32_t va = base + L::v + s * L::kTileBytes;
-#pragma unroll 1
+#pragma unroll(WIDE ? 2 : 1)
             for (int half = 0; half < 2; ++half) {         // the first weights while the others are taken
                 go = tc::bar_wait(bar(kPFull + 2 * half + t), i & 1, &gave_up);
                 if (!go) break;

@@ -142,6 +142,29 @@ __global__ void __launch_bounds__(32 * kReadWarps) chunk_read_kernel(const Paged
     }
 }
 
+// Packed query rows of slots with one new token each to dense [B][Hq][d] (TO_SLOTS; slots without one
+// get zeros), or dense fp32 outputs [B][Hq][d] to packed rows of e.  One CTA a slot.
+template <bool TO_SLOTS, bool BF16>
+__global__ void __launch_bounds__(kRowThreads) slot_rows_kernel(const ChunkTable t, const Rows rows, uint16_t *q,
+                                                                const float *out, int Hq, int d) {
+    const int b = blockIdx.x;
+    const int64_t row = t.offsets[b];
+    const bool has = t.offsets[b + 1] > row && row >= 0 && row < t.tokens;
+    const int vec = d / 8;
+    for (int i = threadIdx.x; i < Hq * vec; i += kRowThreads) {
+        const int h = i / vec, v = i - h * vec;
+        const int64_t at = (static_cast<int64_t>(b) * Hq + h) * vec + v;
+        uint4 *packed = reinterpret_cast<uint4 *>(rows.p + row * rows.ts + h * rows.hs) + v;
+        if constexpr (TO_SLOTS) {
+            reinterpret_cast<uint4 *>(q)[at] = has ? *packed : make_uint4(0u, 0u, 0u, 0u);
+        } else if (has) {
+            const float4 x = reinterpret_cast<const float4 *>(out)[2 * at], y = reinterpret_cast<const float4 *>(out)[2 * at + 1];
+            *packed = make_uint4(narrow2<BF16>(x.x, x.y), narrow2<BF16>(x.z, x.w), narrow2<BF16>(y.x, y.y),
+                                 narrow2<BF16>(y.z, y.w));
+        }
+    }
+}
+
 template <int D, int N>
 void read_launch(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v, unsigned grid, cudaStream_t s) {
     if (c.bf16) chunk_read_kernel<D, N, true><<<grid, 32 * kReadWarps, 0, s>>>(c, t, k, v);
@@ -156,6 +179,21 @@ cudaError_t launch_chunk_rows(const PagedView &c, const ChunkTable &t, const Row
     const unsigned grid = static_cast<unsigned>(t.tokens);
     if (c.bf16) chunk_rows_kernel<true><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
     else chunk_rows_kernel<false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rows_to_slots(const ChunkTable &t, const Rows &q, uint16_t *dense, int Hq, int d, cudaStream_t s) {
+    slot_rows_kernel<true, true><<<static_cast<unsigned>(t.B), kRowThreads, 0, s>>>(t, q, dense, nullptr, Hq, d);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_slots_to_rows(const ChunkTable &t, const float *dense, const Rows &o, int Hq, int d, bool bf16,
+                                 cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>(t.B);
+    if (bf16) slot_rows_kernel<false, true><<<grid, kRowThreads, 0, s>>>(t, o, nullptr, dense, Hq, d);
+    else slot_rows_kernel<false, false><<<grid, kRowThreads, 0, s>>>(t, o, nullptr, dense, Hq, d);
     count_launches(1);
     return cudaGetLastError();
 }

@@ -1165,7 +1165,8 @@ void split_pieces(std::vector<Piece> &pieces, int32_t kv_heads, int32_t num_sms)
 }
 
 kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t R, const int32_t *counts,
-                      const int32_t *starts, int32_t num_sms, kvq_chunk *out, void *table, size_t table_bytes) {
+                      const int32_t *starts, int32_t num_sms, size_t least_workspace, kvq_chunk *out, void *table,
+                      size_t table_bytes) {
     if (!counts || !out) return fail(KVQ_ERR_INVALID_ARG, "counts and out must be non-NULL");
     if (q_heads / kv_heads > 128)
         return fail(KVQ_ERR_UNSUPPORTED, "at most 128 query heads per kv head (got %d)", q_heads / kv_heads);
@@ -1237,6 +1238,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     out->table_bytes = static_cast<size_t>(l.end) * sizeof(int32_t);
     out->workspace = static_cast<size_t>(parts) * kv_heads * 128 * (d + 2) * sizeof(float) +
                      static_cast<size_t>(kvq::staged_bytes(kv_tiles, q_tiles, kv_heads, d));
+    if (out->workspace < least_workspace) out->workspace = least_workspace;
     out->counts = counts;
     out->starts = starts;
     if (!table) return ok();
@@ -1377,6 +1379,26 @@ kvq::PagedView paged_view(const kvq_paged *h) {
     return v;
 }
 
+// A decode step as a chunk: one new token, the newest, of every slot that holds any, and a decode
+// kernel on the tensor cores for the geometry.  There the codes are operands as they are stored, and
+// a step over 32 slots of 512 to 15872 tokens (32 query, 8 kv heads, d = 128, 2 bits) takes half the
+// narrow attention kernel's time; with 3 or 5 query heads per kv head the decode kernel has no tensor
+// cores and the narrow kernel is the faster one.
+bool is_decode_step(const kvq_paged *h, const kvq_chunk *p) {
+    const kvq_config &c = h->base.cfg;
+    if (h->base.path != kvq::kPathTc) return false;
+    for (int b = 0; b < p->batch; ++b) {
+        if (p->counts[b] > 1 || (p->counts[b] == 0 && h->len[b] > 0)) return false;
+        if (p->counts[b] == 1 && p->starts[b] + int64_t{1} != h->len[b]) return false;
+    }
+    return c.batch == p->batch;
+}
+
+// Scratch of a decode step: queries and outputs [B][Hq][d], then the splits' partial results.
+size_t decode_step_bytes(int64_t batch, int64_t q_heads, int64_t d, int64_t splits) {
+    return static_cast<size_t>(batch * q_heads * (d * 2 + d * 4 + splits * (d + 2) * 4));
+}
+
 kvq::AttendArgs attend_args(const kvq_chunk *p, const kvq_rows *q, const kvq_rows *o, bool bf16) {
     kvq::AttendArgs a{};
     a.t = chunk_table(p);
@@ -1402,7 +1424,13 @@ kvq_status kvq_plan_chunk(const kvq_paged_config *cfg, const int32_t *counts, co
     if (!starts) return fail(KVQ_ERR_INVALID_ARG, "starts is NULL");
     if (num_sms < 1) return fail(KVQ_ERR_INVALID_ARG, "num_sms must be >= 1");
     const kvq_config &g = cfg->geom;
-    return plan_chunk(g.batch, g.q_heads, g.kv_heads, g.head_dim, g.residual, counts, starts, num_sms, out, table,
+    // single tokens may go through the decode kernel, with the splits it would take
+    size_t step = 0;
+    bool single = counts != nullptr;
+    for (int b = 0; single && b < g.batch; ++b) single = counts[b] == 0 || counts[b] == 1;
+    if (single && kvq::decode_path(g.q_heads, g.kv_heads, g.group_k, false) == kvq::kPathTc)
+        step = decode_step_bytes(g.batch, g.q_heads, g.head_dim, max_splits(&g));
+    return plan_chunk(g.batch, g.q_heads, g.kv_heads, g.head_dim, g.residual, counts, starts, num_sms, step, out, table,
                       table_bytes);
 }
 
@@ -1413,7 +1441,7 @@ kvq_status kvq_plan_prompt(int32_t batch, int32_t q_heads, int32_t kv_heads, int
     if (batch > 65535 || q_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "batch and q_heads must be <= 65535");
     if (head_dim != 64 && head_dim != 128)
         return fail(KVQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
-    return plan_chunk(batch, q_heads, kv_heads, head_dim, 0, counts, nullptr, 1, out, table, table_bytes);
+    return plan_chunk(batch, q_heads, kv_heads, head_dim, 0, counts, nullptr, 1, 0, out, table, table_bytes);
 }
 
 kvq_status kvq_prompt_attention(const kvq_chunk *plan, int32_t dtype, const kvq_rows *q, const kvq_rows *k,
@@ -1522,6 +1550,27 @@ kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const 
     if (st != KVQ_OK) return st;
     if (plan->workspace > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < plan->workspace))
         return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold %zu bytes", plan->workspace);
+    if (is_decode_step(h, plan)) {
+        const kvq_config &c = h->base.cfg;
+        const int64_t units = static_cast<int64_t>(c.batch) * c.q_heads;
+        kvq::DecodeArgs d = paged_decode_args(h);
+        paged_plan(h, &d.n_qsplits, &d.tiles_per_split, &d.S);
+        float *out = static_cast<float *>(workspace);
+        d.out = out;
+        uint16_t *dense = reinterpret_cast<uint16_t *>(out + units * c.head_dim);
+        d.q = dense;
+        d.o_part = reinterpret_cast<float *>(dense + units * c.head_dim);
+        d.m_part = d.o_part + units * d.S * c.head_dim;
+        d.l_part = d.m_part + units * d.S;
+        const kvq::ChunkTable t = chunk_table(plan);
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        cudaError_t e = kvq::launch_rows_to_slots(t, rows_of(q), dense, c.q_heads, c.head_dim, s);
+        if (e == cudaSuccess) e = kvq::launch_decode(d, s);
+        if (e == cudaSuccess)
+            e = kvq::launch_slots_to_rows(t, out, rows_of(o), c.q_heads, c.head_dim, c.dtype == KVQ_BF16, s);
+        if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+        return ok();
+    }
     kvq::AttendArgs a = attend_args(plan, q, o, h->base.cfg.dtype == KVQ_BF16);
     a.cache = paged_view(h);
     a.part_tiles = plan->part_tiles;

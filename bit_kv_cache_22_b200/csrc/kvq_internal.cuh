@@ -243,6 +243,12 @@ cudaError_t launch_chunk_rows(const PagedView &c, const ChunkTable &t, const Row
 // The new tokens as the cache holds them, widened to e.  One launch.
 cudaError_t launch_chunk_read(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v, cudaStream_t s);
 
+// Between packed rows of slots with at most one new token each and the decode kernels' dense
+// [B][Hq][d]: queries to e, fp32 outputs from.  One launch each.
+cudaError_t launch_rows_to_slots(const ChunkTable &t, const Rows &q, uint16_t *dense, int Hq, int d, cudaStream_t s);
+cudaError_t launch_slots_to_rows(const ChunkTable &t, const float *dense, const Rows &o, int Hq, int d, bool bf16,
+                                 cudaStream_t s);
+
 struct AttendArgs {
     ChunkTable t;
     Rows q, o;
