@@ -15,8 +15,10 @@
 #include <cstring>
 #include <algorithm>
 #include <atomic>
+#include <functional>
 #include <mutex>
 #include <new>
+#include <queue>
 #include <string>
 #include <utility>
 #include <vector>
@@ -1139,28 +1141,63 @@ struct Piece {
 };
 
 // Splits of the pieces over their keys, of the narrow and the wide slots apart (they are launches of
-// their own): a CTA's share is at most `share` key tiles.  A CTA's start and end cost a few tiles'
-// time (and a wide piece's partial results 128 KB a split), so a share is not below its least, and
-// pieces that give every SM a CTA or more are left whole when they are wide.
-constexpr int64_t kMinShare = 16, kSharesPerSm = 4, kMinWideShare = 24;
+// their own): a CTA's share is at most `share` key tiles, and the share is the one among a few whose
+// CTAs, longest first on the least busy SM (one CTA each), end soonest.  In key tiles' time: a CTA
+// costs kCtaTiles more than its share, a split one kSplitTiles (its partial results, and joining
+// them).
+constexpr int64_t kCtaTiles = 4, kSplitTiles = 4, kLeastShare = 8;
+constexpr size_t kMostSimulated = 4096;
 
 void split_pieces(std::vector<Piece> &pieces, int32_t kv_heads, int32_t num_sms) {
     for (const bool wide : {false, true}) {
-        int64_t total = 0, n = 0;
-        for (const Piece &p : pieces)
-            if (p.wide == wide) {
-                total += p.tiles * kv_heads;
-                n += kv_heads;
-            }
-        if (n == 0 || (wide && n >= num_sms)) continue;
-        const int64_t shares = num_sms * (wide ? 1 : kSharesPerSm), least = wide ? kMinWideShare : kMinShare;
-        int64_t share = (total + shares - 1) / shares;
-        if (share < least) share = least;
+        std::vector<Piece *> own;
+        int64_t total = 0, longest = 0;
         for (Piece &p : pieces)
             if (p.wide == wide) {
-                const int64_t k = (p.tiles + share - 1) / share;
-                p.splits = static_cast<int32_t>(k < 1 ? 1 : k > 1024 ? 1024 : k);
+                own.push_back(&p);
+                total += p.tiles * kv_heads;
+                longest = std::max(longest, p.tiles);
             }
+        if (own.empty()) continue;
+        std::sort(own.begin(), own.end(), [](const Piece *x, const Piece *y) { return x->tiles > y->tiles; });
+        auto parts = [](const Piece &p, int64_t share) {
+            const int64_t k = (p.tiles + share - 1) / share;
+            return k < 1 ? int64_t{1} : k > 1024 ? int64_t{1024} : k;
+        };
+        int64_t best_share = longest > 0 ? longest : 1, best_time = -1;
+        std::vector<int64_t> jobs;
+        for (int64_t k = 0; k <= 8; ++k) {         // 0: whole pieces
+            const int64_t even = k ? (total + num_sms * k - 1) / (num_sms * k) : longest;
+            const int64_t share = std::max(even, kLeastShare);
+            jobs.clear();
+            for (const Piece *p : own) {
+                const int64_t n = parts(*p, share);
+                const int64_t time = (p->tiles + n - 1) / n + kCtaTiles + (n > 1 ? kSplitTiles : 0);
+                if (jobs.size() + n * kv_heads > kMostSimulated) {
+                    jobs.clear();
+                    break;
+                }
+                jobs.insert(jobs.end(), static_cast<size_t>(n * kv_heads), time);
+            }
+            if (jobs.empty()) break;               // plenty of work: whole pieces even out
+            std::sort(jobs.begin(), jobs.end(), std::greater<int64_t>());
+            std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> busy;
+            int64_t end = 0;
+            for (const int64_t t : jobs) {
+                int64_t from = 0;
+                if (static_cast<int64_t>(busy.size()) == num_sms) {
+                    from = busy.top();
+                    busy.pop();
+                }
+                busy.push(from + t);
+                end = std::max(end, from + t);
+            }
+            if (best_time < 0 || end < best_time) {
+                best_time = end;
+                best_share = share;
+            }
+        }
+        for (Piece *p : own) p->splits = static_cast<int32_t>(parts(*p, best_share));
     }
 }
 

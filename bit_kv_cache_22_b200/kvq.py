@@ -427,27 +427,18 @@ class KVQCache:
         return dev_out
 
 
-class _Call:
-    """One call's device and stream: the device is current and its stream is torch's current one,
-    so what the call allocates belongs to the stream its kernels run on."""
+def _on(device: torch.device, stream, call):
+    """call(stream pointer) with the device current and its stream torch's current one, so that what
+    the call allocates belongs to the stream its kernels run on."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(_raw_stream(device.index))
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream must be one of {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(_raw_stream(device.index))
 
-    def __init__(self, device: torch.device, stream=None):
-        self.device, self.stream, self.guards = device, stream, ()
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.guards = (torch.cuda.device(self.device),)
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError(f"the stream must be one of {self.device}")
-            self.guards += (torch.cuda.stream(self.stream),)
-        for g in self.guards:
-            g.__enter__()
-        return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+_raw_stream = torch._C._cuda_getCurrentRawStream    # of a device index, without a Stream object's cost
 
 
 def _servable(t: torch.Tensor) -> bool:
@@ -461,13 +452,13 @@ def _servable(t: torch.Tensor) -> bool:
 def _packed(t: torch.Tensor, name: str, tokens: int, heads: int, d: int, dtype, device) -> torch.Tensor:
     """Packed rows as a kernel takes them: checked, on the device, channels contiguous, rows on 16
     bytes (copied where they are not)."""
-    if tuple(t.shape) != (tokens, heads, d):
+    if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}]")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         t = t.to(device, non_blocking=True)
-    if t.numel() and not _servable(t):
+    if tokens and not _servable(t):
         t = t.contiguous()
         if not _servable(t):
             t = t.clone()
@@ -485,7 +476,8 @@ def _output(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
 
 
 def _rows(t: torch.Tensor):
-    return ctypes.byref(Rows(t.data_ptr(), t.stride(0), t.stride(1)))
+    a, b, _ = t.stride()
+    return ctypes.byref(Rows(t.data_ptr(), a, b))
 
 
 class Rope:
@@ -534,6 +526,7 @@ class ChunkPlan:
         host = torch.empty(self.chunk.table_bytes // 4, dtype=torch.int32)
         _check(fill(host.data_ptr(), self.chunk.table_bytes))
         self.tokens = self.chunk.tokens
+        self.ends = [(b, s + n) for b, (s, n) in enumerate(zip(self.starts, self.counts)) if n]
         self.offsets = host[:batch + 1].tolist()
         self.table = host.to(self.device)
         self.chunk.table = self.table.data_ptr()
@@ -548,16 +541,17 @@ def prompt_attention(plan: ChunkPlan, q: torch.Tensor, k: torch.Tensor, v: torch
                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Causal attention over packed prompts (kvq_prompt_attention): q [tokens, Hq, d], k, v
     [tokens, Hkv, d] (fp16 or bf16, strided views welcome) -> e [tokens, Hq, d]."""
-    c = plan.chunk
+    c, device, n = plan.chunk, plan.device, plan.tokens
     code = _dtype_code(q.dtype)
-    with _Call(plan.device, stream) as s:
-        q = _packed(q, "q", plan.tokens, c.q_heads, c.head_dim, q.dtype, plan.device)
-        k = _packed(k, "k", plan.tokens, c.kv_heads, c.head_dim, q.dtype, plan.device)
-        v = _packed(v, "v", plan.tokens, c.kv_heads, c.head_dim, q.dtype, plan.device)
-        out = _output(out, q.shape, q.dtype, plan.device)
-        _check(load().kvq_prompt_attention(plan.ref, code, _rows(q), _rows(k), _rows(v), _rows(out), None,
-                                           s.cuda_stream))
-        return out
+
+    def call(raw):
+        rows = [_packed(t, name, n, heads, c.head_dim, q.dtype, device)
+                for t, name, heads in ((q, "q", c.q_heads), (k, "k", c.kv_heads), (v, "v", c.kv_heads))]
+        o = _output(out, q.shape, q.dtype, device)
+        _check(load().kvq_prompt_attention(plan.ref, code, *map(_rows, rows), _rows(o), None, raw))
+        return o
+
+    return _on(device, stream, call)
 
 
 class PagedKVQCache:
@@ -741,54 +735,71 @@ class PagedKVQCache:
         """Append the planned tokens t_K, t_V [tokens, Hkv, d] (kvq_paged_append_chunk), keys
         rotated when `rope` is given; with t_Q [tokens, Hq, d], returns the rotated queries (in
         `out` when given), else None."""
-        g = self.geom
-        with _Call(self.device, stream) as s:
-            t_K = _packed(t_K, "t_K", plan.tokens, g.kv_heads, g.head_dim, self.dtype, self.device)
-            t_V = _packed(t_V, "t_V", plan.tokens, g.kv_heads, g.head_dim, self.dtype, self.device)
+        g, device, dtype, n = self.geom, self.device, self.dtype, plan.tokens
+
+        def call(raw):
+            k = _packed(t_K, "t_K", n, g.kv_heads, g.head_dim, dtype, device)
+            v = _packed(t_V, "t_V", n, g.kv_heads, g.head_dim, dtype, device)
+            q = q_out = None
             if t_Q is not None:
-                t_Q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
-                out = _output(out, t_Q.shape, self.dtype, self.device)
-            if rope is not None and rope.cos.device != self.device:
-                raise ValueError(f"the angles must be on {self.device}")
-            need = {}
-            for b, (start, n) in enumerate(zip(plan.starts, plan.counts)):
-                held = max(self.lens[b], 0)
-                whole = (start + n) // g.residual * g.residual
-                if n and start <= held and whole <= g.capacity:
-                    need[b] = -(-whole // self.page_tokens)
-            if sum(max(0, n - len(self.pages[b])) for b, n in need.items()) > len(self.free_pages):
-                raise KVQError(KVQ_ERR_CAPACITY, "the page pool is exhausted")
-            self._grow(need, s)
+                q = _packed(t_Q, "t_Q", n, g.q_heads, g.head_dim, dtype, device)
+                q_out = _output(out, q.shape, dtype, device)
+            if rope is not None and rope.cos.device != device:
+                raise ValueError(f"the angles must be on {device}")
+            if plan.chunk.blocks:
+                self._pages_for(plan, stream)
             _check(self._lib.kvq_paged_append_chunk(
-                self._h, plan.ref, _rows(t_K), _rows(t_V), None if rope is None else rope.ref,
-                None if t_Q is None else _rows(t_Q), None if t_Q is None else _rows(out), s.cuda_stream))
-            for b, (start, n) in enumerate(zip(plan.starts, plan.counts)):
-                if n:
-                    self.lens[b] = start + n
-            return out if t_Q is not None else None
+                self._h, plan.ref, _rows(k), _rows(v), None if rope is None else rope.ref,
+                None if q is None else _rows(q), None if q is None else _rows(q_out), raw))
+            for b, end in plan.ends:
+                self.lens[b] = end
+            return q_out
+
+        return _on(device, stream, call)
+
+    def _pages_for(self, plan: ChunkPlan, stream):
+        """Pages for the blocks the planned tokens complete (the library refuses a plan whose slots do
+        not fit; those get none here)."""
+        g, need, short = self.geom, {}, 0
+        for b, end in plan.ends:
+            whole = end // g.residual * g.residual
+            pages = -(-whole // self.page_tokens)
+            if pages > len(self.pages[b]) and plan.starts[b] <= max(self.lens[b], 0) and whole <= g.capacity:
+                need[b] = pages
+                short += pages - len(self.pages[b])
+        if short > len(self.free_pages):
+            raise KVQError(KVQ_ERR_CAPACITY, "the page pool is exhausted")
+        if need:
+            self._grow(need, stream)
 
     def read_chunk(self, plan: ChunkPlan, stream=None):
         """(k, v) [tokens, Hkv, d]: the planned tokens as the cache holds them."""
         g = self.geom
-        with _Call(self.device, stream) as s:
+
+        def call(raw):
             k = torch.empty((plan.tokens, g.kv_heads, g.head_dim), dtype=self.dtype, device=self.device)
             v = torch.empty_like(k)
-            _check(self._lib.kvq_paged_read_chunk(self._h, plan.ref, _rows(k), _rows(v), s.cuda_stream))
+            _check(self._lib.kvq_paged_read_chunk(self._h, plan.ref, _rows(k), _rows(v), raw))
             return k, v
+
+        return _on(self.device, stream, call)
 
     def chunk_attention(self, plan: ChunkPlan, t_Q: torch.Tensor, out: torch.Tensor | None = None, stream=None):
         """Attention of the planned tokens' queries t_Q [tokens, Hq, d] over the cache, which holds
         them: the token at position p sees tokens 0 .. p.  Returns e [tokens, Hq, d]."""
         g = self.geom
-        with _Call(self.device, stream) as s:
-            t_Q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
-            out = _output(out, t_Q.shape, self.dtype, self.device)
+
+        def call(raw):
+            q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
+            o = _output(out, q.shape, self.dtype, self.device)
             # scratch of the call's own, from torch's pool of its stream (or graph)
             room = plan.chunk.workspace
             work = torch.empty(room, dtype=torch.uint8, device=self.device) if room else None
-            _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, _rows(t_Q), _rows(out),
-                                                       work.data_ptr() if room else None, room, s.cuda_stream))
-            return out
+            _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, _rows(q), _rows(o),
+                                                       work.data_ptr() if room else None, room, raw))
+            return o
+
+        return _on(self.device, stream, call)
 
     def release(self, seq: int, stream=None):
         """End slot `seq`: it becomes inactive and its pages return to the free list (reused by
