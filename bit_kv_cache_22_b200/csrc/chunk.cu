@@ -9,7 +9,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
 // One CTA per new token: its residual rows (keys rotated) when it lies behind its slot's last
 // whole block, and its rotated queries.  The rows of a block's first tokens (positions below
@@ -32,20 +32,33 @@ __global__ void __launch_bounds__(kRowThreads) chunk_rows_kernel(const PagedView
     const RowUnits ru = row_units(c.d, rope), plain = {0, c.d / 8};
     const int n_k = tok >= end / c.R * c.R ? c.Hkv * ru.n : 0, n_v = n_k ? c.Hkv * plain.n : 0;
     const int n_q = q.p ? c.Hq * ru.n : 0;
-    for (int i = threadIdx.x; i < n_k + n_v + n_q; i += kRowThreads) {
-        const bool is_k = i < n_k, is_q = i >= n_k + n_v;
-        const int j = is_k ? i : is_q ? i - n_k - n_v : i - n_k;
-        const int per = is_k || is_q ? ru.n : plain.n;
-        const int h = j / per, u = j - h * per;
-        const Rows &in = is_k ? k : is_q ? q : v;
-        uint16_t *dst = is_q ? q_out.p + row * q_out.ts + h * q_out.hs
-                             : (is_k ? c.kr : c.vr) + ((static_cast<int64_t>(b) * c.Hkv + h) * c.R + tok % c.R) * c.d;
-        int va, vb;
-        uint4 x, y;
-        rotated_unit<BF16>(in.p + row * in.ts + h * in.hs, u, is_k || is_q ? ru : plain, tok,
-                           is_k || is_q ? rope : RopeArgs{}, va, vb, x, y);
-        reinterpret_cast<uint4 *>(dst)[va] = x;
-        if (vb >= 0) reinterpret_cast<uint4 *>(dst)[vb] = y;
+    const int64_t res_row = static_cast<int64_t>(b) * c.Hkv * c.R + tok % c.R;
+    for (int i0 = threadIdx.x; i0 < n_k + n_v + n_q; i0 += 2 * kRowThreads) {
+        LoadedUnit unit[2];
+        uint16_t *dst[2];
+        bool turn[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {              // two units' loads in flight
+            const int i = i0 + x * kRowThreads;
+            dst[x] = nullptr;
+            if (i >= n_k + n_v + n_q) continue;
+            const bool is_k = i < n_k, is_q = i >= n_k + n_v;
+            const int j = is_k ? i : is_q ? i - n_k - n_v : i - n_k;
+            turn[x] = is_k || is_q;
+            const RowUnits &of = turn[x] ? ru : plain;
+            const int h = j / of.n, u = j - h * of.n;
+            const Rows &in = is_k ? k : is_q ? q : v;
+            dst[x] = is_q ? q_out.p + row * q_out.ts + h * q_out.hs
+                          : (is_k ? c.kr : c.vr) + (res_row + static_cast<int64_t>(h) * c.R) * c.d;
+            unit[x] = load_unit(in.p + row * in.ts + h * in.hs, u, of);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (!dst[x]) continue;
+            if (turn[x]) rotate_unit<BF16>(unit[x], tok, rope);
+            __stcs(reinterpret_cast<uint4 *>(dst[x]) + unit[x].va, unit[x].a);
+            if (unit[x].vb >= 0) __stcs(reinterpret_cast<uint4 *>(dst[x]) + unit[x].vb, unit[x].b);
+        }
     }
 }
 
@@ -98,36 +111,55 @@ __global__ void __launch_bounds__(32 * kReadWarps) chunk_read_kernel(const Paged
         const uint32_t *vw = c.vc + (slice * (c.P / 16) + pt / 16) * TW + lane * W;
         const float *s_k = c.ks + (slice * (c.P / c.G) + pt / c.G) * D;
         const int16_t *z_k = c.kz + (slice * (c.P / c.G) + pt / c.G) * D;
-        const int ngv = D / c.Gv, half_levels = 1 << (N - 1);
+        const int ngv = D / c.Gv;
         const float *s_v = c.vs + (slice * c.P + pt) * ngv;
         const int16_t *z_v = c.vz + (slice * c.P + pt) * ngv;
+        constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
+        constexpr float kHalf = static_cast<float>(1 << (N - 1));
+        // four codes (the bytes of b), minus z, times s
+        auto values = [](uint32_t b, const float (&z)[4], const float (&s)[4], float (&f)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {          // (2^23 + code) - (2^23 + z) is exact
+                const float x = __uint_as_float(__byte_perm(b, 0x4b000000u, 0x7540 + e));
+                f[e] = __fmul_rn(__fadd_rn(x, z[e]), s[e]);
+            }
+        };
+        float sv[4], zv[4];
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             const uint32_t kword = kw[j / B], vword = vw[j / B];
+            const float4 s4 = reinterpret_cast<const float4 *>(s_k)[4 * j + (lane & 3)];
+            const float sk[4] = {s4.x, s4.y, s4.z, s4.w};
+            float zk[4] = {-8388608.0f - kHalf, -8388608.0f - kHalf, -8388608.0f - kHalf, -8388608.0f - kHalf};
+            if (!c.sym) {
+                const uint2 z4 = reinterpret_cast<const uint2 *>(z_k)[4 * j + (lane & 3)];
+                zk[0] = -8388608.0f - static_cast<float>(static_cast<int16_t>(z4.x & 0xffffu));
+                zk[1] = -8388608.0f - static_cast<float>(static_cast<int>(z4.x) >> 16);
+                zk[2] = -8388608.0f - static_cast<float>(static_cast<int16_t>(z4.y & 0xffffu));
+                zk[3] = -8388608.0f - static_cast<float>(static_cast<int>(z4.y) >> 16);
+            }
+            if (j == 0 || ((16 * j) & (c.Gv - 1)) == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = (4 * (lane & 3) + e) * ngv + 16 * j / c.Gv;
+                    sv[e] = s_v[at];
+                    zv[e] = -8388608.0f - (c.sym ? kHalf : static_cast<float>(z_v[at]));
+                }
+            }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int sh = N * (2 * (j % B) + half);
                 const int row = (lane >> 2) + 8 * half;       // token of a key, channel of a value
-                uint32_t out[2];
                 float f[4];
+                values((kword >> sh) & kMask, zk, sk, f);
+                *reinterpret_cast<uint2 *>(&ks[row][16 * j + 4 * (lane & 3)]) =
+                    make_uint2(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]));
+                values((vword >> sh) & kMask, zv, sv, f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int ch = 16 * j + 4 * (lane & 3) + e;
-                    const int code = (kword >> (8 * e + sh)) & ((1 << N) - 1);
-                    const int z = c.sym ? half_levels : z_k[ch];
-                    f[e] = __fmul_rn(static_cast<float>(code - z), s_k[ch]);
-                }
-                out[0] = narrow2<BF16>(f[0], f[1]);
-                out[1] = narrow2<BF16>(f[2], f[3]);
-                *reinterpret_cast<uint2 *>(&ks[row][16 * j + 4 * (lane & 3)]) = make_uint2(out[0], out[1]);
-                const int vch = 16 * j + row, g = vch / c.Gv;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int tk = 4 * (lane & 3) + e;
-                    const int code = (vword >> (8 * e + sh)) & ((1 << N) - 1);
-                    const int z = c.sym ? half_levels : z_v[tk * ngv + g];
-                    vs[tk][vch] = static_cast<uint16_t>(
-                        narrow2<BF16>(__fmul_rn(static_cast<float>(code - z), s_v[tk * ngv + g]), 0.0f));
+                for (int e = 0; e < 4; e += 2) {
+                    const uint32_t two = narrow2<BF16>(f[e], f[e + 1]);
+                    vs[4 * (lane & 3) + e][16 * j + row] = static_cast<uint16_t>(two);
+                    vs[4 * (lane & 3) + e + 1][16 * j + row] = static_cast<uint16_t>(two >> 16);
                 }
             }
         }

@@ -51,15 +51,27 @@ __device__ __forceinline__ uint4 read_once(const uint16_t *src, int v) {
     return __ldcs(reinterpret_cast<const uint4 *>(src) + v);
 }
 
-// Unit u of the row at src, rotated by token tok's angles: vectors va, and vb when vb >= 0.
-template <bool BF16>
-__device__ __forceinline__ void rotated_unit(const uint16_t *src, int u, const RowUnits &ru, int64_t tok,
-                                             const RopeArgs &r, int &va, int &vb, uint4 &a, uint4 &b) {
+// Unit u of the row at src: vectors va, and vb when vb >= 0.
+struct LoadedUnit {
+    uint4 a, b;
+    int va, vb;
+};
+__device__ __forceinline__ LoadedUnit load_unit(const uint16_t *src, int u, const RowUnits &ru) {
+    LoadedUnit x;
     const bool pair = u < ru.pairs;
-    va = pair ? u : u + ru.pairs;
-    vb = pair ? u + ru.pairs : -1;
-    a = read_once(src, va);
-    if (pair) b = read_once(src, vb);
+    x.va = pair ? u : u + ru.pairs;
+    x.vb = pair ? u + ru.pairs : -1;
+    x.a = read_once(src, x.va);
+    if (pair) x.b = read_once(src, x.vb);
+    return x;
+}
+
+// The unit rotated by token tok's angles.
+template <bool BF16>
+__device__ __forceinline__ void rotate_unit(LoadedUnit &unit, int64_t tok, const RopeArgs &r) {
+    uint4 &a = unit.a, &b = unit.b;
+    const int va = unit.va;
+    const bool pair = unit.vb >= 0;
     if (!r.cos || 8 * va >= r.rot) return;
     const int half = r.rot / 2;
     const int64_t at = tok < r.positions ? tok : r.positions - 1;   // the host has refused later ones

@@ -1145,6 +1145,12 @@ struct Piece {
 // CTAs, longest first on the least busy SM (one CTA each), end soonest.  In key tiles' time: a CTA
 // costs kCtaTiles more than its share, a split one kSplitTiles (its partial results, and joining
 // them).
+// A slot of at most this many query rows (tokens x query heads of a kv head) is narrow: its codes are
+// unpacked where they are used.  With more, its softmax fills more than a warp a stream, which
+// unpacking beside it slows down: two slots of 66 and 105 rows over 2000 tokens, 32 heads, beside four
+// wide ones took 84 us as a launch of their own, with the joining of its splits, and 43 us among the
+// wide ones.
+constexpr int64_t kNarrowRows = 32;
 constexpr int64_t kCtaTiles = 4, kSplitTiles = 4, kLeastShare = 8;
 constexpr size_t kMostSimulated = 4096;
 
@@ -1209,6 +1215,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         return fail(KVQ_ERR_UNSUPPORTED, "at most 128 query heads per kv head (got %d)", q_heads / kv_heads);
     // a CTA's two query tiles of 128 rows: tokens x the query heads of one kv head
     const int64_t tile_tokens = 128 / (q_heads / kv_heads);
+    auto is_wide = [&](int64_t n) { return R > 0 && n * (q_heads / kv_heads) > kNarrowRows; };
     int64_t tokens = 0, blocks = 0, tiles = 0, n_pieces = 0, kv_tiles = 0, q_tiles = 0;
     for (int b = 0; b < batch; ++b) {
         const int64_t n = counts[b], s = starts ? starts[b] : 0;
@@ -1221,7 +1228,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         if (R > 0) {
             blocks += (s + n) / R - s / R;
             tiles += (s + n + 15) / 16 - s / 16;
-            if (n > tile_tokens) {
+            if (is_wide(n)) {
                 kv_tiles += (s + n + 127) / 128;
                 q_tiles += (n + tile_tokens - 1) / tile_tokens;
             }
@@ -1238,7 +1245,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         for (int64_t i = 0; i < n; i += 2 * tile_tokens) {
             const int64_t last = i + 2 * tile_tokens < n ? i + 2 * tile_tokens : n;
             pieces.push_back({b, static_cast<int32_t>(i), (s + last + 127) / 128, last - i <= tile_tokens,
-                              R > 0 && n > tile_tokens, 1});
+                              is_wide(n), 1});
         }
     }
     if (R > 0) split_pieces(pieces, kv_heads, num_sms);
@@ -1290,7 +1297,7 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         t[l.tiles + b] = tile;
         t[l.kv_tiles + b] = kv;
         t[l.q_tiles + b] = qt;
-        if (R > 0 && n > tile_tokens) {
+        if (is_wide(n)) {
             kv += static_cast<int32_t>((s + n + 127) / 128);
             qt += static_cast<int32_t>((n + tile_tokens - 1) / tile_tokens);
         }

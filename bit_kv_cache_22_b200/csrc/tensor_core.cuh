@@ -22,33 +22,37 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// One poll, suspended for at most about a microsecond.
+// (no suspend-time hint: with one of 1 us the waits ended late enough to cost a third of the attention
+// kernels' speed)
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
         : "r"(bar), "r"(parity)
         : "memory");
     return done != 0;
 }
-// Waits for the barrier's phase `parity`; gives up after about two seconds of polls, or as soon as
-// another role of the CTA gave up, and then raises *gave_up (shared).
-constexpr int kPolls = 1 << 21;
+// Waits for the barrier's phase `parity`; gives up after about two seconds, or as soon as another
+// role of the CTA gave up, and then raises *gave_up (shared).
+constexpr long long kWaitCycles = 4000000000LL;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    if (bar_test(bar, parity)) return true;
+    const long long t0 = clock64();
 #pragma unroll 1
-    for (int polls = 0; !bar_test(bar, parity); ++polls) {
-        if (polls == kPolls) *gave_up = 1;
+    while (!bar_test(bar, parity)) {
+        if (clock64() - t0 > kWaitCycles) *gave_up = 1;
         if (*gave_up) return false;
     }
     return true;
 }
 // The same on the way out, whatever gave up before.
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+    const long long t0 = clock64();
 #pragma unroll 1
-    for (int polls = 0; polls < kPolls && !bar_test(bar, parity); ++polls) {
+    while (!bar_test(bar, parity) && clock64() - t0 < kWaitCycles) {
     }
 }
 // bar_wait for a whole warp: every lane gets the answer all lanes agree on.

@@ -43,7 +43,7 @@ def test_table_of_random_plans():
         assert t[2 * B + 1:3 * B + 2] == [sum(tiles[:b]) for b in range(B + 1)] and out.read_tiles == sum(tiles)
         blocks = [(b, i) for b in range(B) if counts[b]
                   for i in range(starts[b] // R, (starts[b] + counts[b]) // R)]
-        wide = [n > 32 for n in counts]             # more than one query tile of 128 rows: 4 heads a token
+        wide = [4 * n > 32 for n in counts]         # 4 query heads a kv head: more than 32 query rows
         kv = [-(-(s + n) // 128) * w for s, n, w in zip(starts, counts, wide)]
         q = [-(-n // 32) * w for n, w in zip(counts, wide)]
         assert t[3 * B + 2:4 * B + 3] == [sum(kv[:b]) for b in range(B + 1)] and out.kv_tiles == sum(kv)
