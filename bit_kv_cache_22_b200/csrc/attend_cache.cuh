@@ -517,11 +517,12 @@ __device__ __forceinline__ void init_bars(uint32_t bars, int queries, int filled
 
 // Tensor memory (512 columns): S0 | S1 | O0 | O1, P over the first half of its S.
 
-// Issues the CTA's MMAs (one thread).  WIDE: unrolled, for the kernel whose other code is small.
+// Issues the CTA's MMAs (a whole warp).  WIDE: unrolled, for the kernel whose other code is small.
 template <int D, bool WIDE, class L>
 __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, uint32_t tmem, volatile int &gave_up) {
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
+    const uint32_t leader = tc::elect_leader();
     const int n = work.n;
     const bool alternate = work.alternate;
     const int stride = alternate ? 2 : 1;          // of a stream's tiles
@@ -533,22 +534,22 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
         for (int i = 0; i < D / 64; ++i, qa += kRows * 128, ka += kRows * 128)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                tc::mma_ss(tmem + t * 128, tc::desc_k_major(qa + 32 * k), tc::desc_k_major(ka + 32 * k), kDescS, i + k > 0);
-        tc::mma_commit(bar(kSFull + t));
+                tc::mma_ss(tmem + t * 128, tc::desc_k_major(qa + 32 * k), tc::desc_k_major(ka + 32 * k), kDescS, i + k > 0, leader);
+        tc::mma_commit(bar(kSFull + t), leader);
     };
-    bool go = tc::bar_wait(bar(kQFull), 0, &gave_up);
+    bool go = tc::bar_wait_warp(bar(kQFull), 0, &gave_up);
 #pragma unroll 1
     for (int t = 0; t < 2 && go; ++t) {
         const int j = alternate ? t : 0;   // the stream's first tile
         if (j < (t ? n : work.end0)) {
-            go = tc::bar_wait(bar(kKFull + j % kStages), (j / kStages) & 1, &gave_up);
+            go = tc::bar_wait_warp(bar(kKFull + j % kStages), (j / kStages) & 1, &gave_up);
             if (go) issue_s(t, j % kStages);
         }
-        if (go && (alternate ? j < n : t == 1)) tc::mma_commit(bar(kKEmpty + j % kStages));
+        if (go && (alternate ? j < n : t == 1)) tc::mma_commit(bar(kKEmpty + j % kStages), leader);
     }
     for (int j = 0; j < n && go; ++j) {
         const int s = j % kStages, next = j + stride, s1 = next % kStages;
-        go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
+        go = tc::bar_wait_warp(bar(kVFull + s), (j / kStages) & 1, &gave_up);
 #pragma unroll(WIDE ? 2 : 1)
         for (int t = 0; t < 2 && go; ++t) {
             if (j >= (t ? n : work.end0) || (alternate && (j & 1) != t)) continue;
@@ -556,29 +557,29 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
             const uint32_t va = base + L::v + s * L::kTileBytes;
 #pragma unroll(WIDE ? 2 : 1)
             for (int half = 0; half < 2; ++half) {         // the first weights while the others are taken
-                go = tc::bar_wait(bar(kPFull + 2 * half + t), i & 1, &gave_up);
+                go = tc::bar_wait_warp(bar(kPFull + 2 * half + t), i & 1, &gave_up);
                 if (!go) break;
                 tc::fence_after_sync();
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 32 * half + 8 * k,
-                               tc::desc_k_major(va + half * (D * 128) + k * 32), kDescO, i > 0 || half > 0 || k > 0);
+                               tc::desc_k_major(va + half * (D * 128) + k * 32), kDescO, i > 0 || half > 0 || k > 0, leader);
             }
             if (!go) break;
             if (next < (t ? n : work.end0)) {
-                go = tc::bar_wait(bar(kKFull + s1), (next / kStages) & 1, &gave_up);
+                go = tc::bar_wait_warp(bar(kKFull + s1), (next / kStages) & 1, &gave_up);
                 if (go) issue_s(t, s1);
             } else {
-                tc::mma_commit(bar(kOFull + t));
+                tc::mma_commit(bar(kOFull + t), leader);
             }
         }
         if (go) {
-            tc::mma_commit(bar(kVEmpty + s));
-            if (next < n) tc::mma_commit(bar(kKEmpty + s1));
+            tc::mma_commit(bar(kVEmpty + s), leader);
+            if (next < n) tc::mma_commit(bar(kKEmpty + s1), leader);
         }
     }
     // MMAs in flight end before tensor memory is freed
-    tc::mma_commit(bar(kDrain));
+    tc::mma_commit(bar(kDrain), leader);
     tc::bar_drain(bar(kDrain), 0);
 }
 

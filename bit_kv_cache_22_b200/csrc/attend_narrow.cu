@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
         unpack_role<D, N, BF16, L>(a, work, exps, smem, base, warp >= 12, warp % 4, lane, gave_up);
     } else if (warp >= 16) {
         tc::regs_give<64>();
-        if (warp == 16 && lane == 0 && work.n > 0) mma_role<D, false, L>(work, base, tmem, gave_up);
+        if (warp == 16 && work.n > 0) mma_role<D, false, L>(work, base, tmem, gave_up);
     } else {
         tc::regs_take<120>();
         softmax_role<D, BF16, false, L>(a, work, exps, smem, base, tmem, warp, lane, gave_up);

@@ -167,60 +167,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
             }
         } else if (warp == 8) {
             // ------------------------------ MMAs -------------------------------
-            if (lane == 0) {
-                constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, BF16, false);
-                constexpr uint32_t kDescO = tc::mma_desc(kRows, D, BF16, true);
-                auto issue_s = [&](int t, int s) {
-                    const uint64_t qd = tc::desc_k_major(base + L::q + t * L::kTileBytes);
-                    const uint64_t kd = tc::desc_k_major(base + L::k + s * L::kTileBytes);
+            const uint32_t leader = tc::elect_leader();
+            constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, BF16, false);
+            constexpr uint32_t kDescO = tc::mma_desc(kRows, D, BF16, true);
+            auto issue_s = [&](int t, int s) {
+                const uint64_t qd = tc::desc_k_major(base + L::q + t * L::kTileBytes);
+                const uint64_t kd = tc::desc_k_major(base + L::k + s * L::kTileBytes);
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint64_t step = (i / 4) * (kRows * 128 / 16) + (i % 4) * 2;
-                        tc::mma_ss(tmem + t * 128, qd + step, kd + step, kDescS, i > 0);
-                    }
-                    tc::mma_commit(bar(kSFull + t));
-                };
-                bool go = tc::bar_wait(bar(kKFull), 0, &gave_up);
-                for (int t = 0; t < 2 && go; ++t)
-                    if (n_tiles[t]) {
-                        go = tc::bar_wait(bar(kQFull + t), 0, &gave_up);
-                        if (go) issue_s(t, 0);
-                    }
-                if (go) tc::mma_commit(bar(kKEmpty));
-                for (int j = 0; j < n_max && go; ++j) {
-                    const int s = j % kStages, s1 = (j + 1) % kStages;
-                    go = tc::bar_wait(bar(kVFull + s), (j / kStages) & 1, &gave_up);
-                    if (go && j == n_max - 1 && count - j * kRows < kRows) go = tc::bar_wait(bar(kVFixed), 0, &gave_up);
-                    for (int t = 0; t < 2 && go; ++t) {
-                        if (j >= n_tiles[t]) continue;
-                        const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t step = (i / 4) * (kRows * 128 / 16) + (i % 4) * 2;
+                    tc::mma_ss(tmem + t * 128, qd + step, kd + step, kDescS, i > 0, leader);
+                }
+                tc::mma_commit(bar(kSFull + t), leader);
+            };
+            bool go = tc::bar_wait_warp(bar(kKFull), 0, &gave_up);
+            for (int t = 0; t < 2 && go; ++t)
+                if (n_tiles[t]) {
+                    go = tc::bar_wait_warp(bar(kQFull + t), 0, &gave_up);
+                    if (go) issue_s(t, 0);
+                }
+            if (go) tc::mma_commit(bar(kKEmpty), leader);
+            for (int j = 0; j < n_max && go; ++j) {
+                const int s = j % kStages, s1 = (j + 1) % kStages;
+                go = tc::bar_wait_warp(bar(kVFull + s), (j / kStages) & 1, &gave_up);
+                if (go && j == n_max - 1 && count - j * kRows < kRows) go = tc::bar_wait_warp(bar(kVFixed), 0, &gave_up);
+                for (int t = 0; t < 2 && go; ++t) {
+                    if (j >= n_tiles[t]) continue;
+                    const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {     // the first weights while the others are taken
-                            go = go && tc::bar_wait(bar(kPFull + 2 * half + t), j & 1, &gave_up);
-                            if (!go) break;
-                            tc::fence_after_sync();
-#pragma unroll
-                            for (int i = 4 * half; i < 4 * half + 4; ++i)
-                                tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
-                                           j > 0 || i > 0);
-                        }
+                    for (int half = 0; half < 2; ++half) {     // the first weights while the others are taken
+                        go = go && tc::bar_wait_warp(bar(kPFull + 2 * half + t), j & 1, &gave_up);
                         if (!go) break;
-                        if (j + 1 < n_tiles[t]) {
-                            go = tc::bar_wait(bar(kKFull + s1), ((j + 1) / kStages) & 1, &gave_up);
-                            if (go) issue_s(t, s1);
-                        } else {
-                            tc::mma_commit(bar(kOFull + t));
-                        }
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int i = 4 * half; i < 4 * half + 4; ++i)
+                            tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
+                                       j > 0 || i > 0, leader);
                     }
-                    if (go) {
-                        tc::mma_commit(bar(kVEmpty + s));
-                        if (j + 1 < n_max) tc::mma_commit(bar(kKEmpty + s1));
+                    if (!go) break;
+                    if (j + 1 < n_tiles[t]) {
+                        go = tc::bar_wait_warp(bar(kKFull + s1), ((j + 1) / kStages) & 1, &gave_up);
+                        if (go) issue_s(t, s1);
+                    } else {
+                        tc::mma_commit(bar(kOFull + t), leader);
                     }
                 }
-                // MMAs in flight end before tensor memory is freed
-                tc::mma_commit(bar(kDrain));
-                tc::bar_drain(bar(kDrain), 0);
+                if (go) {
+                    tc::mma_commit(bar(kVEmpty + s), leader);
+                    if (j + 1 < n_max) tc::mma_commit(bar(kKEmpty + s1), leader);
+                }
             }
+            // MMAs in flight end before tensor memory is freed
+            tc::mma_commit(bar(kDrain), leader);
+            tc::bar_drain(bar(kDrain), 0);
         }
     } else {
         tc::regs_take<208>();

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const AttendAr
             for (int j = max(0, keys - kStages); j < keys; ++j) tc::bar_drain(bar(kKFull + j % kStages), (j / kStages) & 1);
             for (int j = max(0, values - kStages); j < values; ++j)
                 tc::bar_drain(bar(kVFull + j % kStages), (j / kStages) & 1);
-        } else if (warp == 8 && lane == 0 && work.n > 0) {
+        } else if (warp == 8 && work.n > 0) {
             mma_role<D, true, L>(work, base, tmem, gave_up);
         }
     } else {
