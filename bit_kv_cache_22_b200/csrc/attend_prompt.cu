@@ -47,6 +47,44 @@ struct PromptSmem {
 // exactly as weights below 1, and the sums are rescaled rarely.
 constexpr float kLazyMax = 8.0f;
 
+// A CTA's piece of work: up to 2 * tpt tokens of one slot's prompt from token q0 on, for kv head h.
+struct Job {
+    int first, count, q0, h;                       // the prompt's first row and tokens
+    int tiles[2];                                  // key tiles each query tile sees (0: the tile has no tokens)
+    __device__ __forceinline__ int most() const { return max(tiles[0], tiles[1]); }
+};
+
+// Job i of the CTA; tiles {0, 0} when there is none.  The jobs lie longest first, and the CTAs take
+// them to and fro, so that their sums come out alike.
+__device__ __forceinline__ Job prompt_job(const AttendArgs &a, int i) {
+    Job w{};
+    const int n_ctas = gridDim.x;
+    const int64_t at = static_cast<int64_t>(i) * n_ctas +
+                       (i & 1 ? n_ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+    if (at >= static_cast<int64_t>(a.t.n_items) * a.Hkv) return w;
+    const int4 item = a.t.items[at / a.Hkv];
+    w.h = static_cast<int>(at % a.Hkv);
+    w.q0 = item.y;
+    if (item.x >= 0 && item.x < a.t.B && w.q0 >= 0) {
+        w.first = a.t.offsets[item.x];
+        w.count = a.t.offsets[item.x + 1] - w.first;
+        if (w.first >= 0 && w.count > w.q0 && static_cast<int64_t>(w.first) + w.count <= a.t.tokens) {
+            const int tpt = kRows / (a.Hq / a.Hkv);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tok = w.q0 + t * tpt;
+                w.tiles[t] = tok < w.count ? (min(tok + tpt, w.count) + kRows - 1) / kRows : 0;
+            }
+            return w;
+        }
+    }
+    if (a.status) atomicOr(a.status, 8u);          // not this library's table
+    return w;
+}
+
+// Persistent: the roles go from job to job on their own, so that a job's first loads and products run
+// while the one before is divided and written out.  Tiles, stages and phases are counted over all
+// of the CTA's jobs.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ CUtensorMap map_q,
                                                                    const __grid_constant__ CUtensorMap map_k,
@@ -59,37 +97,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
-
-    // the work item: up to 2 * tpt tokens of one slot's prompt from token q0 on
-    const int h = blockIdx.x % a.Hkv;
-    const int4 item = a.t.items[blockIdx.x / a.Hkv];
     const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
-    const int slot = item.x, q0 = item.y;
-    int first = 0, count = 0;
-    bool good = slot >= 0 && slot < a.t.B && q0 >= 0;
-    if (good) {
-        first = a.t.offsets[slot];
-        count = a.t.offsets[slot + 1] - first;
-        good = first >= 0 && count > q0 && static_cast<int64_t>(first) + count <= a.t.tokens;
-    }
-    if (!good) {                                   // not this library's table
-        if (threadIdx.x == 0 && a.status) atomicOr(a.status, 8u);
-        return;
-    }
-    // key tiles each query tile sees (0: the tile has no tokens)
-    int n_tiles[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int tok = q0 + t * tpt, end = min(tok + tpt, count);
-        n_tiles[t] = tok < count ? (end + kRows - 1) / kRows : 0;
-    }
-    const int n_max = max(n_tiles[0], n_tiles[1]);
+    const int64_t n_jobs = static_cast<int64_t>(a.t.n_items) * a.Hkv;
+    const int rounds = static_cast<int>((n_jobs + gridDim.x - 1) / gridDim.x);
 
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
     // kPFull: [half of the tile's tokens][stream]
-    enum { kQFull = 0, kKFull = 2, kKEmpty = 4, kVFull = 6, kVEmpty = 8, kSFull = 10, kPFull = 12, kOFull = 16,
-           kVFixed = 18, kDrain = 19, kBars = 20 };
+    enum { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 10, kSFull = 12, kPFull = 14,
+           kOFull = 18, kVFixed = 20, kDrain = 21, kBars = 22 };
     if (threadIdx.x == 0) {
         gave_up = 0;
         for (int i = 0; i < kBars; ++i) tc::bar_init(bar(i), i >= kPFull && i < kPFull + 4 ? 4 : 1);
@@ -104,73 +120,75 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
     if (warp >= 8) {
         tc::regs_give<80>();
         if (warp == 9) {
-            // ------------------------------ loads ------------------------------
-            int issued_k = 0, issued = 0;          // key and value tiles asked for
-            if (lane == 0) {
-                const uint32_t q_bytes = static_cast<uint32_t>(hg * tpt * D * 2);
-                auto load = [&](const CUtensorMap *map, uint32_t dst, int head, int tok, uint32_t b) {
+            // ------------------------------ loads --------------------------
+            const uint32_t q_bytes = static_cast<uint32_t>(hg * tpt * D * 2);
+            const uint32_t leader = tc::elect_leader();
+            auto load = [&](const CUtensorMap *map, uint32_t dst, int head, int tok, uint32_t b, uint32_t bytes) {
+                if (!leader) return;
+                tc::bar_expect(b, bytes);
 #pragma unroll
-                    for (int p = 0; p < D / 64; ++p) tc::tma_load_3d(dst + p * kRows * 128, map, 64 * p, head, tok, b);
-                };
-                for (int t = 0; t < 2; ++t) {
-                    if (n_tiles[t]) {
-                        tc::bar_expect(bar(kQFull + t), q_bytes);
-                        load(&map_q, base + L::q + t * L::kTileBytes, h * hg, first + q0 + t * tpt, bar(kQFull + t));
-                    }
-                    if (t == 0) {
-                        tc::bar_expect(bar(kKFull), L::kTileBytes);
-                        load(&map_k, base + L::k, h, first, bar(kKFull));
-                        issued_k = 1;
-                    }
-                }
-                bool go = true;
-                for (int j = 0; j < n_max && go; ++j) {
-                    const int s = j % kStages, phase = (j / kStages) & 1;
-                    if (j > 0) {
-                        if (j >= kStages) go = tc::bar_wait(bar(kKEmpty + s), phase ^ 1, &gave_up);
+                for (int p = 0; p < D / 64; ++p) tc::tma_load_3d(dst + p * kRows * 128, map, 64 * p, head, tok, b);
+            };
+            bool go = true;
+            int keys = 0, values = 0, queries[2] = {0, 0};     // tiles asked for
+            auto load_keys = [&](const Job &w, int j) {
+                const int s = keys % kStages;
+                if (keys >= kStages) go = go && tc::bar_wait_warp(bar(kKEmpty + s), ((keys / kStages) & 1) ^ 1, &gave_up);
+                if (!go) return;
+                load(&map_k, base + L::k + s * L::kTileBytes, w.h, w.first + j * kRows, bar(kKFull + s), L::kTileBytes);
+                ++keys;
+            };
+            Job next = prompt_job(a, 0);
+            for (int i = 0; i < rounds && go; ++i) {
+                const Job w = next;
+                next = prompt_job(a, i + 1);
+                const int n = w.most();
+                for (int t = 0; t < 2 && go; ++t) {
+                    if (w.tiles[t]) {
+                        if (queries[t] > 0) go = tc::bar_wait_warp(bar(kQEmpty + t), (queries[t] - 1) & 1, &gave_up);
                         if (!go) break;
-                        tc::bar_expect(bar(kKFull + s), L::kTileBytes);
-                        load(&map_k, base + L::k + s * L::kTileBytes, h, first + j * kRows, bar(kKFull + s));
-                        issued_k = j + 1;
+                        load(&map_q, base + L::q + t * L::kTileBytes, w.h * hg, w.first + w.q0 + t * tpt, bar(kQFull + t),
+                             q_bytes);
+                        ++queries[t];
                     }
-                    if (j >= kStages) go = tc::bar_wait(bar(kVEmpty + s), phase ^ 1, &gave_up);
-                    if (!go) break;
-                    tc::bar_expect(bar(kVFull + s), L::kTileBytes);
-                    load(&map_v, base + L::v + s * L::kTileBytes, h, first + j * kRows, bar(kVFull + s));
-                    issued = j + 1;
+                    if (t == 0 && n > 0) load_keys(w, 0);
                 }
-            }
-            issued = __shfl_sync(0xffffffffu, issued, 0);
-            // The last value tile may reach past the sequence, into rows that are another's or
-            // anything: their weights are 0, but 0 times an infinity is not, so they are cleared.
-            const int j = n_max - 1, left = count - j * kRows;
-            if (issued == n_max && left < kRows) {
-                const int s = j % kStages;
-                if (tc::bar_wait_warp(bar(kVFull + s), (j / kStages) & 1, &gave_up)) {
+                for (int j = 0; j < n && go; ++j) {
+                    if (j > 0) load_keys(w, j);
+                    const int s = values % kStages;
+                    if (values >= kStages)
+                        go = go && tc::bar_wait_warp(bar(kVEmpty + s), ((values / kStages) & 1) ^ 1, &gave_up);
+                    if (!go) break;
+                    load(&map_v, base + L::v + s * L::kTileBytes, w.h, w.first + j * kRows, bar(kVFull + s), L::kTileBytes);
+                    ++values;
+                }
+                // The last value tile may reach past the sequence, into rows that are another's or
+                // anything: their weights are 0, but 0 times an infinity is not, so they are cleared.
+                const int left = w.count - (n - 1) * kRows;
+                if (go && n > 0 && left < kRows) {
+                    const int s = (values - 1) % kStages;
+                    go = tc::bar_wait_warp(bar(kVFull + s), ((values - 1) / kStages) & 1, &gave_up);
                     unsigned char *v = smem + L::v + s * L::kTileBytes;
-                    for (int i = lane; i < (kRows - left) * 8; i += 32)   // whole 128-byte rows: the swizzle stays inside
+                    for (int k = lane; go && k < (kRows - left) * 8; k += 32)  // whole 128-byte rows: the swizzle stays inside
 #pragma unroll
                         for (int p = 0; p < D / 64; ++p)
-                            *reinterpret_cast<uint4 *>(v + p * kRows * 128 + left * 128 + 16 * i) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(v + p * kRows * 128 + left * 128 + 16 * k) = make_uint4(0, 0, 0, 0);
                     tc::fence_async_proxy();
                     __syncwarp();
                     if (lane == 0) tc::bar_arrive(bar(kVFixed));
                 }
             }
-            if (lane == 0) {                       // copies in flight land before the CTA leaves
-                for (int t = 0; t < 2; ++t)
-                    if (n_tiles[t]) tc::bar_drain(bar(kQFull + t), 0);
-                for (int i = max(0, issued_k - kStages); i < issued_k; ++i)
-                    tc::bar_drain(bar(kKFull + i % kStages), (i / kStages) & 1);
-                for (int i = max(0, issued - kStages); i < issued; ++i)
-                    tc::bar_drain(bar(kVFull + i % kStages), (i / kStages) & 1);
-            }
+            for (int t = 0; t < 2; ++t)            // copies in flight land before the CTA leaves
+                if (queries[t]) tc::bar_drain(bar(kQFull + t), (queries[t] - 1) & 1);
+            for (int k = max(0, keys - kStages); k < keys; ++k) tc::bar_drain(bar(kKFull + k % kStages), (k / kStages) & 1);
+            for (int k = max(0, values - kStages); k < values; ++k)
+                tc::bar_drain(bar(kVFull + k % kStages), (k / kStages) & 1);
         } else if (warp == 8) {
-            // ------------------------------ MMAs -------------------------------
+            // ------------------------------ MMAs ---------------------------
             const uint32_t leader = tc::elect_leader();
             constexpr uint32_t kDescS = tc::mma_desc(kRows, kRows, BF16, false);
             constexpr uint32_t kDescO = tc::mma_desc(kRows, D, BF16, true);
-            auto issue_s = [&](int t, int s) {
+            auto issue_s = [&](int t, int s, bool last) {
                 const uint64_t qd = tc::desc_k_major(base + L::q + t * L::kTileBytes);
                 const uint64_t kd = tc::desc_k_major(base + L::k + s * L::kTileBytes);
 #pragma unroll
@@ -179,42 +197,57 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                     tc::mma_ss(tmem + t * 128, qd + step, kd + step, kDescS, i > 0, leader);
                 }
                 tc::mma_commit(bar(kSFull + t), leader);
+                if (last) tc::mma_commit(bar(kQEmpty + t), leader);
             };
-            bool go = tc::bar_wait_warp(bar(kKFull), 0, &gave_up);
-            for (int t = 0; t < 2 && go; ++t)
-                if (n_tiles[t]) {
-                    go = tc::bar_wait_warp(bar(kQFull + t), 0, &gave_up);
-                    if (go) issue_s(t, 0);
-                }
-            if (go) tc::mma_commit(bar(kKEmpty), leader);
-            for (int j = 0; j < n_max && go; ++j) {
-                const int s = j % kStages, s1 = (j + 1) % kStages;
-                go = tc::bar_wait_warp(bar(kVFull + s), (j / kStages) & 1, &gave_up);
-                if (go && j == n_max - 1 && count - j * kRows < kRows) go = tc::bar_wait_warp(bar(kVFixed), 0, &gave_up);
-                for (int t = 0; t < 2 && go; ++t) {
-                    if (j >= n_tiles[t]) continue;
-                    const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
+            bool go = true;
+            int at = 0, queries[2] = {0, 0}, weights[2] = {0, 0}, fixed = 0;   // key tiles, and the rest, before this job
+            Job next = prompt_job(a, 0);
+            for (int i = 0; i < rounds && go; ++i) {
+                const Job w = next;
+                next = prompt_job(a, i + 1);
+                const int n = w.most();
+                if (n == 0) continue;
+                go = tc::bar_wait_warp(bar(kKFull + at % kStages), (at / kStages) & 1, &gave_up);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {     // the first weights while the others are taken
-                        go = go && tc::bar_wait_warp(bar(kPFull + 2 * half + t), j & 1, &gave_up);
-                        if (!go) break;
-                        tc::fence_after_sync();
-#pragma unroll
-                        for (int i = 4 * half; i < 4 * half + 4; ++i)
-                            tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, vd + i * (2048 / 16), kDescO,
-                                       j > 0 || i > 0, leader);
-                    }
-                    if (!go) break;
-                    if (j + 1 < n_tiles[t]) {
-                        go = tc::bar_wait_warp(bar(kKFull + s1), ((j + 1) / kStages) & 1, &gave_up);
-                        if (go) issue_s(t, s1);
-                    } else {
-                        tc::mma_commit(bar(kOFull + t), leader);
-                    }
+                for (int t = 0; t < 2; ++t) {
+                    if (!go || w.tiles[t] == 0) continue;
+                    go = tc::bar_wait_warp(bar(kQFull + t), queries[t] & 1, &gave_up);
+                    if (go) issue_s(t, at % kStages, w.tiles[t] == 1);
+                    ++queries[t];
                 }
-                if (go) {
-                    tc::mma_commit(bar(kVEmpty + s), leader);
-                    if (j + 1 < n_max) tc::mma_commit(bar(kKEmpty + s1), leader);
+                if (go) tc::mma_commit(bar(kKEmpty + at % kStages), leader);
+                for (int j = 0; j < n && go; ++j, ++at) {
+                    const int s = at % kStages, s1 = (at + 1) % kStages;
+                    go = tc::bar_wait_warp(bar(kVFull + s), (at / kStages) & 1, &gave_up);
+                    if (go && j == n - 1 && w.count - j * kRows < kRows)
+                        go = tc::bar_wait_warp(bar(kVFixed), fixed++ & 1, &gave_up);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!go || j >= w.tiles[t]) continue;
+                        const uint64_t vd = tc::desc_mn_major(base + L::v + s * L::kTileBytes, kRows * 128);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) { // the first weights while the others are taken
+                            go = go && tc::bar_wait_warp(bar(kPFull + 2 * half + t), weights[t] & 1, &gave_up);
+                            if (!go) break;
+                            tc::fence_after_sync();
+#pragma unroll
+                            for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k, vd + k * (2048 / 16), kDescO,
+                                           j > 0 || k > 0, leader);
+                        }
+                        if (!go) continue;
+                        ++weights[t];
+                        if (j + 1 < w.tiles[t]) {
+                            go = tc::bar_wait_warp(bar(kKFull + s1), ((at + 1) / kStages) & 1, &gave_up);
+                            if (go) issue_s(t, s1, j + 2 == w.tiles[t]);
+                        } else {
+                            tc::mma_commit(bar(kOFull + t), leader);
+                        }
+                    }
+                    if (go) {
+                        tc::mma_commit(bar(kVEmpty + s), leader);
+                        if (j + 1 < n) tc::mma_commit(bar(kKEmpty + s1), leader);
+                    }
                 }
             }
             // MMAs in flight end before tensor memory is freed
@@ -225,82 +258,90 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         tc::regs_take<208>();
         // ------------------------------ softmax ----------------------------
         const int t = warp >> 2, r = threadIdx.x & 127;
-        const int tok0 = q0 + t * tpt, tok = tok0 + r / hg;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
         const float scale = a.scale;
-        float m = 0.0f, l = 0.0f;
         bool go = true;
-        for (int j = 0; j < n_tiles[t] && go; ++j) {
-            go = tc::bar_wait_warp(bar(kSFull + t), j & 1, &gave_up);
+        int at = 0, outputs = 0;                   // this stream's tiles and outputs before this job
+        Job next = prompt_job(a, 0);
+        for (int i = 0; i < rounds && go; ++i) {
+            const Job w = next;
+            next = prompt_job(a, i + 1);
+            const int n = t ? w.tiles[1] : w.tiles[0];
+            if (n == 0) continue;
+            const int tok0 = w.q0 + t * tpt, tok = tok0 + r / hg;
+            float m = 0.0f, l = 0.0f;
+            for (int j = 0; j < n && go; ++j, ++at) {
+                go = tc::bar_wait_warp(bar(kSFull + t), at & 1, &gave_up);
+                if (!go) break;
+                tc::fence_after_sync();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::tmem_load(ts + 32 * c, s[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::tmem_arrived(s[c]);
+                if ((j + 1) * kRows > tok0 + 1) {  // tokens ahead of some row
+                    const int seen = tok + 1 - j * kRows;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= seen) s[c][e] = 0xff800000u;
+                }
+                float mxs[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mxs[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mxs[c] = fmaxf(mxs[c], __uint_as_float(s[c][e]));
+                }
+                const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * scale;
+                if (j == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, mx > m + kLazyMax)) {
+                    // O holds every tile before j: S_j was committed after its last MMA
+                    const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
+                    m = mn;
+                    l *= alpha;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tc::tmem_load(to + 32 * c, o);
+                        tc::tmem_arrived(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc::tmem_store(to + 32 * c, o);
+                    }
+                }
+                float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t(&p)[32] = s[2 * half];    // a weight takes the place of a logit read before
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const uint32_t *src = &s[2 * half + e / 16][2 * (e % 16)];
+                        const float2 y = tc::fma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])),
+                                                  make_float2(scale, scale), make_float2(-m, -m));
+                        const float2 wt = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+                        l2[e % 2] = tc::add2(l2[e % 2], wt);
+                        p[e] = narrow2<BF16>(wt.x, wt.y);
+                    }
+                    tc::tmem_store(ts + 32 * half, p);
+                    tc::tmem_stored();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(bar(kPFull + 2 * half + t));
+                }
+                l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+            }
+            if (go) go = tc::bar_wait_warp(bar(kOFull + t), outputs & 1, &gave_up);
             if (!go) break;
-            tc::fence_after_sync();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc::tmem_load(ts + 32 * c, s[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc::tmem_arrived(s[c]);
-            if ((j + 1) * kRows > tok0 + 1) {      // tokens ahead of some row
-                const int seen = tok + 1 - j * kRows;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * c + i >= seen) s[c][i] = 0xff800000u;
-            }
-            float mxs[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mxs[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                for (int i = 1; i < 32; ++i) mxs[c] = fmaxf(mxs[c], __uint_as_float(s[c][i]));
-            }
-            const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * scale;
-            if (j == 0) {
-                m = mx;
-            } else if (__any_sync(0xffffffffu, mx > m + kLazyMax)) {
-                // O holds every tile before j: S_j was committed after its last MMA
-                const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
-                m = mn;
-                l *= alpha;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tc::tmem_load(to + 32 * c, o);
-                    tc::tmem_arrived(o);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tc::tmem_store(to + 32 * c, o);
-                }
-            }
-            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t(&p)[32] = s[2 * half];    // a weight takes the place of a logit read before
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint32_t *src = &s[2 * half + i / 16][2 * (i % 16)];
-                    const float2 y = tc::fma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])),
-                                              make_float2(scale, scale), make_float2(-m, -m));
-                    const float2 w = make_float2(tc::ex2(y.x), tc::ex2(y.y));
-                    l2[i % 2] = tc::add2(l2[i % 2], w);
-                    p[i] = narrow2<BF16>(w.x, w.y);
-                }
-                tc::tmem_store(ts + 32 * half, p);
-                tc::tmem_stored();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(bar(kPFull + 2 * half + t));
-            }
-            l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
-        }
-        if (go && n_tiles[t]) go = tc::bar_wait_warp(bar(kOFull + t), 0, &gave_up);
-        if (go && n_tiles[t]) {
+            ++outputs;
             tc::fence_after_sync();
             const float inv = __fdividef(1.0f, l);
-            const bool mine = r < hg * tpt && tok < count;
-            uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
-                            static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
+            const bool mine = r < hg * tpt && tok < w.count;
+            uint16_t *out = a.o.p + static_cast<int64_t>(w.first + tok) * a.o.ts +
+                            static_cast<int64_t>(w.h * hg + r % hg) * a.o.hs;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -309,16 +350,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                 tc::tmem_arrived(o);
                 if (mine) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t y[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            w[k] = narrow2<BF16>(__uint_as_float(o[8 * i + 2 * k]) * inv,
-                                                 __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                        reinterpret_cast<uint4 *>(out + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                            y[k] = narrow2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                                 __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                        reinterpret_cast<uint4 *>(out + 32 * c)[e] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
             }
+            __syncwarp();
+            tc::fence_before_sync();               // O is read: the next job's weights may change it
         }
     }
     tc::fence_before_sync();
@@ -383,7 +426,13 @@ cudaError_t launch_instance(const AttendArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = true;
     }
-    attend_prompt_kernel<D, BF16><<<static_cast<unsigned>(a.t.n_items) * a.Hkv, kThreads, PromptSmem<D>::bytes, s>>>(
+    static int sms[64] = {};
+    if (dev < 64 && sms[dev] == 0) {
+        e = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t jobs = static_cast<int64_t>(a.t.n_items) * a.Hkv, ctas = dev < 64 ? sms[dev] : 148;
+    attend_prompt_kernel<D, BF16><<<static_cast<unsigned>(jobs < ctas ? jobs : ctas), kThreads, PromptSmem<D>::bytes, s>>>(
         mq, mk, mv, a);
     count_launches(1);
     return cudaGetLastError();
