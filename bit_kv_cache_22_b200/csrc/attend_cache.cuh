@@ -290,6 +290,15 @@ __device__ __forceinline__ bool prepare_unit(const Fetched<D, N> &f, const Paged
     return !wide;
 }
 
+// put for a tile in shared memory
+struct SharedPut {
+    uint32_t tile;
+    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
+        tc::store_shared(tile + offset, x, y);
+    }
+    __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const { tc::store_shared(tile + offset, v); }
+};
+
 // Unit u of a key tile as operands: keys, rows = tokens, channels along a row; values, rows =
 // channels, tokens along a row.  put(offset, a, b) stores 8 bytes of the tile, put(offset, v) 16.
 // words are used up.

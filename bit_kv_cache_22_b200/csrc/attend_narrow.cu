@@ -17,14 +17,6 @@ namespace {
 
 constexpr int kThreads = 640;
 
-struct SharedPut {
-    uint32_t tile;
-    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
-        tc::store_shared(tile + offset, x, y);
-    }
-    __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const { tc::store_shared(tile + offset, v); }
-};
-
 template <int D>
 struct NarrowSmem {
     static constexpr int kTileBytes = kRows * D * 2;

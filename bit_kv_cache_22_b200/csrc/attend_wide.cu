@@ -15,7 +15,7 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kStageThreads = 32 * kUnpackWarps;
+constexpr int kStageThreads = 32 * kUnits;
 
 template <int D>
 struct WideSmem {
@@ -46,60 +46,59 @@ struct Staged {
     }
 };
 
-struct GlobalPut {
-    unsigned char *tile;
-    __device__ __forceinline__ void operator()(int offset, uint32_t x, uint32_t y) const {
-        *reinterpret_cast<uint2 *>(tile + offset) = make_uint2(x, y);
-    }
-    __device__ __forceinline__ void operator()(int offset, const uint32_t (&v)[4]) const {
-        *reinterpret_cast<uint4 *>(tile + offset) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
-};
-
-// CTA (x, h): key tile x of the wide slots, or query tile x - n_kv_tiles.
+// CTA (x, h): keys (x even) or values of key tile x / 2 of the wide slots, or query tile x - 2 n_kv_tiles.
+// The tile is put together in shared memory and leaves in one copy.  Bound by the latency of a tile's
+// chain -- page, codes and scales, parameters through shared memory -- so tiles are CTAs of four
+// warps, five or more an SM.
 template <int D, int N, bool BF16>
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(const AttendArgs a) {
-    __shared__ __align__(16) unsigned char meta_s[kUnpackWarps][kMetaBytes];
+    extern __shared__ __align__(128) unsigned char tile_s[];
+    constexpr int kTileBytes = kRows * D * 2;
     const Staged<D> st(a);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-    if (blockIdx.x < static_cast<unsigned>(a.t.n_kv_tiles)) {
-        const int x = blockIdx.x, slot = slot_of(a.t.kv_tiles, a.t.B, x);
+    const SharedPut put{tc::smem_addr(tile_s)};
+    unsigned char *out;
+    if (blockIdx.x < 2u * a.t.n_kv_tiles) {
+        const int x = blockIdx.x / 2, kv = blockIdx.x % 2, slot = slot_of(a.t.kv_tiles, a.t.B, x);
         const int tok0 = (x - a.t.kv_tiles[slot]) * kRows;
         if (tok0 < 0) return;
         const int64_t at = static_cast<int64_t>(x) * a.Hkv + h;
-        unsigned char *tile = st.kv + at * 2 * Staged<D>::kTileBytes;
         const PagedView &c = a.cache;
         const int len = min(max(c.seq_len[slot], 0), kMaxTokens), tq = len / c.R * c.R;
-        const int kv = w / kUnits, u = w % kUnits, tok = tok0 + 32 * u, pi = tok / c.P;
+        const int tok = tok0 + 32 * w, pi = tok / c.P;
         const int page = tok < tq && pi < c.max_pages ? c.page_table[static_cast<int64_t>(slot) * c.max_pages + pi] : -1;
         const UnitSource<D> src(c, kv, slot, h, len, tq);
         Fetched<D, N> f;
         fetch_unit<D, N>(f, c, src, page, tok % c.P, tok, true, lane);
         int ex;
-        const bool narrow = prepare_unit<D, N, BF16>(f, c, src, tok, lane, meta_s[w], ex);
+        unsigned char *meta = tile_s + kTileBytes + w * kMetaBytes;
+        const bool narrow = prepare_unit<D, N, BF16>(f, c, src, tok, lane, meta, ex);
         if (lane == 0) {
-            if (kv) st.exps[at].exp_v[u] = ex;
-            else st.exps[at].scale_k[u] = pow2(ex);
+            if (kv) st.exps[at].exp_v[w] = ex;
+            else st.exps[at].scale_k[w] = pow2(ex);
         }
-        emit_unit<D, N, BF16>(f.w, f.kind[0], f.kind[1], narrow, c, src, tok, pow2(-ex), u, lane, meta_s[w],
-                              GlobalPut{tile + kv * Staged<D>::kTileBytes});
+        emit_unit<D, N, BF16>(f.w, f.kind[0], f.kind[1], narrow, c, src, tok, pow2(-ex), w, lane, meta, put);
+        out = st.kv + (at * 2 + kv) * kTileBytes;
     } else {
-        const int x = blockIdx.x - a.t.n_kv_tiles, slot = slot_of(a.t.q_tiles, a.t.B, x);
+        const int x = blockIdx.x - 2 * a.t.n_kv_tiles, slot = slot_of(a.t.q_tiles, a.t.B, x);
         const int hg = a.Hq / a.Hkv, tpt = kRows / hg;
         const int first = a.t.offsets[slot], count = a.t.offsets[slot + 1] - first;
         const int q0 = (x - a.t.q_tiles[slot]) * tpt;
         if (first < 0 || q0 < 0 || static_cast<int64_t>(first) + count > a.t.tokens) return;
         const int64_t at = static_cast<int64_t>(x) * a.Hkv + h;
-        const GlobalPut put{st.q + at * Staged<D>::kTileBytes};
         emit_queries<D, BF16>(
-            kRows, w, kUnpackWarps, lane,
+            kRows, w, kUnits, lane,
             [&](int r) -> const uint16_t * {
                 const int tok = q0 + r / hg;
                 if (r >= hg * tpt || tok >= count) return nullptr;
                 return a.q.p + static_cast<int64_t>(first + tok) * a.q.ts + static_cast<int64_t>(h * hg + r % hg) * a.q.hs;
             },
             put, [&](int r, float scale) { st.row_scale[at * kRows + r] = scale; });
+        out = st.q + at * kTileBytes;
     }
+    tc::fence_async_proxy();
+    __syncthreads();
+    if (threadIdx.x == 0) tc::bulk_store(out, tc::smem_addr(tile_s), kTileBytes);
 }
 
 template <int D, bool BF16>
@@ -198,8 +197,9 @@ cudaError_t launch_instance(const AttendArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = true;
     }
-    const dim3 grid(static_cast<unsigned>(a.t.n_kv_tiles + a.t.n_q_tiles), static_cast<unsigned>(a.Hkv));
-    stage_kernel<D, N, BF16><<<grid, kStageThreads, 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>(2 * a.t.n_kv_tiles + a.t.n_q_tiles), static_cast<unsigned>(a.Hkv));
+    constexpr int kStageBytes = kRows * D * 2 + kUnits * kMetaBytes;       // at most 40 KB
+    stage_kernel<D, N, BF16><<<grid, kStageThreads, kStageBytes, s>>>(a);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

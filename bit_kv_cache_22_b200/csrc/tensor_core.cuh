@@ -92,6 +92,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// from shared to global memory, size and addresses as above; returns when it is done
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t size) {
+    asm volatile(
+        "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+        "cp.async.bulk.commit_group;\n\t"
+        "cp.async.bulk.wait_group 0;" ::"l"(dst),
+        "r"(src), "r"(size)
+        : "memory");
+}
+
 // ------------------------------------------------------------------ tensor memory
 
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns) {   // one warp
