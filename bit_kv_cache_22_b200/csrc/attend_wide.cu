@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const AttendArgs a
     }
     tc::fence_async_proxy();
     __syncthreads();
-    if (threadIdx.x == 0) tc::bulk_store(out, tc::smem_addr(tile_s), kTileBytes);
+    if (threadIdx.x == 0) {
+        tc::bulk_store(out, tc::smem_addr(tile_s), kTileBytes);
+        tc::bulk_store_read();
+    }
 }
 
 template <int D, bool BF16>

@@ -92,15 +92,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// from shared to global memory, size and addresses as above; returns when it is done
+// from shared to global memory, size and addresses as above
 __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t size) {
     asm volatile(
         "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
-        "cp.async.bulk.commit_group;\n\t"
-        "cp.async.bulk.wait_group 0;" ::"l"(dst),
+        "cp.async.bulk.commit_group;" ::"l"(dst),
         "r"(src), "r"(size)
         : "memory");
 }
+
+// the thread's bulk stores have read their shared memory
+__device__ __forceinline__ void bulk_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // ------------------------------------------------------------------ tensor memory
 
