@@ -860,10 +860,10 @@ kvq_status check_status_word(unsigned int *word) {
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
     std::string why;
-    if (v & 1u) why += " a decode kernel gave up waiting for a copy into shared memory;";
+    if (v & 1u) why += " a kernel gave up waiting for a copy into shared memory or a product;";
     if (v & 2u) why += " a kernel met a page-table entry outside the pool;";
     if (v & 4u) why += " a quantizer met a scale outside the range the decode kernels serve;";
-    if (v & 8u) why += " a kernel met a list index outside its buffer (bounds-check build);";
+    if (v & 8u) why += " a kernel met an index outside its buffer (a chunk's table; in the bounds-check build, any list);";
     return fail(KVQ_ERR_DEVICE_CHECK, "device check (status 0x%x):%s outputs since the last check are "
                                       "unreliable", v, why.c_str());
 }

@@ -530,6 +530,20 @@ class ChunkPlan:
         self.offsets = host[:batch + 1].tolist()
         self.table = host.to(self.device)
         self.chunk.table = self.table.data_ptr()
+        # a cache has a status word of its own, prompts have the plan's
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device) if cfg is None else None
+
+    def check_device(self):
+        """Raise KVQError if a kernel run with this prompt plan raised a bit of its status word since the
+        last check (waits for the device; a cache's own check_device covers the calls on the cache)."""
+        if self.status is None:
+            raise ValueError("a chunk plan has no status word: the cache's check_device covers its calls")
+        torch.cuda.synchronize(self.device)
+        v = self.status.item()
+        if v:
+            self.status.zero_()
+            raise KVQError(KVQ_ERR_DEVICE_CHECK, f"device check (status 0x{v:x}): outputs since the last check are "
+                                                 "unreliable")
 
 
 def plan_prompt(counts, q_heads: int, kv_heads: int, head_dim: int, device=None) -> ChunkPlan:
@@ -548,7 +562,8 @@ def prompt_attention(plan: ChunkPlan, q: torch.Tensor, k: torch.Tensor, v: torch
         rows = [_packed(t, name, n, heads, c.head_dim, q.dtype, device)
                 for t, name, heads in ((q, "q", c.q_heads), (k, "k", c.kv_heads), (v, "v", c.kv_heads))]
         o = _output(out, q.shape, q.dtype, device)
-        _check(load().kvq_prompt_attention(plan.ref, code, *map(_rows, rows), _rows(o), None, raw))
+        _check(load().kvq_prompt_attention(plan.ref, code, *map(_rows, rows), _rows(o),
+                                           plan.status.data_ptr() if plan.status is not None else None, raw))
         return o
 
     return _on(device, stream, call)
@@ -735,7 +750,7 @@ class PagedKVQCache:
         """Append the planned tokens t_K, t_V [tokens, Hkv, d] (kvq_paged_append_chunk), keys
         rotated when `rope` is given; with t_Q [tokens, Hq, d], returns the rotated queries (in
         `out` when given), else None."""
-        g, device, dtype, n = self.geom, self.device, self.dtype, plan.tokens
+        g, device, dtype, n = self.geom, self._device_of(plan), self.dtype, plan.tokens
 
         def call(raw):
             k = _packed(t_K, "t_K", n, g.kv_heads, g.head_dim, dtype, device)
@@ -757,6 +772,11 @@ class PagedKVQCache:
 
         return _on(device, stream, call)
 
+    def _device_of(self, plan: ChunkPlan) -> torch.device:
+        if plan.device != self.device:
+            raise ValueError(f"the plan's table is on {plan.device}, the cache on {self.device}")
+        return self.device
+
     def _pages_for(self, plan: ChunkPlan, stream):
         """Pages for the blocks the planned tokens complete (the library refuses a plan whose slots do
         not fit; those get none here)."""
@@ -775,6 +795,7 @@ class PagedKVQCache:
     def read_chunk(self, plan: ChunkPlan, stream=None):
         """(k, v) [tokens, Hkv, d]: the planned tokens as the cache holds them."""
         g = self.geom
+        self._device_of(plan)
 
         def call(raw):
             k = torch.empty((plan.tokens, g.kv_heads, g.head_dim), dtype=self.dtype, device=self.device)
@@ -788,6 +809,7 @@ class PagedKVQCache:
         """Attention of the planned tokens' queries t_Q [tokens, Hq, d] over the cache, which holds
         them: the token at position p sees tokens 0 .. p.  Returns e [tokens, Hq, d]."""
         g = self.geom
+        self._device_of(plan)
 
         def call(raw):
             q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)

@@ -310,12 +310,13 @@ KVQ_API int32_t kvq_decode_splits(const kvq_cache *cache);
 /*
  * Reads, waiting for the device to finish its queued work, the status word in
  * this cache's state buffer, which its kernels raise when a check fails: a
- * decode kernel's bounded wait for a copy into shared memory gave up (bit 0; a
- * condition working hardware never reaches -- the wait is bounded so that a
- * fault cannot hang the GPU), or a quantizer met a scale outside the range the
- * decode kernels serve (bit 2; see kvq_prefill_quantize), or -- in the
- * bounds-check build only (include/kvq_check.h) -- a kernel met a list index
- * outside its buffer (bit 3).  KVQ_OK when the word
+ * kernel's bounded wait (for a copy into shared memory, or for the tensor core)
+ * gave up (bit 0; a condition working hardware never reaches -- the wait is
+ * bounded so that a fault cannot hang the GPU), or a quantizer met a scale
+ * outside the range the decode kernels serve (bit 2; see kvq_prefill_quantize),
+ * or a kernel met an index outside its buffer (bit 3: an entry of a chunk's
+ * table, which the caller holds; the library's own lists are checked in the
+ * bounds-check build only, include/kvq_check.h).  KVQ_OK when the word
  * is clear; KVQ_ERR_DEVICE_CHECK when it was raised -- the outputs of the calls
  * since the last check are then unreliable, kvq_last_error() names the checks,
  * and the word is cleared -- or KVQ_ERR_CUDA when the read fails.  The pages
@@ -455,10 +456,11 @@ KVQ_API kvq_status kvq_paged_check_device(kvq_paged *cache);
  * The calls follow the conventions above: asynchronous on `stream`, nothing allocated, an
  * error launches nothing and changes no state.  They may be captured into a CUDA graph: a
  * replay repeats the captured chunk at its captured positions (host lengths advance once, at
- * the capture), reading what the table and the tensors then hold.  It takes the slots to hold
- * the tokens before starts[b] as at the capture: an append that completes a half-filled block
- * reads the block's first tokens from the residual, whose rows it then reuses.  A kernel that meets a table
- * entry or a page outside its buffers skips the access and raises a bit of the cache's status
+ * the capture), reading what the table and the tensors then hold.  It takes the slots to be as at
+ * the capture: an append takes the tokens before starts[b] to be there (one that completes a
+ * half-filled block reads the block's first tokens from the residual, whose rows it then reuses),
+ * a read or an attention call the tokens that the slots held at its capture.  A kernel that meets a
+ * table entry or a page outside its buffers skips the access and raises a bit of the cache's status
  * word (kvq_paged_check_device; kvq_prompt_attention has a status word of its own).
  * ---------------------------------------------------------------------------
  */
@@ -560,8 +562,12 @@ KVQ_API kvq_status kvq_paged_read_chunk(kvq_paged *cache, const kvq_chunk *plan,
  * slot's length (KVQ_ERR_STATE); rows of which the device length leaves nothing to see give
  * zeros.  Logits, softmax statistics and sums are fp32; what meets in a product -- queries, keys,
  * weights, values -- is rounded to fp16 (11 bits) under powers of two that keep it in range, the
- * output once to e.  `workspace`: plan->workspace bytes of device scratch, 16-byte aligned (NULL
- * where that is 0); calls that may overlap on the GPU need workspaces of their own.
+ * output once to e.  Scales s <= 2^31 and queries |q| <= 2^30, as for decoding; finite inputs: a
+ * NaN or infinity reaches rows of its own slot only.  `workspace`: plan->workspace bytes of device
+ * scratch, 16-byte aligned (NULL where that is 0); calls that may overlap on the GPU need
+ * workspaces of their own.  When every slot that holds tokens brings its newest one alone (a decode
+ * step), the call runs the decode kernel, which counts splits in the cache's state: attention calls
+ * on one cache run one after another, as decode calls do.
  */
 KVQ_API kvq_status kvq_paged_chunk_attention(kvq_paged *cache, const kvq_chunk *plan, const kvq_rows *q,
                                              const kvq_rows *o, void *workspace, size_t workspace_bytes,

@@ -357,6 +357,201 @@ def test_repeated_calls_give_the_same_bits():
     assert all(torch.equal(a[0], x) for x in a[1:])
 
 
+# ------------------------------------------------------------------ sizes and values at the variants' edges
+
+def fill(p, counts, make_rows):
+    """Slots of tokens from make_rows(total, kv heads) -> (k, v), on both sides."""
+    plan = p.cache.plan_chunk(counts)
+    k, v = make_rows(plan.tokens, p.g.kv_heads)
+    p.cache.append_chunk(plan, k.cuda(), v.cuda())
+    for b, (s, n) in enumerate(zip(plan.starts, plan.counts)):
+        if n:
+            rows = slice(plan.offsets[b], plan.offsets[b + 1])
+            p.plain[b].append(s, k[rows], v[rows])
+    return plan
+
+
+@pytest.mark.parametrize("name", ["g16", "small"])
+def test_zeros_beyond_eleven_bits(name):
+    """Keys and values far from 0 with little spread: code minus zero no longer fits in fp16.  Chunks
+    that are unpacked in the attention kernel and chunks that are unpacked before it."""
+    p = make(name)
+
+    def rows(n, heads):
+        step = torch.randint(0, 2, (2, n, heads, p.g.head_dim), generator=p.gen) * 2.0 ** -5
+        k, v = (48.0 + step).to(FP16)
+        k[..., ::2] *= -1                                    # logits of both signs
+        return k, v
+
+    R = p.g.residual
+    fill(p, [3 * R + 5, 2 * R, R + 1] + [0] * (p.g.batch - 3), rows)
+    rest = [0] * (p.g.batch - 3)
+    plan = p.cache.plan_chunk([2, R, R] + rest, [3 * R + 3, R, 1] + rest)
+    zeros = p.cache.k_zeros
+    assert zeros.abs().max() > 1024
+    p.check_attention(plan, p.new(plan.tokens, p.g.q_heads, 2.0 ** -6))
+    p.cache.check_device()
+
+
+@pytest.mark.parametrize("name,rows", [("gqa2", 4), ("mha4", 1), ("sym4", 3)])
+def test_chunk_sizes_around_the_tiles(name, rows):
+    """Chunks of one token more and less than what a tile, two tiles and the narrow form hold."""
+    p = make(name, capacity=2048)
+    sizes = sorted({n + e for n in (32 // rows, 128 // rows, 256 // rows) for e in (0, 1)})
+    p.append([150, 7, 131, 0][:p.g.batch])
+    for i in range(0, len(sizes), 2):
+        plan, _, _ = p.append(([0] + sizes[i:i + 2] + [0])[:p.g.batch])
+        p.check_attention(plan, what=f"{sizes[i:i + 2]}")
+    p.cache.check_device()
+
+
+@pytest.mark.parametrize("hq,hkv", [(128, 1), (33, 1), (66, 2), (7, 7)])
+def test_chunk_attention_head_counts(hq, hkv):
+    p = ct.Pair(2, hq, hkv, 64, 32, 32, 64, 2, False, BF16, 512, 64, seed=hq)
+    p.append([150, 64])
+    for counts in ([1, 0], [3, 1], [5, 40]):
+        plan, _, _ = p.append(counts)
+        p.check_attention(plan, what=str(counts))
+
+
+def test_decode_steps_as_chunks():
+    """Every slot's newest token: slots that hold nothing, strided queries and outputs, then slots
+    that keep still, which leave the decode kernel's form."""
+    p = make("gqa2")
+    p.append([500, 0, 1, 127])
+    fused = torch.zeros(3, 13, 128, dtype=BF16, device="cuda")
+    out = torch.full((5, 11, 128), 7.0, dtype=BF16, device="cuda")
+    for _ in range(3):                                       # slot 3 fills a block
+        plan, _, _ = p.append([1, 0, 1, 1])
+        q = p.new(3, 8)
+        fused[:, 2:10] = q.cuda()
+        got = p.cache.chunk_attention(plan, fused[:, 2:10], out=out[1:4, 3:])
+        p.check_attention(plan, q, got=got)
+    keep = out.clone()
+    keep[1:4, 3:] = 7.0
+    assert (keep == 7.0).all()
+    plan, _, _ = p.append([1, 0, 0, 1])                      # slot 2 holds tokens and brings none
+    p.check_attention(plan)
+    p.cache.release(0)
+    p.plain[0] = ct.PlainSlot(p.g, BF16)
+    plan, _, _ = p.append([0, 0, 1, 1])
+    p.check_attention(plan)
+    p.cache.check_device()
+
+
+def test_many_slots():
+    """More slots than a warp has lanes, most without tokens."""
+    p = ct.Pair(150, 2, 1, 64, 16, 16, 32, 4, False, BF16, 128, 64, seed=5)
+    counts = [(b * 7) % 45 if b % 3 else 0 for b in range(150)]
+    plan, _, _ = p.append(counts)
+    p.check_read(plan)
+    p.check_attention(plan)
+    plan, _, _ = p.append([1 if b % 5 else 0 for b in range(150)])
+    p.check_attention(plan)
+    p.check_state()
+
+
+@pytest.mark.parametrize("counts", [[2, 2, 2, 0], [20, 60, 20, 0]])
+def test_a_slot_with_infinities_leaves_the_others_alone(counts):
+    p = make("gqa2")
+    p.append([200, 0, 50, 0])
+    plan = p.cache.plan_chunk(counts)
+    k, v, q = p.new(plan.tokens, 2), p.new(plan.tokens, 2), p.new(plan.tokens, 8)
+    bad = slice(plan.offsets[1], plan.offsets[2])
+    k[bad], v[bad], q[bad] = float("nan"), float("inf"), float("nan")
+    p.cache.append_chunk(plan, k.cuda(), v.cuda())
+    got = p.cache.chunk_attention(plan, q.cuda())
+    for b in (0, 2):
+        rows = slice(plan.offsets[b], plan.offsets[b + 1])
+        p.plain[b].append(plan.starts[b], k[rows], v[rows])
+        hk, hv = p.plain[b].held()
+        ct.check_attention(got[rows], *ct.attend(ct.wide(q[rows]), hk, hv, plan.starts[b]), hk.shape[1], BF16, True)
+
+
+def test_captured_wide_chunk_and_decode_step_replay():
+    """Two graphs captured on one cache, a long chunk over a split cache and a decode step, replayed in
+    turn and back to back: each keeps scratch of its own."""
+    p = make("gqa2", capacity=4096)
+    p.append([3000, 700, 200, 1])
+    wide = p.cache.plan_chunk([100, 300, 9, 0], [2900, 400, 191, 0])
+    step = p.cache.plan_chunk([1] * 4, [2999, 699, 199, 0])
+    qw, qs = (torch.zeros(n, 8, 128, dtype=BF16, device="cuda") for n in (wide.tokens, 4))
+    p.cache.chunk_attention(wide, qw), p.cache.chunk_attention(step, qs)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for plan, q in ((wide, qw), (step, qs)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(p.cache.chunk_attention(plan, q))
+    for _ in range(2):
+        hw, hs = p.new(wide.tokens, 8), p.new(4, 8)
+        qw.copy_(hw), qs.copy_(hs)
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        p.check_attention(wide, hw, got=outs[0])
+        p.check_attention(step, hs, got=outs[1])
+    eager = p.cache.chunk_attention(wide, qw)
+    assert torch.equal(eager, outs[0])
+
+
+def test_wide_chunks_on_two_streams():
+    """Attention calls of two caches that may run at once."""
+    pairs = [make("gqa2", capacity=2048, seed=s) for s in (1, 2)]
+    jobs = []
+    for p in pairs:
+        p.append([900, 300, 40, 0])
+        plan, _, _ = p.append([200, 90, 1, 3])
+        q = p.new(plan.tokens, 8)
+        jobs.append((p, plan, q, q.cuda(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[p.cache.chunk_attention(plan, dq, stream=s) for p, plan, _, dq, s in jobs] for _ in range(4)]
+    torch.cuda.synchronize()
+    for got in outs:
+        for (p, plan, q, _, _), o in zip(jobs, got):
+            p.check_attention(plan, q, got=o)
+
+
+def test_repeated_wide_calls_give_the_same_bits():
+    p = make("gqa2", capacity=4096)
+    p.append([3500, 700, 200, 1])
+    plan = p.cache.plan_chunk([500, 90, 1, 0], [3000, 600, 199, 0])
+    q = p.new(plan.tokens, 8).cuda()
+    a = [p.cache.chunk_attention(plan, q) for _ in range(4)]
+    assert all(torch.equal(a[0], x) for x in a[1:])
+
+
+def test_status_of_prompts_and_plans():
+    plan = kvq.plan_prompt([40, 9], 8, 2, 128)
+    q, k, v = (torch.randn(49, h, 128, device="cuda").to(BF16) for h in (8, 2, 2))
+    kvq.prompt_attention(plan, q, k, v)
+    plan.check_device()
+    items = plan.table.clone()
+    plan.table[-4] = 7                                       # the last piece's slot: there are two
+    kvq.prompt_attention(plan, q, k, v)
+    with pytest.raises(kvq.KVQError) as e:
+        plan.check_device()
+    assert e.value.status == kvq.KVQ_ERR_DEVICE_CHECK
+    plan.check_device()                                      # cleared
+    plan.table.copy_(items)
+    p = make("gqa2")
+    p.append([70, 0, 3, 0])
+    chunk = p.cache.plan_chunk([2, 0, 3, 0], [68, 0, 0, 0])
+    with pytest.raises(ValueError):
+        chunk.check_device()
+    with pytest.raises(kvq.KVQError):
+        kvq.prompt_attention(chunk, q[:5], k[:5], v[:5])
+    with pytest.raises(kvq.KVQError):
+        p.cache.chunk_attention(plan, q)
+    keep, chunk.device = chunk.device, torch.device("cuda", 99)
+    for call in (lambda: p.cache.chunk_attention(chunk, q[:5]), lambda: p.cache.read_chunk(chunk),
+                 lambda: p.cache.append_chunk(chunk, k[:5], v[:5])):
+        with pytest.raises(ValueError):
+            call()
+    chunk.device = keep
+    p.check_attention(chunk)
+
+
 # ------------------------------------------------------------------ refusals and bad tables
 
 def test_refused_calls_change_nothing():
