@@ -11,26 +11,29 @@ namespace {
 
 constexpr int kRowThreads = 128;
 
-// One CTA per new token: its residual rows (keys rotated) when it lies behind its slot's last
-// whole block, and its rotated queries.  The rows of a block's first tokens (positions below
-// R floor(end / R)) were quantized by the launch before.  The CTA of a slot's first new token
-// sets the slot's length, which no CTA reads.
+// The residual rows (keys rotated) of the new tokens behind their slots' last whole blocks, R floor(end /
+// R); those before were quantized by the launch before.  BLOCKS: that launch was made, and turned the
+// queries: CTA (b, i) has the i-th such token of slot b.  Otherwise one CTA per new token, which also
+// turns its queries.  A slot's first CTA sets the slot's length, which no CTA reads.
 // Bound by memory: each row is read and written once, 16 bytes a thread.
-template <bool BF16>
+template <bool BF16, bool BLOCKS>
 __global__ void __launch_bounds__(kRowThreads) chunk_rows_kernel(const PagedView c, const ChunkTable t, const Rows k,
                                                                  const Rows v, const RopeArgs rope, const Rows q,
                                                                  const Rows q_out) {
-    const int64_t row = blockIdx.x;
-    const int b = slot_of(t.offsets, t.B, row);
+    const int b = BLOCKS ? static_cast<int>(blockIdx.y) : slot_of(t.offsets, t.B, blockIdx.x);
     const int64_t first = t.offsets[b], start = t.starts[b], end = start + t.offsets[b + 1] - first;
-    const int64_t tok = start + row - first;
-    if (first > row || end <= tok || start < 0) {           // not this library's table
+    if (BLOCKS && end == start) return;
+    const int64_t kept = max(start, end / c.R * c.R);          // the first that stays in the residual
+    const int64_t row = BLOCKS ? first + kept - start + blockIdx.x : blockIdx.x, tok = start + row - first;
+    if (start < 0 || end < start || first < 0 || first + end - start > t.tokens || row < first ||
+        (!BLOCKS && tok >= end)) {                 // not this library's table
         if (threadIdx.x == 0) atomicOr(c.status, 8u);
         return;
     }
-    if (row == first && threadIdx.x == 0) c.seq_len[b] = static_cast<int32_t>(end);
+    if (threadIdx.x == 0 && (BLOCKS ? blockIdx.x == 0 : row == first)) c.seq_len[b] = static_cast<int32_t>(end);
+    if (BLOCKS && tok >= end) return;
     const RowUnits ru = row_units(c.d, rope), plain = {0, c.d / 8};
-    const int n_k = tok >= end / c.R * c.R ? c.Hkv * ru.n : 0, n_v = n_k ? c.Hkv * plain.n : 0;
+    const int n_k = tok >= kept ? c.Hkv * ru.n : 0, n_v = n_k ? c.Hkv * plain.n : 0;
     const int n_q = q.p ? c.Hq * ru.n : 0;
     const int64_t res_row = static_cast<int64_t>(b) * c.Hkv * c.R + tok % c.R;
     for (int i0 = threadIdx.x; i0 < n_k + n_v + n_q; i0 += 2 * kRowThreads) {
@@ -208,9 +211,16 @@ void read_launch(const PagedView &c, const ChunkTable &t, const Rows &k, const R
 cudaError_t launch_chunk_rows(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v,
                               const RopeArgs &rope, const Rows &q, const Rows &q_out, cudaStream_t s) {
     if (t.tokens == 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>(t.tokens);
-    if (c.bf16) chunk_rows_kernel<true><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
-    else chunk_rows_kernel<false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
+    if (t.n_blocks > 0) {
+        const dim3 grid(static_cast<unsigned>(c.R), static_cast<unsigned>(t.B));
+        const Rows none{};
+        if (c.bf16) chunk_rows_kernel<true, true><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, none, none);
+        else chunk_rows_kernel<false, true><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, none, none);
+    } else {
+        const unsigned grid = static_cast<unsigned>(t.tokens);
+        if (c.bf16) chunk_rows_kernel<true, false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
+        else chunk_rows_kernel<false, false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
+    }
     count_launches(1);
     return cudaGetLastError();
 }

@@ -26,8 +26,9 @@ __device__ __forceinline__ float2 widen_pair(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 
-// x cos - y sin and y cos + x sin, each operation rounded on its own (no contraction): the
-// rotated key decides codes, so every evaluation of the formula has to agree on its bits.
+// x cos - y sin and y cos + x sin, each operation rounded on its own (no contraction, which the packed
+// forms of two products or sums do not rule out): the rotated key decides codes, so every
+// evaluation of the formula has to agree on its bits.
 __device__ __forceinline__ float turn_x(float x, float y, float c, float s) {
     return __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
 }
@@ -66,48 +67,61 @@ __device__ __forceinline__ LoadedUnit load_unit(const uint16_t *src, int u, cons
     return x;
 }
 
-// The unit rotated by token tok's angles.
-template <bool BF16>
-__device__ __forceinline__ void rotate_unit(LoadedUnit &unit, int64_t tok, const RopeArgs &r) {
-    uint4 &a = unit.a, &b = unit.b;
-    const int va = unit.va;
-    const bool pair = unit.vb >= 0;
-    if (!r.cos || 8 * va >= r.rot) return;
-    const int half = r.rot / 2;
-    const int64_t at = tok < r.positions ? tok : r.positions - 1;   // the host has refused later ones
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w};
-    uint32_t ox[4];
+// Token tok's angles for a unit whose first vector is va: of its eight channels, or of its four pairs of
+// neighbours.
+struct UnitAngles {
+    float4 c[2], s[2];
+    bool on;
+};
+__device__ __forceinline__ UnitAngles unit_angles(int va, bool pair, int64_t tok, const RopeArgs &r) {
+    UnitAngles x;
+    x.on = r.cos && 8 * va < r.rot;
+    if (!x.on) return x;
+    const int64_t at = (tok < r.positions ? tok : r.positions - 1) * (r.rot / 2);   // the host has refused later ones
+    const int first = pair ? 8 * va : 4 * va;
+    const float4 *c = reinterpret_cast<const float4 *>(r.cos + at + first);
+    const float4 *s = reinterpret_cast<const float4 *>(r.sin + at + first);
+    x.c[0] = c[0];
+    x.s[0] = s[0];
     if (pair) {
-        const uint32_t y[4] = {b.x, b.y, b.z, b.w};
-        uint32_t oy[4];
-        const float4 *c4 = reinterpret_cast<const float4 *>(r.cos + at * half + 8 * va);
-        const float4 *s4 = reinterpret_cast<const float4 *>(r.sin + at * half + 8 * va);
+        x.c[1] = c[1];
+        x.s[1] = s[1];
+    }
+    return x;
+}
+
+// The unit rotated by these angles.
+template <bool BF16>
+__device__ __forceinline__ void turn_unit(LoadedUnit &unit, const UnitAngles &g) {
+    if (!g.on) return;
+    uint32_t x[4] = {unit.a.x, unit.a.y, unit.a.z, unit.a.w};
+    if (unit.vb >= 0) {
+        uint32_t y[4] = {unit.b.x, unit.b.y, unit.b.z, unit.b.w};
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-            const float4 c = c4[k2], s = s4[k2];
-            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int k = 2 * k2 + j;
-                const float2 p = widen_pair<BF16>(x[k]), q = widen_pair<BF16>(y[k]);
-                ox[k] = narrow2<BF16>(turn_x(p.x, q.x, cs[2 * j], sn[2 * j]),
-                                      turn_x(p.y, q.y, cs[2 * j + 1], sn[2 * j + 1]));
-                oy[k] = narrow2<BF16>(turn_y(p.x, q.x, cs[2 * j], sn[2 * j]),
-                                      turn_y(p.y, q.y, cs[2 * j + 1], sn[2 * j + 1]));
-            }
+        for (int k = 0; k < 4; ++k) {
+            const float4 c4 = g.c[k / 2], s4 = g.s[k / 2];
+            const float2 c = k % 2 ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+            const float2 s = k % 2 ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+            const float2 p = widen_pair<BF16>(x[k]), q = widen_pair<BF16>(y[k]);
+            x[k] = narrow2<BF16>(turn_x(p.x, q.x, c.x, s.x), turn_x(p.y, q.y, c.y, s.y));
+            y[k] = narrow2<BF16>(turn_y(p.x, q.x, c.x, s.x), turn_y(p.y, q.y, c.y, s.y));
         }
-        b = make_uint4(oy[0], oy[1], oy[2], oy[3]);
+        unit.b = make_uint4(y[0], y[1], y[2], y[3]);
     } else {                                       // neighbouring channels: rot is a multiple of 16
-        const float4 c = *reinterpret_cast<const float4 *>(r.cos + at * half + 4 * va);
-        const float4 s = *reinterpret_cast<const float4 *>(r.sin + at * half + 4 * va);
-        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+        const float cs[4] = {g.c[0].x, g.c[0].y, g.c[0].z, g.c[0].w}, sn[4] = {g.s[0].x, g.s[0].y, g.s[0].z, g.s[0].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 p = widen_pair<BF16>(x[k]);
-            ox[k] = narrow2<BF16>(turn_x(p.x, p.y, cs[k], sn[k]), turn_y(p.x, p.y, cs[k], sn[k]));
+            x[k] = narrow2<BF16>(turn_x(p.x, p.y, cs[k], sn[k]), turn_y(p.x, p.y, cs[k], sn[k]));
         }
     }
-    a = make_uint4(ox[0], ox[1], ox[2], ox[3]);
+    unit.a = make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// The unit rotated by token tok's angles.
+template <bool BF16>
+__device__ __forceinline__ void rotate_unit(LoadedUnit &unit, int64_t tok, const RopeArgs &r) {
+    turn_unit<BF16>(unit, unit_angles(unit.va, unit.vb >= 0, tok, r));
 }
 
 // The slot whose rows offsets[slot] .. offsets[slot + 1] - 1 hold row i (0 <= i < offsets[B]);

@@ -1557,11 +1557,14 @@ kvq_status kvq_paged_append_chunk(kvq_paged *h, const kvq_chunk *plan, const kvq
     a.chunk.kr = static_cast<const uint16_t *>(h->base.buf.k_residual);
     a.chunk.vr = static_cast<const uint16_t *>(h->base.buf.v_residual);
     a.chunk.R = c.residual;
+    if (q) {
+        a.chunk.q = rows_of(q);
+        a.chunk.q_out = rows_of(q_out);
+        a.chunk.Hq = c.q_heads;
+    }
     cudaError_t e = kvq::launch_quantize_chunk(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "chunk quantize launch");
-    const kvq::Rows none{};
-    e = kvq::launch_chunk_rows(paged_view(h), a.chunk.t, a.chunk.k, a.chunk.v, r, q ? rows_of(q) : none,
-                               q ? rows_of(q_out) : none, s);
+    e = kvq::launch_chunk_rows(paged_view(h), a.chunk.t, a.chunk.k, a.chunk.v, r, a.chunk.q, a.chunk.q_out, s);
     if (e != cudaSuccess) return cuda_fail(e, "chunk rows launch");
     for (int b = 0; b < c.batch; ++b)
         if (plan->counts[b] > 0) h->len[b] = static_cast<int64_t>(plan->starts[b]) + plan->counts[b];

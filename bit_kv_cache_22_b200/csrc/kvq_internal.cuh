@@ -78,6 +78,9 @@ struct ChunkSource {
     RopeArgs rope;
     const uint16_t *kr, *vr;     // residual [B * Hkv][R][d]
     int R;
+    // queries rotated on the way, from q to q_out (q.p NULL: none), by n_turns CTAs of turn_rows rows
+    Rows q, q_out;
+    int Hq, n_turns, turn_rows;
 };
 
 struct QuantizeArgs {
@@ -114,7 +117,7 @@ struct QuantizeArgs {
     ChunkSource chunk;           // launch_quantize_chunk: where the rows come from
 };
 cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t s);
-// The blocks of a chunk (a.chunk), into the paged pool of `a`.
+// The blocks of a chunk (a.chunk), into the paged pool of `a`, and its queries.
 cudaError_t launch_quantize_chunk(const QuantizeArgs &a, cudaStream_t s);
 
 // For both (src, dst) pairs: dst[bh][dst_row0 + i][:] = src[bh][src_row0 + i][:],
@@ -236,8 +239,9 @@ struct PagedView {
     bool sym, bf16;
 };
 
-// Rows of the new tokens that stay in the residual (keys rotated), the queries rotated from q
-// to q_out (q.p NULL: none), and seq_len of every slot with new tokens.  One launch.
+// Rows of the new tokens that stay in the residual (keys rotated) and seq_len of every slot with new
+// tokens; where no block was quantized, also the queries rotated from q to q_out (q.p NULL: none).
+// One launch.
 cudaError_t launch_chunk_rows(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v,
                               const RopeArgs &rope, const Rows &q, const Rows &q_out, cudaStream_t s);
 // The new tokens as the cache holds them, widened to e.  One launch.

@@ -315,31 +315,71 @@ __device__ void load_chunk_group(const ChunkSource &c, const Rows &rows, const R
                                  int b, int h, int Hkv, int64_t tok0, unsigned int *status, uint16_t *dst, int G,
                                  int d) {
     const int64_t start = c.t.starts[b], row0 = static_cast<int64_t>(c.t.offsets[b]) - start;
-    const uint16_t *res_h = res + (static_cast<int64_t>(b) * Hkv + h) * c.R * d;
+    // (the group lies in one block, so its residual rows follow one another)
+    const uint16_t *res_h = res + ((static_cast<int64_t>(b) * Hkv + h) * c.R + tok0 % c.R) * d;
     uint4 *d4 = reinterpret_cast<uint4 *>(dst);
+    if (tok0 + G > start && (row0 + max(tok0, start) < 0 || row0 + tok0 + G > c.t.tokens)) {
+        if (threadIdx.x == 0) atomicOr(status, 8u);            // not this library's table
+        for (int i = threadIdx.x; i < G * (d / 8); i += kQuantThreads) d4[i] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    // a thread keeps its unit of the rows
     const RowUnits ru = row_units(d, rope);
-    for (int i = threadIdx.x; i < G * ru.n; i += blockDim.x) {
-        const int t = i / ru.n, u = i - t * ru.n;
-        const int64_t tok = tok0 + t, row = row0 + tok;
-        LoadedUnit unit;
-        if (tok >= start && (row < 0 || row >= c.t.tokens)) {
-            atomicOr(status, 8u);
-            unit.va = u < ru.pairs ? u : u + ru.pairs;
-            unit.vb = u < ru.pairs ? u + ru.pairs : -1;
-            unit.a = unit.b = make_uint4(0u, 0u, 0u, 0u);
-        } else {
-            unit = load_unit(tok < start ? res_h + tok % c.R * d : rows.p + row * rows.ts + h * rows.hs, u, ru);
-            if (tok >= start) rotate_unit<BF16>(unit, tok, rope);
-        }
+    const int step = kQuantThreads / ru.n, u = threadIdx.x % ru.n, fresh = static_cast<int>(max(start - tok0, int64_t{0}));
+    if (threadIdx.x >= step * ru.n) return;
+    const uint16_t *src = rows.p + (row0 + tok0) * rows.ts + h * rows.hs;
+    for (int t = threadIdx.x / ru.n; t < G; t += step) {
+        LoadedUnit unit = load_unit(t < fresh ? res_h + t * d : src + t * rows.ts, u, ru);
+        if (t >= fresh) rotate_unit<BF16>(unit, tok0 + t, rope);
         d4[t * (d / 8) + unit.va] = unit.a;
         if (unit.vb >= 0) d4[t * (d / 8) + unit.vb] = unit.b;
+    }
+}
+
+// Rows row0 .. row0 + n - 1 (n <= kMostTurns) of the queries, turned by their tokens' positions.
+constexpr int kMostTurns = 8;
+template <bool BF16>
+__device__ void turn_queries(const ChunkSource &c, int64_t row0, int n, int d, unsigned int *status, int *at_s) {
+    if (threadIdx.x < n) {
+        const int64_t row = row0 + threadIdx.x;
+        const int b = slot_of(c.t.offsets, c.t.B, row);
+        const int64_t first = c.t.offsets[b], tok = c.t.starts[b] + row - first;
+        const bool good = first <= row && c.t.starts[b] >= 0 && row < c.t.tokens;
+        at_s[threadIdx.x] = good ? static_cast<int>(tok) : -1;
+        if (!good) atomicOr(status, 8u);
+    }
+    __syncthreads();
+    // a thread keeps its row and unit, so its angles, and goes through the heads: two loads in flight
+    const RowUnits ru = row_units(d, c.rope);
+    const int lot = n * ru.n, parts = kQuantThreads / lot, part = threadIdx.x / lot;       // lot <= 128
+    const int r = threadIdx.x % lot / ru.n, u = threadIdx.x % ru.n, tok = at_s[r];
+    if (part >= parts || tok < 0) return;
+    const bool pair = u < ru.pairs;
+    const UnitAngles angles = unit_angles(pair ? u : u + ru.pairs, pair, tok, c.rope);
+    const uint16_t *src = c.q.p + (row0 + r) * c.q.ts;
+    uint16_t *dst = c.q_out.p + (row0 + r) * c.q_out.ts;
+    for (int h = part; h < c.Hq; h += 2 * parts) {
+        LoadedUnit unit[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (h + x * parts < c.Hq) unit[x] = load_unit(src + (h + x * parts) * c.q.hs, u, ru);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (h + x * parts >= c.Hq) continue;
+            turn_unit<BF16>(unit[x], angles);
+            uint4 *to = reinterpret_cast<uint4 *>(dst + (h + x * parts) * c.q_out.hs);
+            __stcs(to + unit[x].va, unit[x].a);
+            if (unit[x].vb >= 0) __stcs(to + unit[x].vb, unit[x].b);
+        }
     }
 }
 
 // BATCH: the value parameters batched per warp (groups of 64 tokens or more, four or more
 // token pairs per warp); else computed per token pair.  UNROLL: the value phase's token-pair
 // loops unrolled by two (eight or more token pairs per warp).  BF16: the inputs are bf16, else
-// fp16.  CHUNK: a chunk's blocks (a.chunk), CTA x = block * (CTAs per block) + part, y = kv head.
+// fp16.  CHUNK: a chunk's blocks (a.chunk), (block * (CTAs per block) + part, kv head) per CTA; every
+// other CTA turns queries while there are any, so that the one's memory traffic passes under the
+// other's arithmetic.
 template <int D, int N, bool BATCH, bool UNROLL, bool BF16, bool CHUNK>
 __global__ void __launch_bounds__(kQuantThreads, 4) quantize_pack_kernel(const QuantizeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -356,8 +396,26 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quantize_pack_kernel(const Q
     // value groups: [G][d / Gv] entries of 4 floats: (min, max), then (RN(1/s), M + off, cut, s)
     float4 *vg = reinterpret_cast<float4 *>(ch_c + d);
 
-    const int64_t grp = blockIdx.x;
-    const int64_t bh = blockIdx.y;                 // input slice
+    int64_t grp = blockIdx.x, bh = blockIdx.y;     // bh: input slice
+    if constexpr (CHUNK) {
+        const int n_pairs = 2 * min(a.chunk.n_turns, static_cast<int>(gridDim.x) - a.chunk.n_turns);
+        int at = blockIdx.x;                       // of the groups, or of the turns
+        bool turn = at < n_pairs && (at & 1);
+        if (at < n_pairs) {
+            at >>= 1;
+        } else {
+            turn = n_pairs / 2 < a.chunk.n_turns;
+            at -= n_pairs / 2;
+        }
+        if (turn) {
+            const int64_t row0 = static_cast<int64_t>(at) * a.chunk.turn_rows;
+            turn_queries<BF16>(a.chunk, row0, static_cast<int>(min(static_cast<int64_t>(a.chunk.turn_rows), a.chunk.t.tokens - row0)), d,
+                               a.status, reinterpret_cast<int *>(smem));
+            return;
+        }
+        grp = at / a.Hkv;
+        bh = at % a.Hkv;
+    }
     const int64_t in_tok = a.in_tok0 + grp * G;
     int64_t out_tok = a.out_tok0 + grp * G;
     int64_t slice = bh, cap = a.cap;               // output slice and its token capacity
@@ -844,9 +902,14 @@ cudaError_t launch_quantize_chunk(const QuantizeArgs &a, cudaStream_t s) {
     QuantizeArgs b = a;
     const int groups = a.chunk.R / a.G;
     b.gpc = (a.G / 2 < 4 * (kQuantThreads / 32) && groups % 2 == 0) ? 2 : 1;
-    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.chunk.t.n_blocks) * (groups / b.gpc)),
-                    static_cast<unsigned>(a.Hkv));
-    return launch_instance<true>(b, grid, s);
+    const int64_t quants = static_cast<int64_t>(a.chunk.t.n_blocks) * (groups / b.gpc) * a.Hkv;
+    b.chunk.n_turns = 0;
+    if (a.chunk.q.p) {                             // as many CTAs that turn queries, of up to kMostTurns rows
+        const int64_t rows = (a.chunk.t.tokens + quants - 1) / quants;
+        b.chunk.turn_rows = static_cast<int>(rows < kMostTurns ? rows : kMostTurns);
+        b.chunk.n_turns = static_cast<int>((a.chunk.t.tokens + b.chunk.turn_rows - 1) / b.chunk.turn_rows);
+    }
+    return launch_instance<true>(b, dim3(static_cast<unsigned>(quants + b.chunk.n_turns)), s);
 }
 
 cudaError_t launch_copy_rows(const uint16_t *src0, const uint16_t *src1, int64_t src_bh_stride,
