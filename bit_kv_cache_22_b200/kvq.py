@@ -496,7 +496,8 @@ class Rope:
 class ChunkPlan:
     """counts[b] new tokens of each slot from position starts[b] on, planned once on the host and
     used for the chunk calls of every layer (kvq_chunk).  `tokens` packed rows in all; slot b's are
-    rows offsets[b] .. offsets[b + 1] - 1.  Made by PagedKVQCache.plan_chunk and plan_prompt."""
+    rows offsets[b] .. offsets[b + 1] - 1.  Made by PagedKVQCache.plan_chunk and plan_prompt; a graph
+    that captured its calls needs it alive."""
 
     def __init__(self, counts, starts, device, cfg=None, heads=None):
         counts = [int(n) for n in counts]
@@ -523,15 +524,22 @@ class ChunkPlan:
             return lib.kvq_plan_prompt(batch, *heads, self._counts, self.ref, table, room)
 
         _check(fill(None, 0))
-        host = torch.empty(self.chunk.table_bytes // 4, dtype=torch.int32)
+        words = self.chunk.table_bytes // 4
+        host = torch.zeros(words + 1, dtype=torch.int32)
         _check(fill(host.data_ptr(), self.chunk.table_bytes))
         self.tokens = self.chunk.tokens
         self.ends = [(b, s + n) for b, (s, n) in enumerate(zip(self.starts, self.counts)) if n]
         self.offsets = host[:batch + 1].tolist()
-        self.table = host.to(self.device)
+        dev_table = host.to(self.device)
+        self.table = dev_table[:words]
         self.chunk.table = self.table.data_ptr()
         # a cache has a status word of its own, prompts have the plan's
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device) if cfg is None else None
+        self.status = dev_table[words:] if cfg is None else None
+
+    def used_on(self, stream):
+        """The table's memory outlives what is queued on `stream` (None: the stream it was made on)."""
+        if stream is not None:
+            self.table.record_stream(stream)
 
     def check_device(self):
         """Raise KVQError if a kernel run with this prompt plan raised a bit of its status word since the
@@ -564,6 +572,7 @@ def prompt_attention(plan: ChunkPlan, q: torch.Tensor, k: torch.Tensor, v: torch
         o = _output(out, q.shape, q.dtype, device)
         _check(load().kvq_prompt_attention(plan.ref, code, *map(_rows, rows), _rows(o),
                                            plan.status.data_ptr() if plan.status is not None else None, raw))
+        plan.used_on(stream)
         return o
 
     return _on(device, stream, call)
@@ -735,7 +744,10 @@ class PagedKVQCache:
         whole = tokens // g.residual * g.residual
         if whole > g.capacity:
             raise KVQError(KVQ_ERR_CAPACITY, f"{tokens} tokens exceed capacity {g.capacity}")
-        self._grow({seq: -(-whole // self.page_tokens)}, stream)
+        pages = -(-whole // self.page_tokens)
+        if pages - len(self.pages[seq]) > len(self.free_pages):
+            raise KVQError(KVQ_ERR_CAPACITY, "the page pool is exhausted")
+        self._grow({seq: pages}, stream)
         return self
 
     def plan_chunk(self, counts, starts=None) -> ChunkPlan:
@@ -768,6 +780,7 @@ class PagedKVQCache:
                 None if q is None else _rows(q), None if q is None else _rows(q_out), raw))
             for b, end in plan.ends:
                 self.lens[b] = end
+            plan.used_on(stream)
             return q_out
 
         return _on(device, stream, call)
@@ -801,6 +814,7 @@ class PagedKVQCache:
             k = torch.empty((plan.tokens, g.kv_heads, g.head_dim), dtype=self.dtype, device=self.device)
             v = torch.empty_like(k)
             _check(self._lib.kvq_paged_read_chunk(self._h, plan.ref, _rows(k), _rows(v), raw))
+            plan.used_on(stream)
             return k, v
 
         return _on(self.device, stream, call)
@@ -819,6 +833,7 @@ class PagedKVQCache:
             work = torch.empty(room, dtype=torch.uint8, device=self.device) if room else None
             _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, _rows(q), _rows(o),
                                                        work.data_ptr() if room else None, room, raw))
+            plan.used_on(stream)
             return o
 
         return _on(self.device, stream, call)

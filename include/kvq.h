@@ -564,7 +564,9 @@ KVQ_API kvq_status kvq_paged_read_chunk(kvq_paged *cache, const kvq_chunk *plan,
  * weights, values -- is rounded to fp16 (11 bits) under powers of two that keep it in range, the
  * output once to e.  Scales s <= 2^31 and queries |q| <= 2^30, as for decoding; finite inputs: a
  * NaN or infinity reaches rows of its own slot only.  `workspace`: plan->workspace bytes of device
- * scratch, 16-byte aligned (NULL where that is 0); calls that may overlap on the GPU need
+ * scratch, 16-byte aligned (NULL where that is 0; a slot with more than 32 query rows per kv head --
+ * new tokens x query heads -- takes 4 head_dim bytes per token and kv head of what it holds, as its
+ * keys and values are unpacked once for all its rows); calls that may overlap on the GPU need
  * workspaces of their own.  When every slot that holds tokens brings its newest one alone (a decode
  * step), the call runs the decode kernel, which counts splits in the cache's state: attention calls
  * on one cache run one after another, as decode calls do.

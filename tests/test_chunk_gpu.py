@@ -601,6 +601,9 @@ def test_an_exhausted_pool_refuses_and_keeps_the_state():
         p.cache.append_chunk(p.cache.plan_chunk([0, 256, 0, 0]), k[:256], k[:256])
     assert e.value.status == kvq.KVQ_ERR_CAPACITY
     assert len(p.cache.free_pages) == 1
+    with pytest.raises(kvq.KVQError) as e:
+        p.cache.reserve(1, 256)
+    assert e.value.status == kvq.KVQ_ERR_CAPACITY and len(p.cache.free_pages) == 1
     p.append([100, 0, 0, 0])
     p.check_state()
 
