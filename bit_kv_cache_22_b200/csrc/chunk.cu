@@ -65,18 +65,23 @@ __global__ void __launch_bounds__(kRowThreads) chunk_rows_kernel(const PagedView
     }
 }
 
-// One warp per (16-token tile of a slot that meets its chunk, kv head): the tile's tokens as e.
-// A quantized tile's words are unpacked from the fragment layout (include/kvq.h): each lane holds
-// two tokens x four channels per chunk of keys, two channels x four tokens of values; the
-// elements go through shared memory so that rows leave in 16-byte vectors.
+// One warp per (16-token tile of a slot that meets its chunk, kv head, keys or values): the tile's
+// tokens as e.  A quantized tile's words are unpacked from the fragment layout (include/kvq.h): each
+// lane holds two tokens x four channels per chunk of keys, two channels x four tokens of values; the
+// elements go through shared memory so that rows leave in 16-byte vectors.  Bound by the latency of a
+// warp's chain (offsets, page, codes, parameters), so keys and values are warps of their own: 43 us
+// for four prompts of 8192 tokens (8 kv heads, d = 128, 2-bit; 0.16 GB moved), 50 us with both in one.
+// Rows turned about vector by vector instead of padded have no bank conflicts but more address
+// arithmetic: 48 us.
 constexpr int kReadWarps = 4;
 
 template <int D, int N, bool BF16>
 __global__ void __launch_bounds__(32 * kReadWarps) chunk_read_kernel(const PagedView c, const ChunkTable t,
                                                                      const Rows k_out, const Rows v_out) {
-    __shared__ __align__(16) uint16_t tile_s[kReadWarps][2][16][D + 8];
+    __shared__ __align__(16) uint16_t tile_s[kReadWarps][16][D + 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kReadWarps + warp;
+    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kReadWarps + warp) / 2;
+    const bool is_v = warp & 1;
     if (unit >= static_cast<int64_t>(t.n_tiles) * c.Hkv) return;
     const int64_t ti = unit / c.Hkv;
     const int h = static_cast<int>(unit % c.Hkv);
@@ -89,17 +94,15 @@ __global__ void __launch_bounds__(32 * kReadWarps) chunk_read_kernel(const Paged
         if (lane == 0) atomicOr(c.status, 8u);
         return;
     }
-    uint16_t(*ks)[D + 8] = tile_s[warp][0];
-    uint16_t(*vs)[D + 8] = tile_s[warp][1];
+    uint16_t(*tile)[D + 8] = tile_s[warp];
     if (tok0 >= tq) {
+        const uint16_t *res = is_v ? c.vr : c.kr;
         for (int i = lane; i < 16 * (D / 8); i += 32) {
             const int r = i / (D / 8), v = i % (D / 8);
             const int64_t tok = tok0 + r;
-            if (tok >= start && tok < end) {
-                const int64_t at = ((static_cast<int64_t>(b) * c.Hkv + h) * c.R + tok % c.R) * D;
-                reinterpret_cast<uint4 *>(ks[r])[v] = reinterpret_cast<const uint4 *>(c.kr + at)[v];
-                reinterpret_cast<uint4 *>(vs[r])[v] = reinterpret_cast<const uint4 *>(c.vr + at)[v];
-            }
+            if (tok >= start && tok < end)
+                reinterpret_cast<uint4 *>(tile[r])[v] = reinterpret_cast<const uint4 *>(
+                    res + ((static_cast<int64_t>(b) * c.Hkv + h) * c.R + tok % c.R) * D)[v];
         }
     } else {
         const int64_t pi = tok0 / c.P;
@@ -110,15 +113,16 @@ __global__ void __launch_bounds__(32 * kReadWarps) chunk_read_kernel(const Paged
         }
         constexpr int W = D * N / 64, TW = D * N / 2, B = 4 / N;
         const int64_t slice = static_cast<int64_t>(page) * c.Hkv + h, pt = tok0 - pi * c.P;
-        const uint32_t *kw = c.kc + (slice * (c.P / 16) + pt / 16) * TW + lane * W;
-        const uint32_t *vw = c.vc + (slice * (c.P / 16) + pt / 16) * TW + lane * W;
-        const float *s_k = c.ks + (slice * (c.P / c.G) + pt / c.G) * D;
-        const int16_t *z_k = c.kz + (slice * (c.P / c.G) + pt / c.G) * D;
-        const int ngv = D / c.Gv;
-        const float *s_v = c.vs + (slice * c.P + pt) * ngv;
-        const int16_t *z_v = c.vz + (slice * c.P + pt) * ngv;
+        const uint32_t *words = (is_v ? c.vc : c.kc) + (slice * (c.P / 16) + pt / 16) * TW + lane * W;
         constexpr uint32_t kMask = 0x01010101u * ((1u << N) - 1);
         constexpr float kHalf = static_cast<float>(1 << (N - 1));
+        uint32_t code[W];
+#pragma unroll
+        for (int i = 0; i < W; i += 2) {
+            const uint2 x = reinterpret_cast<const uint2 *>(words)[i / 2];
+            code[i] = x.x;
+            code[i + 1] = x.y;
+        }
         // four codes (the bytes of b), minus z, times s
         auto values = [](uint32_t b, const float (&z)[4], const float (&s)[4], float (&f)[4]) {
 #pragma unroll
@@ -127,53 +131,65 @@ __global__ void __launch_bounds__(32 * kReadWarps) chunk_read_kernel(const Paged
                 f[e] = __fmul_rn(__fadd_rn(x, z[e]), s[e]);
             }
         };
-        float sv[4], zv[4];
+        float f[4];
+        if (!is_v) {
+            const float *s_k = c.ks + (slice * (c.P / c.G) + pt / c.G) * D;
+            const int16_t *z_k = c.kz + (slice * (c.P / c.G) + pt / c.G) * D;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const uint32_t kword = kw[j / B], vword = vw[j / B];
-            const float4 s4 = reinterpret_cast<const float4 *>(s_k)[4 * j + (lane & 3)];
-            const float sk[4] = {s4.x, s4.y, s4.z, s4.w};
-            float zk[4] = {-8388608.0f - kHalf, -8388608.0f - kHalf, -8388608.0f - kHalf, -8388608.0f - kHalf};
-            if (!c.sym) {
-                const uint2 z4 = reinterpret_cast<const uint2 *>(z_k)[4 * j + (lane & 3)];
-                zk[0] = -8388608.0f - static_cast<float>(static_cast<int16_t>(z4.x & 0xffffu));
-                zk[1] = -8388608.0f - static_cast<float>(static_cast<int>(z4.x) >> 16);
-                zk[2] = -8388608.0f - static_cast<float>(static_cast<int16_t>(z4.y & 0xffffu));
-                zk[3] = -8388608.0f - static_cast<float>(static_cast<int>(z4.y) >> 16);
-            }
-            if (j == 0 || ((16 * j) & (c.Gv - 1)) == 0) {
+            for (int j = 0; j < D / 16; ++j) {
+                const float4 s4 = reinterpret_cast<const float4 *>(s_k)[4 * j + (lane & 3)];
+                const float sk[4] = {s4.x, s4.y, s4.z, s4.w};
+                float zk[4] = {-8388608.0f - kHalf, -8388608.0f - kHalf, -8388608.0f - kHalf, -8388608.0f - kHalf};
+                if (!c.sym) {
+                    const uint2 z4 = reinterpret_cast<const uint2 *>(z_k)[4 * j + (lane & 3)];
+                    zk[0] = -8388608.0f - static_cast<float>(static_cast<int16_t>(z4.x & 0xffffu));
+                    zk[1] = -8388608.0f - static_cast<float>(static_cast<int>(z4.x) >> 16);
+                    zk[2] = -8388608.0f - static_cast<float>(static_cast<int16_t>(z4.y & 0xffffu));
+                    zk[3] = -8388608.0f - static_cast<float>(static_cast<int>(z4.y) >> 16);
+                }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int at = (4 * (lane & 3) + e) * ngv + 16 * j / c.Gv;
-                    sv[e] = s_v[at];
-                    zv[e] = -8388608.0f - (c.sym ? kHalf : static_cast<float>(z_v[at]));
+                for (int half = 0; half < 2; ++half) {
+                    values((code[j / B] >> (N * (2 * (j % B) + half))) & kMask, zk, sk, f);
+                    *reinterpret_cast<uint2 *>(&tile[(lane >> 2) + 8 * half][16 * j + 4 * (lane & 3)]) =
+                        make_uint2(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]));
                 }
             }
+        } else {
+            const int ngv = D / c.Gv;
+            const float *s_v = c.vs + (slice * c.P + pt) * ngv;
+            const int16_t *z_v = c.vz + (slice * c.P + pt) * ngv;
+            float sv[4], zv[4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int sh = N * (2 * (j % B) + half);
-                const int row = (lane >> 2) + 8 * half;       // token of a key, channel of a value
-                float f[4];
-                values((kword >> sh) & kMask, zk, sk, f);
-                *reinterpret_cast<uint2 *>(&ks[row][16 * j + 4 * (lane & 3)]) =
-                    make_uint2(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]));
-                values((vword >> sh) & kMask, zv, sv, f);
+            for (int j = 0; j < D / 16; ++j) {
+                if (j == 0 || ((16 * j) & (c.Gv - 1)) == 0) {
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const uint32_t two = narrow2<BF16>(f[e], f[e + 1]);
-                    vs[4 * (lane & 3) + e][16 * j + row] = static_cast<uint16_t>(two);
-                    vs[4 * (lane & 3) + e + 1][16 * j + row] = static_cast<uint16_t>(two >> 16);
+                    for (int e = 0; e < 4; ++e) {
+                        const int g = (4 * (lane & 3) + e) * ngv + 16 * j / c.Gv;
+                        sv[e] = s_v[g];
+                        zv[e] = -8388608.0f - (c.sym ? kHalf : static_cast<float>(z_v[g]));
+                    }
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    values((code[j / B] >> (N * (2 * (j % B) + half))) & kMask, zv, sv, f);
+                    const int ch = 16 * j + (lane >> 2) + 8 * half;
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const uint32_t two = narrow2<BF16>(f[e], f[e + 1]);
+                        tile[4 * (lane & 3) + e][ch] = static_cast<uint16_t>(two);
+                        tile[4 * (lane & 3) + e + 1][ch] = static_cast<uint16_t>(two >> 16);
+                    }
                 }
             }
         }
     }
     __syncwarp();
+    const Rows &out = is_v ? v_out : k_out;
     for (int i = lane; i < 16 * (D / 8); i += 32) {
         const int r = i / (D / 8), v = i % (D / 8);
         const int64_t tok = tok0 + r, row = first + tok - start;
         if (tok < start || tok >= end || row < 0 || row >= t.tokens) continue;
-        reinterpret_cast<uint4 *>(k_out.p + row * k_out.ts + h * k_out.hs)[v] = reinterpret_cast<uint4 *>(ks[r])[v];
-        reinterpret_cast<uint4 *>(v_out.p + row * v_out.ts + h * v_out.hs)[v] = reinterpret_cast<uint4 *>(vs[r])[v];
+        reinterpret_cast<uint4 *>(out.p + row * out.ts + h * out.hs)[v] = reinterpret_cast<uint4 *>(tile[r])[v];
     }
 }
 
@@ -242,7 +258,7 @@ cudaError_t launch_slots_to_rows(const ChunkTable &t, const float *dense, const 
 
 cudaError_t launch_chunk_read(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v, cudaStream_t s) {
     if (t.n_tiles == 0) return cudaSuccess;
-    const int64_t units = static_cast<int64_t>(t.n_tiles) * c.Hkv;
+    const int64_t units = 2 * static_cast<int64_t>(t.n_tiles) * c.Hkv;
     const unsigned grid = static_cast<unsigned>((units + kReadWarps - 1) / kReadWarps);
     if (c.d == 64 && c.bits == 2) read_launch<64, 2>(c, t, k, v, grid, s);
     else if (c.d == 64) read_launch<64, 4>(c, t, k, v, grid, s);
