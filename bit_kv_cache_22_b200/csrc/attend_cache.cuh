@@ -44,7 +44,6 @@ namespace {
 constexpr int kRows = 128;                 // rows of a query tile, tokens of a key tile
 constexpr int kStages = 2;                 // key and value operand tiles, each
 constexpr int kUnits = 4;                  // of 32 tokens in a key tile: a warp's work for keys or values
-constexpr int kUnpackWarps = 2 * kUnits;
 constexpr int kExps = 8;                   // key tiles whose exponents are kept (at most kStages + 1 are live)
 constexpr int kValueStep = 4;              // values' exponents are multiples of this: they rarely differ
 constexpr float kLazyMax = 8.0f;           // the running maximum is raised when a logit passes it by this
@@ -517,10 +516,11 @@ __device__ __forceinline__ CacheItem cache_item(const AttendArgs &a, const int4 
 enum { kQFull = 0, kKFull = 1, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages, kVEmpty = kKEmpty + kStages,
        kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kOFull = kPFull + 4, kDrain = kOFull + 2, kBars };
 
-// queries, filled: arrivals that fill the queries, a tile's keys or values
-__device__ __forceinline__ void init_bars(uint32_t bars, int queries, int filled) {
+// queries, filled, weighed: arrivals that fill the queries, a tile's keys or values, half its weights
+__device__ __forceinline__ void init_bars(uint32_t bars, int queries, int filled, int weighed) {
     for (int i = 0; i < kBars; ++i)
-        tc::bar_init(bars + 8u * i, i == kQFull ? queries : i < kKEmpty ? filled : i >= kPFull && i < kPFull + 4 ? 4 : 1);
+        tc::bar_init(bars + 8u * i,
+                     i == kQFull ? queries : i < kKEmpty ? filled : i >= kPFull && i < kPFull + 4 ? weighed : 1);
     tc::fence_barrier_init();
 }
 
@@ -594,7 +594,7 @@ __device__ __forceinline__ void mma_role(const CacheItem &work, uint32_t base, u
 
 // The softmax of one query row a thread, warps 0-3 for stream 0, 4-7 for stream 1; then the row's
 // output, or its part of it.  WHOLE: a row's 128 logits are held in registers at once; else they are
-// read twice, 32 at a time, by rolled loops.
+// read twice, 32 at a time, by rolled loops, and the rows are at most 32, of warps 0 and 4.
 template <int D, bool BF16, bool WHOLE, class L>
 __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheItem &work, const TileExps *exps,
                                              unsigned char *smem, uint32_t base, uint32_t tmem, int warp, int lane,
@@ -788,7 +788,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                 }
             }
         }
-        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if constexpr (WHOLE) asm volatile("bar.sync 2, 256;" ::: "memory");
+        else asm volatile("bar.sync 2, 64;" ::: "memory");
         if (t == 0 && any && go) {
             tc::fence_after_sync();
             const float m1 = ml[r], l1 = ml[kRows + r];

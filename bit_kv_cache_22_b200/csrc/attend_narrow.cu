@@ -2,11 +2,11 @@
 // steps, drafts): one query tile of 128 rows holds all of a slot's rows, so each code is used by one
 // tile only and is unpacked where it is used.
 //
-//   warps 0-3, 4-7   softmax of stream 0, 1: alternate key tiles
-//   warps 8-11       keys' operands: each warp 32 tokens of each key tile
-//   warps 12-15      values'
-//   warp 16          issues the MMAs (warps 17-19 fill the warpgroup, which gives its registers to the
-//                    softmax: 2 x 128 x 120 + 2 x 128 x 88 + 128 x 64 <= 640 x 96)
+//   warps 0, 4       softmax of stream 0, 1: alternate key tiles, at most 32 rows (the warps that
+//                    reach the tensor memory of rows 0-31)
+//   warp 1           issues the MMAs
+//   warps 8-15       keys' operands: each warp 32 tokens of every other key tile
+//   warps 16-23      values'
 #include <algorithm>
 #include <cstdint>
 
@@ -15,7 +15,9 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
+constexpr int kTurns = 2;                  // key tiles in hand at a time
+constexpr int kUnpackWarps = 2 * kTurns * kUnits;
 
 template <int D>
 struct NarrowSmem {
@@ -47,34 +49,35 @@ __device__ __forceinline__ void emit_queries_of(const AttendArgs &a, const Cache
     if (lane == 0) tc::bar_arrive(base + L::bars + 8u * kQFull);
 }
 
-// Warp u of the four that unpack keys (kv 0) or values (1): unit u of every key tile, fetched a tile
-// ahead, its page number two.
+// Warp of those that unpack keys (kv 0) or values (1): unit u of key tiles `turn`, turn + kTurns, ...,
+// fetched a tile ahead, its page number two.  Each tile is a chain -- parameters, shared memory, codes,
+// stores -- that a warp cannot hide from itself.
 template <int D, int N, bool BF16, class L>
 __device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem &work, TileExps *exps,
-                                            unsigned char *smem, uint32_t base, int kv, int u, int lane,
+                                            unsigned char *smem, uint32_t base, int kv, int turn, int u, int lane,
                                             volatile int &gave_up) {
     const PagedView &c = a.cache;
-    unsigned char *meta = smem + L::meta + (kUnits * kv + u) * kMetaBytes;
+    unsigned char *meta = smem + L::meta + (kUnits * (kTurns * kv + turn) + u) * kMetaBytes;
     const int n = work.n;
     constexpr int W = D * N / 64;
     const UnitSource<D> src(c, kv, work.slot, work.h, work.len, work.tq);
     const int32_t *pages = c.page_table + static_cast<int64_t>(work.slot) * c.max_pages;
-    int tok = work.tile0 * kRows + 32 * u;         // of the tile in hand
+    int tok = (work.tile0 + turn) * kRows + 32 * u;         // of the tile in hand
     int at_page = tok / c.P, at_tok = tok % c.P;   // of the tile to fetch
     auto page_at = [&](int t) { return t < src.tq && at_page < c.max_pages ? pages[at_page] : -1; };
     auto advance = [&] {
-        at_tok += kRows;
+        at_tok += kTurns * kRows;
         while (at_tok >= c.P) {
             at_tok -= c.P;
             ++at_page;
         }
     };
     Fetched<D, N> f;
-    fetch_unit<D, N>(f, c, src, page_at(tok), at_tok, tok, n > 0, lane);
+    fetch_unit<D, N>(f, c, src, page_at(tok), at_tok, tok, turn < n, lane);
     advance();
-    int page = page_at(tok + kRows);
-    emit_queries_of<D, BF16, L>(a, work, smem, base, kUnits * kv + u, lane);
-    for (int j = 0; j < n; ++j, tok += kRows) {
+    int page = page_at(tok + kTurns * kRows);
+    emit_queries_of<D, BF16, L>(a, work, smem, base, kUnits * (kTurns * kv + turn) + u, lane);
+    for (int j = turn; j < n; j += kTurns, tok += kTurns * kRows) {
         const int s = j % kStages, kind0 = f.kind[0], kind1 = f.kind[1];
         int ex;
         const bool narrow = prepare_unit<D, N, BF16>(f, c, src, tok, lane, meta, ex);
@@ -84,9 +87,9 @@ __device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem
             words[0][i] = f.w[0][i];
             words[1][i] = f.w[1][i];
         }
-        fetch_unit<D, N>(f, c, src, page, at_tok, tok + kRows, j + 1 < n, lane);
+        fetch_unit<D, N>(f, c, src, page, at_tok, tok + kTurns * kRows, j + kTurns < n, lane);
         advance();
-        page = page_at(tok + 2 * kRows);
+        page = page_at(tok + 2 * kTurns * kRows);
         if (j >= kStages &&
             !tc::bar_wait_warp(base + L::bars + 8u * ((kv ? kVEmpty : kKEmpty) + s), ((j / kStages) & 1) ^ 1, &gave_up))
             break;
@@ -116,33 +119,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     if (threadIdx.x == 0) {
         work = cache_item(a, a.t.items[a.t.n_wide + blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
         gave_up = 0;
-        init_bars(base + L::bars, kUnpackWarps, kUnits);
+        init_bars(base + L::bars, kUnpackWarps, kUnits, 1);
     }
     __syncthreads();
-    if (!work.good || !work.alternate) {           // not this library's table
+    if (!work.good || work.count > 32 / work.hg) {           // not this library's table
         if (threadIdx.x == 0) atomicOr(a.status, 8u);
         return;
     }
-    if (warp == 16) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
+    if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
-    if (warp >= 8 && warp < 16) {
-        tc::regs_give<88>();
-        unpack_role<D, N, BF16, L>(a, work, exps, smem, base, warp >= 12, warp % 4, lane, gave_up);
-    } else if (warp >= 16) {
-        tc::regs_give<64>();
-        if (warp == 16 && work.n > 0) mma_role<D, false, L>(work, base, tmem, gave_up);
-    } else {
-        tc::regs_take<120>();
+    if (warp >= 8) {
+        unpack_role<D, N, BF16, L>(a, work, exps, smem, base, warp >= 16, (warp / kUnits) % kTurns, warp % kUnits, lane,
+                                   gave_up);
+    } else if (warp == 1) {
+        if (work.n > 0) mma_role<D, false, L>(work, base, tmem, gave_up);
+    } else if (warp % 4 == 0) {
         softmax_role<D, BF16, false, L>(a, work, exps, smem, base, tmem, warp, lane, gave_up);
     }
     tc::fence_before_sync();
     __syncthreads();
     if (threadIdx.x == 0 && gave_up) atomicOr(a.status, 1u);
-    if (warp == 16) {
+    if (warp == 1) {
         tc::fence_after_sync();
         tc::tmem_free(tmem, 512);
     }

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const AttendAr
                 work.good = false;
         }
         gave_up = 0;
-        init_bars(base + L::bars, 1, 1);
+        init_bars(base + L::bars, 1, 1, 4);
     }
     __syncthreads();
     if (!work.good) {                              // not this library's table
