@@ -307,9 +307,10 @@ __device__ void load_group(const uint16_t *slice, int64_t tok0, const int32_t *r
 
 // The rows of one group of a chunk's block, tokens tok0 .. tok0+G-1 of slot b: those before the
 // chunk's start from the residual (rotated when they were new), the others from the packed rows,
-// rotated as `rope` says between load and store.  (The kernel is bound by instruction issue: a
-// pass of its own over shared memory for the rotation, with the loads batched, took 133 us where this
-// takes 115 us for four prompts of 8192 tokens, and two units' loads in flight 125 us.)
+// rotated as `rope` says between load and store.  (The kernel is bound by instruction issue.  Four
+// prompts of 8192 tokens, 32 query / 8 kv heads, d = 128, 2-bit, take 187 us with their queries turned,
+// 0.69 GB; quantized alone 115 us, then turned by a launch of its own 109 us.  Alone, a pass over shared
+// memory for the rotation, with the loads batched, took 133 us, and two units' loads in flight 125 us.)
 template <bool BF16>
 __device__ void load_chunk_group(const ChunkSource &c, const Rows &rows, const RopeArgs &rope, const uint16_t *res,
                                  int b, int h, int Hkv, int64_t tok0, unsigned int *status, uint16_t *dst, int G,
