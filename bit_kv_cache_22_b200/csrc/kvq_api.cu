@@ -1611,7 +1611,13 @@ kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const 
         d.l_part = d.m_part + units * d.S;
         const kvq::ChunkTable t = chunk_table(plan);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        cudaError_t e = kvq::launch_rows_to_slots(t, rows_of(q), dense, c.q_heads, c.head_dim, s);
+        cudaError_t e = cudaSuccess;
+        // packed rows that lie slot by slot already
+        if (plan->tokens == c.batch && (c.q_heads < 2 || q->head_stride == c.head_dim) &&
+            (c.batch < 2 || q->token_stride == static_cast<int64_t>(c.q_heads) * c.head_dim))
+            d.q = static_cast<const uint16_t *>(q->data);
+        else
+            e = kvq::launch_rows_to_slots(t, rows_of(q), dense, c.q_heads, c.head_dim, s);
         if (e == cudaSuccess) e = kvq::launch_decode(d, s);
         if (e == cudaSuccess)
             e = kvq::launch_slots_to_rows(t, out, rows_of(o), c.q_heads, c.head_dim, c.dtype == KVQ_BF16, s);

@@ -430,7 +430,7 @@ class KVQCache:
 def _on(device: torch.device, stream, call):
     """call(stream pointer) with the device current and its stream torch's current one, so that what
     the call allocates belongs to the stream its kernels run on."""
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and _current_device() == device.index:
         return call(_raw_stream(device.index))
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream must be one of {device}")
@@ -438,46 +438,48 @@ def _on(device: torch.device, stream, call):
         return call(_raw_stream(device.index))
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream    # of a device index, without a Stream object's cost
+# (without a Stream object's cost, and torch's check whether CUDA is up: there is a plan on the device)
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _servable(t: torch.Tensor) -> bool:
-    """Packed rows the kernels take as they are: channels contiguous, rows on 16 bytes, strides positive."""
-    a, b, c = t.stride()
-    n, h, _ = t.shape
-    return c == 1 and t.data_ptr() % 16 == 0 and (n < 2 or (a > 0 and a % 8 == 0)) and \
-        (h < 2 or (b > 0 and b % 8 == 0))
+def _servable(at: int, a: int, b: int, c: int, tokens: int, heads: int) -> bool:
+    """Rows the kernels take as they are: channels contiguous, rows on 16 bytes, strides positive."""
+    return c == 1 and not at & 15 and (tokens < 2 or (a > 0 and not a & 7)) and (heads < 2 or (b > 0 and not b & 7))
 
 
-def _packed(t: torch.Tensor, name: str, tokens: int, heads: int, d: int, dtype, device) -> torch.Tensor:
-    """Packed rows as a kernel takes them: checked, on the device, channels contiguous, rows on 16
-    bytes (copied where they are not)."""
+def _packed(t: torch.Tensor, name: str, tokens: int, heads: int, d: int, dtype, device):
+    """Packed rows as a kernel takes them, and the tensor they lie in: checked, on the device, channels
+    contiguous, rows on 16 bytes (copied where they are not)."""
     if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}]")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         t = t.to(device, non_blocking=True)
-    if tokens and not _servable(t):
+    a, b, c = t.stride()
+    at = t.data_ptr()
+    if tokens and not _servable(at, a, b, c, tokens, heads):
         t = t.contiguous()
-        if not _servable(t):
-            t = t.clone()
-    return t
+        a, b, c = t.stride()
+        if not _servable(t.data_ptr(), a, b, c, tokens, heads):
+            t = t.clone(memory_format=torch.contiguous_format)
+            a, b, c = t.stride()
+        at = t.data_ptr()
+    return Rows(at, a, b), t
 
 
-def _output(out: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
+def _output(out: torch.Tensor | None, like: torch.Tensor):
+    """Rows of `out`, or of a new tensor, of `like`'s shape, type and device; and the tensor."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.shape != shape or out.dtype != dtype or out.device != device:
-        raise ValueError(f"out must be {dtype} {list(shape)} on {device}")
-    if out.numel() and not _servable(out):
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+    elif out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+        raise ValueError(f"out must be {like.dtype} {list(like.shape)} on {like.device}")
+    tokens, heads, _ = out.shape
+    a, b, c = out.stride()
+    at = out.data_ptr()
+    if tokens and not _servable(at, a, b, c, tokens, heads):
         raise ValueError("out's channels must be contiguous and its rows start on 16 bytes")
-    return out
-
-
-def _rows(t: torch.Tensor):
-    a, b, _ = t.stride()
-    return ctypes.byref(Rows(t.data_ptr(), a, b))
+    return Rows(at, a, b), out
 
 
 class Rope:
@@ -535,6 +537,7 @@ class ChunkPlan:
         self.chunk.table = self.table.data_ptr()
         # a cache has a status word of its own, prompts have the plan's
         self.status = dev_table[words:] if cfg is None else None
+        self.status_at = self.status.data_ptr() if cfg is None else None
 
     def used_on(self, stream):
         """The table's memory outlives what is queued on `stream` (None: the stream it was made on)."""
@@ -567,11 +570,12 @@ def prompt_attention(plan: ChunkPlan, q: torch.Tensor, k: torch.Tensor, v: torch
     code = _dtype_code(q.dtype)
 
     def call(raw):
-        rows = [_packed(t, name, n, heads, c.head_dim, q.dtype, device)
-                for t, name, heads in ((q, "q", c.q_heads), (k, "k", c.kv_heads), (v, "v", c.kv_heads))]
-        o = _output(out, q.shape, q.dtype, device)
-        _check(load().kvq_prompt_attention(plan.ref, code, *map(_rows, rows), _rows(o),
-                                           plan.status.data_ptr() if plan.status is not None else None, raw))
+        d, dtype = c.head_dim, q.dtype
+        q_rows, dq = _packed(q, "q", n, c.q_heads, d, dtype, device)
+        k_rows, dk = _packed(k, "k", n, c.kv_heads, d, dtype, device)
+        v_rows, dv = _packed(v, "v", n, c.kv_heads, d, dtype, device)
+        o_rows, o = _output(out, dq)
+        _check(load().kvq_prompt_attention(plan.ref, code, q_rows, k_rows, v_rows, o_rows, plan.status_at, raw))
         plan.used_on(stream)
         return o
 
@@ -765,19 +769,18 @@ class PagedKVQCache:
         g, device, dtype, n = self.geom, self._device_of(plan), self.dtype, plan.tokens
 
         def call(raw):
-            k = _packed(t_K, "t_K", n, g.kv_heads, g.head_dim, dtype, device)
-            v = _packed(t_V, "t_V", n, g.kv_heads, g.head_dim, dtype, device)
-            q = q_out = None
+            k_rows, k = _packed(t_K, "t_K", n, g.kv_heads, g.head_dim, dtype, device)
+            v_rows, v = _packed(t_V, "t_V", n, g.kv_heads, g.head_dim, dtype, device)
+            q_rows = o_rows = q_out = None
             if t_Q is not None:
-                q = _packed(t_Q, "t_Q", n, g.q_heads, g.head_dim, dtype, device)
-                q_out = _output(out, q.shape, dtype, device)
+                q_rows, q = _packed(t_Q, "t_Q", n, g.q_heads, g.head_dim, dtype, device)
+                o_rows, q_out = _output(out, q)
             if rope is not None and rope.cos.device != device:
                 raise ValueError(f"the angles must be on {device}")
             if plan.chunk.blocks:
                 self._pages_for(plan, stream)
             _check(self._lib.kvq_paged_append_chunk(
-                self._h, plan.ref, _rows(k), _rows(v), None if rope is None else rope.ref,
-                None if q is None else _rows(q), None if q is None else _rows(q_out), raw))
+                self._h, plan.ref, k_rows, v_rows, None if rope is None else rope.ref, q_rows, o_rows, raw))
             for b, end in plan.ends:
                 self.lens[b] = end
             plan.used_on(stream)
@@ -813,7 +816,9 @@ class PagedKVQCache:
         def call(raw):
             k = torch.empty((plan.tokens, g.kv_heads, g.head_dim), dtype=self.dtype, device=self.device)
             v = torch.empty_like(k)
-            _check(self._lib.kvq_paged_read_chunk(self._h, plan.ref, _rows(k), _rows(v), raw))
+            head, token = g.head_dim, g.kv_heads * g.head_dim
+            _check(self._lib.kvq_paged_read_chunk(self._h, plan.ref, Rows(k.data_ptr(), token, head),
+                                                  Rows(v.data_ptr(), token, head), raw))
             plan.used_on(stream)
             return k, v
 
@@ -826,12 +831,12 @@ class PagedKVQCache:
         self._device_of(plan)
 
         def call(raw):
-            q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
-            o = _output(out, q.shape, self.dtype, self.device)
+            q_rows, q = _packed(t_Q, "t_Q", plan.tokens, g.q_heads, g.head_dim, self.dtype, self.device)
+            o_rows, o = _output(out, q)
             # scratch of the call's own, from torch's pool of its stream (or graph)
             room = plan.chunk.workspace
             work = torch.empty(room, dtype=torch.uint8, device=self.device) if room else None
-            _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, _rows(q), _rows(o),
+            _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, q_rows, o_rows,
                                                        work.data_ptr() if room else None, room, raw))
             plan.used_on(stream)
             return o
