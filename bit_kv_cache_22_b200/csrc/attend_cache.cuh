@@ -473,11 +473,25 @@ struct CacheItem {
     int tile0, n;
     int end0;                                      // tiles below it concern stream 0 (stream 1: n)
     int split, n_splits, part;                     // first partial tile
+    int kv_at, q_at;                               // STAGED: the slot's first staged key and query tile
     bool alternate;                                // one query tile, alternate key tiles
     bool good;
 };
 
+// Every load of the table is under way before the first check (a CTA waits for two in a row, not five).
+template <bool STAGED>
 __device__ __forceinline__ CacheItem cache_item(const AttendArgs &a, const int4 item, int h) {
+    const int slot = min(max(item.x, 0), a.t.B - 1);
+    const int first = a.t.offsets[slot], behind = a.t.offsets[slot + 1], start = a.t.starts[slot];
+    const int len = a.cache.seq_len[slot];
+    int kv[2] = {0, 0}, q[2] = {0, 0};
+    if constexpr (STAGED) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            kv[e] = a.t.kv_tiles[slot + e];
+            q[e] = a.t.q_tiles[slot + e];
+        }
+    }
     CacheItem w{};
     w.h = h;
     w.hg = a.Hq / a.Hkv;
@@ -489,9 +503,9 @@ __device__ __forceinline__ CacheItem cache_item(const AttendArgs &a, const int4 
     w.part = item.w;
     w.good = w.slot >= 0 && w.slot < a.t.B && w.q0 >= 0 && w.split < w.n_splits && w.part >= 0;
     if (!w.good) return w;
-    w.first = a.t.offsets[w.slot];
-    w.count = a.t.offsets[w.slot + 1] - w.first;
-    w.start = a.t.starts[w.slot];
+    w.first = first;
+    w.count = behind - first;
+    w.start = start;
     w.alternate = w.count - w.q0 <= w.tpt;
     w.good = w.first >= 0 && w.count > w.q0 && w.start >= 0 && w.start <= kMaxTokens - w.count &&
              static_cast<int64_t>(w.first) + w.count <= a.t.tokens &&
@@ -499,7 +513,7 @@ __device__ __forceinline__ CacheItem cache_item(const AttendArgs &a, const int4 
               w.part + static_cast<int64_t>(w.n_splits) * (w.alternate ? 1 : 2) <= a.part_tiles);
     if (!w.good) return w;
     // (positions stay below 2^31 - 1024, so a tile's tokens are 32-bit numbers)
-    w.len = min(max(a.cache.seq_len[w.slot], 0), kMaxTokens);
+    w.len = min(max(len, 0), kMaxTokens);
     w.tq = w.len / a.cache.R * a.cache.R;
     const int last = min(w.q0 + 2 * w.tpt, w.count);
     const int all = (min(w.start + last, w.len) + kRows - 1) / kRows;
@@ -509,6 +523,13 @@ __device__ __forceinline__ CacheItem cache_item(const AttendArgs &a, const int4 
     w.end0 = w.n;
     if (!w.alternate)
         w.end0 = max(0, min(w.n, (min(w.start + w.q0 + w.tpt, w.len) + kRows - 1) / kRows - w.tile0));
+    if constexpr (STAGED) {
+        w.kv_at = kv[0];
+        w.q_at = q[0];
+        w.good = kv[0] >= 0 && kv[0] <= a.t.n_kv_tiles && kv[0] + w.tile0 + w.n <= kv[1] && kv[1] <= a.t.n_kv_tiles &&
+                 q[0] >= 0 && q[0] <= a.t.n_q_tiles && q[0] + (w.count + w.tpt - 1) / w.tpt <= q[1] &&
+                 q[1] <= a.t.n_q_tiles;
+    }
     return w;
 }
 

@@ -124,15 +124,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     __shared__ CacheItem work;                     // in shared memory: each role keeps what it needs of it
     __shared__ TileExps exps[kExps];
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        work = cache_item(a, a.t.items[a.t.n_wide + blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
+    if (threadIdx.x == 0) work = cache_item<false>(a, a.t.items[a.t.n_wide + blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
+    if (threadIdx.x == 64) {
         gave_up = 0;
         init_bars(base + L::bars, kUnpackWarps, kUnits, 1);
-    }
-    __syncthreads();
-    if (!work.good || work.count > 32 / work.hg) {           // not this library's table
-        if (threadIdx.x == 0) atomicOr(a.status, 8u);
-        return;
     }
     if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
     tc::fence_before_sync();
@@ -140,7 +135,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
-    if (warp >= 8) {
+    if (!work.good || work.count > 32 / work.hg) { // not this library's table
+        if (threadIdx.x == 0) atomicOr(a.status, 8u);
+    } else if (warp >= 8) {
         unpack_role<D, N, BF16, L>(a, work, exps, smem, base, warp >= 16, (warp / kUnits) % kTurns, warp % kUnits, lane,
                                    gave_up);
     } else if (warp == 1) {

@@ -123,44 +123,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const AttendAr
     __shared__ volatile int gave_up;
     __shared__ CacheItem work;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        work = cache_item(a, a.t.items[blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
-        if (work.good) {                           // its tiles have been staged
-            const int kv = a.t.kv_tiles[work.slot], q = a.t.q_tiles[work.slot];
-            if (kv < 0 || kv + work.tile0 + work.n > a.t.kv_tiles[work.slot + 1] || q < 0 ||
-                a.t.kv_tiles[work.slot + 1] > a.t.n_kv_tiles || a.t.q_tiles[work.slot + 1] > a.t.n_q_tiles ||
-                q + (work.count + work.tpt - 1) / work.tpt > a.t.q_tiles[work.slot + 1])
-                work.good = false;
-        }
+    if (threadIdx.x == 0) work = cache_item<true>(a, a.t.items[blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
+    if (threadIdx.x == 32) {
         gave_up = 0;
         init_bars(base + L::bars, 1, 1, 4);
-    }
-    __syncthreads();
-    if (!work.good) {                              // not this library's table
-        if (threadIdx.x == 0) atomicOr(a.status, 8u);
-        return;
     }
     if (warp == 8) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
+    const bool good = work.good;                   // else not this library's table
+    if (!good && threadIdx.x == 0) atomicOr(a.status, 8u);
     auto bar = [&](int i) { return base + L::bars + 8u * i; };
 
     if (warp >= 8) {
         tc::regs_give<80>();
-        if (warp == 9 && lane == 0 && work.n > 0) {
+        if (warp == 9 && lane == 0 && good && work.n > 0) {
             // ------------------------------ copies -------------------------
             const Staged<D> st(a);
             const int n = work.n, h = work.h, q_tiles = work.alternate ? 1 : 2;
-            const int64_t q_at = static_cast<int64_t>(a.t.q_tiles[work.slot] + work.q0 / work.tpt);
+            const int64_t q_at = static_cast<int64_t>(work.q_at + work.q0 / work.tpt);
             tc::bar_expect(bar(kQFull), q_tiles * (L::kTileBytes + kRows * 4));
             for (int t = 0; t < q_tiles; ++t) {
                 const int64_t at = (q_at + t) * a.Hkv + h;
                 tc::bulk_load(base + L::q + t * L::kTileBytes, st.q + at * L::kTileBytes, L::kTileBytes, bar(kQFull));
                 tc::bulk_load(base + L::row_scale + t * kRows * 4, st.row_scale + at * kRows, kRows * 4, bar(kQFull));
             }
-            int64_t at = static_cast<int64_t>(a.t.kv_tiles[work.slot] + work.tile0) * a.Hkv + h;
+            int64_t at = static_cast<int64_t>(work.kv_at + work.tile0) * a.Hkv + h;
             int keys = 0, values = 0;
             for (int j = 0; j < n; ++j, at += a.Hkv) {
                 const int s = j % kStages, phase = (j / kStages) & 1;
@@ -180,12 +170,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const AttendAr
             for (int j = max(0, keys - kStages); j < keys; ++j) tc::bar_drain(bar(kKFull + j % kStages), (j / kStages) & 1);
             for (int j = max(0, values - kStages); j < values; ++j)
                 tc::bar_drain(bar(kVFull + j % kStages), (j / kStages) & 1);
-        } else if (warp == 8 && work.n > 0) {
+        } else if (warp == 8 && good && work.n > 0) {
             mma_role<D, true, L>(work, base, tmem, gave_up);
         }
     } else {
         tc::regs_take<208>();
-        softmax_role<D, BF16, true, L>(a, work, reinterpret_cast<const TileExps *>(smem + L::exps), smem, base, tmem, warp,
+        if (good)
+            softmax_role<D, BF16, true, L>(a, work, reinterpret_cast<const TileExps *>(smem + L::exps), smem, base, tmem, warp,
                                        lane, gave_up);
     }
     tc::fence_before_sync();
