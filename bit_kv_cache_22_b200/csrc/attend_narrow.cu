@@ -5,8 +5,9 @@
 //   warps 0, 4       softmax of stream 0, 1: alternate key tiles, at most 32 rows (the warps that
 //                    reach the tensor memory of rows 0-31)
 //   warp 1           issues the MMAs
-//   warps 8-15       keys' operands: each warp 32 tokens of every other key tile
-//   warps 16-23      values'
+//   warp 16          nothing
+//   the others       sixteen that unpack, keys or values, each 32 tokens of every other key tile: two on
+//                    the SM quarter of the softmax warps (0, 4, ...), four and five on the others
 //
 // Bound by instruction issue, nearly all of it unpacking (about 1200 instructions a warp for 32 tokens
 // x 128 channels).  One new token for each of 31 slots of 512 to 15872 tokens (32 query / 8 kv heads, d =
@@ -23,7 +24,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 768;
+constexpr int kThreads = 640;
 constexpr int kTurns = 2;                  // key tiles in hand at a time
 constexpr int kUnpackWarps = 2 * kTurns * kUnits;
 
@@ -137,13 +138,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
 
     if (!work.good || work.count > 32 / work.hg) { // not this library's table
         if (threadIdx.x == 0) atomicOr(a.status, 8u);
-    } else if (warp >= 8) {
-        unpack_role<D, N, BF16, L>(a, work, exps, smem, base, warp >= 16, (warp / kUnits) % kTurns, warp % kUnits, lane,
-                                   gave_up);
+    } else if (warp == 0 || warp == 4) {
+        softmax_role<D, BF16, false, L>(a, work, exps, smem, base, tmem, warp, lane, gave_up);
     } else if (warp == 1) {
         if (work.n > 0) mma_role<D, false, L>(work, base, tmem, gave_up);
-    } else if (warp % 4 == 0) {
-        softmax_role<D, BF16, false, L>(a, work, exps, smem, base, tmem, warp, lane, gave_up);
+    } else if (warp != 16) {
+        const int i = warp - 2 - (warp > 4) - (warp > 16);     // 0 .. 15
+        unpack_role<D, N, BF16, L>(a, work, exps, smem, base, i / (kTurns * kUnits), i / kUnits % kTurns, i % kUnits, lane,
+                                   gave_up);
     }
     tc::fence_before_sync();
     __syncthreads();
