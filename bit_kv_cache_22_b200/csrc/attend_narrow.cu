@@ -10,12 +10,15 @@
 //                    the SM quarter of the softmax warps (0, 4, ...), four and five on the others
 //
 // Bound by instruction issue, nearly all of it unpacking (about 1200 instructions a warp for 32 tokens
-// x 128 channels).  One new token for each of 31 slots of 512 to 15872 tokens (32 query / 8 kv heads, d =
-// 128, 2-bit; 0.23 GB): 269 us, 1.9 us a key tile and CTA.  With eight unpacking warps, and registers
-// moved from them to eight softmax warps, of which six had no rows, it took 289 us.  (The decode kernel,
-// whose operands are smaller, takes 157 us, so steps of single newest tokens go there.)  Three slots of
-// 100 to 400 tokens with up to six new ones: 15 us, a launch and the latency of one tile's chain after
-// another.
+// x 128 channels), and by a stream's chain: product, 128 logits of a row by one thread, product, some
+// 5000 cycles for every other key tile.  One new token for each of 31 slots of 512 to 15872 tokens (32
+// query / 8 kv heads, d = 128, 2-bit; 0.23 GB): 261 us, 1.8 us a key tile and CTA.  With eight unpacking
+// warps, and registers moved from them to eight softmax warps, of which six had no rows, it took 289
+// us, with the sixteen spread evenly over the SM's quarters 269 us, with 64 logits read at a time instead
+// of 32 269 us.  (The decode kernel, whose operands are smaller, takes 156 us, so steps of single newest
+// tokens go there.)  Three slots of 100 to 400 tokens with up to six new ones: 15 us, a launch and one
+// CTA's chain: 1 us for the table and tensor memory, 3.5 us until the first keys are unpacked, 2.7 us a
+// tile and stream.
 #include <algorithm>
 #include <cstdint>
 
