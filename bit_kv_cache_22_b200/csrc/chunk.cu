@@ -12,27 +12,27 @@ namespace {
 constexpr int kRowThreads = 128;
 
 // The residual rows (keys rotated) of the new tokens behind their slots' last whole blocks, R floor(end /
-// R); those before were quantized by the launch before.  BLOCKS: that launch was made, and turned the
-// queries: CTA (b, i) has the i-th such token of slot b.  Otherwise one CTA per new token, which also
-// turns its queries.  A slot's first CTA sets the slot's length, which no CTA reads.
+// R); those before were quantized by the launch before.  SLOTS: CTA (b, i) has the i-th such token of slot b.
+// Otherwise one CTA per new token, which also turns its queries unless the launch before did.  A
+// slot's first CTA sets the slot's length, which no CTA reads.
 // Bound by memory: each row is read and written once, 16 bytes a thread; queries of 32768 tokens and 32
 // heads alone, 0.54 GB, in 109 us.  Behind quantized blocks little is left: 3 to 6 us.
-template <bool BF16, bool BLOCKS>
+template <bool BF16, bool SLOTS>
 __global__ void __launch_bounds__(kRowThreads) chunk_rows_kernel(const PagedView c, const ChunkTable t, const Rows k,
                                                                  const Rows v, const RopeArgs rope, const Rows q,
                                                                  const Rows q_out) {
-    const int b = BLOCKS ? static_cast<int>(blockIdx.y) : slot_of(t.offsets, t.B, blockIdx.x);
+    const int b = SLOTS ? static_cast<int>(blockIdx.y) : slot_of(t.offsets, t.B, blockIdx.x);
     const int64_t first = t.offsets[b], start = t.starts[b], end = start + t.offsets[b + 1] - first;
-    if (BLOCKS && end == start) return;
+    if (SLOTS && end == start) return;
     const int64_t kept = max(start, end / c.R * c.R);          // the first that stays in the residual
-    const int64_t row = BLOCKS ? first + kept - start + blockIdx.x : blockIdx.x, tok = start + row - first;
+    const int64_t row = SLOTS ? first + kept - start + blockIdx.x : blockIdx.x, tok = start + row - first;
     if (start < 0 || end < start || first < 0 || first + end - start > t.tokens || row < first ||
-        (!BLOCKS && tok >= end)) {                 // not this library's table
+        (!SLOTS && tok >= end)) {                 // not this library's table
         if (threadIdx.x == 0) atomicOr(c.status, 8u);
         return;
     }
-    if (threadIdx.x == 0 && (BLOCKS ? blockIdx.x == 0 : row == first)) c.seq_len[b] = static_cast<int32_t>(end);
-    if (BLOCKS && tok >= end) return;
+    if (threadIdx.x == 0 && (SLOTS ? blockIdx.x == 0 : row == first)) c.seq_len[b] = static_cast<int32_t>(end);
+    if (SLOTS && tok >= end) return;
     const RowUnits ru = row_units(c.d, rope), plain = {0, c.d / 8};
     const int n_k = tok >= kept ? c.Hkv * ru.n : 0, n_v = n_k ? c.Hkv * plain.n : 0;
     const int n_q = q.p ? c.Hq * ru.n : 0;
@@ -228,15 +228,17 @@ void read_launch(const PagedView &c, const ChunkTable &t, const Rows &k, const R
 cudaError_t launch_chunk_rows(const PagedView &c, const ChunkTable &t, const Rows &k, const Rows &v,
                               const RopeArgs &rope, const Rows &q, const Rows &q_out, cudaStream_t s) {
     if (t.tokens == 0) return cudaSuccess;
-    if (t.n_blocks > 0) {
+    const Rows none{};
+    const bool turned = t.n_blocks > 0;            // the quantizer's launch did
+    // long chunks leave little behind their blocks: the smaller grid
+    if (turned && t.tokens > static_cast<int64_t>(c.R) * t.B) {
         const dim3 grid(static_cast<unsigned>(c.R), static_cast<unsigned>(t.B));
-        const Rows none{};
         if (c.bf16) chunk_rows_kernel<true, true><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, none, none);
         else chunk_rows_kernel<false, true><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, none, none);
     } else {
         const unsigned grid = static_cast<unsigned>(t.tokens);
-        if (c.bf16) chunk_rows_kernel<true, false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
-        else chunk_rows_kernel<false, false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, q, q_out);
+        if (c.bf16) chunk_rows_kernel<true, false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, turned ? none : q, q_out);
+        else chunk_rows_kernel<false, false><<<grid, kRowThreads, 0, s>>>(c, t, k, v, rope, turned ? none : q, q_out);
     }
     count_launches(1);
     return cudaGetLastError();

@@ -539,7 +539,7 @@ KVQ_API kvq_status kvq_prompt_attention(const kvq_chunk *plan, int32_t dtype, co
  * they start with) and the rest kept in the residual: the state that appending one by one
  * leaves.  The caller has filled the page-table entries of the new blocks.
  * q (or NULL): queries e [tokens][q_heads][d] of the same tokens, rotated into q_out (may be the
- * same rows as q; needs rope).  KVQ_ERR_CAPACITY when a block would pass capacity,
+ * same rows as q, and overlaps neither k nor v; needs rope).  KVQ_ERR_CAPACITY when a block would pass capacity,
  * KVQ_ERR_INVALID_ARG when a position has no angles.  One launch, two when a block fills.
  */
 KVQ_API kvq_status kvq_paged_append_chunk(kvq_paged *cache, const kvq_chunk *plan, const kvq_rows *k,

@@ -56,6 +56,21 @@ def test_append_chunk_rotates_keys_and_queries(name, rot, pairs):
         p.check_read(plan)
 
 
+@pytest.mark.parametrize("name", ["small", "g16", "gqa2"])
+def test_long_chunks_with_queries(name):
+    """More tokens than all slots' residual rows: blocks, rests and queries of every slot."""
+    p = make(name)
+    R, B = p.g.residual, p.g.batch
+    rope = ct.angles(1024, 32)
+    p.append([3, 0, R - 1, 1, 2][:B], rope=rope)
+    for counts in ([2 * R + 1, R + 5, 3 * R, 2 * R, 0][:B], [R, 3 * R, 1, 2 * R + 3, R][:B]):
+        assert sum(counts) > R * B
+        plan, got, want = p.append(counts, rope=rope, queries=True, strided=True)
+        assert torch.equal(got.cpu().view(torch.int16), want.view(torch.int16))
+        p.check_state(str(counts))
+        p.check_read(plan)
+
+
 def test_queries_rotate_in_place_and_into_a_strided_output():
     p = make("gqa2")
     rope = kvq.Rope(*(x.cuda() for x in ct.angles(512, 128)))
