@@ -4,8 +4,9 @@
 //
 //   warps 0, 4       softmax of stream 0, 1: alternate key tiles, at most 32 rows (the warps that
 //                    reach the tensor memory of rows 0-31)
-//   warp 1           issues the MMAs
-//   warp 16          nothing
+//   warps 1, 16      the queries' operands (rows 32 to 127 of the tile stay as they lie: a row of the tile
+//                    reaches its own row of the logits and the sums, and those are not read)
+//   warp 1           then issues the MMAs
 //   the others       sixteen that unpack, keys or values, each 32 tokens of every other key tile: two on
 //                    the SM quarter of the softmax warps (0, 4, ...), four and five on the others
 //
@@ -30,6 +31,8 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kTurns = 2;                  // key tiles in hand at a time
 constexpr int kUnpackWarps = 2 * kTurns * kUnits;
+constexpr int kMostRows = 32;              // of a slot here
+constexpr int kQueryWarps = 2;
 
 template <int D>
 struct NarrowSmem {
@@ -51,7 +54,7 @@ __device__ __forceinline__ void emit_queries_of(const AttendArgs &a, const Cache
     const uint16_t *src = a.q.p + static_cast<int64_t>(work.first + work.q0) * a.q.ts +
                           static_cast<int64_t>(work.h) * hg * a.q.hs;
     emit_queries<D, BF16>(
-        kRows, w, kUnpackWarps, lane,
+        kMostRows, w, kQueryWarps, lane,
         [&](int r) -> const uint16_t * {
             return r < rows ? src + static_cast<int64_t>(r / hg) * a.q.ts + static_cast<int64_t>(r % hg) * a.q.hs : nullptr;
         },
@@ -88,7 +91,6 @@ __device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem
     fetch_unit<D, N>(f, c, src, page_at(tok), at_tok, tok, turn < n, lane);
     advance();
     int page = page_at(tok + kTurns * kRows);
-    emit_queries_of<D, BF16, L>(a, work, smem, base, kUnits * (kTurns * kv + turn) + u, lane);
     for (int j = turn; j < n; j += kTurns, tok += kTurns * kRows) {
         const int s = j % kStages, kind0 = f.kind[0], kind1 = f.kind[1];
         int ex;
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     if (threadIdx.x == 0) work = cache_item<false>(a, a.t.items[a.t.n_wide + blockIdx.x / a.Hkv], blockIdx.x % a.Hkv);
     if (threadIdx.x == 64) {
         gave_up = 0;
-        init_bars(base + L::bars, kUnpackWarps, kUnits, 1);
+        init_bars(base + L::bars, kQueryWarps, kUnits, 1);
     }
     if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
     tc::fence_before_sync();
@@ -139,13 +141,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
-    if (!work.good || work.count > 32 / work.hg) { // not this library's table
+    if (!work.good || work.count > kMostRows / work.hg) { // not this library's table
         if (threadIdx.x == 0) atomicOr(a.status, 8u);
     } else if (warp == 0 || warp == 4) {
         softmax_role<D, BF16, false, L>(a, work, exps, smem, base, tmem, warp, lane, gave_up);
     } else if (warp == 1) {
+        emit_queries_of<D, BF16, L>(a, work, smem, base, 0, lane);
         if (work.n > 0) mma_role<D, false, L>(work, base, tmem, gave_up);
-    } else if (warp != 16) {
+    } else if (warp == 16) {
+        emit_queries_of<D, BF16, L>(a, work, smem, base, 1, lane);
+    } else {
         const int i = warp - 2 - (warp > 4) - (warp > 16);     // 0 .. 15
         unpack_role<D, N, BF16, L>(a, work, exps, smem, base, i / (kTurns * kUnits), i / kUnits % kTurns, i % kUnits, lane,
                                    gave_up);
