@@ -1438,9 +1438,39 @@ bool is_decode_step(const kvq_paged *h, const kvq_chunk *p) {
     return c.batch == p->batch;
 }
 
-// Scratch of a decode step: queries and outputs [B][Hq][d], then the splits' partial results.
+// Scratch of a decode step: queries and outputs [B][Hq][d], then the splits' partial results.  The splits
+// follow from the cache, whose groups and capacity may be others than those the plan was made for: the
+// call takes the decode kernel only where its workspace holds this, else the narrow attention kernel,
+// whose scratch follows from the plan alone.
 size_t decode_step_bytes(int64_t batch, int64_t q_heads, int64_t d, int64_t splits) {
     return static_cast<size_t>(batch * q_heads * (d * 2 + d * 4 + splits * (d + 2) * 4));
+}
+
+// The chunk attention of a decode step: d has its splits, workspace decode_step_bytes of room.
+kvq_status attend_decode_step(const kvq_paged *h, const kvq_chunk *plan, kvq::DecodeArgs d, const kvq_rows *q,
+                              const kvq_rows *o, void *workspace, cudaStream_t s) {
+    const kvq_config &c = h->base.cfg;
+    const int64_t units = static_cast<int64_t>(c.batch) * c.q_heads;
+    float *out = static_cast<float *>(workspace);
+    d.out = out;
+    uint16_t *dense = reinterpret_cast<uint16_t *>(out + units * c.head_dim);
+    d.q = dense;
+    d.o_part = reinterpret_cast<float *>(dense + units * c.head_dim);
+    d.m_part = d.o_part + units * d.S * c.head_dim;
+    d.l_part = d.m_part + units * d.S;
+    const kvq::ChunkTable t = chunk_table(plan);
+    cudaError_t e = cudaSuccess;
+    // packed rows that lie slot by slot already
+    if (plan->tokens == c.batch && (c.q_heads < 2 || q->head_stride == c.head_dim) &&
+        (c.batch < 2 || q->token_stride == static_cast<int64_t>(c.q_heads) * c.head_dim))
+        d.q = static_cast<const uint16_t *>(q->data);
+    else
+        e = kvq::launch_rows_to_slots(t, rows_of(q), dense, c.q_heads, c.head_dim, s);
+    if (e == cudaSuccess) e = kvq::launch_decode(d, s);
+    if (e == cudaSuccess)
+        e = kvq::launch_slots_to_rows(t, out, rows_of(o), c.q_heads, c.head_dim, c.dtype == KVQ_BF16, s);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+    return ok();
 }
 
 kvq::AttendArgs attend_args(const kvq_chunk *p, const kvq_rows *q, const kvq_rows *o, bool bf16) {
@@ -1597,32 +1627,12 @@ kvq_status kvq_paged_chunk_attention(kvq_paged *h, const kvq_chunk *plan, const 
     if (st != KVQ_OK) return st;
     if (plan->workspace > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < plan->workspace))
         return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold %zu bytes", plan->workspace);
-    if (is_decode_step(h, plan)) {
+    if (is_decode_step(h, plan) && workspace && aligned16(workspace)) {
         const kvq_config &c = h->base.cfg;
-        const int64_t units = static_cast<int64_t>(c.batch) * c.q_heads;
         kvq::DecodeArgs d = paged_decode_args(h);
         paged_plan(h, &d.n_qsplits, &d.tiles_per_split, &d.S);
-        float *out = static_cast<float *>(workspace);
-        d.out = out;
-        uint16_t *dense = reinterpret_cast<uint16_t *>(out + units * c.head_dim);
-        d.q = dense;
-        d.o_part = reinterpret_cast<float *>(dense + units * c.head_dim);
-        d.m_part = d.o_part + units * d.S * c.head_dim;
-        d.l_part = d.m_part + units * d.S;
-        const kvq::ChunkTable t = chunk_table(plan);
-        cudaStream_t s = static_cast<cudaStream_t>(stream);
-        cudaError_t e = cudaSuccess;
-        // packed rows that lie slot by slot already
-        if (plan->tokens == c.batch && (c.q_heads < 2 || q->head_stride == c.head_dim) &&
-            (c.batch < 2 || q->token_stride == static_cast<int64_t>(c.q_heads) * c.head_dim))
-            d.q = static_cast<const uint16_t *>(q->data);
-        else
-            e = kvq::launch_rows_to_slots(t, rows_of(q), dense, c.q_heads, c.head_dim, s);
-        if (e == cudaSuccess) e = kvq::launch_decode(d, s);
-        if (e == cudaSuccess)
-            e = kvq::launch_slots_to_rows(t, out, rows_of(o), c.q_heads, c.head_dim, c.dtype == KVQ_BF16, s);
-        if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
-        return ok();
+        if (workspace_bytes >= decode_step_bytes(c.batch, c.q_heads, c.head_dim, d.S))
+            return attend_decode_step(h, plan, d, q, o, workspace, static_cast<cudaStream_t>(stream));
     }
     kvq::AttendArgs a = attend_args(plan, q, o, h->base.cfg.dtype == KVQ_BF16);
     a.cache = paged_view(h);

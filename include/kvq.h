@@ -509,7 +509,7 @@ typedef struct {
  * or only the sizes when `table` is NULL.  Host only, no device needed.  KVQ_ERR_INVALID_ARG
  * for a negative count or start, too little room, or sums past 2^31 - 1; KVQ_ERR_UNSUPPORTED
  * for more than 128 query heads per kv head.  The attention over the cache is cut into pieces for a
- * GPU of num_sms SMs.  A prompt plan needs no cache: head_dim 64 or 128,
+ * GPU of num_sms SMs.  A plan serves every paged cache of the same batch, heads, head_dim and residual.  A prompt plan needs no cache: head_dim 64 or 128,
  * q_heads a multiple of kv_heads.
  */
 KVQ_API kvq_status kvq_plan_chunk(const kvq_paged_config *cfg, const int32_t *counts, const int32_t *starts,
@@ -569,8 +569,9 @@ KVQ_API kvq_status kvq_paged_read_chunk(kvq_paged *cache, const kvq_chunk *plan,
  * new tokens x query heads -- takes 4 head_dim bytes per token and kv head of what it holds, as its
  * keys and values are unpacked once for all its rows); calls that may overlap on the GPU need
  * workspaces of their own.  When every slot that holds tokens brings its newest one alone (a decode
- * step), the call runs the decode kernel, which counts splits in the cache's state: attention calls
- * on one cache run one after another, as decode calls do.
+ * step) and the workspace has room for the decode kernel's splits, as that of a plan made for this
+ * cache's groups and capacity has, the call runs the decode kernel, which counts splits in the
+ * cache's state: attention calls on one cache run one after another, as decode calls do.
  */
 KVQ_API kvq_status kvq_paged_chunk_attention(kvq_paged *cache, const kvq_chunk *plan, const kvq_rows *q,
                                              const kvq_rows *o, void *workspace, size_t workspace_bytes,
