@@ -109,9 +109,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
 
     const uint32_t bars = base + L::bars;
     auto bar = [&](int i) { return bars + 8u * i; };
-    // kPFull: [half of the tile's tokens][stream]
+    // kPFull: [half of the tile's tokens][stream].  kVFixed: [stage], so that kVEmpty of the stage, committed
+    // behind the wait for it, comes between two of its arrivals (short jobs may follow one another while the
+    // MMA warp waits for a query tile).
     enum { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 10, kSFull = 12, kPFull = 14,
-           kOFull = 18, kVFixed = 20, kDrain = 21, kBars = 22 };
+           kOFull = 18, kVFixed = 20, kDrain = 22, kBars = 23 };
     if (threadIdx.x == 0) {
         gave_up = 0;
         for (int i = 0; i < kBars; ++i) tc::bar_init(bar(i), i >= kPFull && i < kPFull + 4 ? 4 : 1);
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                             *reinterpret_cast<uint4 *>(v + p * kRows * 128 + left * 128 + 16 * k) = make_uint4(0, 0, 0, 0);
                     tc::fence_async_proxy();
                     __syncwarp();
-                    if (lane == 0) tc::bar_arrive(bar(kVFixed));
+                    if (lane == 0) tc::bar_arrive(bar(kVFixed + s));
                 }
             }
             for (int t = 0; t < 2; ++t)            // copies in flight land before the CTA leaves
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                 if (last) tc::mma_commit(bar(kQEmpty + t), leader);
             };
             bool go = true;
-            int at = 0, queries[2] = {0, 0}, weights[2] = {0, 0}, fixed = 0;   // key tiles, and the rest, before this job
+            int at = 0, queries[2] = {0, 0}, weights[2] = {0, 0}, fixed = 0;   // key tiles, and the rest, before this job; kVFixed's phases
             Job next = prompt_job(a, 0);
             for (int i = 0; i < rounds && go; ++i) {
                 const Job w = next;
@@ -225,8 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                 for (int j = 0; j < n && go; ++j, ++at) {
                     const int s = at % kStages, s1 = (at + 1) % kStages;
                     go = tc::bar_wait_warp(bar(kVFull + s), (at / kStages) & 1, &gave_up);
-                    if (go && j == n - 1 && w.count - j * kRows < kRows)
-                        go = tc::bar_wait_warp(bar(kVFixed), fixed++ & 1, &gave_up);
+                    if (go && j == n - 1 && w.count - j * kRows < kRows) {
+                        go = tc::bar_wait_warp(bar(kVFixed + s), (fixed >> s) & 1, &gave_up);
+                        fixed ^= 1 << s;
+                    }
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!go || j >= w.tiles[t]) continue;

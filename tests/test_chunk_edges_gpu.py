@@ -1,5 +1,7 @@
 """The chunk operators on the GPU at the edges of what their documents allow: plans shared by caches of
-different groups and capacities, against the plain 64-bit forms (chunk_testlib)."""
+different groups and capacities, many short prompts, against the plain 64-bit forms (chunk_testlib)."""
+import random
+
 import pytest
 import torch
 
@@ -15,6 +17,16 @@ FP16, BF16 = torch.float16, torch.bfloat16
 
 def pair(slots=4, hq=8, hkv=2, d=128, G=32, Gv=32, R=128, bits=2, sym=False, dtype=BF16, capacity=1024, page=128, seed=0):
     return ct.Pair(slots, hq, hkv, d, G, Gv, R, bits, sym, dtype, capacity, page, seed)
+
+
+def check_prompt(got, q, k, v, lens, what=""):
+    at = 0
+    for n in lens:
+        if n:
+            rows = slice(at, at + n)
+            plain = ct.attend(ct.wide(q[rows]), ct.wide(k[rows]).transpose(1, 0, 2), ct.wide(v[rows]).transpose(1, 0, 2), 0)
+            ct.check_attention(got[rows], *plain, n, q.dtype, False, f"{what} rows {rows}")
+        at += n
 
 
 # ------------------------------------------------------------------ one plan, several caches
@@ -66,3 +78,22 @@ def test_a_decode_step_planned_for_a_smaller_capacity():
         assert (guard == 77).all()
         assert lib.kvq_paged_chunk_attention(p.cache._h, use.ref, *rows, work.data_ptr() + 8, room, stream) == \
             kvq.KVQ_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ many short prompts
+
+@pytest.mark.parametrize("hq,hkv,d,lo,hi", [(8, 2, 128, 33, 64), (8, 2, 64, 1, 127), (4, 4, 128, 1, 127), (6, 2, 128, 120, 260)])
+def test_several_hundred_short_prompts(hq, hkv, d, lo, hi):
+    """Many jobs a CTA, nearly each ending in a key tile that its prompt fills in part, of one query
+    tile and of two."""
+    rng = random.Random(hq + hi)
+    lens = [rng.randint(lo, hi) for _ in range(500)]
+    gen = torch.Generator().manual_seed(hi)
+    q, k, v = (torch.randn(sum(lens), h, d, generator=gen).to(BF16) for h in (hq, hkv, hkv))
+    plan = kvq.plan_prompt(lens, hq, hkv, d)
+    assert plan.chunk.items * hkv > 3 * 148
+    dev = [x.cuda() for x in (q, k, v)]
+    got = [kvq.prompt_attention(plan, *dev) for _ in range(5)]
+    plan.check_device()
+    check_prompt(got[0], q, k, v, lens)
+    assert all(torch.equal(got[0], x) for x in got[1:])
