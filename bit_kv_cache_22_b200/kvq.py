@@ -442,6 +442,22 @@ def _on(device: torch.device, stream, call):
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
+class _Lent:
+    """Tensors of this object's own that calls on any stream read: their memory is not reused before the
+    work queued there is done, also when the object is dropped right after a call."""
+
+    def _lend(self, device: torch.device, *tensors: torch.Tensor):
+        self._tensors = tensors
+        self._streams = {_raw_stream(device.index)}        # they were made on its current one
+
+    def used_on(self, raw: int):
+        """A call was queued on the stream `raw`, torch's current one of its device."""
+        if raw not in self._streams:
+            for t in self._tensors:
+                t.record_stream(torch.cuda.current_stream(t.device))
+            self._streams.add(raw)
+
+
 def _servable(at: int, a: int, b: int, c: int, tokens: int, heads: int) -> bool:
     """Rows the kernels take as they are: channels contiguous, rows on 16 bytes, strides positive."""
     return c == 1 and not at & 15 and (tokens < 2 or (a > 0 and not a & 7)) and (heads < 2 or (b > 0 and not b & 7))
@@ -482,7 +498,7 @@ def _output(out: torch.Tensor | None, like: torch.Tensor):
     return Rows(at, a, b), out
 
 
-class Rope:
+class Rope(_Lent):
     """Rotary angles cos, sin (float32 [positions, rot_dim / 2], CUDA): row p turns token p."""
 
     def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
@@ -490,12 +506,13 @@ class Rope:
                 not cos.is_cuda or cos.device != sin.device:
             raise ValueError("cos and sin must be float32 CUDA tensors [positions, rot_dim / 2]")
         self.cos, self.sin = cos.contiguous(), sin.contiguous()
+        self._lend(cos.device, self.cos, self.sin)
         self.args = RopeArgs(self.cos.data_ptr(), self.sin.data_ptr(), cos.shape[0], 2 * cos.shape[1],
                              int(bool(interleaved)))
         self.ref = ctypes.byref(self.args)
 
 
-class ChunkPlan:
+class ChunkPlan(_Lent):
     """counts[b] new tokens of each slot from position starts[b] on, planned once on the host and
     used for the chunk calls of every layer (kvq_chunk).  `tokens` packed rows in all; slot b's are
     rows offsets[b] .. offsets[b + 1] - 1.  Made by PagedKVQCache.plan_chunk and plan_prompt; a graph
@@ -534,15 +551,11 @@ class ChunkPlan:
         self.offsets = host[:batch + 1].tolist()
         dev_table = host.to(self.device)
         self.table = dev_table[:words]
+        self._lend(self.device, dev_table)
         self.chunk.table = self.table.data_ptr()
         # a cache has a status word of its own, prompts have the plan's
         self.status = dev_table[words:] if cfg is None else None
         self.status_at = self.status.data_ptr() if cfg is None else None
-
-    def used_on(self, stream):
-        """The table's memory outlives what is queued on `stream` (None: the stream it was made on)."""
-        if stream is not None:
-            self.table.record_stream(stream)
 
     def check_device(self):
         """Raise KVQError if a kernel run with this prompt plan raised a bit of its status word since the
@@ -576,7 +589,7 @@ def prompt_attention(plan: ChunkPlan, q: torch.Tensor, k: torch.Tensor, v: torch
         v_rows, dv = _packed(v, "v", n, c.kv_heads, d, dtype, device)
         o_rows, o = _output(out, dq)
         _check(load().kvq_prompt_attention(plan.ref, code, q_rows, k_rows, v_rows, o_rows, plan.status_at, raw))
-        plan.used_on(stream)
+        plan.used_on(raw)
         return o
 
     return _on(device, stream, call)
@@ -783,7 +796,9 @@ class PagedKVQCache:
                 self._h, plan.ref, k_rows, v_rows, None if rope is None else rope.ref, q_rows, o_rows, raw))
             for b, end in plan.ends:
                 self.lens[b] = end
-            plan.used_on(stream)
+            plan.used_on(raw)
+            if rope is not None:
+                rope.used_on(raw)
             return q_out
 
         return _on(device, stream, call)
@@ -819,7 +834,7 @@ class PagedKVQCache:
             head, token = g.head_dim, g.kv_heads * g.head_dim
             _check(self._lib.kvq_paged_read_chunk(self._h, plan.ref, Rows(k.data_ptr(), token, head),
                                                   Rows(v.data_ptr(), token, head), raw))
-            plan.used_on(stream)
+            plan.used_on(raw)
             return k, v
 
         return _on(self.device, stream, call)
@@ -838,7 +853,7 @@ class PagedKVQCache:
             work = torch.empty(room, dtype=torch.uint8, device=self.device) if room else None
             _check(self._lib.kvq_paged_chunk_attention(self._h, plan.ref, q_rows, o_rows,
                                                        work.data_ptr() if room else None, room, raw))
-            plan.used_on(stream)
+            plan.used_on(raw)
             return o
 
         return _on(self.device, stream, call)

@@ -1,5 +1,6 @@
 """The chunk operators on the GPU at the edges of what their documents allow: plans shared by caches of
-different groups and capacities, many short prompts, against the plain 64-bit forms (chunk_testlib)."""
+different groups and capacities, many short prompts, plans and
+angles dropped while another stream still reads them, against the plain 64-bit forms (chunk_testlib)."""
 import random
 
 import pytest
@@ -97,3 +98,68 @@ def test_several_hundred_short_prompts(hq, hkv, d, lo, hi):
     plan.check_device()
     check_prompt(got[0], q, k, v, lens)
     assert all(torch.equal(got[0], x) for x in got[1:])
+
+
+# ------------------------------------------------------------------ memory that another stream still reads
+
+def busy(ms=200):
+    """Work on the current stream for about `ms`."""
+    x = torch.zeros(1 << 28, dtype=torch.float32, device="cuda")           # 1 GiB: over 0.3 ms a pass
+    for _ in range(3 * ms):
+        x.add_(1.0)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_plan_dropped_after_a_call_on_another_stream(given):
+    """The plan is made on one stream and used on another, torch's current one or the call's own; its
+    memory, and that of the angles' copies, is not handed out while calls wait there."""
+    p, first = pair(), pair(seed=1)
+    for x in (p, first):
+        x.append([300, 10, 200, 1])
+        x.cache.reserve(2, 260)
+    cos, sin = (x.cuda() for x in ct.angles(512, 128))
+    k, v, q = p.new(64, 2), p.new(64, 2), p.new(64, 8)
+    dk, dv, dq = k.cuda(), v.cuda(), q.cuda()
+    side = torch.cuda.Stream()
+
+    def copies():                                   # not contiguous: Rope copies them
+        return kvq.Rope(torch.stack([cos, cos], 2)[..., 0], torch.stack([sin, sin], 2)[..., 0])
+
+    def plans(cache):
+        return cache.plan_chunk([1, 2, 60, 1]), copies(), kvq.plan_prompt([40, 24], 8, 2, 128)
+
+    def calls(cache, plan, rope, prompts, **on):
+        turned = cache.append_chunk(plan, dk, dv, rope, dq, **on)
+        return (turned, cache.chunk_attention(plan, turned, **on), cache.read_chunk(plan, **on)[0],
+                kvq.prompt_attention(prompts, dq, dk, dv, **on))
+
+    calls(first.cache, *plans(first.cache))         # (a kernel's first call may wait for the device)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy()
+    plan, rope, prompts = plans(p.cache)
+    torch.cuda.default_stream().synchronize()
+    if given:
+        got = calls(p.cache, plan, rope, prompts, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            got = calls(p.cache, plan, rope, prompts)
+    lent = {t.data_ptr() for x in (plan, rope, prompts) for t in x._tensors}
+    starts, offsets = plan.starts, plan.offsets
+    positions = [s + i for s, n in zip(plan.starts, plan.counts) for i in range(n)]
+    del plan, rope, prompts
+    later = [x for _ in range(20) for x in (p.cache.plan_chunk([2, 1, 1, 60]), copies(),
+                                            kvq.plan_prompt([24, 40], 8, 2, 128))]
+    assert not side.query(), "the calls ended before the memory could be asked for again"
+    assert not lent & {t.data_ptr() for x in later for t in x._tensors}
+    side.synchronize()
+    k, turned = (ct.rotate(x, positions, *ct.angles(512, 128), False) for x in (k, q))
+    assert torch.equal(got[0].cpu(), turned)
+    for b in range(4):
+        rows = slice(offsets[b], offsets[b + 1])
+        p.plain[b].append(starts[b], k[rows], v[rows])
+    p.check_state()
+    plan = p.cache.plan_chunk([1, 2, 60, 1], starts)
+    p.check_attention(plan, turned, got=got[1])
+    assert torch.equal(got[2], p.cache.read_chunk(plan)[0])
+    check_prompt(got[3], q, dk.cpu(), v, [40, 24])
