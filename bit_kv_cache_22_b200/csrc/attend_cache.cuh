@@ -706,10 +706,14 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             for (int g = 0; g < kUnits; ++g) top = max(top, evs[g]);
 #pragma unroll
             for (int g = 0; g < kUnits; ++g) even = even && evs[g] == top;
+            const bool far = fabsf(mx) > kFarLogit && mx > kNoMax;
+            bool careful = false;
             if (i == 0) {
                 m = mx;
                 e_ref = top;
-            } else if (top != e_ref || __any_sync(0xffffffffu, mx > m + kLazyMax)) {
+                careful = __any_sync(0xffffffffu, far);
+            } else if (top != e_ref || __any_sync(0xffffffffu, mx - m > kLazyMax || far)) {
+                careful = __any_sync(0xffffffffu, far);
                 // O holds every tile of the stream before j: S_j was committed after its last MMA
                 const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
                 const float alpha_o = alpha * tc::ex2(static_cast<float>(e_ref - top));
@@ -728,16 +732,20 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             }
             float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             // the weights of 32 columns, packed, take the place of their first logits
-            auto weights = [&](int k, const uint32_t(&x)[32], uint32_t *p) {
+            auto weights = [&](int k, uint32_t(&x)[32], uint32_t *p) {
+                if (careful)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) subtract_rounded<16>(&x[16 * g], row_s * scales[unit(k, g)], m);
+                const float from = careful ? 0.0f : m;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float sc = row_s * scales[unit(k, g)];
+                    const float sc = careful ? 1.0f : row_s * scales[unit(k, g)];
                     const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[unit(k, g)] - top));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t *y = &x[16 * g + 2 * e];
                         const float2 z = tc::fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
-                                                  make_float2(sc, sc), make_float2(-m, -m));
+                                                  make_float2(sc, sc), make_float2(-from, -from));
                         float2 wt = make_float2(tc::ex2(z.x), tc::ex2(z.y));
                         l2[e % 2] = tc::add2(l2[e % 2], wt);
                         if (!even) wt = tc::mul2(wt, make_float2(down, down));

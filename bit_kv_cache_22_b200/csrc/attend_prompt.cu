@@ -52,6 +52,7 @@ struct PromptSmem {
 // A value above which the running maximum is raised: weights stay below 2^8, which e holds as
 // exactly as weights below 1, and the sums are rescaled rarely.
 constexpr float kLazyMax = 8.0f;
+constexpr float kNoMax = -1e30f;           // below it: no logits
 
 // A CTA's piece of work: up to 2 * tpt tokens of one slot's prompt from token q0 on, for kv head h.
 struct Job {
@@ -306,9 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                     for (int e = 1; e < 32; ++e) mxs[c] = fmaxf(mxs[c], __uint_as_float(s[c][e]));
                 }
                 const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * scale;
+                const bool far = fabsf(mx) > kFarLogit && mx > kNoMax;
+                bool careful = false;
                 if (j == 0) {
                     m = mx;
-                } else if (__any_sync(0xffffffffu, mx > m + kLazyMax)) {
+                    careful = __any_sync(0xffffffffu, far);
+                } else if (__any_sync(0xffffffffu, mx - m > kLazyMax || far)) {
+                    careful = __any_sync(0xffffffffu, far);
                     // O holds every tile before j: S_j was committed after its last MMA
                     const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
                     m = mn;
@@ -323,6 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                         tc::tmem_store(to + 32 * c, o);
                     }
                 }
+                if (careful)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) subtract_rounded<32>(s[c], scale, m);
+                const float sc = careful ? 1.0f : scale, from = careful ? 0.0f : m;
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                     for (int e = 0; e < 32; ++e) {
                         const uint32_t *src = &s[2 * half + e / 16][2 * (e % 16)];
                         const float2 y = tc::fma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])),
-                                                  make_float2(scale, scale), make_float2(-m, -m));
+                                                  make_float2(sc, sc), make_float2(-from, -from));
                         const float2 wt = make_float2(tc::ex2(y.x), tc::ex2(y.y));
                         l2[e % 2] = tc::add2(l2[e % 2], wt);
                         p[e] = narrow2<BF16>(wt.x, wt.y);

@@ -261,4 +261,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 }
 
 }  // namespace tc
+
+// A softmax takes y - m, y = sc x, in one operation, which does not round y.  Where |y| passes 2^20 (its
+// steps are 1/16 and more) that is no longer small at the maximum itself: m is a rounded y.  Such
+// logits are rounded first, as m was, so that the largest weight is 1 and no weight overflows.
+constexpr float kFarLogit = 1048576.0f;
+template <int N>
+__device__ __forceinline__ void subtract_rounded(uint32_t *x, float sc, float m) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(x[e]), sc), -m));
+}
+
 }  // namespace kvq

@@ -163,3 +163,70 @@ def test_a_plan_dropped_after_a_call_on_another_stream(given):
     p.check_attention(plan, turned, got=got[1])
     assert torch.equal(got[2], p.cache.read_chunk(plan)[0])
     check_prompt(got[3], q, dk.cpu(), v, [40, 24])
+
+
+# ------------------------------------------------------------------ large logits
+
+def one_hot_rows(q, k, first, margin):
+    """(rows and heads whose largest logit leads by more than `margin`, which token that is): [n, Hq]."""
+    n, hq, d = q.shape
+    y = torch.einsum("nhd,hld->nhl", torch.from_numpy(q), torch.from_numpy(k).repeat_interleave(hq // k.shape[0], 0)) / d ** 0.5
+    y[(torch.arange(k.shape[1])[None] > first + torch.arange(n)[:, None])[:, None].expand_as(y)] = -float("inf")
+    top = torch.nn.functional.pad(y, (0, 1), value=-float("inf")).topk(2, -1)
+    return top.values[..., 0] - top.values[..., 1] > margin, top.indices[..., 0]
+
+
+def check_one_hot(got, q, k, v, first, dtype, what):
+    """Logits of 2^30: their fp32 sums are off by many powers of two, so a row whose largest logit leads by
+    more than that is one token's value, rounded once on the way (the cache's values to 11 bits) and
+    once at the end, and the others lie among their tokens' values."""
+    S = (abs(q).max(-1).max() * abs(k).max()) * q.shape[2] / q.shape[2] ** 0.5
+    clear, token = one_hot_rows(q, k, first, 4 * (q.shape[2] + 8) * 2.0 ** -24 * S + 4 * 2.0 ** -11 * S)
+    hg = q.shape[1] // k.shape[0]
+    out = torch.from_numpy(ct.wide(got))
+    assert torch.isfinite(out).all(), f"{what}: not finite"
+    u = ct.half_step(dtype)
+    vt = torch.from_numpy(v)
+    assert (out.abs() <= vt.abs().max() * (1 + u) * (1 + 2.0 ** -10)).all(), what
+    want = torch.stack([vt[h // hg][token[:, h]] for h in range(q.shape[1])], 1)
+    off = (out - want).abs() <= want.abs() * (u + 2.0 ** -10) + 2.0 ** -24 * vt.abs().max()
+    assert off[clear].all(), what
+    return int(clear.sum())
+
+
+@pytest.mark.parametrize("dtype,size", [(BF16, 2.0 ** 16), (FP16, 2.0 ** 13), (BF16, 2.0 ** 20)])
+@pytest.mark.parametrize("counts", [[2, 1, 3, 0], [40, 130, 60, 0]])
+def test_large_logits_over_the_cache(dtype, size, counts):
+    p = pair(dtype=dtype, bits=4, capacity=4096)
+    held = [3000, 10, 300, 50]
+    for c in (held, counts):
+        plan = p.cache.plan_chunk(c)
+        k, v = p.new(plan.tokens, 2, size), p.new(plan.tokens, 2)
+        p.cache.append_chunk(plan, k.cuda(), v.cuda())
+        for b, (s, n) in enumerate(zip(plan.starts, plan.counts)):
+            rows = slice(plan.offsets[b], plan.offsets[b + 1])
+            p.plain[b].append(s, k[rows], v[rows])
+    q = p.new(plan.tokens, 8, size)
+    got = p.cache.chunk_attention(plan, q.cuda())
+    p.cache.check_device()
+    clear = 0
+    for b in range(3):
+        hk, hv = p.plain[b].held()
+        rows = slice(plan.offsets[b], plan.offsets[b + 1])
+        clear += check_one_hot(got[rows], ct.wide(q[rows]), hk, hv, plan.starts[b], dtype, f"slot {b}")
+    assert clear > 0
+
+
+@pytest.mark.parametrize("dtype,size", [(BF16, 2.0 ** 16), (FP16, 2.0 ** 13), (BF16, 2.0 ** 20)])
+def test_large_logits_of_prompts(dtype, size):
+    lens, hq, hkv, d = [600, 1, 130], 4, 2, 128
+    gen = torch.Generator().manual_seed(5)
+    q, k, v = ((torch.randn(sum(lens), h, d, generator=gen) * s).to(dtype) for h, s in ((hq, size), (hkv, size), (hkv, 1.0)))
+    got = kvq.prompt_attention(kvq.plan_prompt(lens, hq, hkv, d), q.cuda(), k.cuda(), v.cuda())
+    at = clear = 0
+    for n in lens:
+        rows = slice(at, at + n)
+        clear += check_one_hot(got[rows], ct.wide(q[rows]), ct.wide(k[rows]).transpose(1, 0, 2),
+                               ct.wide(v[rows]).transpose(1, 0, 2), 0, dtype, f"rows {rows}")
+        at += n
+    assert clear > 0
