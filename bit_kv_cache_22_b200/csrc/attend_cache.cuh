@@ -803,7 +803,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             if (any && go) {
                 ml[r] = m;
                 ml[kRows + r] = l;
-                const float up = pow2(e_ref);
+                // divided by its own sum of weights: a sum of large values may pass the range of fp32
+                const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f, up = pow2(e_ref);
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -813,7 +814,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        ox[(32 * cc + e) * kRows + r] = had ? __uint_as_float(o[e]) * up : 0.0f;
+                        ox[(32 * cc + e) * kRows + r] = had ? __uint_as_float(o[e]) * inv * up : 0.0f;
                 }
             }
         }
@@ -823,8 +824,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             tc::fence_after_sync();
             const float m1 = ml[r], l1 = ml[kRows + r];
             const float mn = fmaxf(m, m1), w0 = tc::ex2(m - mn), w1 = tc::ex2(m1 - mn);
-            const float sum = l * w0 + l1 * w1, inv = n_splits > 1 ? 1.0f : sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
-            const float f0 = w0 * inv * pow2(e_ref), f1 = w1 * inv;
+            const float sum = l * w0 + l1 * w1, inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
+            const float f0 = w0 * inv, f1 = l1 * w1 * inv, up = pow2(e_ref);
             uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                             static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
             const int64_t tile = (static_cast<int64_t>(work.part) + split) * a.Hkv + h;
@@ -847,7 +848,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                     float y[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        y[k] = (had ? __uint_as_float(o[e + k]) * f0 : 0.0f) + ox[(32 * cc + e + k) * kRows + r] * f1;
+                        y[k] = (had ? __uint_as_float(o[e + k]) * f0 * up : 0.0f) + ox[(32 * cc + e + k) * kRows + r] * f1;
                     if (n_splits > 1) {
                         reinterpret_cast<float4 *>(part + 32 * cc + e)[0] = make_float4(y[0], y[1], y[2], y[3]);
                         reinterpret_cast<float4 *>(part + 32 * cc + e)[1] = make_float4(y[4], y[5], y[6], y[7]);
@@ -861,7 +862,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
         }
     } else if (any && go) {
         tc::fence_after_sync();
-        const float f0 = (n_splits > 1 ? 1.0f : l > 0.0f ? __fdividef(1.0f, l) : 0.0f) * pow2(e_ref);
+        const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f, up = pow2(e_ref);
         uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                         static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
         const int64_t tile = (static_cast<int64_t>(work.part) + 2 * split + t) * a.Hkv + h;
@@ -883,7 +884,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             for (int e = 0; e < 32; e += 8) {
                 float y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = had ? __uint_as_float(o[e + k]) * f0 : 0.0f;
+                for (int k = 0; k < 8; ++k) y[k] = had ? __uint_as_float(o[e + k]) * inv * up : 0.0f;
                 if (n_splits > 1) {
                     reinterpret_cast<float4 *>(part + 32 * cc + e)[0] = make_float4(y[0], y[1], y[2], y[3]);
                     reinterpret_cast<float4 *>(part + 32 * cc + e)[1] = make_float4(y[4], y[5], y[6], y[7]);

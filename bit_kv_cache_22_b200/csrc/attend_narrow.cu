@@ -164,8 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
     }
 }
 
-// Joins an item's splits: one warp per (query token, query head) of its rows, o = sum_s 2^(m_s - M)
-// o_s / sum_s 2^(m_s - M) l_s, in the splits' order.  merges: [n][4] = (slot, first query token, splits,
+// Joins an item's splits: one warp per (query token, query head) of its rows, o = sum_s w_s o_s /
+// sum_s w_s with w_s = 2^(m_s - M) l_s, in the splits' order (o_s: the split's own output; weighed by shares of 1, so that
+// no sum passes the range of the values).  merges: [n][4] = (slot, first query token, splits,
 // first partial tile).  Bound by memory: 0.14 GB of partial sums (2048 tokens x 32 heads in four splits,
 // d = 128) in 44 us.
 constexpr int kMergeWarps = 8;
@@ -196,11 +197,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_splits_kernel(const At
     for (int s = lane; s < n_splits; s += 32) M = fmaxf(M, a.part_ml[tile(s) * 2 * kRows + r]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float l = 0.0f;
+    for (int s = lane; s < n_splits; s += 32)
+        l = fmaf(tc::ex2(a.part_ml[tile(s) * 2 * kRows + r] - M), a.part_ml[(tile(s) * 2 + 1) * kRows + r], l);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f;
     constexpr int E = D / 32;
-    float o[E] = {}, l = 0.0f;
+    float o[E] = {};
     for (int s = 0; s < n_splits; ++s) {
-        const float w = tc::ex2(a.part_ml[tile(s) * 2 * kRows + r] - M);
-        l = fmaf(w, a.part_ml[(tile(s) * 2 + 1) * kRows + r], l);
+        const float w = tc::ex2(a.part_ml[tile(s) * 2 * kRows + r] - M) * a.part_ml[(tile(s) * 2 + 1) * kRows + r] * inv;
         const float *p = a.part_o + (tile(s) * kRows + r) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
@@ -209,11 +215,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_splits_kernel(const At
             o[e + 1] = fmaf(w, x.y, o[e + 1]);
         }
     }
-    const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f;
     uint16_t *out = a.o.p + static_cast<int64_t>(first + q0 + tok) * a.o.ts + static_cast<int64_t>(hq) * a.o.hs + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
-        reinterpret_cast<uint32_t *>(out)[e / 2] = narrow2<BF16>(o[e] * inv, o[e + 1] * inv);
+        reinterpret_cast<uint32_t *>(out)[e / 2] = narrow2<BF16>(o[e], o[e + 1]);
 }
 
 template <int D, int N, bool BF16>

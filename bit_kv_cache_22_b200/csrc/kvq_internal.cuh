@@ -262,7 +262,7 @@ struct AttendArgs {
     bool bf16;
     float scale;                 // log2(e) / sqrt(d)
     int64_t most_tokens;         // of any slot's chunk
-    // splits' partial results, tiles of 128 query rows: [part_tiles][Hkv][128][d], and maxima and sums
+    // splits' own outputs, tiles of 128 query rows: [part_tiles][Hkv][128][d], and their maxima and sums
     // [part_tiles][Hkv][2][128]
     float *part_o, *part_ml;
     int64_t part_tiles;

@@ -230,3 +230,56 @@ def test_large_logits_of_prompts(dtype, size):
                                ct.wide(v[rows]).transpose(1, 0, 2), 0, dtype, f"rows {rows}")
         at += n
     assert clear > 0
+
+
+# ------------------------------------------------------------------ values of different size, large values
+
+def largest_share(q, k, v, first):
+    """max over 32 tokens of (the largest weight among them times the largest value among them), for each
+    query row: the largest thing the row's sum is made of, [n, Hq, 1]."""
+    n, hq, d = q.shape
+    hkv, tokens, _ = k.shape
+    out = torch.zeros(n, hq, 1, dtype=torch.float64).numpy()
+    pad = -tokens % 32
+    for h in range(hq):
+        y = q[:, h] @ k[h // (hq // hkv)].T / d ** 0.5
+        y[torch.arange(tokens)[None].numpy() > first + torch.arange(n)[:, None].numpy()] = -float("inf")
+        p = torch.softmax(torch.from_numpy(y), 1)
+        p = torch.nn.functional.pad(p, (0, pad)).view(n, -1, 32).amax(2)
+        w = torch.nn.functional.pad(torch.from_numpy(abs(v[h // (hq // hkv)]).max(1)), (0, pad)).view(-1, 32).amax(1)
+        out[:, h, 0] = (p * w).amax(1).numpy()
+    return out
+
+
+def check_by_what_rows_see(p, b, plan, q, got):
+    """As Pair.check_attention, with the weights' absolute rounding measured by the row itself.  A weight
+    meets its 32 tokens' values under a power of two; the products' scale is such that the largest
+    of (weight x 2^e of its values) lies at 2^5 or above, and fp16 is off by at most 2^-25 below 2^-14: of a
+    bound on the values, 2^e is at most 2^-11, a value at most 2^15 2^e, and a bound at most twice the
+    largest value, so a token's share is off by 2^-25 2^-5 2^-11 2^15 2 = 2^-25 of the largest share."""
+    k, v = p.plain[b].held()
+    rows = slice(plan.offsets[b], plan.offsets[b + 1])
+    qw = ct.wide(q[rows])
+    o, A, S, _ = ct.attend(qw, k, v, plan.starts[b])
+    share = largest_share(qw, k, v, plan.starts[b])
+    ct.check_attention(got[rows], o, A, S, share, k.shape[1], p.dtype, True)
+
+@pytest.mark.parametrize("held,count", [(6090, 2), (6050, 40), (245, 2), (210, 40)])
+def test_large_values_in_the_residual(held, count):
+    """bf16 values of 1e37 in the rows that are not quantized: their weighted sum before it is divided
+    passes the range of fp32, their average does not.  Over a split cache and a short one, with few and
+    with many rows."""
+    p = pair(slots=1, capacity=8192)
+    for n in (held, count):
+        plan = p.cache.plan_chunk([n])
+        start = plan.starts[0]
+        k, v = p.new(n, 2, 0.1), (1.0 + p.new(n, 2, 0.25)).abs()
+        first = max(0, (held + count) // 128 * 128 - start)          # of those that stay in the residual
+        v[first:] *= 1e37
+        p.cache.append_chunk(plan, k.cuda(), v.cuda())
+        p.plain[0].append(start, k, v)
+    q = p.new(count, 8)
+    k, v = p.plain[0].held()
+    assert k.shape[1] % 128 > 60
+    check_by_what_rows_see(p, 0, plan, q, p.cache.chunk_attention(plan, q.cuda()))
+    p.cache.check_device()
