@@ -49,9 +49,15 @@ struct PromptSmem {
     static constexpr int bytes = (bars + 256 > 120 * 1024 ? bars + 256 : 120 * 1024) + 1024;
 };
 
-// A value above which the running maximum is raised: weights stay below 2^8, which e holds as
-// exactly as weights below 1, and the sums are rescaled rarely.
+// The running maximum is raised when a logit passes it by this: weights grow by up to 2^8 over that of
+// the maximum, and the sums are rescaled rarely.
 constexpr float kLazyMax = 8.0f;
+// The weight of the maximum is 2^kTopWeight.  fp16 holds weights up to 2^15, so that those far below the
+// maximum keep their bits (with 2^0 instead of 2^7 a hundred thousand weights of 2^-26 would be lost).
+// bf16 has bits to spare below, and its values may be as large as fp32 goes: their sum over 2^16 tokens
+// stays in range before it is divided.
+template <bool BF16>
+constexpr float kTopWeight = BF16 ? -24.0f : 7.0f;
 constexpr float kNoMax = -1e30f;           // below it: no logits
 
 // A CTA's piece of work: up to 2 * tpt tokens of one slot's prompt from token q0 on, for kv head h.
@@ -310,12 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
                 const bool far = fabsf(mx) > kFarLogit && mx > kNoMax;
                 bool careful = false;
                 if (j == 0) {
-                    m = mx;
+                    m = mx - kTopWeight<BF16>;
                     careful = __any_sync(0xffffffffu, far);
-                } else if (__any_sync(0xffffffffu, mx - m > kLazyMax || far)) {
+                } else if (__any_sync(0xffffffffu, mx - m > kLazyMax + kTopWeight<BF16> || far)) {
                     careful = __any_sync(0xffffffffu, far);
                     // O holds every tile before j: S_j was committed after its last MMA
-                    const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
+                    const float mn = fmaxf(m, mx - kTopWeight<BF16>), alpha = tc::ex2(m - mn);
                     m = mn;
                     l *= alpha;
 #pragma unroll

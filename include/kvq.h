@@ -522,7 +522,8 @@ KVQ_API kvq_status kvq_plan_prompt(int32_t batch, int32_t q_heads, int32_t kv_he
  * p_i = softmax_j(q_i . k_j / sqrt(d)).  q, o: [tokens][q_heads][d]; k, v: [tokens][kv_heads][d],
  * packed as planned (a prompt plan); all of element type `dtype` (kvq_dtype); o must overlap no
  * input.  Logits, softmax statistics and sums are fp32; the weights are rounded to e before
- * they meet v, the output once.  Finite inputs: a NaN or infinity reaches rows of its own
+ * they meet v (in fp16 under 2^7, so that one down to 2^-21 of the largest keeps 11 bits), the output
+ * once.  Finite inputs: a NaN or infinity reaches rows of its own
  * sequence only.  `status`: device word (4 bytes, or NULL) whose bits the kernel raises (bit 0:
  * a bounded wait gave up; bit 3: a table entry outside the tensors).
  */

@@ -1,6 +1,7 @@
 """The chunk operators on the GPU at the edges of what their documents allow: plans shared by caches of
 different groups and capacities, many short prompts, plans and
 angles dropped while another stream still reads them, against the plain 64-bit forms (chunk_testlib)."""
+import math
 import random
 
 import pytest
@@ -283,3 +284,30 @@ def test_large_values_in_the_residual(held, count):
     assert k.shape[1] % 128 > 60
     check_by_what_rows_see(p, 0, plan, q, p.cache.chunk_attention(plan, q.cuda()))
     p.cache.check_device()
+
+
+def test_large_values_of_prompts():
+    """bf16 values up to 3e38, whose weighted sums before they are divided pass the range of fp32."""
+    lens, hq, hkv, d = [700, 3, 150], 4, 2, 128
+    gen = torch.Generator().manual_seed(6)
+    q, k = (torch.randn(sum(lens), h, d, generator=gen).to(BF16) for h in (hq, hkv))
+    v = ((2.5 + torch.rand(sum(lens), hkv, d, generator=gen) / 2) * 1e38).to(BF16)
+    plan = kvq.plan_prompt(lens, hq, hkv, d)
+    check_prompt(kvq.prompt_attention(plan, q.cuda(), k.cuda(), v.cuda()), q, k, v, lens)
+    plan.check_device()
+
+
+def test_a_hundred_thousand_small_weights():
+    """fp16: a first token with nearly all the weight, and 100000 whose weights of 2^-26 are together a
+    six-hundredth of it; the last rows, against their formula.  The weights' rounding (2^-11, and 2^-25 2^-7
+    each below 2^-14) and the output's; logits are 0 but for the first."""
+    n, d = 100000, 64
+    q, k = torch.zeros(n, 1, d, dtype=FP16), torch.zeros(n, 1, d, dtype=FP16)
+    q[..., 0], k[0, 0, 0] = 8.0, 26 * math.log(2)
+    v = torch.ones(n, 1, d, dtype=FP16)
+    v[0] = 0.0
+    got = kvq.prompt_attention(kvq.plan_prompt([n], 1, 1, d), q.cuda(), k.cuda(), v.cuda())[-100:].cpu().double()
+    seen = torch.arange(n - 100, n, dtype=torch.float64)
+    w = torch.exp(-q[0, 0, 0].double() * k[0, 0, 0].double() / d ** 0.5)
+    want = (seen * w / (1 + seen * w))[:, None, None].expand_as(got)
+    assert ((got - want).abs() <= 2.0 ** -10 * want + 1e5 * 2.0 ** -32 + 2.0 ** -25).all()
