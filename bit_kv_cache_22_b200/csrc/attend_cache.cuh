@@ -16,9 +16,12 @@
 // a rounding as large as the output's own).  What fp16 lacks is range, so operands carry powers of
 // two of their own: a query row that of its largest channel, 16 tokens' keys and values those of
 // bounds on their elements, so that the largest lies in [2^14, 2^15) -- values' in steps of 2^4.
-// They are undone in the logits' scale and at the end: weights that meet a smaller power of values
-// than the largest so far are scaled down, and the sums in tensor memory when the largest grows.
-// An element far below the largest of its 16 tokens loses bits under 2^-36 of it.
+// They are undone in the logits' scale, and for the values in the weights: a row's sums stand for
+// 2^(m + e) of what they hold, and a weight that meets values under 2^ev enters as 2^(y - m) 2^(ev - e).  e
+// follows, as m follows the logits, the largest (weight x 2^ev) that the row has met, so that a
+// weight is rounded by what it adds to its row: to 11 bits, and by at most 2^-30 of the row's largest
+// share.  Large values that hardly weigh, or that the row does not see, cost it nothing.
+// An element far below the largest of its 32 tokens loses bits under 2^-36 of it.
 //
 // Unpacking is bound by the integer pipe, so codes stay in 16-bit pairs: bytes 0 and 2 (1 and 3) of a
 // word's slot, OR 0x6400, are the fp16 numbers 1024 + code; minus (1024 + z), exact for |z| <= 1024,
@@ -46,12 +49,14 @@ constexpr int kStages = 2;                 // key and value operand tiles, each
 constexpr int kUnits = 4;                  // of 32 tokens in a key tile: a warp's work for keys or values
 constexpr int kExps = 8;                   // key tiles whose exponents are kept (at most kStages + 1 are live)
 constexpr int kValueStep = 4;              // values' exponents are multiples of this: they rarely differ
-constexpr float kLazyMax = 8.0f;           // the running maximum is raised when a logit passes it by this
+// Weights, as they meet the values, lie below 2^(kTopWeight + kLazyMax); where the maximum, or e, is raised
+// the largest becomes about 2^kTopWeight.
+constexpr float kTopWeight = 7.0f, kLazyMax = 8.0f;
 constexpr float kNoMax = -1e30f;           // the maximum of no logits: finite, so differences stay numbers
 constexpr int kMaxTokens = 0x7fffffff - 1024;   // of a sequence (the planner refuses more)
 // Least exponents of operands: values' 2^e and 2^-e stay normal; those of queries and keys keep
 // their product, the logits' scale, above 0 (what they cost a logit is below 2^-60 of the other).
-constexpr int kMinExp = -112, kMinLogitExp = -56;
+constexpr int kMinExp = -112, kMinLogitExp = -56;      // kMinExp: a multiple of kValueStep
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
@@ -159,7 +164,7 @@ __device__ __forceinline__ void widen_zeros(uint2 z, bool sym, int half_levels, 
 // The powers of two of a key tile's units: 2^e of the keys, then e of the values.
 struct TileExps {
     float scale_k[kUnits];
-    int exp_v[kUnits];
+    float exp_v[kUnits];
 };
 
 // Fetches the 32 tokens tok .. ; at_tok: the first one's place in its page.
@@ -639,8 +644,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
     const int stride = alternate ? 2 : 1, n = work.n;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
-    float m = kNoMax, l = 0.0f, row_s = 0.0f;
-    int e_ref = kMinExp;
+    // weights are 2^(y - m) with sum l; O holds the sums of 2^(y - m) v 2^-e_ref
+    float m = kNoMax, l = 0.0f, row_s = 0.0f, e_ref = kMinExp;
     bool go = n == 0 || tc::bar_wait_warp(bar(kQFull), 0, &gave_up);
     if (go && n > 0) row_s = row_scale[qt * kRows + r] * a.scale;
     const int end = t == 0 ? work.end0 : n;
@@ -665,63 +670,69 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             };
             // 16 columns from 32 k + 16 g on are of one unit
             auto unit = [&](int k, int g) { return 2 * (k / 2) + g; };
+            float big[kUnits] = {kNoMax, kNoMax, kNoMax, kNoMax};      // the units' largest logits
             auto largest = [&](int k, const uint32_t(&x)[32]) {
-                float big = kNoMax;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     float m2[2] = {__uint_as_float(x[16 * g]), __uint_as_float(x[16 * g + 1])};
 #pragma unroll
                     for (int e = 2; e < 16; ++e) m2[e % 2] = fmaxf(m2[e % 2], __uint_as_float(x[16 * g + e]));
-                    big = fmaxf(big, fmaxf(m2[0], m2[1]) * (row_s * scales[unit(k, g)]));
+                    const float y = fmaxf(m2[0], m2[1]) * (row_s * scales[unit(k, g)]);
+                    if constexpr (WHOLE) {
+                        if (k < 2) big[g] = fmaxf(big[g], y);
+                        else big[2 + g] = fmaxf(big[2 + g], y);
+                    } else {                       // (rolled: no branch)
+                        big[g] = fmaxf(big[g], k < 2 ? y : kNoMax);
+                        big[2 + g] = fmaxf(big[2 + g], k < 2 ? kNoMax : y);
+                    }
                 }
-                return big;
             };
             constexpr int kHeld = WHOLE ? 4 : 1;
             uint32_t x[kHeld][32];
-            float mx = kNoMax;
             if constexpr (WHOLE) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tc::tmem_load(ts + 32 * k, x[k]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     logits(k, x[k]);
-                    mx = fmaxf(mx, largest(k, x[k]));
+                    largest(k, x[k]);
                 }
             } else {
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
                     tc::tmem_load(ts + 32 * k, x[0]);
                     logits(k, x[0]);
-                    mx = fmaxf(mx, largest(k, x[0]));
+                    largest(k, x[0]);
                 }
             }
             if constexpr (!WHOLE) {                // the values' powers come with the values
                 go = tc::bar_wait_warp(bar(kVFull + j % kStages), (j / kStages) & 1, &gave_up);
                 if (!go) break;
             }
-            const int *evs = exps[j % kExps].exp_v;
-            int top = e_ref;
-            bool even = true;
-#pragma unroll
-            for (int g = 0; g < kUnits; ++g) top = max(top, evs[g]);
-#pragma unroll
-            for (int g = 0; g < kUnits; ++g) even = even && evs[g] == top;
+            const float *evs = exps[j % kExps].exp_v;
+            const float mx = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
             const bool far = fabsf(mx) > kFarLogit && mx > kNoMax;
-            bool careful = false;
-            if (i == 0) {
-                m = mx;
-                e_ref = top;
+            // the row's largest weight, times 2^ev, where weights are 2^(y - from)
+            auto share = [&](float from) {
+                return fmaxf(fmaxf(big[0] - from + evs[0], big[1] - from + evs[1]),
+                             fmaxf(big[2] - from + evs[2], big[3] - from + evs[3]));
+            };
+            auto level = [&] { return evs[0] == e_ref && evs[1] == e_ref && evs[2] == e_ref && evs[3] == e_ref; };
+            bool careful = false, even = __all_sync(0xffffffffu, level());
+            if (i == 0 || __any_sync(0xffffffffu, fmaxf(mx - m, even ? kNoMax : share(m) - e_ref) > kTopWeight + kLazyMax || far)) {
                 careful = __any_sync(0xffffffffu, far);
-            } else if (top != e_ref || __any_sync(0xffffffffu, mx - m > kLazyMax || far)) {
-                careful = __any_sync(0xffffffffu, far);
-                // O holds every tile of the stream before j: S_j was committed after its last MMA
-                const float mn = fmaxf(m, mx), alpha = tc::ex2(m - mn);
-                const float alpha_o = alpha * tc::ex2(static_cast<float>(e_ref - top));
+                const float mn = fmaxf(m, mx - kTopWeight), down = m - mn;
+                // in steps of the values' own exponents, so that it comes to equal them
+                const float er = fmaxf(rintf(fmaxf(down + e_ref, share(mn) - kTopWeight) * (1.0f / kValueStep)) * kValueStep,
+                                       kMinExp);
+                const float alpha_o = tc::ex2(down + (e_ref - er));
                 m = mn;
-                l *= alpha;
-                e_ref = top;
+                l *= tc::ex2(down);
+                e_ref = er;
+                even = __all_sync(0xffffffffu, level());
+                // O holds every tile of the stream before j: S_j was committed after its last MMA
 #pragma unroll 1
-                for (int cc = 0; cc < D / 32; ++cc) {
+                for (int cc = i == 0 ? D / 32 : 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
                     tc::tmem_load(to + 32 * cc, o);
                     tc::tmem_arrived(o);
@@ -740,7 +751,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const float sc = careful ? 1.0f : row_s * scales[unit(k, g)];
-                    const float down = even ? 1.0f : tc::ex2(static_cast<float>(evs[unit(k, g)] - top));
+                    const float down = even ? 1.0f : tc::ex2(fminf(evs[unit(k, g)] - e_ref, 126.0f));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t *y = &x[16 * g + 2 * e];
@@ -804,7 +815,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
                 ml[r] = m;
                 ml[kRows + r] = l;
                 // divided by its own sum of weights: a sum of large values may pass the range of fp32
-                const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f, up = pow2(e_ref);
+                const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f, up = tc::ex2(e_ref);
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -825,7 +836,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
             const float m1 = ml[r], l1 = ml[kRows + r];
             const float mn = fmaxf(m, m1), w0 = tc::ex2(m - mn), w1 = tc::ex2(m1 - mn);
             const float sum = l * w0 + l1 * w1, inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
-            const float f0 = w0 * inv, f1 = l1 * w1 * inv, up = pow2(e_ref);
+            const float f0 = w0 * inv, f1 = l1 * w1 * inv, up = tc::ex2(e_ref);
             uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                             static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
             const int64_t tile = (static_cast<int64_t>(work.part) + split) * a.Hkv + h;
@@ -862,7 +873,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs &a, const CacheIte
         }
     } else if (any && go) {
         tc::fence_after_sync();
-        const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f, up = pow2(e_ref);
+        const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f, up = tc::ex2(e_ref);
         uint16_t *out = a.o.p + static_cast<int64_t>(first + tok) * a.o.ts +
                         static_cast<int64_t>(h * hg + r % hg) * a.o.hs;
         const int64_t tile = (static_cast<int64_t>(work.part) + 2 * split + t) * a.Hkv + h;

@@ -108,7 +108,7 @@ __device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem
             !tc::bar_wait_warp(base + L::bars + 8u * ((kv ? kVEmpty : kKEmpty) + s), ((j / kStages) & 1) ^ 1, &gave_up))
             break;
         if (lane == 0) {
-            if (kv) exps[j % kExps].exp_v[u] = ex;
+            if (kv) exps[j % kExps].exp_v[u] = static_cast<float>(ex);
             else exps[j % kExps].scale_k[u] = pow2(ex);
         }
         emit_unit<D, N, BF16>(words, kind0, kind1, narrow, c, src, tok, pow2(-ex), u, lane, meta,

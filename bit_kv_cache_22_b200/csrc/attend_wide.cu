@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const AttendArgs a
         unsigned char *meta = tile_s + kTileBytes + w * kMetaBytes;
         const bool narrow = prepare_unit<D, N, BF16>(f, c, src, tok, lane, meta, ex);
         if (lane == 0) {
-            if (kv) st.exps[at].exp_v[w] = ex;
+            if (kv) st.exps[at].exp_v[w] = static_cast<float>(ex);
             else st.exps[at].scale_k[w] = pow2(ex);
         }
         emit_unit<D, N, BF16>(f.w, f.kind[0], f.kind[1], narrow, c, src, tok, pow2(-ex), w, lane, meta, put);

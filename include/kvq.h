@@ -562,8 +562,8 @@ KVQ_API kvq_status kvq_paged_read_chunk(kvq_paged *cache, const kvq_chunk *plan,
  * q, o: e [tokens][q_heads][d]; o must not overlap q.  starts[b] + counts[b] must not pass the
  * slot's length (KVQ_ERR_STATE); rows of which the device length leaves nothing to see give
  * zeros.  Logits, softmax statistics and sums are fp32; what meets in a product -- queries, keys,
- * weights, values -- is rounded to fp16 (11 bits) under powers of two that keep it in range, the
- * output once to e.  (The keys' rounding moves a logit by up to 2^-11 sum_c |q_c k_c| / sqrt(d): beside
+ * weights, values -- is rounded to fp16 (11 bits) under powers of two that keep it in range (a weight
+ * also by up to 2^-30 of the largest share, weight x value, of its row's sum), the output once to e.  (The keys' rounding moves a logit by up to 2^-11 sum_c |q_c k_c| / sqrt(d): beside
  * bf16 outputs little, beside fp16 ones several roundings where single channels are large.)  Scales s <= 2^31 and queries |q| <= 2^30, as for decoding; finite inputs: a
  * NaN or infinity reaches rows of its own slot only.  `workspace`: plan->workspace bytes of device
  * scratch, 16-byte aligned (NULL where that is 0; a slot with more than 32 query rows per kv head --

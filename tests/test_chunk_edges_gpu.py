@@ -1,6 +1,7 @@
 """The chunk operators on the GPU at the edges of what their documents allow: plans shared by caches of
-different groups and capacities, many short prompts, plans and
-angles dropped while another stream still reads them, against the plain 64-bit forms (chunk_testlib)."""
+different groups and capacities, many short prompts, plans and angles dropped while another stream still
+reads them, large logits, large values, values of very different size; against the plain 64-bit forms
+(chunk_testlib)."""
 import math
 import random
 
@@ -311,3 +312,45 @@ def test_a_hundred_thousand_small_weights():
     w = torch.exp(-q[0, 0, 0].double() * k[0, 0, 0].double() / d ** 0.5)
     want = (seen * w / (1 + seen * w))[:, None, None].expand_as(got)
     assert ((got - want).abs() <= 2.0 ** -10 * want + 1e5 * 2.0 ** -32 + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("dtype,bits", [(BF16, 2), (FP16, 4)])
+@pytest.mark.parametrize("count", [3, 100])
+@pytest.mark.parametrize("at", ["before", "between", "ahead"])
+@pytest.mark.parametrize("power", [8, 18])
+def test_large_values_that_hardly_weigh(dtype, bits, count, at, power):
+    """One token with two fifths of the weight, thousands that share the rest, and a block of values 2^power
+    times the others', of weight next to none, before them, among them or behind the queries.  All
+    values are positive, so that what is lost of the many shows."""
+    p = pair(slots=1, dtype=dtype, bits=bits, capacity=8192)
+    n = 6000
+    k, v = p.new(n, 2, 0.02), (1.0 + p.new(n, 2, 0.25)).abs() / 16
+    big = {"before": slice(0, 96), "between": slice(2944, 3040), "ahead": slice(n - 100, n)}[at]
+    k[..., 7] = 0.0
+    k[150 if at == "ahead" else big.stop + 14, :, 7] = 23.5   # 8.3 nats, 12 powers of two, above the others
+    k[big, :, 7] = -46.0                             # 23 powers of two below them
+    v[big] *= 2.0 ** power
+    plan = p.cache.plan_chunk([n])
+    p.cache.append_chunk(plan, k.cuda(), v.cuda())
+    p.plain[0].append(0, k, v)
+    start = n - 130 - (0 if at == "ahead" else count - 30)
+    plan = p.cache.plan_chunk([count], [start if at != "ahead" else n - 100 - count])
+    q = p.new(count, 8, 0.05)
+    q[..., 7] = 4.0
+    check_by_what_rows_see(p, 0, plan, q, p.cache.chunk_attention(plan, q.cuda()))
+
+
+@pytest.mark.parametrize("count", [2, 60])
+def test_values_of_every_size(count):
+    """Values that grow and shrink by 2^20 from block to block, weights that follow no order."""
+    p = pair(slots=1, capacity=8192, seed=count)
+    n = 5000
+    k, v = p.new(n, 2, 1.5), (1.0 + p.new(n, 2, 0.25)).abs()
+    for i in range(0, n, 128):
+        v[i:i + 128] *= 2.0 ** ((i * 7 // 128) % 21 - 10)
+    plan = p.cache.plan_chunk([n])
+    p.cache.append_chunk(plan, k.cuda(), v.cuda())
+    p.plain[0].append(0, k, v)
+    plan = p.cache.plan_chunk([count], [n - count])
+    q = p.new(count, 8, 1.5)
+    check_by_what_rows_see(p, 0, plan, q, p.cache.chunk_attention(plan, q.cuda()))
