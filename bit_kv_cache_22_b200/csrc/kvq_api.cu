@@ -1207,9 +1207,10 @@ void split_pieces(std::vector<Piece> &pieces, int32_t kv_heads, int32_t num_sms)
     }
 }
 
-kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t R, const int32_t *counts,
-                      const int32_t *starts, int32_t num_sms, size_t least_workspace, kvq_chunk *out, void *table,
-                      size_t table_bytes) {
+// (throws std::bad_alloc: the lists grow with the plan)
+kvq_status make_plan(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t R, const int32_t *counts,
+                     const int32_t *starts, int32_t num_sms, size_t least_workspace, kvq_chunk *out, void *table,
+                     size_t table_bytes) {
     if (!counts || !out) return fail(KVQ_ERR_INVALID_ARG, "counts and out must be non-NULL");
     if (q_heads / kv_heads > 128)
         return fail(KVQ_ERR_UNSUPPORTED, "at most 128 query heads per kv head (got %d)", q_heads / kv_heads);
@@ -1326,6 +1327,17 @@ kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
         part += p.splits * (p.one_tile ? 1 : 2);
     }
     return ok();
+}
+
+kvq_status plan_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t R, const int32_t *counts,
+                      const int32_t *starts, int32_t num_sms, size_t least_workspace, kvq_chunk *out, void *table,
+                      size_t table_bytes) {
+    try {
+        return make_plan(batch, q_heads, kv_heads, d, R, counts, starts, num_sms, least_workspace, out, table,
+                         table_bytes);
+    } catch (const std::bad_alloc &) {
+        return fail(KVQ_ERR_INVALID_ARG, "out of host memory");
+    }
 }
 
 kvq::ChunkTable chunk_table(const kvq_chunk *p) {
