@@ -790,10 +790,15 @@ class PagedKVQCache:
                 o_rows, q_out = _output(out, q)
             if rope is not None and rope.cos.device != device:
                 raise ValueError(f"the angles must be on {device}")
-            if plan.chunk.blocks:
-                self._pages_for(plan, stream)
-            _check(self._lib.kvq_paged_append_chunk(
-                self._h, plan.ref, k_rows, v_rows, None if rope is None else rope.ref, q_rows, o_rows, raw))
+            had = self._pages_for(plan, stream) if plan.chunk.blocks else {}
+            try:
+                _check(self._lib.kvq_paged_append_chunk(
+                    self._h, plan.ref, k_rows, v_rows, None if rope is None else rope.ref, q_rows, o_rows, raw))
+            except KVQError:
+                for b in reversed(had):                    # refused: the pages go back
+                    self.free_pages.extend(reversed(self.pages[b][had[b]:]))
+                    del self.pages[b][had[b]:]
+                raise
             for b, end in plan.ends:
                 self.lens[b] = end
             plan.used_on(raw)
@@ -810,18 +815,19 @@ class PagedKVQCache:
 
     def _pages_for(self, plan: ChunkPlan, stream):
         """Pages for the blocks the planned tokens complete (the library refuses a plan whose slots do
-        not fit; those get none here)."""
-        g, need, short = self.geom, {}, 0
+        not fit; those get none here).  Returns how many the slots that got some had."""
+        g, need, had, short = self.geom, {}, {}, 0
         for b, end in plan.ends:
             whole = end // g.residual * g.residual
             pages = -(-whole // self.page_tokens)
             if pages > len(self.pages[b]) and plan.starts[b] <= max(self.lens[b], 0) and whole <= g.capacity:
-                need[b] = pages
-                short += pages - len(self.pages[b])
+                need[b], had[b] = pages, len(self.pages[b])
+                short += pages - had[b]
         if short > len(self.free_pages):
             raise KVQError(KVQ_ERR_CAPACITY, "the page pool is exhausted")
         if need:
             self._grow(need, stream)
+        return had
 
     def read_chunk(self, plan: ChunkPlan, stream=None):
         """(k, v) [tokens, Hkv, d]: the planned tokens as the cache holds them."""

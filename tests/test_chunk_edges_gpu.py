@@ -354,3 +354,24 @@ def test_values_of_every_size(count):
     plan = p.cache.plan_chunk([count], [n - count])
     q = p.new(count, 8, 1.5)
     check_by_what_rows_see(p, 0, plan, q, p.cache.chunk_attention(plan, q.cuda()))
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_a_refused_append_gives_its_pages_back():
+    """Angles that end before the tokens do: refused by the library, after the pages were looked for."""
+    p = ct.Pair(4, 8, 2, 128, 32, 32, 128, 2, False, BF16, 1024, 128, num_pages=6)
+    p.append([200, 10, 0, 0])
+    free = list(p.cache.free_pages)
+    short = kvq.Rope(*(x.cuda() for x in ct.angles(250, 128)))
+    k = p.new(900, 2).cuda()
+    for counts in ([100, 250, 0, 0], [100, 0, 300, 200], [0, 0, 0, 640]):
+        n = sum(counts)
+        with pytest.raises(kvq.KVQError) as e:
+            p.cache.append_chunk(p.cache.plan_chunk(counts), k[:n], k[:n], short)
+        assert e.value.status == kvq.KVQ_ERR_INVALID_ARG
+        assert p.cache.free_pages == free and [len(x) for x in p.cache.pages] == [1, 0, 0, 0]
+    plan, _, _ = p.append([0, 118, 512, 5])         # all that is left
+    assert not p.cache.free_pages
+    p.check_state()
+    p.check_read(plan)
