@@ -92,6 +92,7 @@ __device__ __forceinline__ void unpack_role(const AttendArgs &a, const CacheItem
     advance();
     int page = page_at(tok + kTurns * kRows);
     for (int j = turn; j < n; j += kTurns, tok += kTurns * kRows) {
+        if (kCheck && !kv && blockIdx.x == 0 && j + 1 == a.stall_tile) break;
         const int s = j % kStages, kind0 = f.kind[0], kind1 = f.kind[1];
         int ex;
         const bool narrow = prepare_unit<D, N, BF16>(f, c, src, tok, lane, meta, ex);

@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
             bool go = true;
             int keys = 0, values = 0, queries[2] = {0, 0};     // tiles asked for
             auto load_keys = [&](const Job &w, int j) {
+                if (kCheck && blockIdx.x == 0 && keys + 1 == a.stall_tile) go = false;
+                if (!go) return;
                 const int s = keys % kStages;
                 if (keys >= kStages) go = go && tc::bar_wait_warp(bar(kKEmpty + s), ((keys / kStages) & 1) ^ 1, &gave_up);
                 if (!go) return;

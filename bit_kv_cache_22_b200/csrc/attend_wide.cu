@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const AttendAr
             for (int j = 0; j < n; ++j, at += a.Hkv) {
                 const int s = j % kStages, phase = (j / kStages) & 1;
                 const unsigned char *tile = st.kv + at * 2 * L::kTileBytes;
+                if (kCheck && blockIdx.x == 0 && j + 1 == a.stall_tile) break;
                 if (j >= kStages && !tc::bar_wait(bar(kKEmpty + s), phase ^ 1, &gave_up)) break;
                 tc::bar_expect(bar(kKFull + s), L::kTileBytes + static_cast<int>(sizeof(TileExps)));
                 tc::bulk_load(base + L::k + s * L::kTileBytes, tile, L::kTileBytes, bar(kKFull + s));

@@ -1485,6 +1485,8 @@ kvq_status attend_decode_step(const kvq_paged *h, const kvq_chunk *plan, kvq::De
     return ok();
 }
 
+int g_stall_tile = 0;                  // bounds-check builds: see kvq_debug_set_attention_stall
+
 kvq::AttendArgs attend_args(const kvq_chunk *p, const kvq_rows *q, const kvq_rows *o, bool bf16) {
     kvq::AttendArgs a{};
     a.t = chunk_table(p);
@@ -1496,6 +1498,7 @@ kvq::AttendArgs attend_args(const kvq_chunk *p, const kvq_rows *q, const kvq_row
     a.d = p->head_dim;
     a.bf16 = bf16;
     a.scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(p->head_dim)));
+    a.stall_tile = g_stall_tile;
     return a;
 }
 
@@ -1883,6 +1886,12 @@ kvq_status kvq_debug_set_stall(kvq_cache *h, int32_t polls) {
     if (!h) return fail(KVQ_ERR_INVALID_ARG, "cache is NULL");
     if (polls < 0 || polls > 4096) return fail(KVQ_ERR_INVALID_ARG, "polls must be in 0..4096");
     h->stall_polls = polls;
+    return ok();
+}
+
+kvq_status kvq_debug_set_attention_stall(int32_t tile) {
+    if (tile < 0) return fail(KVQ_ERR_INVALID_ARG, "tile must be >= 0");
+    g_stall_tile = tile;
     return ok();
 }
 

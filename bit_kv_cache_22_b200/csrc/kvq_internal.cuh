@@ -268,6 +268,8 @@ struct AttendArgs {
     int64_t part_tiles;
     unsigned char *staged;       // staged_bytes: operand tiles of the wide slots
     unsigned int *status;        // or NULL
+    int stall_tile;              // bounds-check builds: the first CTA's keys end before its key tile
+                                 // stall_tile - 1 (0: none), so that what waits for them gives up
 };
 // Over the cache: slots of at most one query tile, slots of more, and the joining of splits.
 cudaError_t launch_attend_narrow(const AttendArgs &a, cudaStream_t s);

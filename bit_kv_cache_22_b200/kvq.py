@@ -155,6 +155,8 @@ def load() -> ctypes.CDLL:
         if check_build():
             lib.kvq_debug_set_stall.argtypes = [P, i32]
             lib.kvq_debug_set_stall.restype = ctypes.c_int
+            lib.kvq_debug_set_attention_stall.argtypes = [i32]
+            lib.kvq_debug_set_attention_stall.restype = ctypes.c_int
             lib.kvq_debug_gather_rows.argtypes = [P, P, i64, P, i32, P, P]
             lib.kvq_debug_gather_rows.restype = ctypes.c_int
         lib.kvq_check_device.argtypes = [P]

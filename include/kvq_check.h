@@ -29,6 +29,14 @@ extern "C" {
 KVQ_API kvq_status kvq_debug_set_stall(kvq_cache *cache, int32_t polls);
 
 /*
+ * From the next call on, the keys of the first CTA of the prompt and chunk attention
+ * kernels end before its key tile number `tile` (counted from 1; 0 turns it off).  What
+ * waits for that tile gives up after about two seconds, the CTA's other roles with it: it
+ * raises bit 0 of the status word, writes no outputs and returns through the normal exit.
+ */
+KVQ_API kvq_status kvq_debug_set_attention_stall(int32_t tile);
+
+/*
  * dst[i] = src[idx[i]] for i < n (rows of head_dim e elements of this cache's
  * geometry; src has src_rows rows), through the gather kernel the LogQuant
  * prefill uses, raising bit 3 of the cache's status word for an index outside
