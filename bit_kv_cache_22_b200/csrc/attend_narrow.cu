@@ -206,14 +206,22 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_splits_kernel(const At
     const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f;
     constexpr int E = D / 32;
     float o[E] = {};
-    for (int s = 0; s < n_splits; ++s) {
-        const float w = tc::ex2(a.part_ml[tile(s) * 2 * kRows + r] - M) * a.part_ml[(tile(s) * 2 + 1) * kRows + r] * inv;
-        const float *p = a.part_o + (tile(s) * kRows + r) * D + lane * E;
+    for (int s0 = 0; s0 < n_splits; s0 += 32) {    // a lane has the share of split s0 + lane
+        float share = 0.0f;
+        if (s0 + lane < n_splits)
+            share = tc::ex2(a.part_ml[tile(s0 + lane) * 2 * kRows + r] - M) *
+                    a.part_ml[(tile(s0 + lane) * 2 + 1) * kRows + r] * inv;
+        const int n = min(32, n_splits - s0);
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float w = __shfl_sync(0xffffffffu, share, s);
+            const float *p = a.part_o + (tile(s0 + s) * kRows + r) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(p + e);
-            o[e] = fmaf(w, x.x, o[e]);
-            o[e + 1] = fmaf(w, x.y, o[e + 1]);
+            for (int e = 0; e < E; e += 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(p + e);
+                o[e] = fmaf(w, x.x, o[e]);
+                o[e + 1] = fmaf(w, x.y, o[e + 1]);
+            }
         }
     }
     uint16_t *out = a.o.p + static_cast<int64_t>(first + q0 + tok) * a.o.ts + static_cast<int64_t>(hq) * a.o.hs + lane * E;
