@@ -14,19 +14,24 @@
 //
 // Operands in fp16 for caches of either type: (code - z) s is rounded to 11 bits (bf16 would leave 8,
 // a rounding as large as the output's own).  What fp16 lacks is range, so operands carry powers of
-// two of their own: a query row that of its largest channel, 16 tokens' keys and values those of
+// two of their own: a query row that of its largest channel, 32 tokens' keys and values those of
 // bounds on their elements, so that the largest lies in [2^14, 2^15) -- values' in steps of 2^4.
 // They are undone in the logits' scale, and for the values in the weights: a row's sums stand for
 // 2^(m + e) of what they hold, and a weight that meets values under 2^ev enters as 2^(y - m) 2^(ev - e).  e
-// follows, as m follows the logits, the largest (weight x 2^ev) that the row has met, so that a
-// weight is rounded by what it adds to its row: to 11 bits, and by at most 2^-30 of the row's largest
-// share.  Large values that hardly weigh, or that the row does not see, cost it nothing.
+// follows, as m follows the logits, the largest weight x 2^ev that 32 tokens brought the row, so that a
+// weight is rounded by what it adds: to 11 bits, and its token's share by at most 2^-26 of (the largest
+// weight x the largest value) of some 32 tokens.  (That weight lies at 2^5 or above, where others are
+// off by 2^-25; operands reach 2^15, and bounds lie 2^11 or more above 2^ev.)  Large values that hardly
+// weigh, or that the row does not see, cost it nothing unless they lie among the 32 tokens of one that
+// weighs.
 // An element far below the largest of its 32 tokens loses bits under 2^-36 of it.
 //
 // Unpacking is bound by the integer pipe, so codes stay in 16-bit pairs: bytes 0 and 2 (1 and 3) of a
 // word's slot, OR 0x6400, are the fp16 numbers 1024 + code; minus (1024 + z), exact for |z| <= 1024,
 // times s -- in fp16 caches in two fp16 parts, lest s's own rounding double the element's; next to a
-// bf16 output it is an eighth of a rounding and s goes as one.
+// bf16 output s goes as one.  Keys carry nearly all of the error, since a logit's error grows with its
+// terms: with one channel ten times the others, d = 128, outputs are off 64 bits by 0.0009 in fp16 (the
+// output's own rounding: 0.0002) and by 0.0020 in bf16 (0.0017).
 //
 // The order of channels in keys and queries, and of tokens in keys and values, is free as long as
 // both agree.  A lane unpacks four neighbouring channels (tokens) at a time, which lie in the operand as

@@ -10,14 +10,15 @@
 //   the others       sixteen that unpack, keys or values, each 32 tokens of every other key tile: two on
 //                    the SM quarter of the softmax warps (0, 4, ...), four and five on the others
 //
-// Bound by instruction issue, nearly all of it unpacking (about 1200 instructions a warp for 32 tokens
-// x 128 channels), and by a stream's chain: product, 128 logits of a row by one thread, product, some
-// 5000 cycles for every other key tile.  One new token for each of 31 slots of 512 to 15872 tokens (32
-// query / 8 kv heads, d = 128, 2-bit; 0.23 GB): 261 us, 1.8 us a key tile and CTA.  With eight unpacking
+// Bound by instruction issue (busy 63% of the cycles), nearly all of it unpacking (about 1200 instructions a
+// warp for 32 tokens x 128 channels), and by a stream's chain: product, 128 logits of a row by one thread,
+// product, some 5000 cycles for every other key tile.  One new token for each of 31 slots of 512 to 15872
+// tokens (32 query / 8 kv heads, d = 128, 2-bit; 0.23 GB): 259 us, 1.8 us a key tile and CTA; four new
+// tokens for each of 32: 267 us.  With eight unpacking
 // warps, and registers moved from them to eight softmax warps, of which six had no rows, it took 289
 // us, with the sixteen spread evenly over the SM's quarters 269 us, with 64 logits read at a time instead
 // of 32 269 us.  (The decode kernel, whose operands are smaller, takes 156 us, so steps of single newest
-// tokens go there.)  Three slots of 100 to 400 tokens with up to six new ones: 15 us, a launch and one
+// tokens go there.)  Three slots of 100 to 400 tokens with up to six new ones: 14 us, a launch and one
 // CTA's chain: 1 us for the table and tensor memory, 3.5 us until the first keys are unpacked, 2.7 us a
 // tile and stream.
 #include <algorithm>
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_narrow_kernel(const Attend
 // sum_s w_s with w_s = 2^(m_s - M) l_s, in the splits' order (o_s: the split's own output; weighed by shares of 1, so that
 // no sum passes the range of the values).  merges: [n][4] = (slot, first query token, splits,
 // first partial tile).  Bound by memory: 0.14 GB of partial sums (2048 tokens x 32 heads in four splits,
-// d = 128) in 44 us.
+// d = 128) in 48 us.
 constexpr int kMergeWarps = 8;
 
 template <int D, bool BF16>

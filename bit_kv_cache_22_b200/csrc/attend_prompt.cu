@@ -19,10 +19,12 @@
 // Tensor memory (512 columns): S0 | S1 | O0 | O1, P over the first half of its S.
 //
 // Bound by the tensor cores and, under a lasting load, by the power limit.  One prompt of 8192 tokens (32
-// query / 8 kv heads, d = 128, bf16; 0.55 TFLOP): 414 us in a burst, 1327 TFLOP/s, and 477 us where
-// calls follow one another for a second.  Two of 4096 (32 / 32 heads, fp16): 252 and 294 us.  Twelve of
-// 32 to 2048 (32 / 8 heads; 0.12 TFLOP): 133 and 154 us; with a CTA a piece instead of persistent ones
-// 156 us in a burst.  A few of up to 160 (2 heads, d = 64): 8 us.
+// query / 8 kv heads, d = 128, bf16; 0.55 TFLOP): 418 us in a burst, 1315 TFLOP/s, and 485 us where
+// calls follow one another for a second.  Two of 4096 (32 / 32 heads, fp16): 255 and 303 us.  Twelve of
+// 32 to 2048 (32 / 8 heads; 0.12 TFLOP): 137 and 156 us; with a CTA a piece instead of persistent ones
+// 156 us in a burst.  A few of up to 160 (2 heads, d = 64): 8 us.  What short jobs cost is their border, where
+// the first product of the next job waits for both streams' last of this one: the twelve are 1424 jobs of
+// 6 key tiles on average, whose padding (1.13) and dealing (1.05) explain little of the way from 72 us.
 #include <cuda.h>
 
 #include <cstdint>

@@ -9,11 +9,12 @@
 //                    softmax: 2 x 128 x 208 + 128 x 80 <= 384 x 168)
 //
 // Bound by the tensor cores, at the clock that the power limit leaves: 2048 tokens behind 126976 (32
-// query / 8 kv heads, d = 128, 2-bit; 4.29 TFLOP) take 3.65 ms, 1177 TFLOP/s, with 0.13 ms of staging
-// before and 0.04 ms of joining splits behind.  With the codes unpacked in the attention kernel, anew for
-// each 256 query rows and beside the softmax, an earlier form took 11.8 ms.  Six chunks of 66 to 613 tokens behind 586 to 2557 (32 / 32 heads,
-// 4-bit; 45 GFLOP): 92 us, after 63 us of staging.  There pieces of fewer than 256 rows leave tensor
-// core rows idle, and CTAs of 7 to 21 key tiles start 2.6 times on each SM.
+// query / 8 kv heads, d = 128, 2-bit; 4.29 TFLOP) take 3.74 ms in a burst, 1147 TFLOP/s, with 0.12 ms of
+// staging before and 0.05 ms of joining splits behind.  With the codes unpacked in the attention kernel,
+// anew for each 256 query rows and beside the softmax, an earlier form took 11.8 ms.  Six chunks of 66 to
+// 613 tokens behind 586 to 2557 (32 / 32 heads, 4-bit; 45 GFLOP): 95 us, after 63 us of staging.  There
+// pieces of fewer than 256 rows leave tensor core rows idle (1.35 times the operations), and CTAs of 7 to
+// 21 key tiles start 2.6 times on each SM, each with its table, its tensor memory and its first tiles.
 #include <cstdint>
 
 #include "attend_cache.cuh"
@@ -55,8 +56,8 @@ struct Staged {
 
 // CTA (x, h): keys (x even) or values of key tile x / 2 of the wide slots, or query tile x - 2 n_kv_tiles.
 // The tile is put together in shared memory and leaves in one copy.  Bound by the latency of a tile's
-// chain -- page, codes and scales, parameters through shared memory -- so tiles are CTAs of four
-// warps, five or more an SM: 0.18 GB of tiles in 63 us (keys and values of 11243 tokens, 32 heads, d = 128,
+// chain -- page, codes and scales, parameters through shared memory -- (issue 50% of the cycles, memory 43%
+// of its rate), so tiles are CTAs of four warps, five or more an SM: 0.18 GB of tiles in 63 us (keys and values of 11243 tokens, 32 heads, d = 128,
 // 4-bit).  With both in one CTA of eight warps whose lanes store their 8 bytes to global memory, 73
 // us; with CTAs of four heads that fetch the next head's codes ahead, but hold 96 registers, 94 us.
 template <int D, int N, bool BF16>

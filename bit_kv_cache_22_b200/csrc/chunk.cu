@@ -69,9 +69,9 @@ __global__ void __launch_bounds__(kRowThreads) chunk_rows_kernel(const PagedView
 // One warp per (16-token tile of a slot that meets its chunk, kv head, keys or values): the tile's
 // tokens as e.  A quantized tile's words are unpacked from the fragment layout (include/kvq.h): each
 // lane holds two tokens x four channels per chunk of keys, two channels x four tokens of values; the
-// elements go through shared memory so that rows leave in 16-byte vectors.  Bound by the latency of a
-// warp's chain (offsets, page, codes, parameters), so keys and values are warps of their own: 43 us
-// for four prompts of 8192 tokens (8 kv heads, d = 128, 2-bit; 0.16 GB moved), 50 us with both in one.
+// elements go through shared memory so that rows leave in 16-byte vectors.  Bound by instruction issue (74%
+// of the cycles) and the latency of a warp's chain (offsets, page, codes, parameters), so keys and values
+// are warps of their own: 43 us for four prompts of 8192 tokens (8 kv heads, d = 128, 2-bit; 0.16 GB moved), 50 us with both in one.
 // Rows turned about vector by vector instead of padded have no bank conflicts but more address
 // arithmetic: 48 us.
 constexpr int kReadWarps = 4;

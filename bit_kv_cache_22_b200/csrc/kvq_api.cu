@@ -1146,10 +1146,11 @@ struct Piece {
 // costs kCtaTiles more than its share, a split one kSplitTiles (its partial results, and joining
 // them).
 // A slot of at most this many query rows (tokens x query heads of a kv head) is narrow: its codes are
-// unpacked where they are used.  With more, its softmax fills more than a warp a stream, which
-// unpacking beside it slows down: two slots of 66 and 105 rows over 2000 tokens, 32 heads, beside four
-// wide ones took 84 us as a launch of their own, with the joining of its splits, and 43 us among the
-// wide ones.
+// unpacked where they are used.  The narrow kernel's softmax holds no more rows, and up to there it is the
+// faster: 32 slots of 500, 2000, 8000 and 16000 tokens (8 kv heads, d = 128, 2-bit) with 32 rows each take
+// 46, 95, 295 and 554 us as narrow slots and 56, 144, 459 and 867 us as wide ones (4 rows: 44, 93, 292,
+// 549 and 55, 140, 451, 849; 40 rows, wide: 56, 146, 468, 883), four such slots 25, 37, 63 and 89 us and
+// 27, 41, 85 and 134 us.
 constexpr int64_t kNarrowRows = 32;
 constexpr int64_t kCtaTiles = 4, kSplitTiles = 4, kLeastShare = 8;
 constexpr size_t kMostSimulated = 4096;

@@ -271,7 +271,7 @@ struct AttendArgs {
     int stall_tile;              // bounds-check builds: the first CTA's keys end before its key tile
                                  // stall_tile - 1 (0: none), so that what waits for them gives up
 };
-// Over the cache: slots of at most one query tile, slots of more, and the joining of splits.
+// Over the cache: slots of at most 32 query rows, slots of more, and the joining of splits.
 cudaError_t launch_attend_narrow(const AttendArgs &a, cudaStream_t s);
 cudaError_t launch_attend_wide(const AttendArgs &a, cudaStream_t s);
 cudaError_t launch_merge_splits(const AttendArgs &a, cudaStream_t s);

@@ -562,10 +562,14 @@ KVQ_API kvq_status kvq_paged_read_chunk(kvq_paged *cache, const kvq_chunk *plan,
  * q, o: e [tokens][q_heads][d]; o must not overlap q.  starts[b] + counts[b] must not pass the
  * slot's length (KVQ_ERR_STATE); rows of which the device length leaves nothing to see give
  * zeros.  Logits, softmax statistics and sums are fp32; what meets in a product -- queries, keys,
- * weights, values -- is rounded to fp16 (11 bits) under powers of two that keep it in range (a weight
- * also by up to 2^-30 of the largest share, weight x value, of its row's sum), the output once to e.  (The keys' rounding moves a logit by up to 2^-11 sum_c |q_c k_c| / sqrt(d): beside
- * bf16 outputs little, beside fp16 ones several roundings where single channels are large.)  Scales s <= 2^31 and queries |q| <= 2^30, as for decoding; finite inputs: a
- * NaN or infinity reaches rows of its own slot only.  `workspace`: plan->workspace bytes of device
+ * weights, values -- is rounded to fp16 (11 bits) under powers of two that keep it in range (a token's
+ * weighted value also by up to 2^-26 of the largest weight x the largest value of some 32 tokens that
+ * its row sees), the output once to e.  The keys' rounding moves a logit by up to 2^-11 sum_c |q_c k_c|
+ * / sqrt(d), beside bf16 outputs by twice that, as their scales are rounded first: with one channel
+ * ten times the others, outputs are off by 0.0019 to 0.0023 in bf16, whose own rounding is 0.0017, and
+ * by 0.0006 to 0.0013 in fp16, whose own is 0.0002 (the decode kernel, which serves decode steps, keeps
+ * 16 bits).  Scales s <= 2^31 and queries |q| <= 2^30, as for decoding; finite inputs: a NaN or
+ * infinity reaches rows of its own slot only.  `workspace`: plan->workspace bytes of device
  * scratch, 16-byte aligned (NULL where that is 0; a slot with more than 32 query rows per kv head --
  * new tokens x query heads -- takes 4 head_dim bytes per token and kv head of what it holds, as its
  * keys and values are unpacked once for all its rows); calls that may overlap on the GPU need
