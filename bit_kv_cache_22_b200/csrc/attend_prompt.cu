@@ -60,7 +60,7 @@ constexpr float kLazyMax = 8.0f;
 // stays in range before it is divided.
 template <bool BF16>
 constexpr float kTopWeight = BF16 ? -24.0f : 7.0f;
-constexpr float kNoMax = -1e30f;           // below it: no logits
+constexpr float kNoMax = -3.4e38f;         // below it: no logits
 
 // A CTA's piece of work: up to 2 * tpt tokens of one slot's prompt from token q0 on, for kv head h.
 struct Job {

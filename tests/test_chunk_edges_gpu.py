@@ -219,7 +219,7 @@ def test_large_logits_over_the_cache(dtype, size, counts):
     assert clear > 0
 
 
-@pytest.mark.parametrize("dtype,size", [(BF16, 2.0 ** 16), (FP16, 2.0 ** 13), (BF16, 2.0 ** 20)])
+@pytest.mark.parametrize("dtype,size", [(BF16, 2.0 ** 16), (FP16, 2.0 ** 13), (BF16, 2.0 ** 20), (BF16, 2.0 ** 56)])
 def test_large_logits_of_prompts(dtype, size):
     lens, hq, hkv, d = [600, 1, 130], 4, 2, 128
     gen = torch.Generator().manual_seed(5)
@@ -232,6 +232,15 @@ def test_large_logits_of_prompts(dtype, size):
                                ct.wide(v[rows]).transpose(1, 0, 2), 0, dtype, f"rows {rows}")
         at += n
     assert clear > 0
+
+
+def test_rows_whose_logits_all_lie_far_below_zero():
+    """One token a prompt, attended by queries opposite to its key: logits of -2^113, weight 1."""
+    gen = torch.Generator().manual_seed(9)
+    k, v = ((torch.randn(20, 2, 128, generator=gen) * s).to(BF16) for s in (2.0 ** 55, 1.0))
+    plan = kvq.plan_prompt([1] * 20, 2, 2, 128)
+    got = kvq.prompt_attention(plan, -k.cuda(), k.cuda(), v.cuda())
+    assert torch.equal(got.cpu(), v)
 
 
 # ------------------------------------------------------------------ values of different size, large values
