@@ -1,5 +1,6 @@
 // tensor_core.cuh -- the fifth-generation tensor core (tcgen05), tensor memory, TMA and mbarrier
-// instructions the attention kernels use, one function each, and the descriptors they take.
+// instructions the attention kernels use, one function each, and the descriptors they take; and the
+// step of the softmax that they share.
 #pragma once
 
 #include <cstdint>
@@ -264,7 +265,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // A softmax takes y - m, y = sc x, in one operation, which does not round y.  Where |y| passes 2^20 (its
 // steps are 1/16 and more) that is no longer small at the maximum itself: m is a rounded y.  Such
-// logits are rounded first, as m was, so that the largest weight is 1 and no weight overflows.
+// logits are rounded first, as m was, so that the largest weight is what it should be and none overflows.
 constexpr float kFarLogit = 1048576.0f;
 template <int N>
 __device__ __forceinline__ void subtract_rounded(uint32_t *x, float sc, float m) {

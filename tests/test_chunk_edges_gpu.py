@@ -22,10 +22,10 @@ def pair(slots=4, hq=8, hkv=2, d=128, G=32, Gv=32, R=128, bits=2, sym=False, dty
     return ct.Pair(slots, hq, hkv, d, G, Gv, R, bits, sym, dtype, capacity, page, seed)
 
 
-def check_prompt(got, q, k, v, lens, what=""):
+def check_prompt(got, q, k, v, lens, what="", every=1):
     at = 0
-    for n in lens:
-        if n:
+    for i, n in enumerate(lens):
+        if n and i % every == 0:
             rows = slice(at, at + n)
             plain = ct.attend(ct.wide(q[rows]), ct.wide(k[rows]).transpose(1, 0, 2), ct.wide(v[rows]).transpose(1, 0, 2), 0)
             ct.check_attention(got[rows], *plain, n, q.dtype, False, f"{what} rows {rows}")
@@ -98,7 +98,7 @@ def test_several_hundred_short_prompts(hq, hkv, d, lo, hi):
     dev = [x.cuda() for x in (q, k, v)]
     got = [kvq.prompt_attention(plan, *dev) for _ in range(5)]
     plan.check_device()
-    check_prompt(got[0], q, k, v, lens)
+    check_prompt(got[0], q, k, v, lens, every=4)
     assert all(torch.equal(got[0], x) for x in got[1:])
 
 
